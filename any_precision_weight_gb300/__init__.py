@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import numpy as np
 
@@ -38,12 +39,16 @@ PW_PLANE_HOST, PW_PLANE_HOST_PAGED, PW_PLANE_MOVING, PW_PLANE_DEVICE = 0, 1, 2, 
 KIND_GATE_UP = 0
 KIND_DOWN = 1
 MAX_BITS = 8
+PW_F16, PW_BF16, PW_F32 = 0, 1, 2
+MAX_K_I8 = 131071
+MAX_TOP = 32
 
 _lib = None
 
 _sz = ctypes.c_size_t
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
+_i64 = ctypes.c_int64
 _pi = ctypes.POINTER(ctypes.c_int)
 
 _SIGS = {
@@ -82,6 +87,11 @@ _SIGS = {
     "pw_block_release": (_i, [_vp, _i, _i, _i, _i, ctypes.POINTER(_vp)]),
     "pw_block_attach_pages": (_i, [_vp, _i, _i, _i, ctypes.POINTER(_vp)]),
     "pw_plane_states": (_i, [_vp, _i, _i, _i, _pi]),
+    "pw_rms_norm": (_i, [_vp, _i64, _vp, _i64, _vp, ctypes.c_float, _i, _i, _i, _vp, _i64, _vp, _i64, _vp, _i64,
+                         _vp, _vp]),
+    "pw_quant_i8": (_i, [_vp, _i64, _i, _i, _i, _vp, _i64, _vp, _vp]),
+    "pw_linear_i8": (_i, [_vp, _i64, _vp, _vp, _i64, _vp, _vp, _i, _i, _i, _i, _vp, _i64, _vp]),
+    "pw_logprobs": (_i, [_vp, _i64, _i, _i, _i, _vp, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp]),
 }
 
 
@@ -495,3 +505,169 @@ class PagedMoE:
             self.close()
         except Exception:
             pass
+
+
+# ----------------------------------------------------------------------------- operators around the layer
+
+_codes = None
+
+
+def _code(dtype) -> int:
+    """The C ABI's code of a torch element type."""
+    global _codes
+    if _codes is None:
+        import torch
+        _codes = {torch.float16: PW_F16, torch.bfloat16: PW_BF16, torch.float32: PW_F32}
+    try:
+        return _codes[dtype]
+    except KeyError:
+        raise TypeError(f"{dtype}: float16, bfloat16 or float32 is needed") from None
+
+
+def _rows(t, name: str, dtype=None, shape=None):
+    """Row stride of a CUDA matrix whose rows are consecutive elements."""
+    if not t.is_cuda or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: a CUDA matrix with consecutive row elements is needed")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name}: {dtype} is needed, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(shape)} is needed, got {tuple(t.shape)}")
+    # a row alone has no stride of its own
+    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 15) // 16 * 16
+
+
+def _vec(t, name: str, dtype, n: int):
+    if not t.is_cuda or t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name}: a contiguous CUDA vector of {n} {dtype} is needed")
+    return t.data_ptr()
+
+
+def rows_i8(T: int, K: int, device="cuda"):
+    """An uninitialised int8 matrix [T][K] whose rows start on 16-byte
+    boundaries, as pw_linear_i8 wants them (a view of a padded one)."""
+    import torch
+    return torch.empty((T, (K + 15) // 16 * 16), dtype=torch.int8, device=device)[:, :K]
+
+
+def _norm(what, x, weight, eps, residual, sum_out, y, q, scale, stream):
+    T, H = x.shape
+    dt = x.dtype
+    rc = lib().pw_rms_norm(
+        x.data_ptr(), _rows(x, "x"), _ptr(residual), 0 if residual is None else _rows(residual, "residual", dt, x.shape),
+        _vec(weight, "weight", dt, H), eps, T, H, _code(dt),
+        _ptr(sum_out), 0 if sum_out is None else _rows(sum_out, "sum_out", dt, x.shape),
+        _ptr(y), 0 if y is None else _rows(y, "out", dt, x.shape),
+        _ptr(q), 0 if q is None else _rows(q, "q", _torch().int8, x.shape),
+        None if scale is None else _vec(scale, "scale", _torch().float32, T), _stream(stream))
+    _check(rc, what)
+
+
+def _torch():
+    import torch
+    return torch
+
+
+def pw_rms_norm(x, weight, eps: float = 1e-6, residual=None, out=None, sum_out=None, stream=None):
+    """Root-mean-square norm of the rows of x (+ residual).  Returns out, or
+    (out, sum_out) with a residual; sum_out (the new residual stream) may be
+    the residual itself."""
+    torch = _torch()
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if residual is not None and sum_out is None:
+        sum_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _norm("pw_rms_norm", x, weight, eps, residual, sum_out, out, None, None, stream)
+    return out if residual is None else (out, sum_out)
+
+
+def pw_rms_norm_i8(x, weight, eps: float = 1e-6, residual=None, q=None, scale=None, out=None, sum_out=None,
+                   stream=None):
+    """pw_rms_norm with an int8 output and a scale per row: the input of
+    pw_linear_i8.  ``out`` also receives the unquantised norm if given.
+    Returns (q, scale), or (q, scale, sum_out) with a residual."""
+    torch = _torch()
+    T, H = x.shape
+    if q is None:
+        q = rows_i8(T, H, x.device)
+    if scale is None:
+        scale = torch.empty(T, dtype=torch.float32, device=x.device)
+    if residual is not None and sum_out is None:
+        sum_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _norm("pw_rms_norm_i8", x, weight, eps, residual, sum_out, out, q, scale, stream)
+    return (q, scale) if residual is None else (q, scale, sum_out)
+
+
+def pw_quant_i8(x, q=None, scale=None, stream=None):
+    """(q, scale): the rows of x as int8 with one scale per row."""
+    torch = _torch()
+    T, K = x.shape
+    if q is None:
+        q = rows_i8(T, K, x.device)
+    if scale is None:
+        scale = torch.empty(T, dtype=torch.float32, device=x.device)
+    _check(lib().pw_quant_i8(x.data_ptr(), _rows(x, "x"), T, K, _code(x.dtype), q.data_ptr(),
+                             _rows(q, "q", torch.int8, x.shape), _vec(scale, "scale", torch.float32, T),
+                             _stream(stream)), "pw_quant_i8")
+    return q, scale
+
+
+def pw_linear_i8(x, x_scale, w, w_scale, bias=None, out=None, out_dtype=None, stream=None):
+    """out [T][N] = (x . w^T) * x_scale[t] * w_scale[n] + bias[n], x [T][K] and
+    w [N][K] int8 with 16-byte aligned rows (rows_i8), the sum exact.  out has
+    type out_dtype (default float16) where it is not given."""
+    torch = _torch()
+    T, K = x.shape
+    N = w.shape[0]
+    if w.shape[1] != K:
+        raise ValueError(f"pw_linear_i8: x has {K} columns and w {w.shape[1]}")
+    if out is None:
+        out = torch.empty((T, N), dtype=out_dtype or torch.float16, device=x.device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"pw_linear_i8: out is {out.dtype}, not {out_dtype}")
+    f32, i8 = torch.float32, torch.int8
+    rc = lib().pw_linear_i8(x.data_ptr(), _rows(x, "x", i8), _vec(x_scale, "x_scale", f32, T), w.data_ptr(),
+                            _rows(w, "w", i8), _vec(w_scale, "w_scale", f32, N),
+                            None if bias is None else _vec(bias, "bias", out.dtype, N), T, N, K, _code(out.dtype),
+                            out.data_ptr(), _rows(out, "out", None, (T, N)), _stream(stream))
+    _check(rc, "pw_linear_i8")
+    return out
+
+
+class LogProbs(NamedTuple):
+    """What pw_logprobs returns; logprob and rank are None without ids,
+    top_ids and top_logprobs are [T][0] without alternatives."""
+    logprob: object
+    rank: object
+    entropy: object
+    top_ids: object
+    top_logprobs: object
+
+
+def pw_logprobs(logits, ids=None, top: int = 0, out=None, stream=None):
+    """Log probability and rank of the given tokens, entropy and the ``top``
+    likeliest alternatives of every row of logits.  ids: int32 or int64 [T], or
+    None.  out: a LogProbs (or tuple) of tensors to write into."""
+    torch = _torch()
+    T, V = logits.shape
+    f32, i32 = torch.float32, torch.int32
+    if out is None:
+        dev = logits.device
+        new = lambda dt, *shape: torch.empty(shape, dtype=dt, device=dev)
+        out = (None if ids is None else new(f32, T), None if ids is None else new(i32, T), new(f32, T),
+               new(i32, T, top), new(f32, T, top))
+    lp, rank, ent, ti, tl = out
+    ids64 = 0
+    if ids is not None:
+        ids64 = int(ids.dtype == torch.int64)
+        pid = _vec(ids, "ids", torch.int64 if ids64 else i32, T)
+    for name, t, dt in (("top_ids", ti, i32), ("top_logprobs", tl, f32)):
+        if top and (t.shape != (T, top) or t.dtype != dt or not t.is_contiguous() or not t.is_cuda):
+            raise ValueError(f"{name}: a contiguous CUDA matrix [{T}][{top}] of {dt} is needed")
+    rc = lib().pw_logprobs(logits.data_ptr(), _rows(logits, "logits"), _code(logits.dtype), T, V,
+                           None if ids is None else pid, ids64, top,
+                           None if lp is None else _vec(lp, "logprob", f32, T),
+                           None if rank is None else _vec(rank, "rank", i32, T),
+                           None if ent is None else _vec(ent, "entropy", f32, T),
+                           _ptr(ti) if top else None, _ptr(tl) if top else None, _stream(stream))
+    _check(rc, "pw_logprobs")
+    return LogProbs(lp, rank, ent, ti, tl)

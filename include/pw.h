@@ -535,6 +535,100 @@ int pw_noalloc_status(pw_stream_t s, int* status);
  */
 int pw_profile_attach(void* const* events, int n_events);
 
+/* ------------------------------------------------------------------ operators around the layer */
+
+/*
+ * The rest of a decode step around the expert layer: the norm in front of it,
+ * products with dense int8 weights (router, shared expert, projections, head)
+ * and the log probabilities of what the model answers with.  The pages leave
+ * these to the serving system; they are runtime additions of this library.
+ *
+ * Conventions of the four calls: device pointers; element types are PW_F16,
+ * PW_BF16 or PW_F32; a matrix is rows of consecutive elements whose starts are
+ * `ld*` elements apart (ld >= the row's length, 64-bit), so padded and sliced
+ * matrices need no copy.  Work is enqueued on `s` and nothing waits; no
+ * workspace is needed and nothing is kept between calls, so calls on several
+ * streams may overlap.  T = 0 is a no-op.  A call may be captured into a CUDA
+ * graph.  Results do not depend on what else runs: a call repeated on the same
+ * inputs gives the same bits.
+ */
+#define PW_F16  0
+#define PW_BF16 1
+#define PW_F32  2
+
+#define PW_MAX_K_I8 131071   /* longest row of pw_linear_i8: its int32 sums cannot overflow */
+#define PW_MAX_TOP  32       /* most alternatives of pw_logprobs */
+
+/*
+ * pw_rms_norm -- root-mean-square norm of rows, with the residual's addition.
+ *   s = x + residual (fp32; residual NULL: s = x)
+ *   sum_out[t] = s, rounded once (may be x or residual themselves)
+ *   y[t]       = s * weight / sqrt(mean(s^2) + eps), rounded once from the
+ *                fp32 s (not from the rounded sum_out)
+ *   scale[t]   = max|y[t]| / 127;  q[t] = y[t] / scale[t], rounded to the
+ *                nearest whole number (ties to even), y unrounded; a row of
+ *                zeros has scale 0 and q 0
+ * x, residual, weight [H], sum_out and y have element type dtype; q is int8,
+ * scale fp32 [T].  residual, sum_out, y and q (with scale) may each be NULL,
+ * y and q not both.  A row with a NaN or an infinity gives non-finite y and
+ * scale.  Rows on 16-byte boundaries (q: 8, or 4 for PW_F32) are read 16 bytes
+ * at a time, others element by element.
+ * Errors: PW_EINVAL (shapes, strides, null or misaligned pointers, dtype, eps
+ * negative or NaN), PW_ECUDA.
+ */
+int pw_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight, float eps,
+                int T, int H, int dtype, void* sum_out, int64_t lds, void* y, int64_t ldy, int8_t* q,
+                int64_t ldq, float* scale, pw_stream_t s);
+
+/*
+ * pw_quant_i8 -- rows to int8 with one scale per row: scale[t] = max|x[t]| / 127,
+ * q[t] = x[t] / scale[t] rounded to the nearest whole number (ties to even).
+ * For activations that no norm makes (rows are tokens) and for dense weights
+ * (rows are output channels).  A row of zeros has scale 0 and q 0; a row with a
+ * NaN or an infinity has that scale and q 0.
+ * Errors: PW_EINVAL (shapes, strides, null or misaligned pointers, dtype), PW_ECUDA.
+ */
+int pw_quant_i8(const void* x, int64_t ldx, int T, int K, int dtype, int8_t* q, int64_t ldq, float* scale,
+                pw_stream_t s);
+
+/*
+ * pw_linear_i8 -- product of int8 rows with int8 weights:
+ *   out[t][n] = (sum_k x[t][k] * w[n][k]) * x_scale[t] * w_scale[n] + bias[n]
+ * The sum is exact in int32; the rest is fp32, rounded once to out_dtype.
+ *   x  [T][K] int8 with x_scale [T];  w [N][K] int8 with w_scale [N]: as
+ *      pw_rms_norm and pw_quant_i8 write them
+ *   bias [N] of out_dtype or NULL;  out [T][N] of out_dtype
+ * Rows of x and w start on 16-byte boundaries (pointers and ldx, ldw multiples
+ * of 16); K itself is any number from 1 to PW_MAX_K_I8, and bytes past K are
+ * never used.  out has any stride.
+ * Errors: PW_EINVAL (shapes, strides, null or misaligned pointers, dtype), PW_ECUDA.
+ */
+int pw_linear_i8(const int8_t* x, int64_t ldx, const float* x_scale, const int8_t* w, int64_t ldw,
+                 const float* w_scale, const void* bias, int T, int N, int K, int out_dtype, void* out,
+                 int64_t ldo, pw_stream_t s);
+
+/*
+ * pw_logprobs -- what a row of logits says about a token, and its alternatives.
+ *   logits  [T][V] of dtype;  ids [T] int32 (ids64 = 0) or int64, or NULL
+ *   logprob [T] or NULL   ln softmax(logits[t])[ids[t]]; 0 where ids[t] is
+ *                         outside [0, V) (no token: nothing is read for it)
+ *   rank    [T] or NULL   how many tokens come before ids[t] in descending
+ *                         order, ties to the lower index; -1 for no token or a NaN
+ *   entropy [T] or NULL   -sum p ln p in nats (masked tokens, -inf, add nothing)
+ *   top     0..PW_MAX_TOP alternatives: top_ids [T][top] int32 in descending
+ *                         order, ties to the lower index, and their log
+ *                         probabilities top_logprobs [T][top]
+ * A row of -inf alone (a mask that leaves nothing): logprob and top_logprobs
+ * are -inf, entropy is 0.  A row with a NaN or +inf has NaN there; a NaN is
+ * never an alternative (places left over hold id -1 and NaN).
+ * Sums are fp32; rows start anywhere.
+ * Errors: PW_EINVAL (shapes, top > V, missing outputs, strides, null or
+ * misaligned pointers, dtype), PW_ECUDA.
+ */
+int pw_logprobs(const void* logits, int64_t ld, int dtype, int T, int V, const void* ids, int ids64, int top,
+                float* logprob, int32_t* rank, float* entropy, int32_t* top_ids, float* top_logprobs,
+                pw_stream_t s);
+
 #ifdef __cplusplus
 }
 #endif
