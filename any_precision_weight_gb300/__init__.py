@@ -91,6 +91,7 @@ _SIGS = {
                          _vp, _vp]),
     "pw_quant_i8": (_i, [_vp, _i64, _i, _i, _i, _vp, _i64, _vp, _vp]),
     "pw_linear_i8": (_i, [_vp, _i64, _vp, _vp, _i64, _vp, _vp, _i, _i, _i, _i, _vp, _i64, _vp]),
+    "pw_linear_i8_status": (_i, [_vp, _pi]),
     "pw_logprobs": (_i, [_vp, _i64, _i, _i, _i, _vp, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp]),
 }
 
@@ -509,35 +510,59 @@ class PagedMoE:
 
 # ----------------------------------------------------------------------------- operators around the layer
 
-_codes = None
+_torch_mod = None
+_codes = {}
+
+
+def _torch():
+    """torch, imported at the first call that needs it (and the C ABI's codes
+    of its element types)."""
+    global _torch_mod
+    if _torch_mod is None:
+        import torch
+        _codes.update({torch.float16: PW_F16, torch.bfloat16: PW_BF16, torch.float32: PW_F32})
+        _torch_mod = torch
+    return _torch_mod
 
 
 def _code(dtype) -> int:
     """The C ABI's code of a torch element type."""
-    global _codes
-    if _codes is None:
-        import torch
-        _codes = {torch.float16: PW_F16, torch.bfloat16: PW_BF16, torch.float32: PW_F32}
     try:
         return _codes[dtype]
     except KeyError:
         raise TypeError(f"{dtype}: float16, bfloat16 or float32 is needed") from None
 
 
-def _rows(t, name: str, dtype=None, shape=None):
+def _raw_stream(torch, stream, t):
+    """The given stream, or the current one of t's device (looked up without
+    building a Stream object, which costs more than a launch)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _rows(t, name: str, dtype, shape):
     """Row stride of a CUDA matrix whose rows are consecutive elements."""
-    if not t.is_cuda or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name}: a CUDA matrix with consecutive row elements is needed")
-    if dtype is not None and t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: {dtype} is needed, got {t.dtype}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(shape)} is needed, got {tuple(t.shape)}")
+    if t.shape != shape or not t.is_cuda:
+        raise ValueError(f"{name}: a CUDA matrix of shape {tuple(shape)} is needed, got {tuple(t.shape)} on {t.device}")
+    ld, one = t.stride()
+    if one != 1 and shape[1] > 1:
+        raise ValueError(f"{name}: the elements of a row must be consecutive")
     # a row alone has no stride of its own
-    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 15) // 16 * 16
+    return ld if shape[0] > 1 else (shape[1] + 15) // 16 * 16
+
+
+def _matrix(t, name: str):
+    """(rows, columns) of a matrix."""
+    if t.dim() != 2:
+        raise ValueError(f"{name}: a matrix is needed, got {t.dim()} dimensions")
+    return t.shape
 
 
 def _vec(t, name: str, dtype, n: int):
-    if not t.is_cuda or t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    if t.dtype is not dtype or not t.is_cuda or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous CUDA vector of {n} {dtype} is needed")
     return t.data_ptr()
 
@@ -545,26 +570,26 @@ def _vec(t, name: str, dtype, n: int):
 def rows_i8(T: int, K: int, device="cuda"):
     """An uninitialised int8 matrix [T][K] whose rows start on 16-byte
     boundaries, as pw_linear_i8 wants them (a view of a padded one)."""
-    import torch
+    torch = _torch()
     return torch.empty((T, (K + 15) // 16 * 16), dtype=torch.int8, device=device)[:, :K]
 
 
-def _norm(what, x, weight, eps, residual, sum_out, y, q, scale, stream):
-    T, H = x.shape
+def _norm(torch, what, x, shape, weight, eps, residual, sum_out, y, q, scale, stream):
     dt = x.dtype
-    rc = lib().pw_rms_norm(
-        x.data_ptr(), _rows(x, "x"), _ptr(residual), 0 if residual is None else _rows(residual, "residual", dt, x.shape),
-        _vec(weight, "weight", dt, H), eps, T, H, _code(dt),
-        _ptr(sum_out), 0 if sum_out is None else _rows(sum_out, "sum_out", dt, x.shape),
-        _ptr(y), 0 if y is None else _rows(y, "out", dt, x.shape),
-        _ptr(q), 0 if q is None else _rows(q, "q", _torch().int8, x.shape),
-        None if scale is None else _vec(scale, "scale", _torch().float32, T), _stream(stream))
-    _check(rc, what)
-
-
-def _torch():
-    import torch
-    return torch
+    pr = ps = py = pq = pc = None
+    lr = ls = ly = lq = 0
+    lx = _rows(x, "x", dt, shape)
+    if residual is not None:
+        lr, pr = _rows(residual, "residual", dt, shape), residual.data_ptr()
+    if sum_out is not None:
+        ls, ps = _rows(sum_out, "sum_out", dt, shape), sum_out.data_ptr()
+    if y is not None:
+        ly, py = _rows(y, "out", dt, shape), y.data_ptr()
+    if q is not None:
+        lq, pq = _rows(q, "q", torch.int8, shape), q.data_ptr()
+        pc = _vec(scale, "scale", torch.float32, shape[0])
+    _check(lib().pw_rms_norm(x.data_ptr(), lx, pr, lr, _vec(weight, "weight", dt, shape[1]), eps, shape[0], shape[1],
+                             _code(dt), ps, ls, py, ly, pq, lq, pc, _raw_stream(torch, stream, x)), what)
 
 
 def pw_rms_norm(x, weight, eps: float = 1e-6, residual=None, out=None, sum_out=None, stream=None):
@@ -572,11 +597,12 @@ def pw_rms_norm(x, weight, eps: float = 1e-6, residual=None, out=None, sum_out=N
     (out, sum_out) with a residual; sum_out (the new residual stream) may be
     the residual itself."""
     torch = _torch()
+    shape = _matrix(x, "x")
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
     if residual is not None and sum_out is None:
-        sum_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _norm("pw_rms_norm", x, weight, eps, residual, sum_out, out, None, None, stream)
+        sum_out = torch.empty(shape, dtype=x.dtype, device=x.device)
+    _norm(torch, "pw_rms_norm", x, shape, weight, eps, residual, sum_out, out, None, None, stream)
     return out if residual is None else (out, sum_out)
 
 
@@ -586,28 +612,29 @@ def pw_rms_norm_i8(x, weight, eps: float = 1e-6, residual=None, q=None, scale=No
     pw_linear_i8.  ``out`` also receives the unquantised norm if given.
     Returns (q, scale), or (q, scale, sum_out) with a residual."""
     torch = _torch()
-    T, H = x.shape
+    shape = _matrix(x, "x")
     if q is None:
-        q = rows_i8(T, H, x.device)
+        q = rows_i8(*shape, x.device)
     if scale is None:
-        scale = torch.empty(T, dtype=torch.float32, device=x.device)
+        scale = torch.empty(shape[0], dtype=torch.float32, device=x.device)
     if residual is not None and sum_out is None:
-        sum_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _norm("pw_rms_norm_i8", x, weight, eps, residual, sum_out, out, q, scale, stream)
+        sum_out = torch.empty(shape, dtype=x.dtype, device=x.device)
+    _norm(torch, "pw_rms_norm_i8", x, shape, weight, eps, residual, sum_out, out, q, scale, stream)
     return (q, scale) if residual is None else (q, scale, sum_out)
 
 
 def pw_quant_i8(x, q=None, scale=None, stream=None):
     """(q, scale): the rows of x as int8 with one scale per row."""
     torch = _torch()
-    T, K = x.shape
+    shape = _matrix(x, "x")
+    T, K = shape
     if q is None:
         q = rows_i8(T, K, x.device)
     if scale is None:
         scale = torch.empty(T, dtype=torch.float32, device=x.device)
-    _check(lib().pw_quant_i8(x.data_ptr(), _rows(x, "x"), T, K, _code(x.dtype), q.data_ptr(),
-                             _rows(q, "q", torch.int8, x.shape), _vec(scale, "scale", torch.float32, T),
-                             _stream(stream)), "pw_quant_i8")
+    _check(lib().pw_quant_i8(x.data_ptr(), _rows(x, "x", x.dtype, shape), T, K, _code(x.dtype), q.data_ptr(),
+                             _rows(q, "q", torch.int8, shape), _vec(scale, "scale", torch.float32, T),
+                             _raw_stream(torch, stream, x)), "pw_quant_i8")
     return q, scale
 
 
@@ -616,21 +643,26 @@ def pw_linear_i8(x, x_scale, w, w_scale, bias=None, out=None, out_dtype=None, st
     w [N][K] int8 with 16-byte aligned rows (rows_i8), the sum exact.  out has
     type out_dtype (default float16) where it is not given."""
     torch = _torch()
-    T, K = x.shape
-    N = w.shape[0]
-    if w.shape[1] != K:
-        raise ValueError(f"pw_linear_i8: x has {K} columns and w {w.shape[1]}")
+    T, K = _matrix(x, "x")
+    N = _matrix(w, "w")[0]
     if out is None:
         out = torch.empty((T, N), dtype=out_dtype or torch.float16, device=x.device)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"pw_linear_i8: out is {out.dtype}, not {out_dtype}")
-    f32, i8 = torch.float32, torch.int8
-    rc = lib().pw_linear_i8(x.data_ptr(), _rows(x, "x", i8), _vec(x_scale, "x_scale", f32, T), w.data_ptr(),
-                            _rows(w, "w", i8), _vec(w_scale, "w_scale", f32, N),
-                            None if bias is None else _vec(bias, "bias", out.dtype, N), T, N, K, _code(out.dtype),
-                            out.data_ptr(), _rows(out, "out", None, (T, N)), _stream(stream))
-    _check(rc, "pw_linear_i8")
+    dt, f32, i8 = out.dtype, torch.float32, torch.int8
+    _check(lib().pw_linear_i8(x.data_ptr(), _rows(x, "x", i8, (T, K)), _vec(x_scale, "x_scale", f32, T),
+                              w.data_ptr(), _rows(w, "w", i8, (N, K)), _vec(w_scale, "w_scale", f32, N),
+                              None if bias is None else _vec(bias, "bias", dt, N), T, N, K, _code(dt),
+                              out.data_ptr(), _rows(out, "out", dt, (T, N)), _raw_stream(torch, stream, x)),
+           "pw_linear_i8")
     return out
+
+
+def pw_linear_i8_status(stream=None) -> int:
+    """Status bits that pw_linear_i8 calls ordered before `stream`'s work have raised."""
+    st = _i()
+    _check(lib().pw_linear_i8_status(_stream(stream), ctypes.byref(st)), "pw_linear_i8_status")
+    return st.value
 
 
 class LogProbs(NamedTuple):
@@ -646,9 +678,10 @@ class LogProbs(NamedTuple):
 def pw_logprobs(logits, ids=None, top: int = 0, out=None, stream=None):
     """Log probability and rank of the given tokens, entropy and the ``top``
     likeliest alternatives of every row of logits.  ids: int32 or int64 [T], or
-    None.  out: a LogProbs (or tuple) of tensors to write into."""
+    None.  out: a LogProbs (or tuple) of tensors to write into; its entries may
+    be None for what is not wanted."""
     torch = _torch()
-    T, V = logits.shape
+    T, V = _matrix(logits, "logits")
     f32, i32 = torch.float32, torch.int32
     if out is None:
         dev = logits.device
@@ -656,18 +689,19 @@ def pw_logprobs(logits, ids=None, top: int = 0, out=None, stream=None):
         out = (None if ids is None else new(f32, T), None if ids is None else new(i32, T), new(f32, T),
                new(i32, T, top), new(f32, T, top))
     lp, rank, ent, ti, tl = out
-    ids64 = 0
+    pid, ids64 = None, 0
     if ids is not None:
-        ids64 = int(ids.dtype == torch.int64)
+        ids64 = 1 if ids.dtype is torch.int64 else 0
         pid = _vec(ids, "ids", torch.int64 if ids64 else i32, T)
-    for name, t, dt in (("top_ids", ti, i32), ("top_logprobs", tl, f32)):
-        if top and (t.shape != (T, top) or t.dtype != dt or not t.is_contiguous() or not t.is_cuda):
-            raise ValueError(f"{name}: a contiguous CUDA matrix [{T}][{top}] of {dt} is needed")
-    rc = lib().pw_logprobs(logits.data_ptr(), _rows(logits, "logits"), _code(logits.dtype), T, V,
-                           None if ids is None else pid, ids64, top,
-                           None if lp is None else _vec(lp, "logprob", f32, T),
-                           None if rank is None else _vec(rank, "rank", i32, T),
-                           None if ent is None else _vec(ent, "entropy", f32, T),
-                           _ptr(ti) if top else None, _ptr(tl) if top else None, _stream(stream))
-    _check(rc, "pw_logprobs")
+    if top:
+        for name, t, dt in (("top_ids", ti, i32), ("top_logprobs", tl, f32)):
+            if t.shape != (T, top) or t.dtype is not dt or not t.is_contiguous() or not t.is_cuda:
+                raise ValueError(f"{name}: a contiguous CUDA matrix [{T}][{top}] of {dt} is needed")
+    _check(lib().pw_logprobs(logits.data_ptr(), _rows(logits, "logits", logits.dtype, (T, V)), _code(logits.dtype),
+                             T, V, pid, ids64, top,
+                             None if lp is None else _vec(lp, "logprob", f32, T),
+                             None if rank is None else _vec(rank, "rank", i32, T),
+                             None if ent is None else _vec(ent, "entropy", f32, T),
+                             ti.data_ptr() if top else None, tl.data_ptr() if top else None,
+                             _raw_stream(torch, stream, logits)), "pw_logprobs")
     return LogProbs(lp, rank, ent, ti, tl)

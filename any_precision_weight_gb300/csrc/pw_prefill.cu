@@ -33,6 +33,7 @@
 #include <cstdint>
 
 #include "pw_route.cuh"
+#include "pw_tc.cuh"
 
 namespace pw {
 namespace {
@@ -55,65 +56,10 @@ constexpr int kOffBar = kOffPl + 2 * kPlaneChunkBytes;
 constexpr int kMiscBytes = 64 + 16 + 4 * (256 + 1) + 64;   // barriers, TMEM address, item prefix per expert
 constexpr int kPSmemBytes = kOffBar + kMiscBytes + 1024;   // + slack to align the base to 1 KB
 constexpr uint32_t kTmemCols = 512;           // kMT 128-column fp32 accumulators (power-of-two allocation)
-constexpr long long kWaitLimit = 1ll << 22;
 
-__device__ __forceinline__ uint32_t saddr(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
-// ---------------------------------------------------------------- mbarrier
-
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-// Bounded wait for the phase of the given parity; false when the limit runs
-// out or when another thread has raised the abort flag.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const volatile int* abort) {
-  for (long long i = 0; i < kWaitLimit; ++i) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (done) return true;
-    if (*abort) return false;
-  }
-  return false;
-}
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
 // Barrier of the dequantising warps only (the issue warp keeps running).
 __device__ __forceinline__ void named_sync_dq() {
   asm volatile("bar.sync 1, %0;" ::"n"(kDqThreads) : "memory");
-}
-
-// ---------------------------------------------------------------- TMA / tcgen05
-
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y,
-                                            uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-      : "memory");
-}
-
-// Shared-memory matrix descriptor: K-major operand, 128-byte swizzle, 8-row
-// groups 1024 bytes apart (stride byte offset), descriptor version 1.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((addr & 0x3FFFF) >> 4);          // start address      [0, 14)
-  d |= static_cast<uint64_t>(1) << 16;                        // leading byte offset [16, 30)
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;                // stride byte offset  [32, 46)
-  d |= static_cast<uint64_t>(1) << 46;                        // version             [46, 48)
-  d |= static_cast<uint64_t>(2) << 61;                        // 128-byte swizzle    [61, 64)
-  return d;
 }
 
 // Instruction descriptor, kind::f16: fp16 A and B (K-major), fp32 D, M x N.
@@ -121,28 +67,6 @@ constexpr uint32_t kIdesc = (1u << 4)                             // D format: f
                             | (0u << 7) | (0u << 10)              // A, B: f16
                             | (static_cast<uint32_t>(kBN >> 3) << 17)
                             | (static_cast<uint32_t>(kBM >> 4) << 24);
-
-__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-      ::"r"(d_tmem), "l"(a), "l"(b), "r"(kIdesc), "r"(acc)
-      : "memory");
-}
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-               : "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void proxy_fence_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
 
 // 32 consecutive fp32 columns of this thread's TMEM lane.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
@@ -313,7 +237,8 @@ k_prefill(const Fwd p, const __grid_constant__ CUtensorMap tmA) {
             const uint32_t a0 = sbase + kOffA + (s * kMT + m) * kTileBytes;
 #pragma unroll
             for (int kk = 0; kk < kBK / 16; ++kk)
-              mma_f16(tmem + m * kBN, smem_desc(a0 + kk * 32), smem_desc(b0 + kk * 32), (ks | kk) != 0);
+              mma_f16(tmem + m * kBN, smem_desc(a0 + kk * 32), smem_desc(b0 + kk * 32), kIdesc,
+                      (ks | kk) != 0);
           }
           mma_commit(bar_mma + 8 * s);
           // step ks+1's tokens go to the stage of step ks-1 once its MMAs are done

@@ -608,6 +608,14 @@ int pw_linear_i8(const int8_t* x, int64_t ldx, const float* x_scale, const int8_
                  int64_t ldo, pw_stream_t s);
 
 /*
+ * pw_linear_i8_status -- the PW_STATUS_* bits that pw_linear_i8 calls on the
+ * current device have raised so far (0, or PW_STATUS_TIMEOUT when a bounded
+ * device-side wait gave up: that call's outputs are not valid).  Covers the
+ * work ordered before this call on `s`; synchronises `s`.
+ */
+int pw_linear_i8_status(pw_stream_t s, int* status);
+
+/*
  * pw_logprobs -- what a row of logits says about a token, and its alternatives.
  *   logits  [T][V] of dtype;  ids [T] int32 (ids64 = 0) or int64, or NULL
  *   logprob [T] or NULL   ln softmax(logits[t])[ids[t]]; 0 where ids[t] is

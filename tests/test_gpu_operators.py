@@ -410,3 +410,7 @@ def test_offsets_past_31_bits():
     big = torch.as_tensor(rng.integers(-127, 128, (40, 4096), dtype=np.int8)).cuda()
     got = pw.pw_linear_i8(big, torch.ones(40, device="cuda"), far, ones, out_dtype=torch.float32)
     assert np.array_equal(f64(got), f64(big) @ f64(q).T)
+
+
+def test_linear_waits_have_all_ended():
+    assert pw.pw_linear_i8_status() == 0
