@@ -1,16 +1,24 @@
 // Log probabilities of given tokens with entropy, rank and top alternatives
 // (pw_logprobs).
 //
-//   m = max x,  s = sum e^(x - m),  u = sum (x - m) e^(x - m)
-//   logprob = (x[id] - m) - ln s;  entropy = ln s - u / s
+// In base 2, with L = log2 e and b a whole number at or just above max x * L:
+//   s = sum 2^(x L - b),  u = sum (x L - b) 2^(x L - b)
+//   logprob = (x[id] L - b - log2 s) / L;  entropy = (log2 s - u / s) / L
 //   rank = #{x > x[id]} + #{x = x[id] at a lower index}
 //   alternatives: the largest x by (value descending, index ascending)
+// A whole b costs no rounding, and a thread that finds a larger b scales its
+// sums by a power of two.
 //
-// One pass over the row.  Every thread keeps its own running (m, s, u); every
-// warp keeps a sorted list of its 32 largest keys, one per lane, and looks at
-// single elements only when the largest of its batch reaches the list's k-th
-// value.  A key is the value's bits in ascending order above the complement of
-// the index, so no two keys are equal and the lists' joins need no tie rule.
+// One pass over the row for the sums, the rank and each thread's largest
+// element.  The k-th largest of the threads' largest elements is a bound that
+// at least k elements reach, so only the threads that reach it are looked at
+// again for the alternatives (about k of them, k / 256 of the row).  A row
+// that few rows leave SMs for is split over a cluster of CTAs, whose results
+// CTA 0 joins through distributed shared memory.
+//
+// Bound by HBM for many rows of 32-bit logits; 16-bit logits are near the
+// issue rate, hence the paired arithmetic (f32x2, and 16-bit pairs for maxima
+// and comparisons).
 
 #include <cmath>
 
@@ -21,8 +29,10 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLeast = -1e30f;   // x - m of masked elements: finite, and so are its sums
+constexpr int kMaxCluster = 16;
+constexpr float kL = 1.44269504088896340736f;       // log2 e
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kLeast = -1e30f;                    // least distance of two bases that is told apart
 
 struct LogArgs {
   const void* x;
@@ -36,252 +46,499 @@ struct LogArgs {
   int V, top, ids64;
 };
 
-struct Stat {
-  float m, s, u;   // max, sum e^(x-m), sum (x-m) e^(x-m)
-};
+using u64 = unsigned long long;
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ u64 pair(float a, float b) {
+  u64 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(u64 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+  u64 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+  u64 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
-// Moves st to the larger maximum m.
-__device__ __forceinline__ void raise_max(Stat& st, float m) {
-  if (m > st.m) {
-    if (st.m > -INFINITY) {   // nothing is in the sums before the first finite maximum
-      const float d = st.m - m, c = exp2_approx(d * kLog2e);
-      st.u = (st.u + fmaxf(d, kLeast) * st.s) * c;
-      st.s *= c;
-    }
-    st.m = m;
+// What differs by element type.  Elements are cut below at kLow before they
+// meet the sums, so that masked ones (-inf) stay finite and the rounding of
+// x L stays small; rows whose largest element is not above kSlowBelow, or is
+// above kSlowAbove (where whole bases lose their last bit), go through slow_row.
+template <typename T> struct Type;
+template <> struct Type<float> {
+  static constexpr float kLow = -0x1p29f, kSlowBelow = -0x1p22f, kSlowAbove = 0x1p22f;
+};
+template <> struct Type<__nv_bfloat16> {
+  using P = __nv_bfloat162;
+  static constexpr float kLow = -0x1p29f, kSlowBelow = -0x1p22f, kSlowAbove = 0x1p22f;
+  static __device__ __forceinline__ float2 wide(P v) { return __bfloat1622float2(v); }
+  static __device__ __forceinline__ P both(float v) { return __float2bfloat162_rn(v); }
+};
+template <> struct Type<__half> {
+  using P = __half2;
+  static constexpr float kLow = -65504.f, kSlowBelow = -65504.f, kSlowAbove = 65504.f;
+  static __device__ __forceinline__ float2 wide(P v) { return __half22float2(v); }
+  static __device__ __forceinline__ P both(float v) { return __float2half2_rn(v); }
+};
+
+// Sums over some elements, relative to the base b (a whole number).
+struct Stat {
+  float m, b, s, u;   // largest element (no NaN); base; sums
+  int before;         // elements that come before the given token
+};
+
+// The sums' factor and shift for a larger base.
+__device__ __forceinline__ float raise(float b, float to, float& d) {
+  d = fmaxf(b - to, kLeast);
+  return exp2_approx(b - to);
+}
+
+__device__ __forceinline__ Stat join(const Stat& a, const Stat& c) {
+  Stat r;
+  r.m = fmaxf(a.m, c.m);
+  r.b = fmaxf(a.b, c.b);
+  r.before = a.before + c.before;
+  float da, dc;
+  const float fa = raise(a.b, r.b, da), fc = raise(c.b, r.b, dc);
+  r.s = a.s * fa + c.s * fc;
+  r.u = (a.u + da * a.s) * fa + (c.u + dc * c.s) * fc;
+  return r;
+}
+
+__device__ __forceinline__ Stat join_lanes(Stat st) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    Stat c;
+    c.m = __shfl_xor_sync(0xffffffffu, st.m, o);
+    c.b = __shfl_xor_sync(0xffffffffu, st.b, o);
+    c.s = __shfl_xor_sync(0xffffffffu, st.s, o);
+    c.u = __shfl_xor_sync(0xffffffffu, st.u, o);
+    c.before = __shfl_xor_sync(0xffffffffu, st.before, o);
+    st = join(st, c);
   }
+  return st;
 }
 
-__device__ __forceinline__ Stat join(Stat a, Stat b) {
-  const float m = fmaxf(a.m, b.m);
-  raise_max(a, m);
-  raise_max(b, m);
-  return Stat{m, a.s + b.s, a.u + b.u};
+constexpr float kNoBase = -1e10f;   // below every base
+__device__ __forceinline__ Stat no_stat() { return Stat{-INFINITY, kNoBase, 0.f, 0.f, 0}; }
+
+// The least number of type T above x (+inf becomes NaN: nothing is above it).
+template <typename T>
+__device__ __forceinline__ float next_up(float x) {
+  if (sizeof(T) == 4) {
+    if (x == 0.f) return __uint_as_float(1u);
+    const uint32_t b = __float_as_uint(x);
+    return __uint_as_float(b & 0x80000000u ? b - 1 : b + 1);
+  }
+  const T t = from_f32<T>(x);
+  uint16_t b = *reinterpret_cast<const uint16_t*>(&t);
+  b = x == 0.f ? 1 : b & 0x8000u ? b - 1 : b + 1;
+  return to_f32<T>(*reinterpret_cast<const T*>(&b));
 }
 
-// One element into st, whose maximum is at least x.  The base of a row that so
-// far holds only -inf is 0, so that -inf - base stays -inf (e = 0); a masked
-// element's (x - m) is cut to a finite value before it meets its e = 0.
-__device__ __forceinline__ void add(Stat& st, float base, float x) {
-  const float d = x - base, e = exp2_approx(d * kLog2e);
-  st.s += e;
-  st.u = fmaf(fmaxf(d, kLeast), e, st.u);
-}
+// The sums of one thread.  The given token's logit is met with >= by the
+// vectors of lower index and with > by the others; its own vector's share of
+// equal elements before it is added apart.
+template <typename T>
+struct Sums {
+  static constexpr int VE = 16 / sizeof(T);
+  float m = -INFINITY, b = kNoBase;
+  u64 s2 = 0, u2 = 0;
+  int before = 0;
 
-__device__ __forceinline__ unsigned long long key_of(float x, int idx) {
+  // NV vectors; t[i]: the least value in vector i that comes before the token
+  template <int NV>
+  __device__ __forceinline__ void add(const uint4 (&raw)[NV], const float (&t)[NV]) {
+    constexpr int NP = NV * VE / 2;
+    u64 x2[NP];
+    float bm;
+    if constexpr (sizeof(T) == 4) {
+      bm = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const float e[4] = {__uint_as_float(raw[i].x), __uint_as_float(raw[i].y), __uint_as_float(raw[i].z),
+                            __uint_as_float(raw[i].w)};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          bm = fmaxf(bm, e[j]);
+          before += e[j] >= t[i] ? 1 : 0;
+        }
+        x2[2 * i] = pair(max_nan(e[0], Type<T>::kLow), max_nan(e[1], Type<T>::kLow));
+        x2[2 * i + 1] = pair(max_nan(e[2], Type<T>::kLow), max_nan(e[3], Type<T>::kLow));
+      }
+    } else {
+      using P = typename Type<T>::P;
+      const P low = Type<T>::both(Type<T>::kLow);
+      P mx = *reinterpret_cast<const P*>(&raw[0].x);
+      uint32_t cnt = 0;   // two 16-bit counts
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const P tt = Type<T>::both(t[i]);
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const P e = *reinterpret_cast<const P*>(&w[j]);
+          mx = __hmax2(mx, e);
+          cnt += __hge2_mask(e, tt) & 0x00010001u;
+          const float2 f = Type<T>::wide(__hmax2_nan(e, low));
+          x2[i * 4 + j] = pair(f.x, f.y);
+        }
+      }
+      const float2 f = Type<T>::wide(mx);
+      bm = fmaxf(f.x, f.y);
+      before += (cnt & 0xffff) + (cnt >> 16);
+    }
+    m = fmaxf(m, bm);
+    base(bm);
+    const u64 nb2 = pair(-b, -b), l2 = pair(kL, kL);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const u64 y2 = fma2(x2[i], l2, nb2);
+      const float2 y = unpair(y2);
+      const u64 e2 = pair(exp2_approx(y.x), exp2_approx(y.y));
+      s2 = add2(s2, e2);
+      u2 = fma2(y2, e2, u2);
+    }
+  }
+  __device__ __forceinline__ void base(float x) {
+    const float nb = ceilf(fmaxf(x, Type<T>::kLow) * kL);
+    if (nb > b) {
+      float d;
+      const float f = raise(b, nb, d);
+      u2 = fma2(pair(d, d), s2, u2);
+      s2 = fma2(s2, pair(f, f), 0);
+      u2 = fma2(u2, pair(f, f), 0);
+      b = nb;
+    }
+  }
+  __device__ __forceinline__ void single(float x, float t) {
+    before += x >= t ? 1 : 0;
+    m = fmaxf(m, x);
+    base(x);
+    const float y = fmaf(max_nan(x, Type<T>::kLow), kL, -b), e = exp2_approx(y);
+    s2 = add2(s2, pair(e, 0.f));
+    u2 = add2(u2, pair(y * e, 0.f));
+  }
+  __device__ __forceinline__ Stat stat() const {
+    const float2 s = unpair(s2), u = unpair(u2);
+    return Stat{m, b, s.x + s.y, u.x + u.y, before};
+  }
+};
+
+// ---------------------------------------------------------------- alternatives
+
+// A key is the value's bits in ascending order above the complement of the
+// index: no two are equal, and 0 is none.
+__device__ __forceinline__ u64 key_of(float x, int idx) {
   const uint32_t b = __float_as_uint(x + 0.f);   // -0 and +0 are equal
   const uint32_t o = b & 0x80000000u ? ~b : b | 0x80000000u;
-  return static_cast<unsigned long long>(o) << 32 | static_cast<uint32_t>(~idx);
+  return static_cast<u64>(o) << 32 | static_cast<uint32_t>(~idx);
 }
-__device__ __forceinline__ float key_value(unsigned long long k) {
+__device__ __forceinline__ float key_value(u64 k) {
   const uint32_t o = static_cast<uint32_t>(k >> 32);
   return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
 }
 
-// The least float above x.
-__device__ __forceinline__ float next_up(float x) {
-  if (x == 0.f) return __uint_as_float(1u);
-  const uint32_t b = __float_as_uint(x);
-  return __uint_as_float(b & 0x80000000u ? b - 1 : b + 1);   // +inf becomes NaN: no x is above it
+// The larger half of two descending lists of 32 (one value a lane), descending.
+template <typename K>
+__device__ __forceinline__ K merge32(K a, K other, int lane) {
+  const K o = __shfl_sync(0xffffffffu, other, 31 - lane);
+  if (o > a) a = o;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) {
+    const K v = __shfl_xor_sync(0xffffffffu, a, d);
+    if (((lane & d) == 0) == (v > a)) a = v;
+  }
+  return a;
 }
 
-// A warp's 32 largest keys, descending over the lanes (0: no key).
+__device__ __forceinline__ float sort32(float a, int lane) {
+#pragma unroll
+  for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll
+    for (int d = k >> 1; d; d >>= 1) {
+      const float v = __shfl_xor_sync(0xffffffffu, a, d);
+      const bool larger = ((lane & d) == 0) == ((lane & k) == 0 || k == 32);
+      a = larger ? fmaxf(a, v) : fminf(a, v);
+    }
+  return a;
+}
+
+// Joins the warps' lists (descending, one value a lane) into warp 0's.
+template <typename K>
+__device__ __forceinline__ K merge_warps(K a, K (*sh)[32], int warp, int lane) {
+#pragma unroll
+  for (int n = kWarps / 2; n; n >>= 1) {
+    if (warp >= n && warp < 2 * n) sh[warp][lane] = a;
+    __syncthreads();
+    if (warp < n) a = merge32(a, sh[warp + n][lane], lane);
+  }
+  return a;
+}
+
+// A warp's 32 largest keys so far, descending over the lanes.
 struct TopList {
-  unsigned long long key;
-  float thr;   // no x below it can enter the first `top` places
-
-  __device__ __forceinline__ void insert(unsigned long long k, int lane) {
-    const int pos = __popc(__ballot_sync(0xffffffffu, key > k));
-    const unsigned long long up = __shfl_up_sync(0xffffffffu, key, 1);
-    if (lane >= pos) key = lane == pos ? k : up;
-  }
-  // Elements come in ascending order of their index (batch by batch), so a
-  // later one that equals the last kept value does not enter.
-  __device__ __forceinline__ void refresh(int top) {
-    const unsigned long long k = __shfl_sync(0xffffffffu, key, top - 1);
-    thr = k ? next_up(key_value(k)) : -INFINITY;
-  }
-  // The 32 largest of this list and another one.
-  __device__ __forceinline__ void merge(unsigned long long other, int lane) {
-    const unsigned long long o = __shfl_sync(0xffffffffu, other, 31 - lane);
-    if (o > key) key = o;
-#pragma unroll
-    for (int d = 16; d; d >>= 1) {
-      const unsigned long long v = __shfl_xor_sync(0xffffffffu, key, d);
-      const bool upper = (lane & d) == 0;
-      if (upper == (v > key)) key = v;
+  u64 key = 0, last = 0;   // last: the key at place `top`
+  __device__ __forceinline__ void offer(u64 k, bool valid, int top, int lane) {
+    unsigned mask = __ballot_sync(0xffffffffu, valid && k > last);
+    while (mask) {
+      const u64 c = __shfl_sync(0xffffffffu, k, __ffs(mask) - 1);
+      mask &= mask - 1;
+      if (c <= last) continue;
+      const int pos = __popc(__ballot_sync(0xffffffffu, key > c));
+      const u64 up = __shfl_up_sync(0xffffffffu, key, 1);
+      if (lane >= pos) key = lane == pos ? c : up;
+      last = __shfl_sync(0xffffffffu, key, top - 1);
     }
   }
 };
 
-// What one warp has seen of the row.
-template <bool TOP>
-struct Pass {
-  Stat st{-INFINITY, 0.f, 0.f};
-  TopList list{0, -INFINITY};
-  int before = 0;     // elements that come before the given token
-  float xt;           // the given token's logit (NaN: none)
-  float xt_up;        // the least float above it
-  int id, top, lane, V;
+// ---------------------------------------------------------------- kernel
 
-  // N elements of this lane, element j at index i0[j]; the warp's elements
-  // come in ascending order from call to call.  Places past the row (index V
-  // and above) hold -inf: they add nothing and are kept out of the list.
-  template <int N>
-  __device__ __forceinline__ void batch(const float (&x)[N], const int (&i0)[N]) {
-    float bm = x[0];
-#pragma unroll
-    for (int j = 1; j < N; ++j) bm = fmaxf(bm, x[j]);
-    raise_max(st, bm);
-    const float base = st.m == -INFINITY ? 0.f : st.m;
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      add(st, base, x[j]);
-      before += x[j] >= (i0[j] < id ? xt : xt_up) ? 1 : 0;
-    }
-    if (TOP && __any_sync(0xffffffffu, bm >= list.thr)) {
-#pragma unroll 1
-      for (int j = 0; j < N; ++j) {
-        float v = x[0];
-        int i = i0[0];
-#pragma unroll
-        for (int l = 1; l < N; ++l)
-          if (l == j) v = x[l], i = i0[l];
-        unsigned mask = __ballot_sync(0xffffffffu, v >= list.thr && i < V);
-        if (!mask) continue;
-        const unsigned long long k = key_of(v, i);
-        while (mask) {
-          list.insert(__shfl_sync(0xffffffffu, k, __ffs(mask) - 1), lane);
-          mask &= mask - 1;
-        }
-      }
-      list.refresh(top);
-    }
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of a shared variable of this CTA in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t in_cta(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(a)
+               : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float ld_cluster_f(uint32_t a) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ u64 ld_cluster_k(uint32_t a) {
+  u64 v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// Rows whose largest element is at an end of the number range (masks of the
+// type's lowest value that leave nothing, rows of -inf, infinities): sums of
+// e^(x - m), in natural units, by one CTA.  Returned as a Stat with b = 0:
+// s and u scaled to base 2.
+template <typename T>
+__device__ __noinline__ Stat slow_row(const T* x, int V, float m, Stat* sh) {
+  Stat st{m, 0.f, 0.f, 0.f, 0};
+  for (int i = threadIdx.x; i < V; i += kThreads) {
+    const float xi = to_f32<T>(x[i]);
+    if (xi == -INFINITY) continue;
+    const float y = fmaxf(xi - m, kLeast) * kL, e = xi != xi || m == INFINITY ? NAN : exp2_approx(y);
+    st.s += e;
+    st.u += y * e;
   }
-  // One element that only lanes with `valid` have.
-  __device__ __forceinline__ void single(float x, int i, bool valid) {
-    if (valid) {
-      raise_max(st, x);
-      add(st, st.m == -INFINITY ? 0.f : st.m, x);
-      before += x >= (i < id ? xt : xt_up) ? 1 : 0;
-    }
-    if (TOP) {
-      unsigned mask = __ballot_sync(0xffffffffu, valid && x >= list.thr);
-      const unsigned long long k = key_of(x, i);
-      while (mask) {
-        list.insert(__shfl_sync(0xffffffffu, k, __ffs(mask) - 1), lane);
-        mask &= mask - 1;
-      }
-      list.refresh(top);
-    }
-  }
-};
+  st = join_lanes(st);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = st;
+  __syncthreads();
+  st = sh[0];
+  for (int w = 1; w < kWarps; ++w) st.s += sh[w].s, st.u += sh[w].u;
+  st.m = m;
+  return st;
+}
 
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(kThreads) k_logprobs(const LogArgs p) {
+__global__ void __launch_bounds__(kThreads, 4) k_logprobs(const LogArgs p, int split) {
   constexpr int VE = 16 / sizeof(T);
-  constexpr int NV = 16 / VE;              // vectors of a batch: 16 elements a lane
-  __shared__ Stat s_stat[kWarps];
-  __shared__ int s_before[kWarps];
-  __shared__ unsigned long long s_list[kWarps][32];
+  constexpr int NV = 2 * (sizeof(T) / 2);        // vectors of a batch: 16 elements a thread
+  __shared__ Stat s_stat[kWarps], s_cta;
+  __shared__ u64 s_list[kWarps][32], s_top[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row = blockIdx.x;
+  const int64_t row = blockIdx.x / split;
+  const int rank = blockIdx.x % split;
   const T* x = static_cast<const T*>(p.x) + row * p.ld;
 
-  Pass<TOP> w;
-  w.lane = lane;
-  w.top = p.top;
-  w.V = p.V;
-  long long id = -1;
-  if (p.ids) id = p.ids64 ? static_cast<const long long*>(p.ids)[row] : static_cast<const int32_t*>(p.ids)[row];
-  const bool has = id >= 0 && id < p.V;
-  w.id = has ? static_cast<int>(id) : -1;
-  w.xt = has ? to_f32<T>(x[w.id]) : NAN;
-  w.xt_up = next_up(w.xt);
+  long long id64 = -1;
+  if (p.ids) id64 = p.ids64 ? static_cast<const long long*>(p.ids)[row] : static_cast<const int32_t*>(p.ids)[row];
+  const bool has = id64 >= 0 && id64 < p.V;
+  const int id = has ? static_cast<int>(id64) : -1;
+  const float xt = has ? to_f32<T>(x[id]) : NAN;
+  const float xt_up = next_up<T>(xt);
 
-  // elements before the first 16-byte boundary, whole vectors, the rest
+  // elements before the first 16-byte boundary, whole vectors, the rest; this
+  // CTA's share of the vectors
   const int off = static_cast<int>(reinterpret_cast<uintptr_t>(x) / sizeof(T) % VE);
   const int head = min(p.V, (VE - off) % VE);
   const int nvec = (p.V - head) / VE;
-  const uint4* xv = reinterpret_cast<const uint4*>(x + head);
-  if (warp == 0 && head) w.single(lane < head ? to_f32<T>(x[lane]) : 0.f, lane, lane < head);
-  for (int v0 = warp * NV * 32; v0 < nvec; v0 += kThreads * NV) {
-    float e[16];
-    int at[16];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int v = v0 + j * 32 + lane;
-      float t[VE];
-      if (v < nvec) {
-        unpack16<T>(xv[v], t);
-      } else {
-#pragma unroll
-        for (int i = 0; i < VE; ++i) t[i] = -INFINITY;
-      }
-#pragma unroll
-      for (int i = 0; i < VE; ++i) e[j * VE + i] = t[i], at[j * VE + i] = v < nvec ? head + v * VE + i : p.V;
-    }
-    w.batch(e, at);
-  }
   const int done = head + nvec * VE;
-  if (warp == kWarps - 1 && done < p.V) {
-    const bool ok = done + lane < p.V;
-    w.single(ok ? to_f32<T>(x[done + lane]) : 0.f, done + lane, ok);
+  const uint4* xv = reinterpret_cast<const uint4*>(x + head);
+  const int va = static_cast<int>(static_cast<int64_t>(nvec) * rank / split);
+  const int vb = static_cast<int>(static_cast<int64_t>(nvec) * (rank + 1) / split);
+  const int vid = id >= head && id < done ? (id - head) / VE : id < head ? -1 : nvec;   // the token's vector
+  const int vlow = min(vid, vb);   // this CTA's vectors below it are met with >=
+  const bool do_head = rank == 0 && warp == 0, do_tail = rank == split - 1 && warp == kWarps - 1;
+
+  Sums<T> sums;
+  if (do_head && lane < head) sums.single(to_f32<T>(x[lane]), lane < id ? xt : xt_up);
+  const uint32_t ninf = sizeof(T) == 4 ? 0xff800000u : sizeof(T) == 2 && Type<T>::kLow == -65504.f ? 0xfc00fc00u : 0xff80ff80u;
+  const uint4 none = make_uint4(ninf, ninf, ninf, ninf);
+  constexpr int kStep = kThreads * NV;
+  const int first = va + warp * NV * 32 + lane;
+  uint4 next[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) next[i] = first + i * 32 < vb ? __ldg(xv + first + i * 32) : none;
+  for (int v = first; v - lane < vb; v += kStep) {
+    uint4 raw[NV];
+    float t[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      raw[i] = next[i];
+      t[i] = v + i * 32 < vlow ? xt : xt_up;
+      const int n = v + kStep + i * 32;
+      next[i] = n < vb ? __ldg(xv + n) : none;
+    }
+    sums.template add<NV>(raw, t);
+  }
+  if (do_tail && done + lane < p.V) sums.single(to_f32<T>(x[done + lane]), done + lane < id ? xt : xt_up);
+  // the token's own vector was met with > throughout: its equal elements before the token
+  if (rank == 0 && warp == 0 && vid >= 0 && vid < nvec) {
+    const int i = head + vid * VE + lane;
+    if (lane < VE && i < id && to_f32<T>(x[i]) == xt) ++sums.before;
   }
 
-  // join: lanes, then warps
+  {
+    const Stat st = join_lanes(sums.stat());
+    if (lane == 0) s_stat[warp] = st;
+  }
+  u64 best = 0;
+  if constexpr (TOP) {
+    // the bound: the top-th largest of the threads' largest elements
+    float* s_thr = reinterpret_cast<float*>(s_top);
+    const float all = merge_warps<float>(sort32(sums.m, lane), reinterpret_cast<float(*)[32]>(s_list), warp, lane);
+    if (warp == 0 && lane == p.top - 1) *s_thr = all;
+    __syncthreads();
+    const float thr = *s_thr;
+    TopList list;
+    auto look = [&](float e, int i, bool valid) { list.offer(key_of(e, i), valid && e >= thr, p.top, lane); };
+    if (do_head) look(lane < head ? to_f32<T>(x[lane]) : 0.f, lane, lane < head);
+    if (do_tail) look(done + lane < p.V ? to_f32<T>(x[done + lane]) : 0.f, done + lane, done + lane < p.V);
+    for (unsigned mask = __ballot_sync(0xffffffffu, sums.m >= thr); mask; mask &= mask - 1) {
+      // that thread's vectors again, one to each lane
+      const int owner = va + warp * NV * 32 + __ffs(mask) - 1;
+      for (int n0 = 0; owner + n0 / NV * kStep < vb; n0 += 32) {
+        const int n = n0 + lane, v = owner + n / NV * kStep + n % NV * 32;
+        const uint4 raw = v < vb ? __ldg(xv + v) : none;
+        float e[VE];
+        unpack16<T>(raw, e);
+        float em = e[0];
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    Stat b;
-    b.m = __shfl_xor_sync(0xffffffffu, w.st.m, o);
-    b.s = __shfl_xor_sync(0xffffffffu, w.st.s, o);
-    b.u = __shfl_xor_sync(0xffffffffu, w.st.u, o);
-    w.st = join(w.st, b);
+        for (int i = 1; i < VE; ++i) em = fmaxf(em, e[i]);
+        if (!__any_sync(0xffffffffu, v < vb && em >= thr)) continue;
+#pragma unroll
+        for (int i = 0; i < VE; ++i) look(e[i], head + v * VE + i, v < vb);
+      }
+    }
+    __syncthreads();
+    best = merge_warps<u64>(list.key, s_list, warp, lane);
+  } else {
+    __syncthreads();
   }
-  w.before = __reduce_add_sync(0xffffffffu, w.before);
-  if (lane == 0) {
-    s_stat[warp] = w.st;
-    s_before[warp] = w.before;
+
+  // this CTA's results, and the cluster's in CTA 0
+  if (warp == 0) {
+    Stat st = lane < kWarps ? s_stat[lane] : no_stat();
+    st = join_lanes(st);
+    if (lane == 0) s_cta = st;
+    if (TOP) s_top[lane] = best;
   }
-  if (TOP) s_list[warp][lane] = w.list.key;
+  if (split > 1) {
+    __syncwarp();
+    cluster_sync();
+    if (rank == 0) {
+      if (warp == 0) {
+        Stat st = no_stat();
+        if (lane < split) {
+          const uint32_t a = in_cta(&s_cta, lane);
+          st = Stat{ld_cluster_f(a), ld_cluster_f(a + 4), ld_cluster_f(a + 8), ld_cluster_f(a + 12),
+                    __float_as_int(ld_cluster_f(a + 16))};
+        }
+        st = join_lanes(st);
+        if (lane == 0) s_cta = st;
+      }
+      if (TOP) {
+        u64 a = warp < split ? ld_cluster_k(in_cta(&s_top[lane], warp)) : 0;
+        if (warp + kWarps < split) a = merge32(a, ld_cluster_k(in_cta(&s_top[lane], warp + kWarps)), lane);
+        best = merge_warps<u64>(a, s_list, warp, lane);
+      }
+    }
+    __syncwarp();
+    cluster_sync();
+    if (rank) return;
+  }
   __syncthreads();
-  if (warp) return;
-  Stat st = s_stat[0];
-  int before = s_before[0];
-  for (int i = 1; i < kWarps; ++i) {
-    st = join(st, s_stat[i]);
-    before += s_before[i];
-    if (TOP) w.list.merge(s_list[i][lane], lane);
+  Stat st = s_cta;
+  const bool slow = !(st.m > Type<T>::kSlowBelow) || st.m > Type<T>::kSlowAbove;
+  if (slow && (st.m != -INFINITY || st.s == st.s)) {
+    const int before = st.before;
+    st = slow_row<T>(x, p.V, st.m, s_stat);
+    st.before = before;
   }
-  const float ls = logf(st.s);   // -inf for a row of -inf alone
+  if (warp) return;
+  // log2 of an element's probability; -inf where nothing has any
   const bool empty = st.m == -INFINITY && st.s == 0.f;
+  const float ls = log2f(st.s);
+  auto logp = [&](float v) {
+    if (empty) return -INFINITY;
+    if (!slow && v < -1e30f) return v - (st.b + ls) * kLn2;   // v L would overflow
+    return ((slow ? (v - st.m) * kL : fmaf(v, kL, -st.b)) - ls) * kLn2;
+  };
   if (lane == 0) {
     if (p.ids) {
-      if (p.logprob) p.logprob[row] = !has ? 0.f : empty ? -INFINITY : (w.xt - st.m) - ls;
-      if (p.rank) p.rank[row] = !has || w.xt != w.xt ? -1 : before;
+      if (p.logprob) p.logprob[row] = has ? logp(xt) : 0.f;
+      if (p.rank) p.rank[row] = !has || xt != xt ? -1 : st.before;
     }
-    if (p.entropy) p.entropy[row] = empty ? 0.f : ls - st.u / st.s;
+    if (p.entropy) p.entropy[row] = empty ? 0.f : (ls - st.u / st.s) * kLn2;
   }
   if (TOP && lane < p.top) {
-    const unsigned long long k = w.list.key;
-    p.top_ids[row * p.top + lane] = k ? static_cast<int32_t>(~static_cast<uint32_t>(k)) : -1;
-    p.top_logprobs[row * p.top + lane] = !k ? NAN : empty ? -INFINITY : (key_value(k) - st.m) - ls;
+    p.top_ids[row * p.top + lane] = best ? static_cast<int32_t>(~static_cast<uint32_t>(best)) : -1;
+    p.top_logprobs[row * p.top + lane] = best ? logp(key_value(best)) : NAN;
   }
+}
+
+template <typename T, bool TOP>
+cudaError_t launch_top(const LogArgs& p, int T_, cudaStream_t s) {
+  // as many CTAs to a row as give every SM two, each with some 2048 elements
+  const int sms = sm_count();
+  int split = 1;
+  while (split < kMaxCluster && static_cast<int64_t>(T_) * split < 2 * sms && p.V >= 4096 * split) split *= 2;
+  if (static_cast<int64_t>(T_) * split > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  if (split > 8) {
+    const cudaError_t e = cudaFuncSetAttribute(k_logprobs<T, TOP>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(T_) * split);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute a{};
+  a.id = cudaLaunchAttributeClusterDimension;
+  a.val.clusterDim = {static_cast<unsigned>(split), 1, 1};
+  cfg.attrs = &a;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_logprobs<T, TOP>, p, split);
 }
 
 template <typename T>
 cudaError_t launch_logprobs(const LogArgs& p, int T_, cudaStream_t s) {
-  if (p.top)
-    k_logprobs<T, true><<<T_, kThreads, 0, s>>>(p);
-  else
-    k_logprobs<T, false><<<T_, kThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return p.top ? launch_top<T, true>(p, T_, s) : launch_top<T, false>(p, T_, s);
 }
 
 }  // namespace
@@ -291,7 +548,8 @@ extern "C" int pw_logprobs(const void* logits, int64_t ld, int dtype, int T, int
                            int top, float* logprob, int32_t* rank, float* entropy, int32_t* top_ids,
                            float* top_logprobs, pw_stream_t s) {
   pw::NvtxCall nvtx_range("pw_logprobs");
-  if (T < 0 || V < 1) return pw::failf(PW_EINVAL, "pw_logprobs: need T >= 0 and V >= 1 (T %d, V %d)", T, V);
+  if (T < 0 || V < 1 || V > PW_MAX_VOCAB)
+    return pw::failf(PW_EINVAL, "pw_logprobs: need T >= 0 and 1 <= V <= %d (T %d, V %d)", PW_MAX_VOCAB, T, V);
   if (!pw::dtype_ok(dtype)) return pw::failf(PW_EINVAL, "pw_logprobs: unknown dtype %d", dtype);
   if (top < 0 || top > PW_MAX_TOP || top > V)
     return pw::failf(PW_EINVAL, "pw_logprobs: top %d outside [0, min(V, %d)]", top, PW_MAX_TOP);

@@ -50,7 +50,7 @@ def test_linear_refuses(kw):
 
 
 @pytest.mark.parametrize("kw", [
-    dict(T=-1), dict(V=0), dict(dt=3), dict(top=-1), dict(top=pw.MAX_TOP + 1), dict(V=4, ld=4, top=5), dict(x=None),
+    dict(T=-1), dict(V=0), dict(V=(1 << 30) + 1, ld=1 << 31), dict(dt=3), dict(top=-1), dict(top=pw.MAX_TOP + 1), dict(V=4, ld=4, top=5), dict(x=None),
     dict(ld=99), dict(ids=None), dict(tl=None), dict(ti=None), dict(x=P + 1), dict(ids=P + 4, ids64=1),
     dict(ids=P + 2), dict(lp=P + 1), dict(rank=P + 2), dict(ent=P + 1), dict(ti=P + 2), dict(tl=P + 2)])
 def test_logprobs_refuses(kw):
