@@ -30,6 +30,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxCluster = 16;
+constexpr int kCand = kWarps * 32;                  // elements that reach the bound, before another way is taken
 constexpr float kL = 1.44269504088896340736f;       // log2 e
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLeast = -1e30f;                    // least distance of two bases that is told apart
@@ -107,28 +108,20 @@ __device__ __forceinline__ float raise(float b, float to, float& d) {
   return exp2_approx(b - to);
 }
 
-__device__ __forceinline__ Stat join(const Stat& a, const Stat& c) {
-  Stat r;
-  r.m = fmaxf(a.m, c.m);
-  r.b = fmaxf(a.b, c.b);
-  r.before = a.before + c.before;
-  float da, dc;
-  const float fa = raise(a.b, r.b, da), fc = raise(c.b, r.b, dc);
-  r.s = a.s * fa + c.s * fc;
-  r.u = (a.u + da * a.s) * fa + (c.u + dc * c.s) * fc;
-  return r;
-}
-
+// The joined sums of a warp's lanes, in every lane.
 __device__ __forceinline__ Stat join_lanes(Stat st) {
+  const float b = static_cast<float>(__reduce_max_sync(0xffffffffu, __float2int_rn(st.b)));   // whole
+  float d;
+  const float f = raise(st.b, b, d);
+  st.u = (st.u + d * st.s) * f;
+  st.s *= f;
+  st.b = b;
+  st.before = __reduce_add_sync(0xffffffffu, st.before);
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
-    Stat c;
-    c.m = __shfl_xor_sync(0xffffffffu, st.m, o);
-    c.b = __shfl_xor_sync(0xffffffffu, st.b, o);
-    c.s = __shfl_xor_sync(0xffffffffu, st.s, o);
-    c.u = __shfl_xor_sync(0xffffffffu, st.u, o);
-    c.before = __shfl_xor_sync(0xffffffffu, st.before, o);
-    st = join(st, c);
+    st.m = fmaxf(st.m, __shfl_xor_sync(0xffffffffu, st.m, o));
+    st.s += __shfl_xor_sync(0xffffffffu, st.s, o);
+    st.u += __shfl_xor_sync(0xffffffffu, st.u, o);
   }
   return st;
 }
@@ -266,21 +259,22 @@ __device__ __forceinline__ K merge32(K a, K other, int lane) {
   return a;
 }
 
-__device__ __forceinline__ float sort32(float a, int lane) {
+// A warp's values, one a lane, in descending order.
+template <typename K>
+__device__ __forceinline__ K sort32(K a, int lane) {
 #pragma unroll
   for (int k = 2; k <= 32; k <<= 1)
 #pragma unroll
     for (int d = k >> 1; d; d >>= 1) {
-      const float v = __shfl_xor_sync(0xffffffffu, a, d);
+      const K v = __shfl_xor_sync(0xffffffffu, a, d);
       const bool larger = ((lane & d) == 0) == ((lane & k) == 0 || k == 32);
-      a = larger ? fmaxf(a, v) : fminf(a, v);
+      if (larger == (v > a)) a = v;
     }
   return a;
 }
 
 // Joins the warps' lists (descending, one value a lane) into warp 0's.
-template <typename K>
-__device__ __forceinline__ K merge_warps(K a, K (*sh)[32], int warp, int lane) {
+__device__ __forceinline__ u64 merge_warps(u64 a, u64 (*sh)[32], int warp, int lane) {
 #pragma unroll
   for (int n = kWarps / 2; n; n >>= 1) {
     if (warp >= n && warp < 2 * n) sh[warp][lane] = a;
@@ -360,7 +354,11 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprobs(const LogArgs p, int s
   constexpr int VE = 16 / sizeof(T);
   constexpr int NV = 2 * (sizeof(T) / 2);        // vectors of a batch: 16 elements a thread
   __shared__ Stat s_stat[kWarps], s_cta;
-  __shared__ u64 s_list[kWarps][32], s_top[32];
+  __shared__ u64 s_cand[kCand], s_top[32];
+  __shared__ float s_group[64];
+  __shared__ uint8_t s_owner[kWarps][32];
+  __shared__ int s_count;
+  u64(*s_list)[32] = reinterpret_cast<u64(*)[32]>(s_cand);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t row = blockIdx.x / split;
   const int rank = blockIdx.x % split;
@@ -420,34 +418,76 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprobs(const LogArgs p, int s
   }
   u64 best = 0;
   if constexpr (TOP) {
-    // the bound: the top-th largest of the threads' largest elements
-    float* s_thr = reinterpret_cast<float*>(s_top);
-    const float all = merge_warps<float>(sort32(sums.m, lane), reinterpret_cast<float(*)[32]>(s_list), warp, lane);
-    if (warp == 0 && lane == p.top - 1) *s_thr = all;
+    // the bound: the top-th largest of 64 groups' largest elements (4 threads
+    // each), so that some 64 ln(64 / (64 - top)) elements reach it: 24 for 20
+    float gm = fmaxf(sums.m, __shfl_xor_sync(0xffffffffu, sums.m, 1));
+    gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 2));
+    if ((lane & 3) == 0) s_group[threadIdx.x >> 2] = gm;
+    if (threadIdx.x == 0) s_count = 0;
     __syncthreads();
-    const float thr = *s_thr;
-    TopList list;
-    auto look = [&](float e, int i, bool valid) { list.offer(key_of(e, i), valid && e >= thr, p.top, lane); };
-    if (do_head) look(lane < head ? to_f32<T>(x[lane]) : 0.f, lane, lane < head);
-    if (do_tail) look(done + lane < p.V ? to_f32<T>(x[done + lane]) : 0.f, done + lane, done + lane < p.V);
-    for (unsigned mask = __ballot_sync(0xffffffffu, sums.m >= thr); mask; mask &= mask - 1) {
-      // that thread's vectors again, one to each lane
-      const int owner = va + warp * NV * 32 + __ffs(mask) - 1;
-      for (int n0 = 0; owner + n0 / NV * kStep < vb; n0 += 32) {
-        const int n = n0 + lane, v = owner + n / NV * kStep + n % NV * 32;
-        const uint4 raw = v < vb ? __ldg(xv + v) : none;
-        float e[VE];
-        unpack16<T>(raw, e);
-        float em = e[0];
+    const float thr = __shfl_sync(
+        0xffffffffu, merge32(sort32(s_group[lane], lane), sort32(s_group[lane + 32], lane), lane), p.top - 1);
+    const unsigned owners = __ballot_sync(0xffffffffu, sums.m >= thr);
+    if (sums.m >= thr) s_owner[warp][__popc(owners & ((1u << lane) - 1))] = static_cast<uint8_t>(lane);
+    __syncwarp();
+    // the elements of this warp's threads that reach the bound, once more: f(element, index, exists)
+    auto again = [&](auto&& f) {
+      if (do_head) f(lane < head ? to_f32<T>(x[lane]) : 0.f, lane, lane < head);
+      if (do_tail) f(done + lane < p.V ? to_f32<T>(x[done + lane]) : 0.f, done + lane, done + lane < p.V);
+      const int w0 = va + warp * NV * 32;
+      const int each = w0 < vb ? ((vb - w0 - 1) / kStep + 1) * NV : 0;   // a thread's vectors, at most
+      const int items = __popc(owners) * each;
+      constexpr int U = 4;                                               // loads in flight
+      for (int i0 = 0; i0 < items; i0 += 32 * U) {
+        uint4 raw[U];
+        int at[U];
 #pragma unroll
-        for (int i = 1; i < VE; ++i) em = fmaxf(em, e[i]);
-        if (!__any_sync(0xffffffffu, v < vb && em >= thr)) continue;
+        for (int k = 0; k < U; ++k) {
+          const int i = i0 + k * 32 + lane;
+          at[k] = vb;
+          if (i < items) {
+            const int n = i % each;
+            at[k] = w0 + s_owner[warp][i / each] + n / NV * kStep + n % NV * 32;
+          }
+          raw[k] = at[k] < vb ? __ldg(xv + at[k]) : none;
+        }
 #pragma unroll
-        for (int i = 0; i < VE; ++i) look(e[i], head + v * VE + i, v < vb);
+        for (int k = 0; k < U; ++k) {
+          float e[VE];
+          unpack16<T>(raw[k], e);
+          float em = e[0];
+#pragma unroll
+          for (int j = 1; j < VE; ++j) em = fmaxf(em, e[j]);
+          if (!__any_sync(0xffffffffu, at[k] < vb && em >= thr)) continue;
+#pragma unroll
+          for (int j = 0; j < VE; ++j) f(e[j], head + at[k] * VE + j, at[k] < vb);
+        }
       }
-    }
+    };
+    again([&](float e, int i, bool exists) {
+      const bool in = exists && e >= thr;
+      const unsigned mask = __ballot_sync(0xffffffffu, in);
+      if (!mask) return;
+      int pos = 0;
+      if (lane == 0) pos = atomicAdd(&s_count, __popc(mask));
+      pos = __shfl_sync(0xffffffffu, pos, 0) + __popc(mask & ((1u << lane) - 1));
+      if (in && pos < kCand) s_cand[pos] = key_of(e, i);
+    });
     __syncthreads();
-    best = merge_warps<u64>(list.key, s_list, warp, lane);
+    const int n = s_count;
+    if (n <= kCand) {
+      if (warp == 0) {
+        for (int i = 0; i < n; i += 32) {
+          const u64 k = sort32(i + lane < n ? s_cand[i + lane] : u64(0), lane);
+          best = i ? merge32(best, k, lane) : k;
+        }
+      }
+    } else {   // many equal elements: a list in each warp
+      TopList list;
+      again([&](float e, int i, bool exists) { list.offer(key_of(e, i), exists && e >= thr, p.top, lane); });
+      __syncthreads();
+      best = merge_warps(list.key, s_list, warp, lane);
+    }
   } else {
     __syncthreads();
   }
@@ -476,7 +516,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprobs(const LogArgs p, int s
       if (TOP) {
         u64 a = warp < split ? ld_cluster_k(in_cta(&s_top[lane], warp)) : 0;
         if (warp + kWarps < split) a = merge32(a, ld_cluster_k(in_cta(&s_top[lane], warp + kWarps)), lane);
-        best = merge_warps<u64>(a, s_list, warp, lane);
+        __syncthreads();
+        best = merge_warps(a, s_list, warp, lane);
       }
     }
     __syncwarp();

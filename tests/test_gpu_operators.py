@@ -298,7 +298,7 @@ def test_logprobs_rows_start_anywhere(off, V):
 
 
 @pytest.mark.parametrize("kind", ["equal", "ascending", "descending", "two_values", "steps", "one_left", "lowest",
-                                  "lowest_mask", "signed_zeros", "far"])
+                                  "lowest_mask", "signed_zeros", "far", "large", "huge", "masks"])
 @pytest.mark.parametrize("V", [40, 3001, 70000])
 @pytest.mark.parametrize("T", [1, 170])
 def test_logprobs_orders_ties_and_masks(kind, V, T):
@@ -309,7 +309,8 @@ def test_logprobs_orders_ties_and_masks(kind, V, T):
            "one_left": np.where(k == V // 3, 2.0, -INF), "lowest": np.full(V, float(np.finfo(np.float32).min)),
            "lowest_mask": np.where(k % 3 == 0, rng.normal(0, 1, V), float(np.finfo(np.float32).min)),
            "signed_zeros": np.where(k % 2 == 0, -0.0, 0.0),
-           "far": np.where(k == 5, 1e4, -1e4)}[kind]
+           "far": np.where(k == 5, 1e4, -1e4), "large": rng.normal(0, 2, V) + 3e6, "huge": rng.normal(0, 1, V) * 1e30,
+           "masks": rng.choice([-1e4, -1e9, -1e30, -INF, 0.5, -2.0], V)}[kind]
     x = place(np.repeat(row[None].astype(np.float32), T, 0), torch.float32)
     ids = torch.as_tensor(rng.integers(0, V, T)).cuda()
     top = 32
