@@ -9,10 +9,11 @@
 // A whole b costs no rounding, and a thread that finds a larger b scales its
 // sums by a power of two.
 //
-// One pass over the row for the sums, the rank and each thread's largest
-// element.  The k-th largest of the threads' largest elements is a bound that
-// at least k elements reach, so only the threads that reach it are looked at
-// again for the alternatives (about k of them, k / 256 of the row).  A row
+// One pass over the row for the sums, the rank and the largest element of each
+// thread's batch (16 elements), kept in 16 bits.  The k-th largest of groups of
+// the threads' largest elements is a bound that at least k elements reach, so
+// only the batches that reach it, about k of them, are read again for the
+// alternatives.  A row
 // that few rows leave SMs for is split over a cluster of CTAs, whose results
 // CTA 0 joins through distributed shared memory.
 //
@@ -30,7 +31,8 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxCluster = 16;
-constexpr int kCand = kWarps * 32;                  // elements that reach the bound, before another way is taken
+constexpr int kKept = 48;                           // batches of a thread whose largest elements are kept
+constexpr int kCand = kWarps * 32;                  // batches or elements that reach the bound, before another way is taken
 constexpr float kL = 1.44269504088896340736f;       // log2 e
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLeast = -1e30f;                    // least distance of two bases that is told apart
@@ -82,15 +84,21 @@ __device__ __forceinline__ u64 add2(u64 a, u64 b) {
 template <typename T> struct Type;
 template <> struct Type<float> {
   static constexpr float kLow = -0x1p29f, kSlowBelow = -0x1p22f, kSlowAbove = 0x1p22f;
+  using B = __nv_bfloat16;   // a batch's largest element, not rounded down
+  static __device__ __forceinline__ B above(float v) { return __float2bfloat16_ru(v); }
 };
 template <> struct Type<__nv_bfloat16> {
   using P = __nv_bfloat162;
+  using B = __nv_bfloat16;
+  static __device__ __forceinline__ B above(float v) { return __float2bfloat16_rn(v); }
   static constexpr float kLow = -0x1p29f, kSlowBelow = -0x1p22f, kSlowAbove = 0x1p22f;
   static __device__ __forceinline__ float2 wide(P v) { return __bfloat1622float2(v); }
   static __device__ __forceinline__ P both(float v) { return __float2bfloat162_rn(v); }
 };
 template <> struct Type<__half> {
   using P = __half2;
+  using B = __half;
+  static __device__ __forceinline__ B above(float v) { return __float2half_rn(v); }
   static constexpr float kLow = -65504.f, kSlowBelow = -65504.f, kSlowAbove = 65504.f;
   static __device__ __forceinline__ float2 wide(P v) { return __half22float2(v); }
   static __device__ __forceinline__ P both(float v) { return __float2half2_rn(v); }
@@ -153,9 +161,10 @@ struct Sums {
   u64 s2 = 0, u2 = 0;
   int before = 0;
 
-  // NV vectors; t[i]: the least value in vector i that comes before the token
+  // NV vectors; t[i]: the least value in vector i that comes before the token.
+  // Returns the largest element.
   template <int NV>
-  __device__ __forceinline__ void add(const uint4 (&raw)[NV], const float (&t)[NV]) {
+  __device__ __forceinline__ float add(const uint4 (&raw)[NV], const float (&t)[NV]) {
     constexpr int NP = NV * VE / 2;
     u64 x2[NP];
     float bm;
@@ -206,6 +215,7 @@ struct Sums {
       s2 = add2(s2, e2);
       u2 = fma2(y2, e2, u2);
     }
+    return bm;
   }
   __device__ __forceinline__ void base(float x) {
     const float nb = ceilf(fmaxf(x, Type<T>::kLow) * kL);
@@ -356,8 +366,9 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprobs(const LogArgs p, int s
   __shared__ Stat s_stat[kWarps], s_cta;
   __shared__ u64 s_cand[kCand], s_top[32];
   __shared__ float s_group[64];
-  __shared__ uint8_t s_owner[kWarps][32];
-  __shared__ int s_count;
+  __shared__ typename Type<T>::B s_batch[TOP ? kKept : 1][kThreads];
+  __shared__ int s_at[TOP ? kCand : 1];
+  __shared__ int s_count, s_found;
   u64(*s_list)[32] = reinterpret_cast<u64(*)[32]>(s_cand);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t row = blockIdx.x / split;
@@ -386,13 +397,18 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprobs(const LogArgs p, int s
 
   Sums<T> sums;
   if (do_head && lane < head) sums.single(to_f32<T>(x[lane]), lane < id ? xt : xt_up);
-  const uint32_t ninf = sizeof(T) == 4 ? 0xff800000u : sizeof(T) == 2 && Type<T>::kLow == -65504.f ? 0xfc00fc00u : 0xff80ff80u;
+  const uint32_t ninf = sizeof(T) == 4 ? 0xff800000u : Type<T>::kLow == -65504.f ? 0xfc00fc00u : 0xff80ff80u;
   const uint4 none = make_uint4(ninf, ninf, ninf, ninf);
   constexpr int kStep = kThreads * NV;
   const int first = va + warp * NV * 32 + lane;
   uint4 next[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) next[i] = first + i * 32 < vb ? __ldg(xv + first + i * 32) : none;
+  // 2^ws batches of a thread share a place among those kept
+  int ws = 0;
+  while (TOP && (vb - va + kStep - 1) / kStep > kKept << ws) ++ws;
+  float wm = -INFINITY;
+  int batch = 0;
   for (int v = first; v - lane < vb; v += kStep) {
     uint4 raw[NV];
     float t[NV];
@@ -403,7 +419,12 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprobs(const LogArgs p, int s
       const int n = v + kStep + i * 32;
       next[i] = n < vb ? __ldg(xv + n) : none;
     }
-    sums.template add<NV>(raw, t);
+    const float bm = sums.template add<NV>(raw, t);
+    if (TOP) {
+      wm = fmaxf(batch & ((1 << ws) - 1) ? wm : -INFINITY, bm);
+      s_batch[batch >> ws][threadIdx.x] = Type<T>::above(wm);
+      ++batch;
+    }
   }
   if (do_tail && done + lane < p.V) sums.single(to_f32<T>(x[done + lane]), done + lane < id ? xt : xt_up);
   // the token's own vector was met with > throughout: its equal elements before the token
@@ -423,68 +444,68 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprobs(const LogArgs p, int s
     float gm = fmaxf(sums.m, __shfl_xor_sync(0xffffffffu, sums.m, 1));
     gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 2));
     if ((lane & 3) == 0) s_group[threadIdx.x >> 2] = gm;
-    if (threadIdx.x == 0) s_count = 0;
+    if (threadIdx.x == 0) s_count = s_found = 0;
     __syncthreads();
     const float thr = __shfl_sync(
         0xffffffffu, merge32(sort32(s_group[lane], lane), sort32(s_group[lane + 32], lane), lane), p.top - 1);
-    const unsigned owners = __ballot_sync(0xffffffffu, sums.m >= thr);
-    if (sums.m >= thr) s_owner[warp][__popc(owners & ((1u << lane) - 1))] = static_cast<uint8_t>(lane);
-    __syncwarp();
-    // the elements of this warp's threads that reach the bound, once more: f(element, index, exists)
-    auto again = [&](auto&& f) {
-      if (do_head) f(lane < head ? to_f32<T>(x[lane]) : 0.f, lane, lane < head);
-      if (do_tail) f(done + lane < p.V ? to_f32<T>(x[done + lane]) : 0.f, done + lane, done + lane < p.V);
-      const int w0 = va + warp * NV * 32;
-      const int each = w0 < vb ? ((vb - w0 - 1) / kStep + 1) * NV : 0;   // a thread's vectors, at most
-      const int items = __popc(owners) * each;
-      constexpr int U = 4;                                               // loads in flight
-      for (int i0 = 0; i0 < items; i0 += 32 * U) {
-        uint4 raw[U];
-        int at[U];
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-          const int i = i0 + k * 32 + lane;
-          at[k] = vb;
-          if (i < items) {
-            const int n = i % each;
-            at[k] = w0 + s_owner[warp][i / each] + n / NV * kStep + n % NV * 32;
-          }
-          raw[k] = at[k] < vb ? __ldg(xv + at[k]) : none;
-        }
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-          float e[VE];
-          unpack16<T>(raw[k], e);
-          float em = e[0];
-#pragma unroll
-          for (int j = 1; j < VE; ++j) em = fmaxf(em, e[j]);
-          if (!__any_sync(0xffffffffu, at[k] < vb && em >= thr)) continue;
-#pragma unroll
-          for (int j = 0; j < VE; ++j) f(e[j], head + at[k] * VE + j, at[k] < vb);
+    // the kept batches that reach it, and then their elements
+    if (sums.m >= thr) {
+      const int kept = (batch + (1 << ws) - 1) >> ws;
+#pragma unroll 8
+      for (int k = 0; k < kept; ++k) {
+        if (static_cast<float>(s_batch[k][threadIdx.x]) >= thr) {
+          const int pos = atomicAdd(&s_found, 1);
+          if (pos < kCand) s_at[pos] = k * kThreads + threadIdx.x;
         }
       }
+    }
+    __syncthreads();
+    const int found = s_found;
+    auto keep = [&](float e, int i) {
+      if (e >= thr) {
+        const int pos = atomicAdd(&s_count, 1);
+        if (pos < kCand) s_cand[pos] = key_of(e, i);
+      }
     };
-    again([&](float e, int i, bool exists) {
-      const bool in = exists && e >= thr;
-      const unsigned mask = __ballot_sync(0xffffffffu, in);
-      if (!mask) return;
-      int pos = 0;
-      if (lane == 0) pos = atomicAdd(&s_count, __popc(mask));
-      pos = __shfl_sync(0xffffffffu, pos, 0) + __popc(mask & ((1u << lane) - 1));
-      if (in && pos < kCand) s_cand[pos] = key_of(e, i);
-    });
+    if (found <= kCand) {
+      if (do_head && lane < head) keep(to_f32<T>(x[lane]), lane);
+      if (do_tail && done + lane < p.V) keep(to_f32<T>(x[done + lane]), done + lane);
+      const int per = NV << ws;   // vectors of a kept place
+      for (int i = threadIdx.x; i < found * per; i += kThreads) {
+        const int at = s_at[i / per], n = i % per, k = at / kThreads, owner = at % kThreads;
+        const int v = va + (owner >> 5) * NV * 32 + (owner & 31) + ((k << ws) + n / NV) * kStep + n % NV * 32;
+        if (v >= vb) continue;
+        float e[VE];
+        unpack16<T>(__ldg(xv + v), e);
+#pragma unroll
+        for (int j = 0; j < VE; ++j) keep(e[j], head + v * VE + j);
+      }
+    }
     __syncthreads();
     const int n = s_count;
-    if (n <= kCand) {
+    if (found <= kCand && n <= kCand) {
       if (warp == 0) {
         for (int i = 0; i < n; i += 32) {
           const u64 k = sort32(i + lane < n ? s_cand[i + lane] : u64(0), lane);
           best = i ? merge32(best, k, lane) : k;
         }
       }
-    } else {   // many equal elements: a list in each warp
+    } else {   // many equal elements: every element once more, into a list in each warp
       TopList list;
-      again([&](float e, int i, bool exists) { list.offer(key_of(e, i), exists && e >= thr, p.top, lane); });
+      auto offer = [&](float e, int i, bool exists) { list.offer(key_of(e, i), exists && e >= thr, p.top, lane); };
+      if (do_head) offer(lane < head ? to_f32<T>(x[lane]) : 0.f, lane, lane < head);
+      if (do_tail) offer(done + lane < p.V ? to_f32<T>(x[done + lane]) : 0.f, done + lane, done + lane < p.V);
+      for (int k = 0; k < batch; ++k) {
+        if (!__any_sync(0xffffffffu, static_cast<float>(s_batch[k >> ws][threadIdx.x]) >= thr)) continue;
+#pragma unroll 1
+        for (int i = 0; i < NV; ++i) {
+          const int v = first + k * kStep + i * 32;
+          float e[VE];
+          unpack16<T>(v < vb ? __ldg(xv + v) : none, e);
+#pragma unroll
+          for (int j = 0; j < VE; ++j) offer(e[j], head + v * VE + j, v < vb);
+        }
+      }
       __syncthreads();
       best = merge_warps(list.key, s_list, warp, lane);
     }
