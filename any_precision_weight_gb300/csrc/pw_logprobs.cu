@@ -577,10 +577,10 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprobs(const LogArgs p, int s
 
 template <typename T, bool TOP>
 cudaError_t launch_top(const LogArgs& p, int T_, cudaStream_t s) {
-  // as many CTAs to a row as give every SM two, each with some 2048 elements
+  // as many CTAs to a row as give every SM one, each with some 2048 elements
   const int sms = sm_count();
   int split = 1;
-  while (split < kMaxCluster && static_cast<int64_t>(T_) * split < 2 * sms && p.V >= 4096 * split) split *= 2;
+  while (split < kMaxCluster && static_cast<int64_t>(T_) * split < sms && p.V >= 4096 * split) split *= 2;
   if (static_cast<int64_t>(T_) * split > 0x7fffffff) return cudaErrorInvalidConfiguration;
   if (split > 8) {
     const cudaError_t e = cudaFuncSetAttribute(k_logprobs<T, TOP>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);

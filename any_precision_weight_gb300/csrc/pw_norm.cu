@@ -4,11 +4,18 @@
 //   s = x + residual (fp32);  y = s * w / sqrt(mean(s^2) + eps)
 //   scale = max|y| / 127;     q = rint(y / scale)
 //
-// One CTA per row; the row stays in registers as fp32, so every input is read
-// once.  Both row reductions, sum s^2 and max|s * w|, are taken in one pass and
-// joined behind one barrier: max|y| = max|s * w| * rstd, and
-// y / scale = s * w * 127 / max|s * w| does not need rstd at all.
-// Bound by HBM for many rows, by latency for few.
+// A row stays in registers as fp32, so every input is read once.  Both row
+// reductions, sum s^2 and max|s * w|, are taken in one pass and joined behind
+// one barrier: max|y| = max|s * w| * rstd, and y / scale = s * w * 127 /
+// max|s * w| does not need rstd at all.
+//
+// Bound by latency for few rows, by HBM for many: there one CTA per row leaves
+// the memory idle while it reduces and stores (8192 x 4096 fp16 with residual
+// and int8 output: 50 to 85 us), so persistent CTAs keep the next row's loads
+// in flight (38 us, 6.1 TB/s, 90 % of the copy peak; 28672 x 4096 fp16 to int8:
+// 60 us, 5.8 TB/s, 86 %).
+
+#include <algorithm>
 
 #include "pw_rows.cuh"
 
@@ -28,6 +35,14 @@ struct RowArgs {
   float eps;
 };
 
+// One 16-byte load (a plain reference to it would be read element by element).
+template <typename T>
+__device__ __forceinline__ uint4 load16(const T* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+  return v;
+}
+
 // VE elements at element e0 of a row of H, as fp32 (0 past the end).
 template <typename T, int VE>
 __device__ __forceinline__ void load_chunk(const T* row, int e0, int H, float (&v)[VE]) {
@@ -35,7 +50,7 @@ __device__ __forceinline__ void load_chunk(const T* row, int e0, int H, float (&
     v[0] = e0 < H ? to_f32<T>(row[e0]) : 0.f;
   } else {
     if (e0 + VE <= H) {
-      unpack16<T>(*reinterpret_cast<const uint4*>(row + e0), v);
+      unpack16<T>(load16(row + e0), v);
     } else {
 #pragma unroll
       for (int i = 0; i < VE; ++i) v[i] = e0 + i < H ? to_f32<T>(row[e0 + i]) : 0.f;
@@ -57,58 +72,117 @@ __device__ __forceinline__ void store_chunk(T* row, int e0, int H, const float (
   }
 }
 
-template <int VE>
-__device__ __forceinline__ void store_q(int8_t* row, int e0, int H, const int (&v)[VE]) {
-  if (VE > 1 && e0 + VE <= H) {
-    alignas(8) int8_t e[VE];
-#pragma unroll
-    for (int i = 0; i < VE; ++i) e[i] = static_cast<int8_t>(v[i]);
-    if constexpr (VE == 8) *reinterpret_cast<uint2*>(row + e0) = *reinterpret_cast<const uint2*>(e);
-    if constexpr (VE == 4) *reinterpret_cast<uint32_t*>(row + e0) = *reinterpret_cast<const uint32_t*>(e);
-  } else {
-#pragma unroll
-    for (int i = 0; i < VE; ++i)
-      if (e0 + i < H) row[e0 + i] = static_cast<int8_t>(v[i]);
-  }
-}
-
-// Sum of `a` and largest `b` over the CTA, in every thread.
+// Sum of `a` (where SUM) and largest `b` >= 0 over the CTA, in every thread.  The
+// bits of numbers that are not negative are in their order, and NaN's are above
+// them all.
+template <bool SUM>
 __device__ __forceinline__ void block_reduce(float& a, float& b, float2* sh) {
+  auto warp_max = [](float v) { return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v))); };
+  if (SUM) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, o);
-    b = max_nan(b, __shfl_xor_sync(0xffffffffu, b, o));
+    for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
   }
+  b = warp_max(b);
   const int nw = blockDim.x >> 5;
   if (nw == 1) return;
   if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = make_float2(a, b);
   __syncthreads();
   const float2 v = (threadIdx.x & 31) < nw ? sh[threadIdx.x & 31] : make_float2(0.f, 0.f);
   a = v.x;
-  b = v.y;
+  if (SUM) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, o);
-    b = max_nan(b, __shfl_xor_sync(0xffffffffu, b, o));
+    for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
   }
+  b = warp_max(v.y);
 }
 
-// Factors of a row's outputs: y = s * w * rstd; q = rint(s * w * up * inv).
-// Rows whose largest value is so small that 127 / max overflows are first
-// scaled up by 2^100.
+// Factors of a row's outputs, v = s * w: y = v * rstd; q = v * steps, rounded,
+// with v first times 2^100 where the row's largest value is so small that
+// 127 / max overflows.  Rows without a step (zeros, NaN, infinities) have q 0.
 struct RowScale {
-  float rstd, up, inv, scale;
+  float rstd, steps, scale;
+  bool tiny, none;
 };
 template <bool NORM>
 __device__ __forceinline__ RowScale row_scale(float ss, float amax, int H, float eps) {
   RowScale f;
   f.rstd = NORM ? 1.f / sqrtf(ss / static_cast<float>(H) + eps) : 1.f;
-  f.up = amax < 0x1p-100f ? 0x1p100f : 1.f;
-  f.inv = amax > 0.f ? 127.f / (amax * f.up) : 0.f;   // NaN: the comparison fails, q = 0
+  f.tiny = amax < 0x1p-100f;
+  f.none = !(amax > 0.f && amax < INFINITY);
+  f.steps = 127.f / (f.tiny ? amax * 0x1p100f : amax);
   f.scale = amax * f.rstd / 127.f;
   return f;
 }
 
+// v * steps rounded to the nearest whole number (ties to even), in the low byte:
+// 1.5 * 2^23 is added, above which fp32 holds whole numbers only.
+__device__ __forceinline__ uint32_t to_step(const RowScale& f, float v) {
+  return __float_as_uint(fmaf(v, f.steps, 12582912.f));
+}
+
+template <int VE>
+__device__ __forceinline__ void store_q(int8_t* row, int e0, int H, const float (&v)[VE], const RowScale& f) {
+  uint32_t b[VE];
+#pragma unroll
+  for (int i = 0; i < VE; ++i) b[i] = to_step(f, f.tiny ? v[i] * 0x1p100f : v[i]);
+  if (f.none) {
+#pragma unroll
+    for (int i = 0; i < VE; ++i) b[i] = 0;
+  }
+  if (VE > 1 && e0 + VE <= H) {
+    uint32_t w[(VE + 3) / 4];
+#pragma unroll
+    for (int i = 0; i + 3 < VE; i += 4)
+      w[i / 4] = __byte_perm(__byte_perm(b[i], b[i + 1], 0x0040), __byte_perm(b[i + 2], b[i + 3], 0x0040), 0x5410);
+    if constexpr (VE == 8) *reinterpret_cast<uint2*>(row + e0) = make_uint2(w[0], w[1]);
+    if constexpr (VE == 4) *reinterpret_cast<uint32_t*>(row + e0) = w[0];
+  } else {
+#pragma unroll
+    for (int i = 0; i < VE; ++i)
+      if (e0 + i < H) row[e0 + i] = static_cast<int8_t>(b[i]);
+  }
+}
+
+// A thread's chunks of a row, chunk c at element at(c): from v = x + residual
+// to the row's outputs.  g(c, i) is the weight of element i of chunk c.
+template <typename T, int VE, int VPT, bool NORM, typename At, typename Weight>
+__device__ __forceinline__ void finish_row(const RowArgs& p, int64_t row, float (&v)[VPT][VE], float2* sh, At&& at,
+                                           Weight&& weight) {
+  const int H = p.H;
+  float ss = 0.f, amax = 0.f;
+  if (p.sum) {
+#pragma unroll
+    for (int c = 0; c < VPT; ++c) store_chunk<T, VE>(static_cast<T*>(p.sum) + row * p.lds, at(c), H, v[c]);
+  }
+#pragma unroll
+  for (int c = 0; c < VPT; ++c) {
+    float g[VE];
+    if (NORM) weight(c, g);
+#pragma unroll
+    for (int i = 0; i < VE; ++i) {
+      if (NORM) ss = fmaf(v[c][i], v[c][i], ss), v[c][i] *= g[i];
+      amax = max_nan(amax, fabsf(v[c][i]));
+    }
+  }
+  block_reduce<NORM>(ss, amax, sh);
+  const RowScale f = row_scale<NORM>(ss, amax, H, p.eps);
+  if (p.y) {
+#pragma unroll
+    for (int c = 0; c < VPT; ++c) {
+      float y[VE];
+#pragma unroll
+      for (int i = 0; i < VE; ++i) y[i] = v[c][i] * f.rstd;
+      store_chunk<T, VE>(static_cast<T*>(p.y) + row * p.ldy, at(c), H, y);
+    }
+  }
+  if (p.q) {
+#pragma unroll
+    for (int c = 0; c < VPT; ++c) store_q<VE>(p.q + row * p.ldq, at(c), H, v[c], f);
+    if (threadIdx.x == 0) p.scale[row] = f.scale;
+  }
+}
+
+// One CTA per row: few rows, and rows that are not 16-byte aligned.
 template <typename T, int VE, int VPT, bool NORM>
 __global__ void __launch_bounds__(1024, 1) k_rows(const RowArgs p) {
   __shared__ float2 sh[32];
@@ -116,51 +190,87 @@ __global__ void __launch_bounds__(1024, 1) k_rows(const RowArgs p) {
   const int H = p.H;
   const T* x = static_cast<const T*>(p.x) + row * p.ldx;
   const T* r = p.r ? static_cast<const T*>(p.r) + row * p.ldr : nullptr;
-  const T* w = static_cast<const T*>(p.w);
-  float s[VPT][VE], g[VPT][VE];
-  float ss = 0.f, amax = 0.f;
+  auto at = [&](int c) { return static_cast<int>(threadIdx.x + c * blockDim.x) * VE; };
+  float v[VPT][VE];
 #pragma unroll
-  for (int c = 0; c < VPT; ++c) {
-    const int e0 = (threadIdx.x + c * blockDim.x) * VE;
-    load_chunk<T, VE>(x, e0, H, s[c]);
-    if (NORM) load_chunk<T, VE>(w, e0, H, g[c]);
-    if (r) {
+  for (int c = 0; c < VPT; ++c) load_chunk<T, VE>(x, at(c), H, v[c]);
+  if (r) {
+#pragma unroll
+    for (int c = 0; c < VPT; ++c) {
       float rv[VE];
-      load_chunk<T, VE>(r, e0, H, rv);
+      load_chunk<T, VE>(r, at(c), H, rv);
 #pragma unroll
-      for (int i = 0; i < VE; ++i) s[c][i] += rv[i];
-    }
-#pragma unroll
-    for (int i = 0; i < VE; ++i) {
-      ss = fmaf(s[c][i], s[c][i], ss);
-      amax = max_nan(amax, fabsf(NORM ? s[c][i] * g[c][i] : s[c][i]));
+      for (int i = 0; i < VE; ++i) v[c][i] += rv[i];
     }
   }
-  if (p.sum) {
-    T* d = static_cast<T*>(p.sum) + row * p.lds;
+  finish_row<T, VE, VPT, NORM>(p, row, v, sh, at, [&](int c, float(&g)[VE]) {
+    load_chunk<T, VE>(static_cast<const T*>(p.w), at(c), H, g);
+  });
+}
+
+// A chunk as it was loaded.
+template <typename T, int VE> struct Raw {
+  uint4 v;
+  __device__ __forceinline__ void load(const T* p) { v = load16(p); }
+  __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void unpack(float (&f)[VE]) const { unpack16<T>(v, f); }
+};
+template <typename T> struct Raw<T, 1> {
+  T v;
+  __device__ __forceinline__ void load(const T* p) { v = *p; }
+  __device__ __forceinline__ void zero() { v = from_f32<T>(0.f); }
+  __device__ __forceinline__ void unpack(float (&f)[1]) const { f[0] = to_f32<T>(v); }
+};
+
+// Many rows: persistent CTAs.  The weight stays in registers, and the loads of
+// the next row (RES: with its residual) or of the next two are in flight while
+// this one is reduced and stored.  Whole chunks only.
+template <typename T, int VE, int VPT, bool NORM, bool RES>
+__global__ void __launch_bounds__(1024, 1) k_rows_many(const RowArgs p, int T_) {
+  using R = Raw<T, VE>;
+  __shared__ float2 sh[2][32];
+  const int H = p.H;
+  auto at = [&](int c) { return static_cast<int>(threadIdx.x + c * blockDim.x) * VE; };
+  R w[VPT], x[VPT], r[VPT];   // r: the residual, or the row after next
+  auto fetch = [&](R(&to)[VPT], const void* from, int64_t ld, int64_t row) {
 #pragma unroll
-    for (int c = 0; c < VPT; ++c) store_chunk<T, VE>(d, (threadIdx.x + c * blockDim.x) * VE, H, s[c]);
-  }
-  block_reduce(ss, amax, sh);
-  const RowScale f = row_scale<NORM>(ss, amax, H, p.eps);
+    for (int c = 0; c < VPT; ++c)
+      if (at(c) < H) to[c].load(static_cast<const T*>(from) + row * ld + at(c));
+  };
 #pragma unroll
-  for (int c = 0; c < VPT; ++c) {
-    const int e0 = (threadIdx.x + c * blockDim.x) * VE;
-    if (p.y) {
-      float v[VE];
+  for (int c = 0; c < VPT; ++c) x[c].zero(), r[c].zero(), w[c].zero();
+  const int64_t step = gridDim.x;
+  int64_t row = blockIdx.x;
+  fetch(x, p.x, p.ldx, row);
+  if (RES)
+    fetch(r, p.r, p.ldr, row);
+  else if (row + step < T_)
+    fetch(r, p.x, p.ldx, row + step);
+  if (NORM) fetch(w, p.w, 0, 0);
+  for (int turn = 0; row < T_; row += step, turn ^= 1) {
+    float v[VPT][VE];
 #pragma unroll
-      for (int i = 0; i < VE; ++i) v[i] = NORM ? s[c][i] * f.rstd * g[c][i] : s[c][i];
-      store_chunk<T, VE>(static_cast<T*>(p.y) + row * p.ldy, e0, H, v);
+    for (int c = 0; c < VPT; ++c) {
+      x[c].unpack(v[c]);
+      if (RES) {
+        float rv[VE];
+        r[c].unpack(rv);
+#pragma unroll
+        for (int i = 0; i < VE; ++i) v[c][i] += rv[i];
+      } else {
+        x[c] = r[c];
+      }
     }
-    if (p.q) {
-      int v[VE];
-#pragma unroll
-      for (int i = 0; i < VE; ++i)
-        v[i] = __float2int_rn((NORM ? s[c][i] * g[c][i] : s[c][i]) * f.up * f.inv);
-      store_q<VE>(p.q + row * p.ldq, e0, H, v);
+    if (RES) {
+      if (row + step < T_) {
+        fetch(x, p.x, p.ldx, row + step);
+        fetch(r, p.r, p.ldr, row + step);
+      }
+    } else if (row + 2 * step < T_) {
+      fetch(r, p.x, p.ldx, row + 2 * step);
     }
+    finish_row<T, VE, VPT, NORM>(p, row, v, sh[turn], at, [&](int c, float(&g)[VE]) { w[c].unpack(g); });
   }
-  if (p.q && threadIdx.x == 0) p.scale[row] = f.scale;
 }
 
 // Rows too long for the registers of one CTA: the row is read twice.
@@ -192,7 +302,7 @@ __global__ void __launch_bounds__(1024, 1) k_rows_long(const RowArgs p) {
       amax = max_nan(amax, fabsf(NORM ? s[i] * g[i] : s[i]));
     }
   }
-  block_reduce(ss, amax, sh);
+  block_reduce<NORM>(ss, amax, sh);
   const RowScale f = row_scale<NORM>(ss, amax, H, p.eps);
   for (int64_t e = static_cast<int64_t>(threadIdx.x) * VE; e < H; e += step) {
     const int e0 = static_cast<int>(e);
@@ -200,26 +310,40 @@ __global__ void __launch_bounds__(1024, 1) k_rows_long(const RowArgs p) {
     load(e0, s, g);
     if (p.sum) store_chunk<T, VE>(static_cast<T*>(p.sum) + row * p.lds, e0, H, s);
 #pragma unroll
-    for (int i = 0; i < VE; ++i) v[i] = NORM ? s[i] * f.rstd * g[i] : s[i];
-    if (p.y) store_chunk<T, VE>(static_cast<T*>(p.y) + row * p.ldy, e0, H, v);
-    if (p.q) {
-      int qv[VE];
-#pragma unroll
-      for (int i = 0; i < VE; ++i) qv[i] = __float2int_rn((NORM ? s[i] * g[i] : s[i]) * f.up * f.inv);
-      store_q<VE>(p.q + row * p.ldq, e0, H, qv);
+    for (int i = 0; i < VE; ++i) {
+      if (NORM) s[i] *= g[i];
+      v[i] = s[i] * f.rstd;
     }
+    if (p.y) store_chunk<T, VE>(static_cast<T*>(p.y) + row * p.ldy, e0, H, v);
+    if (p.q) store_q<VE>(p.q + row * p.ldq, e0, H, s, f);
   }
   if (p.q && threadIdx.x == 0) p.scale[row] = f.scale;
 }
 
+template <typename T, int VE, int VPT, bool NORM>
+void launch_many(const RowArgs& p, int T_, int threads, cudaStream_t s) {
+  const int grid = std::min(T_, sm_count() * std::min(32, 1024 / threads));
+  if (p.r)
+    k_rows_many<T, VE, VPT, NORM, true><<<grid, threads, 0, s>>>(p, T_);
+  else
+    k_rows_many<T, VE, VPT, NORM, false><<<grid, threads, 0, s>>>(p, T_);
+}
+
+// Few rows take the shortest way through a row, one chunk a thread; many are
+// streamed by persistent CTAs, 1024 threads to an SM (64 registers a thread).
 template <typename T, int VE, bool NORM>
 cudaError_t launch_ve(const RowArgs& p, int T_, cudaStream_t s) {
+  // chunks of a persistent thread: as many as its registers hold, fp32 rows being twice as long
+  constexpr int kMany = VE == 1 ? 8 : VE == 4 && !NORM ? 4 : 2;
   const int chunks = (p.H + VE - 1) / VE;
   auto threads = [&](int vpt) { return ((chunks + vpt - 1) / vpt + 31) / 32 * 32; };
-  if (chunks <= 512) {
-    k_rows<T, VE, 1, NORM><<<T_, threads(1), 0, s>>>(p);
+  if (T_ >= 2 * sm_count() && p.H % VE == 0 && chunks <= 1024 * kMany) {
+    if (chunks <= 32)
+      launch_many<T, VE, 1, NORM>(p, T_, 32, s);
+    else
+      launch_many<T, VE, kMany, NORM>(p, T_, threads(kMany), s);
   } else if (chunks <= 1024) {
-    k_rows<T, VE, 2, NORM><<<T_, threads(2), 0, s>>>(p);
+    k_rows<T, VE, 1, NORM><<<T_, threads(1), 0, s>>>(p);
   } else if (chunks <= 4096) {
     k_rows<T, VE, 4, NORM><<<T_, threads(4), 0, s>>>(p);
   } else {

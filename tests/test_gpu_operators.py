@@ -102,6 +102,26 @@ def test_norm(T, H, dt, res):
     check_q(i8[0], i8[1], y, rel + 8 * U)
 
 
+@pytest.mark.parametrize("T,H", [(305, 8), (3001, 64), (700, 256), (1300, 264), (999, 513), (2100, 1411), (641, 2048),
+                                 (457, 4096), (310, 8191), (305, 14336), (306, 16384), (304, 32768)])
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("res", [False, True])
+def test_norm_many_rows(T, H, dt, res):
+    """More rows than CTAs: the persistent kernel, whose grids these T do not divide."""
+    rng = gen(T, H, dt, res)
+    x = place(rng.standard_normal((T, H), np.float32) * 2, DT[dt])
+    w = torch.as_tensor(rng.normal(1, 0.3, H)).to(DT[dt]).cuda()
+    r = place(rng.standard_normal((T, H), np.float32) * 3, DT[dt]) if res else None
+    s, y = ops.rms_norm(f64(x), f64(w), 1e-5, f64(r) if res else None)
+    q = pw.pw_rms_norm_i8(x, w, 1e-5, residual=r, out=(out := torch.empty_like(x)))
+    if res:
+        check_out(q[2], s, dt, U)
+    check_out(out, y, dt, 64 * U, extra=np.abs(f64(w)) * 4 * U if res else 0.0)
+    check_q(q[0], q[1], y, 72 * U)
+    if not res:
+        check_q(*pw.pw_quant_i8(x), f64(x), 2 * U)
+
+
 @pytest.mark.parametrize("off,pad", [(0, 8), (1, 0), (3, 5), (8, 16)])
 @pytest.mark.parametrize("H", [63, 128, 1411, 5000])
 def test_norm_strides_and_frames(off, pad, H):
