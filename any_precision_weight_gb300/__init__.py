@@ -90,7 +90,9 @@ _SIGS = {
     "pw_rms_norm": (_i, [_vp, _i64, _vp, _i64, _vp, ctypes.c_float, _i, _i, _i, _vp, _i64, _vp, _i64, _vp, _i64,
                          _vp, _vp]),
     "pw_quant_i8": (_i, [_vp, _i64, _i, _i, _i, _vp, _i64, _vp, _vp]),
-    "pw_linear_i8": (_i, [_vp, _i64, _vp, _vp, _i64, _vp, _vp, _i, _i, _i, _i, _vp, _i64, _vp]),
+    "pw_linear_i8": (_i, [_vp, _i64, _vp, _vp, _i64, _vp, _vp, _i, _i, _i, _i, _vp, _i64, _vp, _sz,
+                          _vp]),
+    "pw_linear_i8_workspace_bytes": (_sz, [_i, _i]),
     "pw_linear_i8_status": (_i, [_vp, _pi]),
     "pw_logprobs": (_i, [_vp, _i64, _i, _i, _i, _vp, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp]),
 }
@@ -638,10 +640,12 @@ def pw_quant_i8(x, q=None, scale=None, stream=None):
     return q, scale
 
 
-def pw_linear_i8(x, x_scale, w, w_scale, bias=None, out=None, out_dtype=None, stream=None):
+def pw_linear_i8(x, x_scale, w, w_scale, bias=None, out=None, out_dtype=None, ws=None, stream=None):
     """out [T][N] = (x . w^T) * x_scale[t] * w_scale[n] + bias[n], x [T][K] and
     w [N][K] int8 with 16-byte aligned rows (rows_i8), the sum exact.  out has
-    type out_dtype (default float16) where it is not given."""
+    type out_dtype (default float16) where it is not given.  ws: a uint8
+    workspace of pw_linear_i8_workspace_bytes(T, K) bytes (allocated here where
+    it is needed and not given)."""
     torch = _torch()
     T, K = _matrix(x, "x")
     N = _matrix(w, "w")[0]
@@ -650,12 +654,24 @@ def pw_linear_i8(x, x_scale, w, w_scale, bias=None, out=None, out_dtype=None, st
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"pw_linear_i8: out is {out.dtype}, not {out_dtype}")
     dt, f32, i8 = out.dtype, torch.float32, torch.int8
-    _check(lib().pw_linear_i8(x.data_ptr(), _rows(x, "x", i8, (T, K)), _vec(x_scale, "x_scale", f32, T),
-                              w.data_ptr(), _rows(w, "w", i8, (N, K)), _vec(w_scale, "w_scale", f32, N),
-                              None if bias is None else _vec(bias, "bias", dt, N), T, N, K, _code(dt),
-                              out.data_ptr(), _rows(out, "out", dt, (T, N)), _raw_stream(torch, stream, x)),
-           "pw_linear_i8")
+    L = lib()
+    if ws is None:
+        need = L.pw_linear_i8_workspace_bytes(T, K)
+        if need and stream is None:
+            ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+        elif need:
+            with torch.cuda.stream(stream):   # the allocator's memory belongs to the call's stream
+                ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+    _check(L.pw_linear_i8(x.data_ptr(), _rows(x, "x", i8, (T, K)), _vec(x_scale, "x_scale", f32, T),
+                          w.data_ptr(), _rows(w, "w", i8, (N, K)), _vec(w_scale, "w_scale", f32, N),
+                          None if bias is None else _vec(bias, "bias", dt, N), T, N, K, _code(dt),
+                          out.data_ptr(), _rows(out, "out", dt, (T, N)), None if ws is None else ws.data_ptr(),
+                          0 if ws is None else ws.numel(), _raw_stream(torch, stream, x)), "pw_linear_i8")
     return out
+
+
+def pw_linear_i8_workspace_bytes(T: int, K: int) -> int:
+    return lib().pw_linear_i8_workspace_bytes(T, K)
 
 
 def pw_linear_i8_status(stream=None) -> int:

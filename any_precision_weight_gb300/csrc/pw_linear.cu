@@ -5,13 +5,14 @@
 //
 // the sum exact in int32 (K <= 131071: 128 * 128 * K < 2^31).
 //
-// Up to 8 tokens: k_gemv, byte dot products on CUDA cores, the weights
-// streamed once.  More tokens: k_tc on the tensor cores.  This GPU's int8
-// tensor rate is a small part of its 16-bit rate, so the tensor work runs in
-// fp16: int8 values are exact in fp16, their products (at most 2^14) are exact
-// in fp32, and so are sums of up to 1024 of them (2^24).  Every 1024 terms the
-// fp32 accumulator moves from tensor memory into int32 registers, so the sum
-// is the whole-number one at any K.
+// Up to 32 tokens: k_few, int8 tensor-core products fed from registers, the
+// weights streamed once.  More tokens: k_tc on the 5th-generation tensor
+// cores.  This GPU's int8 tensor rate is a small part of its 16-bit rate, and
+// tcgen05 has no int8 kind here, so that work runs in fp16: int8 values are
+// exact in fp16, their products (at most 2^14) are exact in fp32, and so are
+// sums of up to 1024 of them (2^24).  Every 1024 terms the fp32 accumulator
+// moves from tensor memory into int32 registers, so the sum is the
+// whole-number one at any K.
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -65,147 +66,156 @@ __device__ __forceinline__ uint4 load_once(const int8_t* p) {
   return v;
 }
 
-__device__ __forceinline__ int dot16(const uint4& a, const uint4& b, int c) {
-  c = __dp4a(static_cast<int>(a.x), static_cast<int>(b.x), c);
-  c = __dp4a(static_cast<int>(a.y), static_cast<int>(b.y), c);
-  c = __dp4a(static_cast<int>(a.z), static_cast<int>(b.z), c);
-  return __dp4a(static_cast<int>(a.w), static_cast<int>(b.w), c);
+// D += A B, int8 16 x 32 by 32 x 8, int32.
+__device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-constexpr int kGemvWarps = 8;
-constexpr int kGemvTokens = 8;
+constexpr int kFewWarps = 8;
+constexpr int kFewTokens = 32;
 
-// A group of KW warps owns R channels and TT tokens and takes K in turns of
-// 512 bytes (16 a lane); KW warps of one group join in shared memory.
-template <typename O, int TT, int R>
-__global__ void __launch_bounds__(kGemvWarps * 32) k_gemv(const LinArgs p, int kw) {
-  __shared__ int s_part[kGemvWarps][R * TT];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int group = blockIdx.x * (kGemvWarps / kw) + warp / kw, turn = warp % kw;
-  const int n0 = group * R;
-  const int8_t* w[R];
+// A group of kw warps owns 16 channels and shares out K in runs of 64 columns.
+// Lane (g, q) = (lane / 4, lane % 4) loads the 16 bytes at column 16 q of
+// channels g and g + 8, and of token g of every 8: the operand registers of two
+// products, with the columns of K in an order of their own that both operands
+// share.  So the weights go from memory to the tensor cores through registers
+// alone, 64 bytes of a channel at a time.  NT: groups of 8 tokens.
+template <typename O, int NT>
+__global__ void __launch_bounds__(kFewWarps * 32, NT <= 2 ? 3 : 2) k_few(const LinArgs p, int kw) {
+  constexpr int kRow = NT * 8 + 1;   // padded against bank conflicts
+  __shared__ int s_part[kFewWarps][16 * kRow];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int groups = kFewWarps / kw, turn = warp % kw;
+  const int n0 = (blockIdx.x * groups + warp / kw) * 16;
+  const int runs = (p.K + 63) / 64;
+  const int r0 = static_cast<int>(static_cast<int64_t>(runs) * turn / kw);
+  const int r1 = static_cast<int>(static_cast<int64_t>(runs) * (turn + 1) / kw);
+  const int8_t* w0 = p.w + min(n0 + g, p.N - 1) * p.ldw + q * 16;
+  const int8_t* w1 = p.w + min(n0 + g + 8, p.N - 1) * p.ldw + q * 16;
+  const int8_t* x[NT];
 #pragma unroll
-  for (int r = 0; r < R; ++r) w[r] = p.w + min(n0 + r, p.N - 1) * p.ldw;
-  int acc[R][TT] = {};
-  const int whole = p.K & ~15;
-  const int step = kw * 512;
-  int k = turn * 512 + lane * 16;
-#pragma unroll 2
-  for (; k < whole; k += step) {
-    uint4 wv[R];
+  for (int j = 0; j < NT; ++j) x[j] = p.x + min(j * 8 + g, p.T - 1) * p.ldx + q * 16;
+  int acc[NT][4] = {};
+  auto step = [&](const uint4& a, const uint4& b, const uint4 (&v)[NT]) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) wv[r] = load_once(w[r] + k);
-#pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      if (t < p.T) {
-        const uint4 xv = __ldg(reinterpret_cast<const uint4*>(p.x + t * p.ldx + k));
-#pragma unroll
-        for (int r = 0; r < R; ++r) acc[r][t] = dot16(wv[r], xv, acc[r][t]);
-      }
+    for (int j = 0; j < NT; ++j) {
+      mma_s8(acc[j], a.x, b.x, a.y, b.y, v[j].x, v[j].y);
+      mma_s8(acc[j], a.z, b.z, a.w, b.w, v[j].z, v[j].w);
     }
+  };
+  const int whole = min(r1, p.K / 64);
+  int k = r0;
+  constexpr int U = 4;   // runs in flight
+  for (; k + U <= whole; k += U) {
+    uint4 a[U], b[U], v[U][NT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      a[u] = load_once(w0 + (k + u) * 64);
+      b[u] = load_once(w1 + (k + u) * 64);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) v[u][j] = __ldg(reinterpret_cast<const uint4*>(x[j] + (k + u) * 64));
+#pragma unroll
+    for (int u = 0; u < U; ++u) step(a[u], b[u], v[u]);
   }
-  if (k == whole && whole < p.K) {   // the lane whose turn the last, partial 16 bytes are
+  for (; k < r1; ++k) {   // single runs, the last one perhaps not whole
+    const int left = p.K - k * 64 - q * 16;
+    auto part = [&](const int8_t* from) {
+      return left >= 16 ? __ldg(reinterpret_cast<const uint4*>(from + k * 64)) : load_tail(from + k * 64, left);
+    };
+    uint4 v[NT];
 #pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      if (t < p.T) {
-        const uint4 xv = load_tail(p.x + t * p.ldx + k, p.K - whole);
-#pragma unroll
-        for (int r = 0; r < R; ++r) acc[r][t] = dot16(load_tail(w[r] + k, p.K - whole), xv, acc[r][t]);
-      }
-    }
+    for (int j = 0; j < NT; ++j) v[j] = part(x[j]);
+    step(part(w0), part(w1), v);
   }
+  // acc[j][0..3]: channels g, g, g + 8, g + 8; tokens 8 j + 2 q + 0, 1, 0, 1
 #pragma unroll
-  for (int r = 0; r < R; ++r)
+  for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      const int v = __reduce_add_sync(0xffffffffu, acc[r][t]);
-      if (lane == 0) s_part[warp][r * TT + t] = v;
-    }
+    for (int i = 0; i < 4; ++i) s_part[warp][(g + (i >> 1) * 8) * kRow + j * 8 + q * 2 + (i & 1)] = acc[j][i];
   __syncthreads();
-  // thread i: value i % (R * TT) of the CTA's group i / (R * TT)
-  const int i = threadIdx.x, g = i / (R * TT), v = i % (R * TT);
-  if (g >= kGemvWarps / kw) return;
-  const int n = (blockIdx.x * (kGemvWarps / kw) + g) * R + v / TT, t = v % TT;
-  if (n >= p.N || t >= p.T) return;
-  int sum = 0;
-  for (int j = 0; j < kw; ++j) sum += s_part[g * kw + j][v];
-  store_out<O>(p, t, n, sum, p.xs[t], p.ws[n], p.bias ? to_f32<O>(static_cast<const O*>(p.bias)[n]) : 0.f);
+  for (int i = threadIdx.x; i < groups * 16 * p.T; i += kFewWarps * 32) {
+    const int c = i % (groups * 16), t = i / (groups * 16), grp = c >> 4;
+    const int n = blockIdx.x * groups * 16 + c;
+    if (n >= p.N) continue;
+    int sum = 0;
+    for (int j = 0; j < kw; ++j) sum += s_part[grp * kw + j][(c & 15) * kRow + t];
+    store_out<O>(p, t, n, sum, p.xs[t], p.ws[n], p.bias ? to_f32<O>(static_cast<const O*>(p.bias)[n]) : 0.f);
+  }
 }
 
-template <typename O, int TT>
-void launch_gemv_t(const LinArgs& p, cudaStream_t s) {
-  // enough warps to fill the GPU: four channels to a warp where there are many
-  // (one read of the tokens serves four), one where there are few, and as many
-  // warps to a channel as it takes, each with at least one turn
-  const int turns = (p.K + 511) / 512;
-  const int want = sm_count() * 16;
-  const int R = p.N >= 4 * sm_count() ? 4 : 1;
-  const int groups = (p.N + R - 1) / R;
+template <typename O, int NT>
+cudaError_t launch_few_nt(const LinArgs& p, cudaStream_t s) {
+  // enough warps to fill the GPU, each with two runs or more: one to 16
+  // channels where there are many (the CTA's warps then share the tokens in
+  // the L1), up to eight where there are few
+  const int groups = (p.N + 15) / 16, runs = (p.K + 63) / 64;
   int kw = 1;
-  while (kw < kGemvWarps && kw < turns && groups * kw < want) kw *= 2;
-  const int grid = (groups + kGemvWarps / kw - 1) / (kGemvWarps / kw);
-  if (R == 4)
-    k_gemv<O, TT, 4><<<grid, kGemvWarps * 32, 0, s>>>(p, kw);
-  else
-    k_gemv<O, TT, 1><<<grid, kGemvWarps * 32, 0, s>>>(p, kw);
+  while (kw < kFewWarps && groups * kw < sm_count() * 16 && runs >= 4 * kw) kw *= 2;
+  const int per = kFewWarps / kw;
+  k_few<O, NT><<<(groups + per - 1) / per, kFewWarps * 32, 0, s>>>(p, kw);
+  return cudaGetLastError();
 }
 
 template <typename O>
-cudaError_t launch_gemv(const LinArgs& p, cudaStream_t s) {
-  if (p.T == 1)
-    launch_gemv_t<O, 1>(p, s);
-  else if (p.T == 2)
-    launch_gemv_t<O, 2>(p, s);
-  else if (p.T <= 4)
-    launch_gemv_t<O, 4>(p, s);
-  else
-    launch_gemv_t<O, 8>(p, s);
-  return cudaGetLastError();
+cudaError_t launch_few(const LinArgs& p, cudaStream_t s) {
+  if (p.T <= 8) return launch_few_nt<O, 1>(p, s);
+  if (p.T <= 16) return launch_few_nt<O, 2>(p, s);
+  return launch_few_nt<O, 4>(p, s);
 }
 
 // ---------------------------------------------------------------- tensor cores
 
-// One CTA per SM; a tile is 128 channels (M, the weights) x NT tokens (N).
+// k_widen writes the tokens as fp16 into the workspace; then one CTA per SM
+// takes tiles of 128 channels (M, the weights) x NT tokens (N).
 // Warps by role:
-//  * warp 0 fetches int8 tiles of BK columns by TMA into a ring of S8 stages;
-//  * the last 8 warps convert a stage to fp16, both operands, into the K-major
-//    128-byte-swizzled layout the MMA reads: a ring of S16 stages.  A byte b
-//    becomes the fp16 number 1024 + (b + 128) by placing it in the low byte of
-//    0x6400, and 1152 is subtracted: five operations for four values;
+//  * the last 8 warps, in 4 groups that take a stage in turn, bring int8
+//    weights from memory through registers into the fp16 operand ring: a
+//    group's loads for its next stage are in flight while it waits for a free
+//    one.  A byte b becomes the fp16 number 1024 + (b + 128) by placing it in
+//    the low byte of 0x6400, and 1152 is subtracted: five operations for four
+//    values, stored in the K-major 128-byte-swizzled layout the MMA reads;
+//  * warp 2 fetches the fp16 tokens into the ring by TMA;
 //  * warp 1 issues tcgen05.mma kind::f16 (fp32 in tensor memory, two
 //    accumulators of NT columns), 1024 columns of K into one accumulator,
 //    then the next 1024 into the other;
 //  * warps 4.. add each finished accumulator to their int32 registers while
 //    the next one fills, and at the tile's end scale and store.
+// What bounds it is the shared-memory data pipe (128 bytes a clock), which the
+// tensor cores' operand reads share with the conversion: converting the tokens
+// here too made 1025 of its clocks for the 512 of a 128 x 256 x 64 step.
 // Where there are few tiles a cluster of CTAs splits K and adds the parts
 // through distributed shared memory; whole numbers, so in any order.
 constexpr int kM = 128;
+constexpr int kBK = 64;         // K columns of a stage: a 128-byte row of fp16
 constexpr int kConvWarps = 8;
-constexpr int kExactK = 1024;   // 2^24 / 2^14 products that fp32 adds exactly
+constexpr int kGroups = 4;      // of converting warps, a stage at a time each
+constexpr int kGroupWarps = kConvWarps / kGroups;
+constexpr int kChunk = 1024 / kBK;   // stages that fp32 adds exactly: 2^24 / 2^14 products
 constexpr int kEpiWarp0 = 4;
 
 template <int NT>
 struct Tile {
-  static constexpr int BK = NT <= 64 ? 128 : 64;          // K columns of a stage
   static constexpr int EW = NT <= 64 ? 4 : 8;             // accumulating warps
   static constexpr int ACC = NT / (EW / 4);               // int32 sums of one of their threads
   static constexpr int kConvWarp0 = kEpiWarp0 + EW;
   static constexpr int kThreads = 32 * (kConvWarp0 + kConvWarps);
-  static constexpr int A8 = kM * BK, B8 = NT * BK;        // bytes of an int8 stage
-  static constexpr int A16 = 2 * A8, B16 = 2 * B8;        // and of an fp16 stage
-  static constexpr int S8 = NT <= 64 ? 4 : NT == 128 ? 5 : 3;
-  static constexpr int S16 = NT <= 64 ? 2 : NT == 128 ? 4 : 3;
-  static constexpr int kRing16 = S16 * (A16 + B16);
-  static constexpr int kOffBar = kRing16 + S8 * (A8 + B8);
-  static constexpr int kSmem = kOffBar + 8 * (2 * S8 + 2 * S16 + 4) + 16 + 1024;
-  static constexpr uint32_t kCols = NT < 16 ? 32 : 2 * NT;
-  static constexpr int kSubs = BK / 64;                   // 64-column halves of a stage
-  static constexpr int kChunk = kExactK / BK;             // stages of one exact sum
+  static constexpr int A = kM * kBK * 2, B = NT * kBK * 2;   // bytes of a stage's operands
+  static constexpr int S = NT <= 128 ? 6 : 4;             // stages
+  static constexpr int kOffBar = S * (A + B);
+  static constexpr int kSmem = kOffBar + 8 * (3 * S + 4) + 16 + 1024;
+  static constexpr uint32_t kCols = 2 * NT;
   // D f32, A and B f16, N / 8 and M / 16
   static constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(NT >> 3) << 17) |
                                      (static_cast<uint32_t>(kM >> 4) << 24);
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
-  static_assert(kM * NT * 4 <= kRing16, "a tile's int32 sums fit the fp16 ring");
+  static_assert(kM * NT * 4 <= kOffBar, "a tile's int32 sums fit the ring");
 };
 
 // Registers by role for NT = 256, whose accumulating threads hold 128 sums:
@@ -233,53 +243,39 @@ __device__ __forceinline__ void to_f16x4(uint32_t v, uint32_t& lo, uint32_t& hi)
   hi = *reinterpret_cast<const uint32_t*>(&y);
 }
 
-__device__ __forceinline__ uint4 lds16(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-  return v;
-}
 __device__ __forceinline__ void sts16(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
-// Address of 16-byte chunk c of row r in an int8 tile as the TMA writes it:
-// rows of 128 bytes with the 128-byte swizzle, or of 64 with the 64-byte one.
-template <int BK>
-__device__ __forceinline__ uint32_t at8(uint32_t base, int r, int c) {
-  return BK == 128 ? base + r * 128 + ((c ^ (r & 7)) << 4) : base + r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-}
-
-// This thread's chunks of an int8 tile of ROWS rows, converted to fp16: 64
-// columns are a 128-byte row of an fp16 half tile, 16 bytes become two chunks.
-template <int BK, int ROWS>
-struct Convert {
-  static constexpr int kTotal = ROWS * BK / 16, kThreads = kConvWarps * 32;
-  static constexpr int kN = (kTotal + kThreads - 1) / kThreads;
+// A converting thread's part of a stage: 16 columns at 16 (tid % 4) of the
+// channels tid / 4 + 16 i.  Four neighbouring threads read 64 bytes of one
+// channel, and eight write 16-byte pieces of two rows to different banks.
+struct Weights {
+  static constexpr int kN = kM / (kGroupWarps * 8);
   uint4 v[kN];
 
-  __device__ __forceinline__ void load(uint32_t src, int tid) {
+  __device__ __forceinline__ void load(const LinArgs& p, int n0, int step, int tid) {
+    const int k = step * kBK + (tid & 3) * 16, left = p.K - k;
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const int at = tid + i * kThreads;
-      if (kTotal % kThreads == 0 || at < kTotal) v[i] = lds16(at8<BK>(src, at % ROWS, at / ROWS));
+      // channels past the end repeat the last one (their sums are not stored);
+      // columns past K meet tokens that are zero there
+      const int8_t* from = p.w + min(n0 + (tid >> 2) + i * (kGroupWarps * 8), p.N - 1) * p.ldw + k;
+      v[i] = left >= 16 ? load_once(from) : load_tail(from, left);
     }
   }
-  __device__ __forceinline__ void store(uint32_t dst, int tid) {
+  __device__ __forceinline__ void store(uint32_t dst, int tid) const {
+    const int j = (tid & 3) * 2;
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const int at = tid + i * kThreads;
-      if (kTotal % kThreads == 0 || at < kTotal) {
-        const int r = at % ROWS, c = at / ROWS;
-        const uint32_t row = dst + (c >> 2) * (ROWS * 128) + r * 128;
-        const int j = (c & 3) * 2;
-        uint32_t h[8];
-        to_f16x4(v[i].x, h[0], h[1]);
-        to_f16x4(v[i].y, h[2], h[3]);
-        to_f16x4(v[i].z, h[4], h[5]);
-        to_f16x4(v[i].w, h[6], h[7]);
-        sts16(row + ((j ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
-        sts16(row + (((j + 1) ^ (r & 7)) << 4), h[4], h[5], h[6], h[7]);
-      }
+      const int r = (tid >> 2) + i * (kGroupWarps * 8);
+      uint32_t h[8];
+      to_f16x4(v[i].x, h[0], h[1]);
+      to_f16x4(v[i].y, h[2], h[3]);
+      to_f16x4(v[i].z, h[4], h[5]);
+      to_f16x4(v[i].w, h[6], h[7]);
+      sts16(dst + r * 128 + ((j ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
+      sts16(dst + r * 128 + (((j + 1) ^ (r & 7)) << 4), h[4], h[5], h[6], h[7]);
     }
   }
 };
@@ -293,17 +289,27 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// The loads issued so far have arrived; r cannot be used before.
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
 
 __device__ __forceinline__ void cta_barrier() { asm volatile("bar.sync 0;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ int ld_cluster(uint32_t addr, uint32_t rank) {
+__device__ __forceinline__ int4 ld_cluster(uint32_t addr, uint32_t rank) {
   uint32_t a;
-  int v;
+  int4 v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
   return v;
 }
 
@@ -337,17 +343,15 @@ __device__ __forceinline__ Use use(uint32_t i) {
 
 template <typename O, int NT>
 __global__ void __launch_bounds__(Tile<NT>::kThreads, 1)
-k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_constant__ CUtensorMap mapx, int split) {
+k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapx, int split) {
   using C = Tile<NT>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);
   const uint32_t base = saddr(smem);
-  const uint32_t full8 = base + C::kOffBar, empty8 = full8 + 8 * C::S8;
-  const uint32_t full16 = empty8 + 8 * C::S8, empty16 = full16 + 8 * C::S16;
-  const uint32_t dfull = empty16 + 8 * C::S16, dempty = dfull + 16;
-  int* s_misc = reinterpret_cast<int*>(smem + C::kOffBar + 8 * (2 * C::S8 + 2 * C::S16 + 4));   // tmem, abort
+  const uint32_t fullw = base + C::kOffBar, fullx = fullw + 8 * C::S, empty = fullx + 8 * C::S;
+  const uint32_t dfull = empty + 8 * C::S, dempty = dfull + 16;
+  int* s_misc = reinterpret_cast<int*>(smem + C::kOffBar + 8 * (3 * C::S + 4));   // tmem, abort
   volatile int* abort = s_misc + 1;
-  const uint32_t ring8 = base + C::kRing16;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t rank = 0;
   if (split > 1) asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -358,8 +362,11 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   if (tid == 0) {
-    for (int i = 0; i < C::S8; ++i) mbar_init(full8 + 8 * i, 1), mbar_init(empty8 + 8 * i, kConvWarps);
-    for (int i = 0; i < C::S16; ++i) mbar_init(full16 + 8 * i, kConvWarps), mbar_init(empty16 + 8 * i, 1);
+    for (int i = 0; i < C::S; ++i) {
+      mbar_init(fullw + 8 * i, kGroupWarps);   // the weights of a stage
+      mbar_init(fullx + 8 * i, 1);             // the tokens
+      mbar_init(empty + 8 * i, 1);
+    }
     for (int i = 0; i < 2; ++i) mbar_init(dfull + 8 * i, 1), mbar_init(dempty + 8 * i, C::EW);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     s_misc[1] = 0;
@@ -379,7 +386,7 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
 
   const int ntn = (p.N + kM - 1) / kM, ntt = (p.T + NT - 1) / NT;
   const int tiles = ntn * ntt;
-  const int steps_all = (p.K + C::BK - 1) / C::BK;
+  const int steps_all = (p.K + kBK - 1) / kBK;
   const int s0 = static_cast<int>(static_cast<int64_t>(steps_all) * rank / split);
   const int s1 = static_cast<int>(static_cast<int64_t>(steps_all) * (rank + 1) / split);
   const int steps = s1 - s0;
@@ -388,29 +395,28 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
   constexpr bool kSplitRegs = NT == 256;
   if (warp < kEpiWarp0) {
     if constexpr (kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-    if (warp == 0 && lane == 0) {
-      // ---- int8 tiles by TMA
+    if (warp == 2 && lane == 0) {
+      // ---- fp16 tokens by TMA, once k_widen has written them
+      asm volatile("griddepcontrol.wait;" ::: "memory");
       uint32_t g = 0;
       bool ok = true;
       for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
-        const int n0 = (tile % ntn) * kM, t0 = (tile / ntn) * NT;
+        const int t0 = (tile / ntn) * NT;
         for (int k = s0; k < s1; ++k, ++g) {
-          const Use u = use<C::S8>(g);
-          if (g >= C::S8 && !wait(empty8 + 8 * u.stage, u.parity ^ 1)) {
+          const Use u = use<C::S>(g);
+          if (g >= C::S && !wait(empty + 8 * u.stage, u.parity ^ 1)) {
             ok = false;
             break;
           }
-          const uint32_t dst = ring8 + u.stage * (C::A8 + C::B8);
-          mbar_expect_tx(full8 + 8 * u.stage, C::A8 + C::B8);
-          tma_load_2d(dst, &mapw, k * C::BK, n0, full8 + 8 * u.stage);
-          tma_load_2d(dst + C::A8, &mapx, k * C::BK, t0, full8 + 8 * u.stage);
+          mbar_expect_tx(fullx + 8 * u.stage, C::B);
+          tma_load_2d(base + u.stage * (C::A + C::B) + C::A, &mapx, k * kBK, t0, fullx + 8 * u.stage);
         }
       }
       // after an abort the copies in flight still land before the CTA ends
       if (*abort) {
         const int none = 0;
-        for (uint32_t i = g > C::S8 ? g - C::S8 : 0; i < g; ++i)
-          wait_clocks(full8 + 8 * use<C::S8>(i).stage, use<C::S8>(i).parity, &none);
+        for (uint32_t i = g > C::S ? g - C::S : 0; i < g; ++i)
+          wait_clocks(fullx + 8 * use<C::S>(i).stage, use<C::S>(i).parity, &none);
       }
     }
     if (warp == 1 && lane == 0) {
@@ -423,29 +429,25 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
           if (d >= 2 && !(ok = wait(dempty + 8 * ud.stage, ud.parity ^ 1))) break;
           tc_fence_after();
           const uint32_t acc = tmem + ud.stage * NT;
-          const int end = min(steps, k + C::kChunk);
+          const int end = min(steps, k + kChunk);
           for (bool first = true; k < end; ++k, ++g) {
-            const Use u = use<C::S16>(g);
-            if (!(ok = wait(full16 + 8 * u.stage, u.parity))) break;
+            const Use u = use<C::S>(g);
+            if (!(ok = wait(fullx + 8 * u.stage, u.parity) && wait(fullw + 8 * u.stage, u.parity))) break;
             tc_fence_after();
-            const uint32_t a = base + u.stage * (C::A16 + C::B16), b = a + C::A16;
+            const uint32_t a = base + u.stage * (C::A + C::B), b = a + C::A;
 #pragma unroll
-            for (int s = 0; s < C::kSubs; ++s)
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk) {
-                mma_f16(acc, smem_desc(a + s * kM * 128 + kk * 32), smem_desc(b + s * NT * 128 + kk * 32), C::kIdesc,
-                        !first || s || kk);
-              }
+            for (int kk = 0; kk < kBK / 16; ++kk)
+              mma_f16(acc, smem_desc(a + kk * 32), smem_desc(b + kk * 32), C::kIdesc, !first || kk);
             first = false;
-            mma_commit(empty16 + 8 * u.stage);
+            mma_commit(empty + 8 * u.stage);
           }
           if (ok) mma_commit(dfull + 8 * ud.stage);
         }
       }
       if (*abort && g) {   // the MMAs in flight end before the CTA does
         const int none = 0;
-        const Use u = use<C::S16>(g - 1);
-        wait_clocks(empty16 + 8 * u.stage, u.parity, &none);
+        const Use u = use<C::S>(g - 1);
+        wait_clocks(empty + 8 * u.stage, u.parity, &none);
       }
     }
     __syncwarp();
@@ -464,7 +466,7 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
       int acc[C::ACC];
 #pragma unroll
       for (int i = 0; i < C::ACC; ++i) acc[i] = 0;
-      for (int k = 0; k < steps; k += C::kChunk, ++d) {
+      for (int k = 0; k < steps; k += kChunk, ++d) {
         const Use ud = use<2>(d);
         ok = __all_sync(0xffffffffu, wait(dfull + 8 * ud.stage, ud.parity));
         if (!ok) break;
@@ -473,7 +475,7 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
         for (int c = 0; c < C::ACC; c += 16) {
           uint32_t r[16];
           tmem_ld16(lanes + ud.stage * NT + c, r);
-          tmem_wait();
+          tmem_wait(r);
 #pragma unroll
           for (int i = 0; i < 16; ++i) acc[c + i] += __float2int_rn(__uint_as_float(r[i]));
         }
@@ -493,7 +495,7 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
           }
         }
       } else {
-        // every stage of the rings has been read: their space takes the sums
+        // every stage of the ring has been read: its space takes the sums
         int* part = reinterpret_cast<int*>(smem);
 #pragma unroll
         for (int i = 0; i < C::ACC; ++i) part[(half * C::ACC + i) * kM + q * 32 + lane] = acc[i];
@@ -507,30 +509,25 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
   } else {
     // ---- int8 to fp16
     if constexpr (kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
-    const int ctid = tid - C::kConvWarp0 * 32;
-    uint32_t g = 0;
-    bool ok = true;
-    for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
-      for (int k = 0; k < steps; ++k, ++g) {
-        const Use u8 = use<C::S8>(g), u16 = use<C::S16>(g);
-        ok = __all_sync(0xffffffffu, wait(full8 + 8 * u8.stage, u8.parity));
-        if (!ok) break;
-        const uint32_t src = ring8 + u8.stage * (C::A8 + C::B8);
-        Convert<C::BK, kM> ca;
-        Convert<C::BK, NT> cb;
-        ca.load(src, ctid);
-        cb.load(src + C::A8, ctid);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty8 + 8 * u8.stage);
-        if (g >= C::S16) ok = __all_sync(0xffffffffu, wait(empty16 + 8 * u16.stage, u16.parity ^ 1));
-        if (!ok) break;
-        const uint32_t dst = base + u16.stage * (C::A16 + C::B16);
-        ca.store(dst, ctid);
-        cb.store(dst + C::A16, ctid);
-        proxy_fence_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(full16 + 8 * u16.stage);
-      }
+    const int ctid = (tid - C::kConvWarp0 * 32) % (kGroupWarps * 32);
+    int tile = tile0, k = (warp - C::kConvWarp0) / kGroupWarps;
+    uint32_t g = k;   // this group's stage among all of the CTA's
+    auto settle = [&] {
+      for (; k >= steps && tile < tiles; tile += tile_step) k -= steps;
+    };
+    Weights w;
+    settle();
+    if (tile < tiles) w.load(p, (tile % ntn) * kM, s0 + k, ctid);
+    for (; tile < tiles; g += kGroups) {
+      const Use u = use<C::S>(g);
+      if (g >= C::S && !__all_sync(0xffffffffu, wait(empty + 8 * u.stage, u.parity ^ 1))) break;
+      w.store(base + u.stage * (C::A + C::B), ctid);
+      proxy_fence_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(fullw + 8 * u.stage);
+      k += kGroups;
+      settle();
+      if (tile < tiles) w.load(p, (tile % ntn) * kM, s0 + k, ctid);
     }
     __syncwarp();
     if constexpr (kSplitRegs) {
@@ -546,12 +543,22 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
     if (!*abort) {
       const int n0 = (tile0 % ntn) * kM, t0 = (tile0 / ntn) * NT;
       const int j0 = NT * rank / split, j1 = NT * (rank + 1) / split;
-      for (int i = j0 * kM + tid; i < j1 * kM; i += C::kThreads) {
-        const int t = t0 + i / kM, n = n0 + i % kM;
+#pragma unroll 2
+      for (int i = j0 * (kM / 4) + tid; i < j1 * (kM / 4); i += C::kThreads) {
+        const int t = t0 + i / (kM / 4), n = n0 + i % (kM / 4) * 4;
         if (t >= p.T || n >= p.N) continue;
-        int sum = 0;
-        for (int r = 0; r < split; ++r) sum += ld_cluster(base + i * 4, r);
-        store_out<O>(p, t, n, sum, p.xs[t], p.ws[n], p.bias ? to_f32<O>(static_cast<const O*>(p.bias)[n]) : 0.f);
+        int4 sum = make_int4(0, 0, 0, 0);
+#pragma unroll 4
+        for (int r = 0; r < split; ++r) {
+          const int4 v = ld_cluster(base + i * 16, r);
+          sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+        }
+        const int v[4] = {sum.x, sum.y, sum.z, sum.w};
+        const float xs = p.xs[t];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (n + c < p.N)
+            store_out<O>(p, t, n + c, v[c], xs, p.ws[n + c], p.bias ? to_f32<O>(static_cast<const O*>(p.bias)[n + c]) : 0.f);
       }
     }
     cluster_sync();
@@ -560,6 +567,26 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
   __syncthreads();
   tc_fence_after();
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols));
+}
+
+// Tokens as fp16, [T][kp] with kp a multiple of 64, zero past K.
+__global__ void __launch_bounds__(256) k_widen(const int8_t* x, int64_t ldx, int T, int K, int kp, __half* out) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int per = kp / 16;
+  for (int64_t i = blockIdx.x * 256 + threadIdx.x; i < static_cast<int64_t>(T) * per; i += gridDim.x * 256) {
+    const int64_t t = i / per;
+    const int k = static_cast<int>(i - t * per) * 16;
+    const int8_t* from = x + t * ldx + k;
+    const uint4 v = k + 16 <= K ? __ldg(reinterpret_cast<const uint4*>(from)) : load_tail(from, K - k);
+    uint32_t h[8];
+    to_f16x4(v.x, h[0], h[1]);
+    to_f16x4(v.y, h[2], h[3]);
+    to_f16x4(v.z, h[4], h[5]);
+    to_f16x4(v.w, h[6], h[7]);
+    uint4* to = reinterpret_cast<uint4*>(out + t * kp + k);
+    to[0] = make_uint4(h[0], h[1], h[2], h[3]);
+    to[1] = make_uint4(h[4], h[5], h[6], h[7]);
+  }
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
@@ -575,26 +602,26 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
 }
 
-// Boxes of bk columns x box rows of an int8 matrix; columns and rows past its
-// ends read as zero.
-cudaError_t map_i8(CUtensorMap* m, const int8_t* base, int64_t ld, int rows, int cols, int bk, int box) {
+// Boxes of kBK columns x box rows of an fp16 matrix; rows past its end read as zero.
+cudaError_t map_f16(CUtensorMap* m, const void* base, int rows, int cols, int box) {
   const auto encode = encoder();
   if (!encode) return cudaErrorNotSupported;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld)};
-  const cuuint32_t boxes[2] = {static_cast<cuuint32_t>(bk), static_cast<cuuint32_t>(box)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
+  const cuuint32_t boxes[2] = {kBK, static_cast<cuuint32_t>(box)};
   const cuuint32_t es[2] = {1, 1};
-  const CUresult r =
-      encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(base), dims, strides, boxes, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, bk == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(base), dims, strides, boxes, es,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
+
+int padded_k(int K) { return (K + 63) & ~63; }
 
 constexpr int kMaxDev = 64;
 
 template <typename O, int NT>
-cudaError_t launch_tc_nt(const LinArgs& p, cudaStream_t s) {
+cudaError_t launch_tc_nt(const LinArgs& p, void* ws, cudaStream_t s) {
   using C = Tile<NT>;
   static std::atomic<bool> ready[kMaxDev];
   int dev = 0;
@@ -610,13 +637,18 @@ cudaError_t launch_tc_nt(const LinArgs& p, cudaStream_t s) {
     if (NT == 256 && at.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
     ready[dev].store(true, std::memory_order_release);
   }
-  CUtensorMap mapw, mapx;
-  e = map_i8(&mapw, p.w, p.ldw, p.N, p.K, C::BK, kM);
-  if (e == cudaSuccess) e = map_i8(&mapx, p.x, p.ldx, p.T, p.K, C::BK, NT);
+  CUtensorMap mapx;
+  const int kp = padded_k(p.K);
+  e = map_f16(&mapx, ws, p.T, kp, NT);
   if (e != cudaSuccess) return e;
   const int sms = sm_count();
+  const int64_t chunks = static_cast<int64_t>(p.T) * (kp / 16);
+  k_widen<<<static_cast<unsigned>(std::min<int64_t>((chunks + 255) / 256, sms * 8)), 256, 0, s>>>(
+      p.x, p.ldx, p.T, p.K, kp, static_cast<__half*>(ws));
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
   const int64_t tiles = static_cast<int64_t>((p.N + kM - 1) / kM) * ((p.T + NT - 1) / NT);
-  const int steps = (p.K + C::BK - 1) / C::BK;
+  const int steps = (p.K + kBK - 1) / kBK;
   int split = 1;
   while (split < 8 && tiles * split * 2 <= sms && steps >= 4 * split) split *= 2;
   cudaLaunchConfig_t cfg{};
@@ -624,22 +656,28 @@ cudaError_t launch_tc_nt(const LinArgs& p, cudaStream_t s) {
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;
-  cudaLaunchAttribute a{};
-  a.id = cudaLaunchAttributeClusterDimension;
-  a.val.clusterDim = {static_cast<unsigned>(split), 1, 1};
-  cfg.attrs = &a;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_tc<O, NT>, p, mapw, mapx, split);
+  cudaLaunchAttribute a[2]{};
+  a[0].id = cudaLaunchAttributeClusterDimension;
+  a[0].val.clusterDim = {static_cast<unsigned>(split), 1, 1};
+  // it may start while k_widen runs: only its token loads wait for k_widen,
+  // which itself started after everything before it had ended
+  a[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = a;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k_tc<O, NT>, p, mapx, split);
 }
 
 template <typename O>
-cudaError_t launch_linear(const LinArgs& p, cudaStream_t s) {
-  if (p.T <= kGemvTokens) return launch_gemv<O>(p, s);
-  if (p.T <= 16) return launch_tc_nt<O, 16>(p, s);
-  if (p.T <= 32) return launch_tc_nt<O, 32>(p, s);
-  if (p.T <= 64) return launch_tc_nt<O, 64>(p, s);
-  if (p.T <= 128) return launch_tc_nt<O, 128>(p, s);
-  return launch_tc_nt<O, 256>(p, s);
+cudaError_t launch_linear(const LinArgs& p, void* ws, cudaStream_t s) {
+  if (p.T <= kFewTokens) return launch_few<O>(p, s);
+  if (p.T <= 64) return launch_tc_nt<O, 64>(p, ws, s);
+  if (p.T <= 128) return launch_tc_nt<O, 128>(p, ws, s);
+  return launch_tc_nt<O, 256>(p, ws, s);
+}
+
+size_t linear_ws_bytes(int T, int K) {
+  return T <= kFewTokens ? 0 : static_cast<size_t>(T) * padded_k(K) * 2;
 }
 
 }  // namespace
@@ -660,9 +698,13 @@ int sm_count() {
 
 extern "C" {
 
+size_t pw_linear_i8_workspace_bytes(int T, int K) {
+  return T < 0 || K < 1 || K > PW_MAX_K_I8 ? 0 : pw::linear_ws_bytes(T, K);
+}
+
 int pw_linear_i8(const int8_t* x, int64_t ldx, const float* x_scale, const int8_t* w, int64_t ldw,
                  const float* w_scale, const void* bias, int T, int N, int K, int out_dtype, void* out, int64_t ldo,
-                 pw_stream_t s) {
+                 void* workspace, size_t ws_bytes, pw_stream_t s) {
   pw::NvtxCall nvtx_range("pw_linear_i8");
   if (T < 0 || N < 1 || K < 1 || K > PW_MAX_K_I8)
     return pw::failf(PW_EINVAL, "pw_linear_i8: need T >= 0, N >= 1, 1 <= K <= %d (T %d, N %d, K %d)", PW_MAX_K_I8, T,
@@ -677,11 +719,16 @@ int pw_linear_i8(const int8_t* x, int64_t ldx, const float* x_scale, const int8_
   const size_t es = pw::dtype_bytes(out_dtype);
   if (!pw::aligned(out, es) || !pw::aligned(bias, es) || !pw::aligned(x_scale, 4) || !pw::aligned(w_scale, 4))
     return pw::failf(PW_EINVAL, "pw_linear_i8: misaligned pointer");
+  const size_t need = pw::linear_ws_bytes(T, K);
+  if (ws_bytes < need || (need && !workspace))
+    return pw::failf(PW_ENOMEM, "pw_linear_i8: workspace of %zu bytes, %zu are needed", workspace ? ws_bytes : 0, need);
+  if (need && !pw::aligned(workspace, 256))
+    return pw::failf(PW_EINVAL, "pw_linear_i8: the workspace must be 256-byte aligned");
   const pw::LinArgs a{x, w, x_scale, w_scale, bias, out, ldx, ldw, ldo, T, N, K};
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(s);
-  const cudaError_t e = out_dtype == PW_F16    ? pw::launch_linear<__half>(a, st)
-                        : out_dtype == PW_BF16 ? pw::launch_linear<__nv_bfloat16>(a, st)
-                                               : pw::launch_linear<float>(a, st);
+  const cudaError_t e = out_dtype == PW_F16    ? pw::launch_linear<__half>(a, workspace, st)
+                        : out_dtype == PW_BF16 ? pw::launch_linear<__nv_bfloat16>(a, workspace, st)
+                                               : pw::launch_linear<float>(a, workspace, st);
   return pw::launch_status(e, "pw_linear_i8");
 }
 

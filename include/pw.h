@@ -546,9 +546,8 @@ int pw_profile_attach(void* const* events, int n_events);
  * Conventions of the four calls: device pointers; element types are PW_F16,
  * PW_BF16 or PW_F32; a matrix is rows of consecutive elements whose starts are
  * `ld*` elements apart (ld >= the row's length, 64-bit), so padded and sliced
- * matrices need no copy.  Work is enqueued on `s` and nothing waits; no
- * workspace is needed and nothing is kept between calls, so calls on several
- * streams may overlap.  T = 0 is a no-op.  A call may be captured into a CUDA
+ * matrices need no copy.  Work is enqueued on `s` and nothing waits; nothing
+ * is kept between calls, so calls on several streams may overlap.  T = 0 is a no-op.  A call may be captured into a CUDA
  * graph.  Results do not depend on what else runs: a call repeated on the same
  * inputs gives the same bits.
  */
@@ -592,6 +591,10 @@ int pw_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, c
 int pw_quant_i8(const void* x, int64_t ldx, int T, int K, int dtype, int8_t* q, int64_t ldq, float* scale,
                 pw_stream_t s);
 
+/* Bytes of device workspace that pw_linear_i8 needs: 0 up to 32 tokens, then
+ * the tokens as fp16.  0 for a bad shape. */
+size_t pw_linear_i8_workspace_bytes(int T, int K);
+
 /*
  * pw_linear_i8 -- product of int8 rows with int8 weights:
  *   out[t][n] = (sum_k x[t][k] * w[n][k]) * x_scale[t] * w_scale[n] + bias[n]
@@ -602,11 +605,15 @@ int pw_quant_i8(const void* x, int64_t ldx, int T, int K, int dtype, int8_t* q, 
  * Rows of x and w start on 16-byte boundaries (pointers and ldx, ldw multiples
  * of 16); K itself is any number from 1 to PW_MAX_K_I8, and bytes past K are
  * never used.  out has any stride.
- * Errors: PW_EINVAL (shapes, strides, null or misaligned pointers, dtype), PW_ECUDA.
+ *   workspace  pw_linear_i8_workspace_bytes(T, K) bytes, 256-byte aligned, or
+ *      NULL where that is 0; it may hold anything, and must not be shared by two
+ *      calls in flight at once
+ * Errors: PW_EINVAL (shapes, strides, null or misaligned pointers, dtype),
+ * PW_ENOMEM (workspace too small), PW_ECUDA.
  */
 int pw_linear_i8(const int8_t* x, int64_t ldx, const float* x_scale, const int8_t* w, int64_t ldw,
                  const float* w_scale, const void* bias, int T, int N, int K, int out_dtype, void* out,
-                 int64_t ldo, pw_stream_t s);
+                 int64_t ldo, void* workspace, size_t ws_bytes, pw_stream_t s);
 
 /*
  * pw_linear_i8_status -- the PW_STATUS_* bits that pw_linear_i8 calls on the

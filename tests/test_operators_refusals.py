@@ -42,11 +42,26 @@ def test_quant_refuses(kw):
     dict(x=P + 8), dict(w=P + 8), dict(ldx=72), dict(ldw=72), dict(out=P + 1), dict(bias=P + 1), dict(xs=P + 2),
     dict(ws=P + 1)])
 def test_linear_refuses(kw):
-    a = dict(x=P, ldx=64, xs=P, w=P, ldw=64, ws=P, bias=None, T=2, N=8, K=64, dt=pw.PW_F16, out=P, ldo=8)
-    a.update(kw)
-    assert pw.lib().pw_linear_i8(*[a[k] for k in ("x", "ldx", "xs", "w", "ldw", "ws", "bias", "T", "N", "K", "dt",
-                                                   "out", "ldo")], None) == pw.PW_EINVAL
+    assert _linear(**kw) == pw.PW_EINVAL
     assert b"pw_linear_i8" in pw.lib().pw_last_error()
+
+
+def _linear(**kw):
+    a = dict(x=P, ldx=64, xs=P, w=P, ldw=64, ws=P, bias=None, T=2, N=8, K=64, dt=pw.PW_F16, out=P, ldo=8, sp=None,
+             sb=0)
+    a.update(kw)
+    return pw.lib().pw_linear_i8(*[a[k] for k in ("x", "ldx", "xs", "w", "ldw", "ws", "bias", "T", "N", "K", "dt",
+                                                   "out", "ldo", "sp", "sb")], None)
+
+
+def test_linear_workspace():
+    assert pw.pw_linear_i8_workspace_bytes(32, 4096) == 0
+    assert pw.pw_linear_i8_workspace_bytes(33, 100) == 33 * 128 * 2
+    assert pw.pw_linear_i8_workspace_bytes(-1, 100) == 0 and pw.pw_linear_i8_workspace_bytes(4, 0) == 0
+    assert _linear(T=33) == pw.PW_ENOMEM
+    assert _linear(T=33, sp=P, sb=33 * 128 - 1) == pw.PW_ENOMEM
+    assert _linear(T=33, sp=None, sb=1 << 20) == pw.PW_ENOMEM
+    assert _linear(T=33, sp=P + 16, sb=1 << 20) == pw.PW_EINVAL
 
 
 @pytest.mark.parametrize("kw", [
@@ -65,7 +80,7 @@ def test_no_rows_is_no_work():
     assert _norm(T=0, x=None, y=None, w=None) == pw.PW_OK
     L = pw.lib()
     assert L.pw_quant_i8(None, 32, 0, 32, pw.PW_F16, None, 32, None, None) == pw.PW_OK
-    assert L.pw_linear_i8(None, 64, None, None, 64, None, None, 0, 8, 64, pw.PW_F16, None, 8, None) == pw.PW_OK
+    assert _linear(T=0, x=None, w=None) == pw.PW_OK
     assert L.pw_logprobs(None, 100, pw.PW_F16, 0, 100, None, 0, 0, None, None, None, None, None, None) == pw.PW_OK
 
 
