@@ -175,13 +175,13 @@ cudaError_t launch_few(const LinArgs& p, cudaStream_t s) {
 // k_widen writes the tokens as fp16 into the workspace; then one CTA per SM
 // takes tiles of 128 channels (M, the weights) x NT tokens (N).
 // Warps by role:
-//  * the last 8 warps, in 4 groups that take a stage in turn, bring int8
-//    weights from memory through registers into the fp16 operand ring: a
-//    group's loads for its next stage are in flight while it waits for a free
-//    one.  A byte b becomes the fp16 number 1024 + (b + 128) by placing it in
-//    the low byte of 0x6400, and 1152 is subtracted: five operations for four
-//    values, stored in the K-major 128-byte-swizzled layout the MMA reads;
-//  * warp 2 fetches the fp16 tokens into the ring by TMA;
+//  * warp 0 fetches int8 weights by TMA into a ring of S8 stages, warp 2 the
+//    fp16 tokens into the operand ring of S stages;
+//  * the last 8 warps, in 4 groups that take a stage in turn, convert the
+//    weights to fp16 in the operand ring.  A byte b becomes the fp16 number
+//    1024 + (b + 128) by placing it in the low byte of 0x6400, and 1152 is
+//    subtracted: five operations for four values, stored in the K-major
+//    128-byte-swizzled layout the MMA reads;
 //  * warp 1 issues tcgen05.mma kind::f16 (fp32 in tensor memory, two
 //    accumulators of NT columns), 1024 columns of K into one accumulator,
 //    then the next 1024 into the other;
@@ -207,15 +207,18 @@ struct Tile {
   static constexpr int kConvWarp0 = kEpiWarp0 + EW;
   static constexpr int kThreads = 32 * (kConvWarp0 + kConvWarps);
   static constexpr int A = kM * kBK * 2, B = NT * kBK * 2;   // bytes of a stage's operands
-  static constexpr int S = NT <= 128 ? 6 : 4;             // stages
-  static constexpr int kOffBar = S * (A + B);
-  static constexpr int kSmem = kOffBar + 8 * (3 * S + 4) + 16 + 1024;
+  static constexpr int A8 = kM * kBK;                     // and of its int8 weights
+  static constexpr int S = NT <= 64 ? 5 : 4;              // operand stages
+  static constexpr int S8 = NT <= 64 ? 12 : NT <= 128 ? 11 : 4;   // int8 stages
+  static constexpr int kRing8 = S * (A + B);
+  static constexpr int kOffBar = kRing8 + S8 * A8;
+  static constexpr int kSmem = kOffBar + 8 * (3 * S + 2 * S8 + 4) + 16 + 1024;
   static constexpr uint32_t kCols = 2 * NT;
   // D f32, A and B f16, N / 8 and M / 16
   static constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(NT >> 3) << 17) |
                                      (static_cast<uint32_t>(kM >> 4) << 24);
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
-  static_assert(kM * NT * 4 <= kOffBar, "a tile's int32 sums fit the ring");
+  static_assert(kM * NT * 4 <= kRing8, "a tile's int32 sums fit the operand ring");
 };
 
 // Registers by role for NT = 256, whose accumulating threads hold 128 sums:
@@ -247,21 +250,25 @@ __device__ __forceinline__ void sts16(uint32_t a, uint32_t x, uint32_t y, uint32
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+
 // A converting thread's part of a stage: 16 columns at 16 (tid % 4) of the
-// channels tid / 4 + 16 i.  Four neighbouring threads read 64 bytes of one
-// channel, and eight write 16-byte pieces of two rows to different banks.
+// channels tid / 4 + 16 i.  Eight neighbouring threads read two rows of 64
+// bytes (with the TMA's 64-byte swizzle) and write 16-byte pieces of two fp16
+// rows, each time to different banks.
 struct Weights {
   static constexpr int kN = kM / (kGroupWarps * 8);
   uint4 v[kN];
 
-  __device__ __forceinline__ void load(const LinArgs& p, int n0, int step, int tid) {
-    const int k = step * kBK + (tid & 3) * 16, left = p.K - k;
+  __device__ __forceinline__ void load(uint32_t src, int tid) {
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      // channels past the end repeat the last one (their sums are not stored);
-      // columns past K meet tokens that are zero there
-      const int8_t* from = p.w + min(n0 + (tid >> 2) + i * (kGroupWarps * 8), p.N - 1) * p.ldw + k;
-      v[i] = left >= 16 ? load_once(from) : load_tail(from, left);
+      const int r = (tid >> 2) + i * (kGroupWarps * 8);
+      v[i] = lds16(src + r * 64 + (((tid & 3) ^ ((r >> 1) & 3)) << 4));
     }
   }
   __device__ __forceinline__ void store(uint32_t dst, int tid) const {
@@ -313,46 +320,68 @@ __device__ __forceinline__ int4 ld_cluster(uint32_t addr, uint32_t rank) {
   return v;
 }
 
-// Waits up to kWaitClocks for the phase of the given parity; false when the
-// time runs out or another thread has raised the abort flag.
-constexpr long long kWaitClocks = 1ll << 31;   // about a second
-__device__ __forceinline__ bool wait_clocks(uint32_t bar, uint32_t parity, const volatile int* abort) {
-  const long long t0 = clock64();
-  for (;;) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (done) return true;
-    if (*abort || clock64() - t0 > kWaitClocks) return false;
-  }
+// Whether the phase of the given parity has ended; never waits.
+__device__ __forceinline__ bool test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done;
 }
 
-// Ring position of the i-th use: stage, and the parity of that use.
-struct Use {
-  uint32_t stage, parity;
-};
-template <int S>
-__device__ __forceinline__ Use use(uint32_t i) {
-  return Use{i % S, (i / S) & 1};
+// Polls up to kPolls times (about a second; PAUSE ns between two) for the phase
+// of the given parity; false, and the abort flag, when they run out or another
+// thread has raised it.
+constexpr int kPolls = 1 << 23;
+template <int PAUSE = 0>
+__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, volatile int* abort) {
+  for (int n = 0; !test_wait(bar, parity); ++n) {
+    if (*abort) return false;
+    if (n == kPolls) {
+      atomicOr(&g_linear_status, PW_STATUS_TIMEOUT);
+      *abort = 1;
+      return false;
+    }
+    if (PAUSE) __nanosleep(PAUSE);
+  }
+  return true;
 }
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
+  return p;
+}
+
+// A position in a ring of S stages, and the parity of its current use.
+template <int S>
+struct Ring {
+  uint32_t stage = 0, parity = 0;
+  bool first = true;   // no stage has been used before
+  __device__ __forceinline__ void next(uint32_t n = 1) {
+    stage += n;
+    if (stage >= S) stage -= S, parity ^= 1, first = false;
+  }
+};
 
 template <typename O, int NT>
 __global__ void __launch_bounds__(Tile<NT>::kThreads, 1)
-k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapx, int split) {
+k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_constant__ CUtensorMap mapx, int split) {
   using C = Tile<NT>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);
   const uint32_t base = saddr(smem);
   const uint32_t fullw = base + C::kOffBar, fullx = fullw + 8 * C::S, empty = fullx + 8 * C::S;
-  const uint32_t dfull = empty + 8 * C::S, dempty = dfull + 16;
-  int* s_misc = reinterpret_cast<int*>(smem + C::kOffBar + 8 * (3 * C::S + 4));   // tmem, abort
+  const uint32_t full8 = empty + 8 * C::S, empty8 = full8 + 8 * C::S8;
+  const uint32_t dfull = empty8 + 8 * C::S8, dempty = dfull + 16;
+  int* s_misc = reinterpret_cast<int*>(smem + C::kOffBar + 8 * (3 * C::S + 2 * C::S8 + 4));   // tmem, abort
   volatile int* abort = s_misc + 1;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // the compiler then knows that it is uniform
   uint32_t rank = 0;
   if (split > 1) asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
 
@@ -367,6 +396,7 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapx, int split) {
       mbar_init(fullx + 8 * i, 1);             // the tokens
       mbar_init(empty + 8 * i, 1);
     }
+    for (int i = 0; i < C::S8; ++i) mbar_init(full8 + 8 * i, 1), mbar_init(empty8 + 8 * i, kGroupWarps);
     for (int i = 0; i < 2; ++i) mbar_init(dfull + 8 * i, 1), mbar_init(dempty + 8 * i, C::EW);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     s_misc[1] = 0;
@@ -374,14 +404,26 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapx, int split) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = static_cast<uint32_t>(s_misc[0]);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, static_cast<uint32_t>(s_misc[0]), 0);
 
-  // a bounded wait; false (and the abort flag) when it runs out
-  auto wait = [&](uint32_t bar, uint32_t parity) {
-    if (wait_clocks(bar, parity, abort)) return true;
-    atomicOr(&g_linear_status, PW_STATUS_TIMEOUT);
-    *abort = 1;
-    return false;
+  // a warp waits through one thread: polls of all its lanes would keep the
+  // other warps' barrier operations waiting
+  auto warp_ok = [&](bool ok) {
+    ok = __all_sync(0xffffffffu, ok);
+    __syncwarp();
+    return ok;
+  };
+  auto wait = [&](uint32_t bar, uint32_t parity) { return warp_ok(lane != 0 || poll(bar, parity, abort)); };
+  // after an abort, what this thread has in flight still ends before the CTA
+  // does: the last use of every stage of a ring, the current lap's below r.stage
+  auto drain = [&](uint32_t bars, uint32_t stages, const auto& r) {
+    volatile int none = 0;
+    for (uint32_t i = 0; i < stages; ++i) {
+      if (i < r.stage)
+        poll(bars + 8 * i, r.parity, &none);
+      else if (!r.first)
+        poll(bars + 8 * i, r.parity ^ 1, &none);
+    }
   };
 
   const int ntn = (p.N + kM - 1) / kM, ntt = (p.T + NT - 1) / NT;
@@ -395,60 +437,69 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapx, int split) {
   constexpr bool kSplitRegs = NT == 256;
   if (warp < kEpiWarp0) {
     if constexpr (kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    if (warp == 0 && lane == 0) {
+      // ---- int8 weights by TMA
+      Ring<C::S8> r;
+      bool ok = true;
+      for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
+        const int n0 = (tile % ntn) * kM;
+        for (int k = s0; k < s1; ++k, r.next()) {
+          if (!r.first && !(ok = poll(empty8 + 8 * r.stage, r.parity ^ 1, abort))) break;
+          mbar_expect_tx(full8 + 8 * r.stage, C::A8);
+          tma_load_2d(base + C::kRing8 + r.stage * C::A8, &mapw, k * kBK, n0, full8 + 8 * r.stage);
+        }
+      }
+      if (*abort) drain(full8, C::S8, r);
+    }
     if (warp == 2 && lane == 0) {
       // ---- fp16 tokens by TMA, once k_widen has written them
       asm volatile("griddepcontrol.wait;" ::: "memory");
-      uint32_t g = 0;
+      Ring<C::S> r;
       bool ok = true;
       for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
         const int t0 = (tile / ntn) * NT;
-        for (int k = s0; k < s1; ++k, ++g) {
-          const Use u = use<C::S>(g);
-          if (g >= C::S && !wait(empty + 8 * u.stage, u.parity ^ 1)) {
-            ok = false;
-            break;
-          }
-          mbar_expect_tx(fullx + 8 * u.stage, C::B);
-          tma_load_2d(base + u.stage * (C::A + C::B) + C::A, &mapx, k * kBK, t0, fullx + 8 * u.stage);
+        for (int k = s0; k < s1; ++k, r.next()) {
+          if (!r.first && !(ok = poll(empty + 8 * r.stage, r.parity ^ 1, abort))) break;
+          mbar_expect_tx(fullx + 8 * r.stage, C::B);
+          tma_load_2d(base + r.stage * (C::A + C::B) + C::A, &mapx, k * kBK, t0, fullx + 8 * r.stage);
         }
       }
-      // after an abort the copies in flight still land before the CTA ends
-      if (*abort) {
-        const int none = 0;
-        for (uint32_t i = g > C::S ? g - C::S : 0; i < g; ++i)
-          wait_clocks(fullx + 8 * use<C::S>(i).stage, use<C::S>(i).parity, &none);
-      }
+      if (*abort) drain(fullx, C::S, r);
     }
-    if (warp == 1 && lane == 0) {
-      // ---- MMA issue
-      uint32_t g = 0, d = 0;
-      bool ok = true;
+    if (warp == 1) {
+      // ---- MMA issue: the whole warp in step, so that the operands stay in
+      // uniform registers, and an elected thread for the instructions.  A
+      // barrier takes over 100 clocks to read, so the next stage's are read
+      // before this stage's MMAs are issued and looked at after
+      Ring<C::S> r;
+      Ring<2> d;
+      bool ok = true, ready = false;
       for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
-        for (int k = 0; k < steps && ok; ++d) {
-          const Use ud = use<2>(d);
-          if (d >= 2 && !(ok = wait(dempty + 8 * ud.stage, ud.parity ^ 1))) break;
+        for (int k = 0; k < steps && ok; d.next()) {
+          if (!d.first && !(ok = wait(dempty + 8 * d.stage, d.parity ^ 1))) break;
           tc_fence_after();
-          const uint32_t acc = tmem + ud.stage * NT;
+          const uint32_t acc = tmem + d.stage * NT;
           const int end = min(steps, k + kChunk);
-          for (bool first = true; k < end; ++k, ++g) {
-            const Use u = use<C::S>(g);
-            if (!(ok = wait(fullx + 8 * u.stage, u.parity) && wait(fullw + 8 * u.stage, u.parity))) break;
+          for (uint32_t more = 0; k < end; ++k) {
+            if (!ready && !(ok = wait(fullx + 8 * r.stage, r.parity) && wait(fullw + 8 * r.stage, r.parity))) break;
             tc_fence_after();
-            const uint32_t a = base + u.stage * (C::A + C::B), b = a + C::A;
+            const uint32_t stage = r.stage;
+            r.next();
+            ready = test_wait(fullx + 8 * r.stage, r.parity) & test_wait(fullw + 8 * r.stage, r.parity);
+            if (elect_one()) {
+              const uint64_t da = smem_desc(base + stage * (C::A + C::B)), db = da + (C::A >> 4);
 #pragma unroll
-            for (int kk = 0; kk < kBK / 16; ++kk)
-              mma_f16(acc, smem_desc(a + kk * 32), smem_desc(b + kk * 32), C::kIdesc, !first || kk);
-            first = false;
-            mma_commit(empty + 8 * u.stage);
+              for (int kk = 0; kk < kBK / 16; ++kk) mma_f16(acc, da + kk * 2, db + kk * 2, C::kIdesc, more | kk);
+              mma_commit(empty + 8 * stage);
+            }
+            ready = __all_sync(0xffffffffu, ready);
+            more = 1;
           }
-          if (ok) mma_commit(dfull + 8 * ud.stage);
+          if (ok && elect_one()) mma_commit(dfull + 8 * d.stage);
+          __syncwarp();
         }
       }
-      if (*abort && g) {   // the MMAs in flight end before the CTA does
-        const int none = 0;
-        const Use u = use<C::S>(g - 1);
-        wait_clocks(empty + 8 * u.stage, u.parity, &none);
-      }
+      if (*abort && lane == 0) drain(empty, C::S, r);
     }
     __syncwarp();
     if constexpr (kSplitRegs) {
@@ -460,27 +511,26 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapx, int split) {
     if constexpr (kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsAcc));
     const int q = warp & 3, half = (warp - kEpiWarp0) >> 2;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * C::ACC;
-    uint32_t d = 0;
+    Ring<2> d;
     bool ok = true;
     for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
       int acc[C::ACC];
 #pragma unroll
       for (int i = 0; i < C::ACC; ++i) acc[i] = 0;
-      for (int k = 0; k < steps; k += kChunk, ++d) {
-        const Use ud = use<2>(d);
-        ok = __all_sync(0xffffffffu, wait(dfull + 8 * ud.stage, ud.parity));
-        if (!ok) break;
+      for (int k = 0; k < steps; k += kChunk, d.next()) {
+        if (!(ok = warp_ok(lane != 0 || poll<100>(dfull + 8 * d.stage, d.parity, abort)))) break;
         tc_fence_after();
 #pragma unroll
         for (int c = 0; c < C::ACC; c += 16) {
           uint32_t r[16];
-          tmem_ld16(lanes + ud.stage * NT + c, r);
+          tmem_ld16(lanes + d.stage * NT + c, r);
           tmem_wait(r);
 #pragma unroll
           for (int i = 0; i < 16; ++i) acc[c + i] += __float2int_rn(__uint_as_float(r[i]));
         }
         tc_fence_before();
-        if (lane == 0) mbar_arrive(dempty + 8 * ud.stage);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(dempty + 8 * d.stage);
       }
       if (!ok) break;
       const int n0 = (tile % ntn) * kM, t0 = (tile / ntn) * NT;
@@ -510,24 +560,24 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapx, int split) {
     // ---- int8 to fp16
     if constexpr (kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
     const int ctid = (tid - C::kConvWarp0 * 32) % (kGroupWarps * 32);
-    int tile = tile0, k = (warp - C::kConvWarp0) / kGroupWarps;
-    uint32_t g = k;   // this group's stage among all of the CTA's
-    auto settle = [&] {
-      for (; k >= steps && tile < tiles; tile += tile_step) k -= steps;
-    };
-    Weights w;
-    settle();
-    if (tile < tiles) w.load(p, (tile % ntn) * kM, s0 + k, ctid);
-    for (; tile < tiles; g += kGroups) {
-      const Use u = use<C::S>(g);
-      if (g >= C::S && !__all_sync(0xffffffffu, wait(empty + 8 * u.stage, u.parity ^ 1))) break;
-      w.store(base + u.stage * (C::A + C::B), ctid);
+    const int group = (warp - C::kConvWarp0) / kGroupWarps;
+    Ring<C::S> r;
+    Ring<C::S8> r8;
+    r.next(group);
+    r8.next(group);
+    const int64_t mine = static_cast<int64_t>(steps) * ((tiles - tile0 + tile_step - 1) / tile_step);
+    for (int64_t g = group; g < mine; g += kGroups, r.next(kGroups), r8.next(kGroups)) {
+      if (!wait(full8 + 8 * r8.stage, r8.parity)) break;
+      Weights w;
+      w.load(base + C::kRing8 + r8.stage * C::A8, ctid);
+      if (!r.first && !wait(empty + 8 * r.stage, r.parity ^ 1)) break;
+      w.store(base + r.stage * (C::A + C::B), ctid);
       proxy_fence_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(fullw + 8 * u.stage);
-      k += kGroups;
-      settle();
-      if (tile < tiles) w.load(p, (tile % ntn) * kM, s0 + k, ctid);
+      if (lane == 0) {
+        mbar_arrive(fullw + 8 * r.stage);
+        mbar_arrive(empty8 + 8 * r8.stage);   // not before the stores: the loads have then arrived for sure
+      }
     }
     __syncwarp();
     if constexpr (kSplitRegs) {
@@ -602,16 +652,18 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
 }
 
-// Boxes of kBK columns x box rows of an fp16 matrix; rows past its end read as zero.
-cudaError_t map_f16(CUtensorMap* m, const void* base, int rows, int cols, int box) {
+// Boxes of kBK columns x box rows of an int8 (size 1) or fp16 (2) matrix of
+// stride ld bytes; columns and rows past its ends read as zero.
+cudaError_t map_tile(CUtensorMap* m, int size, const void* base, int64_t ld, int rows, int cols, int box) {
   const auto encode = encoder();
   if (!encode) return cudaErrorNotSupported;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld)};
   const cuuint32_t boxes[2] = {kBK, static_cast<cuuint32_t>(box)};
   const cuuint32_t es[2] = {1, 1};
-  const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(base), dims, strides, boxes, es,
-                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  const CUresult r = encode(m, size == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                            const_cast<void*>(base), dims, strides, boxes, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            size == 1 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
@@ -637,9 +689,10 @@ cudaError_t launch_tc_nt(const LinArgs& p, void* ws, cudaStream_t s) {
     if (NT == 256 && at.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
     ready[dev].store(true, std::memory_order_release);
   }
-  CUtensorMap mapx;
+  CUtensorMap mapw, mapx;
   const int kp = padded_k(p.K);
-  e = map_f16(&mapx, ws, p.T, kp, NT);
+  e = map_tile(&mapw, 1, p.w, p.ldw, p.N, p.K, kM);
+  if (e == cudaSuccess) e = map_tile(&mapx, 2, ws, kp * int64_t{2}, p.T, kp, NT);
   if (e != cudaSuccess) return e;
   const int sms = sm_count();
   const int64_t chunks = static_cast<int64_t>(p.T) * (kp / 16);
@@ -665,7 +718,7 @@ cudaError_t launch_tc_nt(const LinArgs& p, void* ws, cudaStream_t s) {
   a[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = a;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, k_tc<O, NT>, p, mapx, split);
+  return cudaLaunchKernelEx(&cfg, k_tc<O, NT>, p, mapw, mapx, split);
 }
 
 template <typename O>
