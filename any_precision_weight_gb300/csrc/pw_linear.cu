@@ -187,7 +187,11 @@ cudaError_t launch_few(const LinArgs& p, cudaStream_t s) {
 //    then the next 1024 into the other;
 //  * warps 4.. add each finished accumulator to their int32 registers while
 //    the next one fills, and at the tile's end scale and store.
-// What bounds it is the shared-memory data pipe (128 bytes a clock), which the
+// Above 128 tokens two CTAs of a cluster make a pair (cta_group::2): 256
+// channels x 256 tokens, each CTA with its own 128 channels and half of the
+// tokens, so a stage brings 24 KB to an SM instead of 40 (at 40 the L2 was the
+// bound, about 9.6 TB/s).  The even CTA issues the MMAs for both.
+// What else bounds it is the shared-memory data pipe (128 bytes a clock), which the
 // tensor cores' operand reads share with the conversion: converting the tokens
 // here too made 1025 of its clocks for the 512 of a 128 x 256 x 64 step.
 // Where there are few tiles a cluster of CTAs splits K and adds the parts
@@ -202,23 +206,25 @@ constexpr int kEpiWarp0 = 4;
 
 template <int NT>
 struct Tile {
+  static constexpr bool kPair = NT == 256;                // two CTAs to a tile
   static constexpr int EW = NT <= 64 ? 4 : 8;             // accumulating warps
   static constexpr int ACC = NT / (EW / 4);               // int32 sums of one of their threads
   static constexpr int kConvWarp0 = kEpiWarp0 + EW;
   static constexpr int kThreads = 32 * (kConvWarp0 + kConvWarps);
-  static constexpr int A = kM * kBK * 2, B = NT * kBK * 2;   // bytes of a stage's operands
+  static constexpr int kRowsB = kPair ? NT / 2 : NT;      // tokens that a CTA holds
+  static constexpr int A = kM * kBK * 2, B = kRowsB * kBK * 2;   // bytes of a stage's operands
   static constexpr int A8 = kM * kBK;                     // and of its int8 weights
-  static constexpr int S = NT <= 64 ? 5 : 4;              // operand stages
-  static constexpr int S8 = NT <= 64 ? 12 : NT <= 128 ? 11 : 4;   // int8 stages
+  static constexpr int S = NT == 128 ? 4 : 5;             // operand stages
+  static constexpr int S8 = NT <= 64 ? 12 : NT == 128 ? 11 : 7;   // int8 stages
   static constexpr int kRing8 = S * (A + B);
   static constexpr int kOffBar = kRing8 + S8 * A8;
   static constexpr int kSmem = kOffBar + 8 * (3 * S + 2 * S8 + 4) + 16 + 1024;
   static constexpr uint32_t kCols = 2 * NT;
   // D f32, A and B f16, N / 8 and M / 16
   static constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(NT >> 3) << 17) |
-                                     (static_cast<uint32_t>(kM >> 4) << 24);
+                                     (static_cast<uint32_t>((kPair ? 2 : 1) * kM >> 4) << 24);
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
-  static_assert(kM * NT * 4 <= kRing8, "a tile's int32 sums fit the operand ring");
+  static_assert(kM * NT * 4 <= kRing8, "a CTA's int32 sums fit the operand ring");
 };
 
 // Registers by role for NT = 256, whose accumulating threads hold 128 sums:
@@ -351,6 +357,43 @@ __device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, volatile int
   return true;
 }
 
+// Arrives at the barrier that has this address in CTA `rank` of the cluster.
+// What it reports is shared memory of the arriving CTA, which only the tensor
+// cores read, behind the proxy fence; a release at cluster scope would also wait
+// for everything else in flight (it cost 1000 to 2600 clocks here).
+__device__ __forceinline__ void arrive_at(uint32_t bar, uint32_t rank) {
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\t"
+      "mapa.shared::cluster.u32 a, %0, %1;\n\t"
+      "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar), "r"(rank)
+      : "memory");
+}
+
+// MMA and commit of one CTA or of a pair; a pair's commit arrives in both.
+template <bool PAIR>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  if constexpr (PAIR) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+  } else {
+    mma_f16(d, a, b, idesc, acc);
+  }
+}
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint32_t bar, uint16_t mask) {
+  if constexpr (PAIR) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(mask)
+        : "memory");
+  } else {
+    mma_commit(bar);
+  }
+}
+
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
@@ -382,27 +425,39 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
   volatile int* abort = s_misc + 1;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // the compiler then knows that it is uniform
-  uint32_t rank = 0;
-  if (split > 1) asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  // the CTA's place: in its pair, and among the parts of K
+  constexpr bool kPair = C::kPair;
+  constexpr int kCtas = kPair ? 2 : 1;
+  uint32_t rank;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  const uint32_t side = kPair ? rank & 1 : 0, part = kPair ? rank >> 1 : rank, leader = rank - side;
 
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(s_misc)),
-                 "r"(C::kCols));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    if constexpr (kPair) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(s_misc)),
+                   "r"(C::kCols));
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(s_misc)),
+                   "r"(C::kCols));
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
   }
   if (tid == 0) {
     for (int i = 0; i < C::S; ++i) {
-      mbar_init(fullw + 8 * i, kGroupWarps);   // the weights of a stage
-      mbar_init(fullx + 8 * i, 1);             // the tokens
+      // the weights of a stage, in a pair those of both CTAs and the other's tokens
+      mbar_init(fullw + 8 * i, kPair ? 2 * kGroupWarps + 1 : kGroupWarps);
+      mbar_init(fullx + 8 * i, 1);   // the tokens
       mbar_init(empty + 8 * i, 1);
     }
     for (int i = 0; i < C::S8; ++i) mbar_init(full8 + 8 * i, 1), mbar_init(empty8 + 8 * i, kGroupWarps);
-    for (int i = 0; i < 2; ++i) mbar_init(dfull + 8 * i, 1), mbar_init(dempty + 8 * i, C::EW);
+    for (int i = 0; i < 2; ++i) mbar_init(dfull + 8 * i, 1), mbar_init(dempty + 8 * i, kCtas * C::EW);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     s_misc[1] = 0;
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (kPair) cluster_sync();   // the other CTA's barriers and tensor memory
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, static_cast<uint32_t>(s_misc[0]), 0);
 
@@ -426,13 +481,14 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
     }
   };
 
-  const int ntn = (p.N + kM - 1) / kM, ntt = (p.T + NT - 1) / NT;
+  const int ntn = (p.N + kCtas * kM - 1) / (kCtas * kM), ntt = (p.T + NT - 1) / NT;
   const int tiles = ntn * ntt;
   const int steps_all = (p.K + kBK - 1) / kBK;
-  const int s0 = static_cast<int>(static_cast<int64_t>(steps_all) * rank / split);
-  const int s1 = static_cast<int>(static_cast<int64_t>(steps_all) * (rank + 1) / split);
+  const int s0 = static_cast<int>(static_cast<int64_t>(steps_all) * part / split);
+  const int s1 = static_cast<int>(static_cast<int64_t>(steps_all) * (part + 1) / split);
   const int steps = s1 - s0;
-  const int tile0 = blockIdx.x / split, tile_step = gridDim.x / split;
+  const int tile0 = blockIdx.x / (kCtas * split), tile_step = gridDim.x / (kCtas * split);
+  auto channel0 = [&](int tile) { return ((tile % ntn) * kCtas + static_cast<int>(side)) * kM; };
 
   constexpr bool kSplitRegs = NT == 256;
   if (warp < kEpiWarp0) {
@@ -442,7 +498,7 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
       Ring<C::S8> r;
       bool ok = true;
       for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
-        const int n0 = (tile % ntn) * kM;
+        const int n0 = channel0(tile);
         for (int k = s0; k < s1; ++k, r.next()) {
           if (!r.first && !(ok = poll(empty8 + 8 * r.stage, r.parity ^ 1, abort))) break;
           mbar_expect_tx(full8 + 8 * r.stage, C::A8);
@@ -457,7 +513,7 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
       Ring<C::S> r;
       bool ok = true;
       for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
-        const int t0 = (tile / ntn) * NT;
+        const int t0 = (tile / ntn) * NT + static_cast<int>(side) * C::kRowsB;
         for (int k = s0; k < s1; ++k, r.next()) {
           if (!r.first && !(ok = poll(empty + 8 * r.stage, r.parity ^ 1, abort))) break;
           mbar_expect_tx(fullx + 8 * r.stage, C::B);
@@ -466,13 +522,22 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
       }
       if (*abort) drain(fullx, C::S, r);
     }
-    if (warp == 1) {
+    if (kPair && warp == 1 && side) {
+      // ---- the odd CTA's tokens are reported to the even one
+      if (lane == 0) {
+        Ring<C::S> r;
+        const int64_t all = static_cast<int64_t>(steps) * ((tiles - tile0 + tile_step - 1) / tile_step);
+        for (int64_t g = 0; g < all && poll(fullx + 8 * r.stage, r.parity, abort); ++g, r.next())
+          arrive_at(fullw + 8 * r.stage, leader);
+      }
+    } else if (warp == 1) {
       // ---- MMA issue: the whole warp in step, so that the operands stay in
       // uniform registers, and an elected thread for the instructions.  A
       // barrier takes over 100 clocks to read, so the next stage's are read
       // before this stage's MMAs are issued and looked at after
       Ring<C::S> r;
       Ring<2> d;
+      const uint16_t both = static_cast<uint16_t>(3u << leader);
       bool ok = true, ready = false;
       for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
         for (int k = 0; k < steps && ok; d.next()) {
@@ -489,13 +554,13 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
             if (elect_one()) {
               const uint64_t da = smem_desc(base + stage * (C::A + C::B)), db = da + (C::A >> 4);
 #pragma unroll
-              for (int kk = 0; kk < kBK / 16; ++kk) mma_f16(acc, da + kk * 2, db + kk * 2, C::kIdesc, more | kk);
-              mma_commit(empty + 8 * stage);
+              for (int kk = 0; kk < kBK / 16; ++kk) mma<kPair>(acc, da + kk * 2, db + kk * 2, C::kIdesc, more | kk);
+              commit<kPair>(empty + 8 * stage, both);
             }
             ready = __all_sync(0xffffffffu, ready);
             more = 1;
           }
-          if (ok && elect_one()) mma_commit(dfull + 8 * d.stage);
+          if (ok && elect_one()) commit<kPair>(dfull + 8 * d.stage, both);
           __syncwarp();
         }
       }
@@ -530,10 +595,15 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(dempty + 8 * d.stage);
+        if (lane == 0) {
+          if (kPair)
+            arrive_at(dempty + 8 * d.stage, leader);
+          else
+            mbar_arrive(dempty + 8 * d.stage);
+        }
       }
       if (!ok) break;
-      const int n0 = (tile % ntn) * kM, t0 = (tile / ntn) * NT;
+      const int n0 = channel0(tile), t0 = (tile / ntn) * NT;
       if (split == 1) {
         const int n = n0 + q * 32 + lane;
         if (n < p.N) {
@@ -546,9 +616,9 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
         }
       } else {
         // every stage of the ring has been read: its space takes the sums
-        int* part = reinterpret_cast<int*>(smem);
+        int* sums = reinterpret_cast<int*>(smem);
 #pragma unroll
-        for (int i = 0; i < C::ACC; ++i) part[(half * C::ACC + i) * kM + q * 32 + lane] = acc[i];
+        for (int i = 0; i < C::ACC; ++i) sums[(half * C::ACC + i) * kM + q * 32 + lane] = acc[i];
       }
     }
     __syncwarp();
@@ -575,7 +645,10 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
       proxy_fence_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(fullw + 8 * r.stage);
+        if (kPair)
+          arrive_at(fullw + 8 * r.stage, leader);
+        else
+          mbar_arrive(fullw + 8 * r.stage);
         mbar_arrive(empty8 + 8 * r8.stage);   // not before the stores: the loads have then arrived for sure
       }
     }
@@ -588,11 +661,11 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
 
   __syncwarp();
   if (split > 1) {
-    // the cluster's parts of one tile: CTA r adds and stores its share of the tokens
+    // the parts of one tile: each CTA adds and stores its share of the tokens
     cluster_sync();
     if (!*abort) {
-      const int n0 = (tile0 % ntn) * kM, t0 = (tile0 / ntn) * NT;
-      const int j0 = NT * rank / split, j1 = NT * (rank + 1) / split;
+      const int n0 = channel0(tile0), t0 = (tile0 / ntn) * NT;
+      const int j0 = NT * part / split, j1 = NT * (part + 1) / split;
 #pragma unroll 2
       for (int i = j0 * (kM / 4) + tid; i < j1 * (kM / 4); i += C::kThreads) {
         const int t = t0 + i / (kM / 4), n = n0 + i % (kM / 4) * 4;
@@ -600,7 +673,7 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
         int4 sum = make_int4(0, 0, 0, 0);
 #pragma unroll 4
         for (int r = 0; r < split; ++r) {
-          const int4 v = ld_cluster(base + i * 16, r);
+          const int4 v = ld_cluster(base + i * 16, r * kCtas + side);
           sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
         }
         const int v[4] = {sum.x, sum.y, sum.z, sum.w};
@@ -611,12 +684,17 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
             store_out<O>(p, t, n + c, v[c], xs, p.ws[n + c], p.bias ? to_f32<O>(static_cast<const O*>(p.bias)[n + c]) : 0.f);
       }
     }
-    cluster_sync();
   }
   tc_fence_before();
   __syncthreads();
+  if (kPair || split > 1) cluster_sync();   // nothing of this CTA is read or signalled any more
   tc_fence_after();
-  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols));
+  if (warp == 1) {
+    if constexpr (kPair)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols));
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols));
+  }
 }
 
 // Tokens as fp16, [T][kp] with kp a multiple of 64, zero past K.
@@ -692,7 +770,7 @@ cudaError_t launch_tc_nt(const LinArgs& p, void* ws, cudaStream_t s) {
   CUtensorMap mapw, mapx;
   const int kp = padded_k(p.K);
   e = map_tile(&mapw, 1, p.w, p.ldw, p.N, p.K, kM);
-  if (e == cudaSuccess) e = map_tile(&mapx, 2, ws, kp * int64_t{2}, p.T, kp, NT);
+  if (e == cudaSuccess) e = map_tile(&mapx, 2, ws, kp * int64_t{2}, p.T, kp, C::kRowsB);
   if (e != cudaSuccess) return e;
   const int sms = sm_count();
   const int64_t chunks = static_cast<int64_t>(p.T) * (kp / 16);
@@ -700,18 +778,19 @@ cudaError_t launch_tc_nt(const LinArgs& p, void* ws, cudaStream_t s) {
       p.x, p.ldx, p.T, p.K, kp, static_cast<__half*>(ws));
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int64_t tiles = static_cast<int64_t>((p.N + kM - 1) / kM) * ((p.T + NT - 1) / NT);
+  constexpr int kCtas = C::kPair ? 2 : 1, kN = kCtas * kM;
+  const int64_t tiles = static_cast<int64_t>((p.N + kN - 1) / kN) * ((p.T + NT - 1) / NT);
   const int steps = (p.K + kBK - 1) / kBK;
   int split = 1;
-  while (split < 8 && tiles * split * 2 <= sms && steps >= 4 * split) split *= 2;
+  while (split * kCtas < 8 && tiles * kCtas * split * 2 <= sms && steps >= 4 * split) split *= 2;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(split > 1 ? tiles * split : std::min<int64_t>(tiles, sms)));
+  cfg.gridDim = dim3(static_cast<unsigned>(kCtas * (split > 1 ? tiles * split : std::min<int64_t>(tiles, sms / kCtas))));
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute a[2]{};
   a[0].id = cudaLaunchAttributeClusterDimension;
-  a[0].val.clusterDim = {static_cast<unsigned>(split), 1, 1};
+  a[0].val.clusterDim = {static_cast<unsigned>(kCtas * split), 1, 1};
   // it may start while k_widen runs: only its token loads wait for k_widen,
   // which itself started after everything before it had ended
   a[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
