@@ -173,7 +173,7 @@ cudaError_t launch_few(const LinArgs& p, cudaStream_t s) {
 // ---------------------------------------------------------------- tensor cores
 
 // k_widen writes the tokens as fp16 into the workspace; then one CTA per SM
-// takes tiles of 128 channels (M, the weights) x NT tokens (N).
+// takes tiles of 256 channels (M, the weights) x NT tokens (N) with another.
 // Warps by role:
 //  * warp 0 fetches int8 weights by TMA into a ring of S8 stages, warp 2 the
 //    fp16 tokens into the operand ring of S stages;
@@ -187,10 +187,10 @@ cudaError_t launch_few(const LinArgs& p, cudaStream_t s) {
 //    then the next 1024 into the other;
 //  * warps 4.. add each finished accumulator to their int32 registers while
 //    the next one fills, and at the tile's end scale and store.
-// Above 128 tokens two CTAs of a cluster make a pair (cta_group::2): 256
-// channels x 256 tokens, each CTA with its own 128 channels and half of the
-// tokens, so a stage brings 24 KB to an SM instead of 40 (at 40 the L2 was the
-// bound, about 9.6 TB/s).  The even CTA issues the MMAs for both.
+// Two CTAs of a cluster make a pair (cta_group::2), each with its own 128
+// channels and half of the tokens, so a stage of 256 tokens brings 24 KB to an
+// SM instead of 40 (at 40 the L2 was the bound, about 9.6 TB/s), and one issue
+// serves two SMs.  The even CTA issues the MMAs for both.
 // What else bounds it is the shared-memory data pipe (128 bytes a clock), which the
 // tensor cores' operand reads share with the conversion: converting the tokens
 // here too made 1025 of its clocks for the 512 of a 128 x 256 x 64 step.
@@ -206,23 +206,22 @@ constexpr int kEpiWarp0 = 4;
 
 template <int NT>
 struct Tile {
-  static constexpr bool kPair = NT == 256;                // two CTAs to a tile
   static constexpr int EW = NT <= 64 ? 4 : 8;             // accumulating warps
   static constexpr int ACC = NT / (EW / 4);               // int32 sums of one of their threads
   static constexpr int kConvWarp0 = kEpiWarp0 + EW;
   static constexpr int kThreads = 32 * (kConvWarp0 + kConvWarps);
-  static constexpr int kRowsB = kPair ? NT / 2 : NT;      // tokens that a CTA holds
+  static constexpr int kRowsB = NT / 2;                   // tokens that a CTA holds
   static constexpr int A = kM * kBK * 2, B = kRowsB * kBK * 2;   // bytes of a stage's operands
   static constexpr int A8 = kM * kBK;                     // and of its int8 weights
-  static constexpr int S = NT == 128 ? 4 : 5;             // operand stages
-  static constexpr int S8 = NT <= 64 ? 12 : NT == 128 ? 11 : 7;   // int8 stages
+  static constexpr int S = 5;                             // operand stages
+  static constexpr int S8 = NT <= 64 ? 14 : NT == 128 ? 12 : 7;   // int8 stages
   static constexpr int kRing8 = S * (A + B);
   static constexpr int kOffBar = kRing8 + S8 * A8;
   static constexpr int kSmem = kOffBar + 8 * (3 * S + 2 * S8 + 4) + 16 + 1024;
   static constexpr uint32_t kCols = 2 * NT;
   // D f32, A and B f16, N / 8 and M / 16
   static constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(NT >> 3) << 17) |
-                                     (static_cast<uint32_t>((kPair ? 2 : 1) * kM >> 4) << 24);
+                                     (static_cast<uint32_t>(2 * kM >> 4) << 24);
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
   static_assert(kM * NT * 4 <= kRing8, "a CTA's int32 sums fit the operand ring");
 };
@@ -369,29 +368,19 @@ __device__ __forceinline__ void arrive_at(uint32_t bar, uint32_t rank) {
       : "memory");
 }
 
-// MMA and commit of one CTA or of a pair; a pair's commit arrives in both.
-template <bool PAIR>
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  if constexpr (PAIR) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
-  } else {
-    mma_f16(d, a, b, idesc, acc);
-  }
+// MMA of a pair of CTAs, and a commit that arrives in both (mask: their ranks).
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
 }
-template <bool PAIR>
-__device__ __forceinline__ void commit(uint32_t bar, uint16_t mask) {
-  if constexpr (PAIR) {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"(mask)
-        : "memory");
-  } else {
-    mma_commit(bar);
-  }
+__device__ __forceinline__ void commit_pair(uint32_t bar, uint16_t mask) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(mask)
+      : "memory");
 }
 
 __device__ __forceinline__ bool elect_one() {
@@ -426,38 +415,30 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // the compiler then knows that it is uniform
   // the CTA's place: in its pair, and among the parts of K
-  constexpr bool kPair = C::kPair;
-  constexpr int kCtas = kPair ? 2 : 1;
   uint32_t rank;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-  const uint32_t side = kPair ? rank & 1 : 0, part = kPair ? rank >> 1 : rank, leader = rank - side;
+  const uint32_t side = rank & 1, part = rank >> 1, leader = rank - side;
 
   if (warp == 1) {
-    if constexpr (kPair) {
-      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(s_misc)),
-                   "r"(C::kCols));
-      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
-    } else {
-      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(s_misc)),
-                   "r"(C::kCols));
-      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-    }
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(s_misc)),
+                 "r"(C::kCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
   }
   if (tid == 0) {
     for (int i = 0; i < C::S; ++i) {
-      // the weights of a stage, in a pair those of both CTAs and the other's tokens
-      mbar_init(fullw + 8 * i, kPair ? 2 * kGroupWarps + 1 : kGroupWarps);
-      mbar_init(fullx + 8 * i, 1);   // the tokens
+      // the weights of a stage in both CTAs, and the odd CTA's tokens
+      mbar_init(fullw + 8 * i, 2 * kGroupWarps + 1);
+      mbar_init(fullx + 8 * i, 1);   // the CTA's own tokens
       mbar_init(empty + 8 * i, 1);
     }
     for (int i = 0; i < C::S8; ++i) mbar_init(full8 + 8 * i, 1), mbar_init(empty8 + 8 * i, kGroupWarps);
-    for (int i = 0; i < 2; ++i) mbar_init(dfull + 8 * i, 1), mbar_init(dempty + 8 * i, kCtas * C::EW);
+    for (int i = 0; i < 2; ++i) mbar_init(dfull + 8 * i, 1), mbar_init(dempty + 8 * i, 2 * C::EW);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     s_misc[1] = 0;
   }
   tc_fence_before();
   __syncthreads();
-  if constexpr (kPair) cluster_sync();   // the other CTA's barriers and tensor memory
+  cluster_sync();   // the other CTA's barriers and tensor memory
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, static_cast<uint32_t>(s_misc[0]), 0);
 
@@ -481,14 +462,14 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
     }
   };
 
-  const int ntn = (p.N + kCtas * kM - 1) / (kCtas * kM), ntt = (p.T + NT - 1) / NT;
+  const int ntn = (p.N + 2 * kM - 1) / (2 * kM), ntt = (p.T + NT - 1) / NT;
   const int tiles = ntn * ntt;
   const int steps_all = (p.K + kBK - 1) / kBK;
   const int s0 = static_cast<int>(static_cast<int64_t>(steps_all) * part / split);
   const int s1 = static_cast<int>(static_cast<int64_t>(steps_all) * (part + 1) / split);
   const int steps = s1 - s0;
-  const int tile0 = blockIdx.x / (kCtas * split), tile_step = gridDim.x / (kCtas * split);
-  auto channel0 = [&](int tile) { return ((tile % ntn) * kCtas + static_cast<int>(side)) * kM; };
+  const int tile0 = blockIdx.x / (2 * split), tile_step = gridDim.x / (2 * split);
+  auto channel0 = [&](int tile) { return ((tile % ntn) * 2 + static_cast<int>(side)) * kM; };
 
   constexpr bool kSplitRegs = NT == 256;
   if (warp < kEpiWarp0) {
@@ -522,7 +503,7 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
       }
       if (*abort) drain(fullx, C::S, r);
     }
-    if (kPair && warp == 1 && side) {
+    if (warp == 1 && side) {
       // ---- the odd CTA's tokens are reported to the even one
       if (lane == 0) {
         Ring<C::S> r;
@@ -554,13 +535,13 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
             if (elect_one()) {
               const uint64_t da = smem_desc(base + stage * (C::A + C::B)), db = da + (C::A >> 4);
 #pragma unroll
-              for (int kk = 0; kk < kBK / 16; ++kk) mma<kPair>(acc, da + kk * 2, db + kk * 2, C::kIdesc, more | kk);
-              commit<kPair>(empty + 8 * stage, both);
+              for (int kk = 0; kk < kBK / 16; ++kk) mma_pair(acc, da + kk * 2, db + kk * 2, C::kIdesc, more | kk);
+              commit_pair(empty + 8 * stage, both);
             }
             ready = __all_sync(0xffffffffu, ready);
             more = 1;
           }
-          if (ok && elect_one()) commit<kPair>(dfull + 8 * d.stage, both);
+          if (ok && elect_one()) commit_pair(dfull + 8 * d.stage, both);
           __syncwarp();
         }
       }
@@ -595,24 +576,27 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          if (kPair)
-            arrive_at(dempty + 8 * d.stage, leader);
-          else
-            mbar_arrive(dempty + 8 * d.stage);
-        }
+        if (lane == 0) arrive_at(dempty + 8 * d.stage, leader);
       }
       if (!ok) break;
       const int n0 = channel0(tile), t0 = (tile / ntn) * NT;
       if (split == 1) {
-        const int n = n0 + q * 32 + lane;
-        if (n < p.N) {
-          const float ws = p.ws[n], bias = p.bias ? to_f32<O>(static_cast<const O*>(p.bias)[n]) : 0.f;
+        // the token scales are read ahead and passed around the warp: a load
+        // beside each store would wait for the store (they might be the same memory)
+        const int n = n0 + q * 32 + lane, ts = t0 + half * C::ACC;
+        float xs[C::ACC / 32], ws = 0.f, bias = 0.f;
 #pragma unroll
-          for (int i = 0; i < C::ACC; ++i) {
-            const int t = t0 + half * C::ACC + i;
-            if (t < p.T) store_out<O>(p, t, n, acc[i], p.xs[t], ws, bias);
-          }
+        for (int i = 0; i < C::ACC / 32; ++i) xs[i] = ts + i * 32 + lane < p.T ? p.xs[ts + i * 32 + lane] : 0.f;
+        if (n < p.N) {
+          ws = p.ws[n];
+          if (p.bias) bias = to_f32<O>(static_cast<const O*>(p.bias)[n]);
+        }
+        O* out = static_cast<O*>(p.out) + ts * p.ldo + n;
+#pragma unroll
+        for (int i = 0; i < C::ACC; ++i) {
+          const float x = __shfl_sync(0xffffffffu, xs[i / 32], i % 32);
+          if (n < p.N && ts + i < p.T) *out = from_f32<O>(fmaf(static_cast<float>(acc[i]) * x, ws, bias));
+          out += p.ldo;
         }
       } else {
         // every stage of the ring has been read: its space takes the sums
@@ -645,10 +629,7 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
       proxy_fence_smem();
       __syncwarp();
       if (lane == 0) {
-        if (kPair)
-          arrive_at(fullw + 8 * r.stage, leader);
-        else
-          mbar_arrive(fullw + 8 * r.stage);
+        arrive_at(fullw + 8 * r.stage, leader);
         mbar_arrive(empty8 + 8 * r8.stage);   // not before the stores: the loads have then arrived for sure
       }
     }
@@ -666,35 +647,51 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
     if (!*abort) {
       const int n0 = channel0(tile0), t0 = (tile0 / ntn) * NT;
       const int j0 = NT * part / split, j1 = NT * (part + 1) / split;
-#pragma unroll 2
-      for (int i = j0 * (kM / 4) + tid; i < j1 * (kM / 4); i += C::kThreads) {
-        const int t = t0 + i / (kM / 4), n = n0 + i % (kM / 4) * 4;
-        if (t >= p.T || n >= p.N) continue;
-        int4 sum = make_int4(0, 0, 0, 0);
-#pragma unroll 4
-        for (int r = 0; r < split; ++r) {
-          const int4 v = ld_cluster(base + i * 16, r * kCtas + side);
-          sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
-        }
-        const int v[4] = {sum.x, sum.y, sum.z, sum.w};
-        const float xs = p.xs[t];
+      const int end = j1 * (kM / 4);
+      const int n = n0 + tid % (kM / 4) * 4;   // four channels, the same for all of the thread's tokens
+      float ws[4], bias[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (n + c < p.N)
-            store_out<O>(p, t, n + c, v[c], xs, p.ws[n + c], p.bias ? to_f32<O>(static_cast<const O*>(p.bias)[n + c]) : 0.f);
+      for (int c = 0; c < 4; ++c) {
+        const bool in = n + c < p.N;
+        ws[c] = in ? p.ws[n + c] : 0.f;
+        bias[c] = in && p.bias ? to_f32<O>(static_cast<const O*>(p.bias)[n + c]) : 0.f;
+      }
+      constexpr int U = 4;                     // tokens whose loads are in flight together
+      for (int i0 = j0 * (kM / 4) + tid; i0 < end; i0 += U * C::kThreads) {
+        int4 sum[U];
+        float xs[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = i0 + u * C::kThreads, t = t0 + i / (kM / 4);
+          sum[u] = make_int4(0, 0, 0, 0);
+          xs[u] = i < end && t < p.T ? p.xs[t] : 0.f;
+        }
+        for (int r = 0; r < split; ++r) {
+          int4 v[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) v[u] = ld_cluster(base + min(i0 + u * C::kThreads, end - 1) * 16, r * 2 + side);
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            sum[u].x += v[u].x, sum[u].y += v[u].y, sum[u].z += v[u].z, sum[u].w += v[u].w;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = i0 + u * C::kThreads, t = t0 + i / (kM / 4);
+          if (i >= end || t >= p.T) continue;
+          const int v[4] = {sum[u].x, sum[u].y, sum[u].z, sum[u].w};
+          O* out = static_cast<O*>(p.out) + t * p.ldo + n;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (n + c < p.N) out[c] = from_f32<O>(fmaf(static_cast<float>(v[c]) * xs[u], ws[c], bias[c]));
+        }
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (kPair || split > 1) cluster_sync();   // nothing of this CTA is read or signalled any more
+  cluster_sync();   // nothing of this CTA is read or signalled any more
   tc_fence_after();
-  if (warp == 1) {
-    if constexpr (kPair)
-      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols));
-    else
-      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols));
-  }
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols));
 }
 
 // Tokens as fp16, [T][kp] with kp a multiple of 64, zero past K.
@@ -778,19 +775,18 @@ cudaError_t launch_tc_nt(const LinArgs& p, void* ws, cudaStream_t s) {
       p.x, p.ldx, p.T, p.K, kp, static_cast<__half*>(ws));
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  constexpr int kCtas = C::kPair ? 2 : 1, kN = kCtas * kM;
-  const int64_t tiles = static_cast<int64_t>((p.N + kN - 1) / kN) * ((p.T + NT - 1) / NT);
+  const int64_t tiles = static_cast<int64_t>((p.N + 2 * kM - 1) / (2 * kM)) * ((p.T + NT - 1) / NT);
   const int steps = (p.K + kBK - 1) / kBK;
   int split = 1;
-  while (split * kCtas < 8 && tiles * kCtas * split * 2 <= sms && steps >= 4 * split) split *= 2;
+  while (split < 4 && tiles * split * 4 <= sms && steps >= 4 * split) split *= 2;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(kCtas * (split > 1 ? tiles * split : std::min<int64_t>(tiles, sms / kCtas))));
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * (split > 1 ? tiles * split : std::min<int64_t>(tiles, sms / 2))));
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute a[2]{};
   a[0].id = cudaLaunchAttributeClusterDimension;
-  a[0].val.clusterDim = {static_cast<unsigned>(kCtas * split), 1, 1};
+  a[0].val.clusterDim = {static_cast<unsigned>(2 * split), 1, 1};
   // it may start while k_widen runs: only its token loads wait for k_widen,
   // which itself started after everything before it had ended
   a[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
