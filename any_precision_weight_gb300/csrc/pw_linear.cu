@@ -5,8 +5,8 @@
 //
 // the sum exact in int32 (K <= 131071: 128 * 128 * K < 2^31).
 //
-// Up to 32 tokens: k_few, int8 tensor-core products fed from registers, the
-// weights streamed once.  More tokens: k_tc on the 5th-generation tensor
+// Up to 32 tokens: k_few, tensor-core products fed from registers, the weights
+// streamed once.  More tokens: k_tc on the 5th-generation tensor
 // cores.  This GPU's int8 tensor rate is a small part of its 16-bit rate, and
 // tcgen05 has no int8 kind here, so that work runs in fp16: int8 values are
 // exact in fp16, their products (at most 2^14) are exact in fp32, and so are
@@ -25,6 +25,8 @@
 
 namespace pw {
 namespace {
+
+constexpr int kMaxDev = 64;
 
 struct LinArgs {
   const int8_t* x;
@@ -75,18 +77,91 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// D += A B, fp16 16 x 16 by 16 x 8, fp32.
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+  return d;
+}
+
+// Four int8 values as two fp16 pairs: a byte b becomes the fp16 number
+// 1024 + (b + 128) in the low byte of 0x6400, and 1152 is subtracted.
+__device__ __forceinline__ void to_f16x4(uint32_t v, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = v ^ 0x80808080u;                       // b + 128
+  const __half2 k = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));   // 1152
+  uint32_t a = prmt(u, 0x64646464u, 0x4140), b = prmt(u, 0x64646464u, 0x4342);
+  const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), k), y = __hsub2(*reinterpret_cast<__half2*>(&b), k);
+  lo = *reinterpret_cast<const uint32_t*>(&x);
+  hi = *reinterpret_cast<const uint32_t*>(&y);
+}
+__device__ __forceinline__ void to_f16x16(const uint4& v, uint32_t (&h)[8]) {
+  to_f16x4(v.x, h[0], h[1]);
+  to_f16x4(v.y, h[2], h[3]);
+  to_f16x4(v.z, h[4], h[5]);
+  to_f16x4(v.w, h[6], h[7]);
+}
+
+// The sums of 16 channels x 8 NT tokens in a warp's registers.  Up to 8 tokens
+// in int8 (256 products a clock and SM, the weights need 190 at the memory's
+// rate); above, where int8 would be the bound, in fp16, whose fp32 sums move to
+// int32 every 1024 columns (run `n` of 16 ends one).
+template <int NT>
+struct FewSums {
+  int acc[NT][4] = {};
+  float part[NT][4] = {};
+  __device__ __forceinline__ void add(const uint4& a, const uint4& b, const uint4 (&x)[NT], int n) {
+    if constexpr (NT == 1) {
+      mma_s8(acc[0], a.x, b.x, a.y, b.y, x[0].x, x[0].y);
+      mma_s8(acc[0], a.z, b.z, a.w, b.w, x[0].z, x[0].w);
+    } else {
+      uint32_t ha[8], hb[8];
+      to_f16x16(a, ha);
+      to_f16x16(b, hb);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        uint32_t hx[8];
+        to_f16x16(x[j], hx);
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) mma_f16_16816(part[j], ha[i], hb[i], ha[i + 1], hb[i + 1], hx[i], hx[i + 1]);
+      }
+      if (n % 16 == 15) flush();
+    }
+  }
+  __device__ __forceinline__ void flush() {
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[j][i] += __float2int_rn(part[j][i]), part[j][i] = 0.f;
+  }
+};
+
 constexpr int kFewWarps = 8;
+constexpr int kInt8Tokens = 8;
 constexpr int kFewTokens = 32;
+constexpr int kManyChannels = 40000;
 
 // A group of kw warps owns 16 channels and shares out K in runs of 64 columns.
 // Lane (g, q) = (lane / 4, lane % 4) loads the 16 bytes at column 16 q of
-// channels g and g + 8, and of token g of every 8: the operand registers of two
+// channels g and g + 8, and of token g of every 8: the operand registers of its
 // products, with the columns of K in an order of their own that both operands
 // share.  So the weights go from memory to the tensor cores through registers
-// alone, 64 bytes of a channel at a time.  NT: groups of 8 tokens.
+// alone, 64 bytes of a channel at a time.  NT: groups of 8 tokens.  One group
+// has the registers for three CTAs of an SM, and their other warps' loads are
+// in flight while one multiplies (28672 x 4096, one token: 22.5 us; 26 us with
+// the next U runs loaded ahead by two CTAs); more groups load ahead.
 template <typename O, int NT>
-__global__ void __launch_bounds__(kFewWarps * 32, NT <= 2 ? 3 : 2) k_few(const LinArgs p, int kw) {
+__global__ void __launch_bounds__(kFewWarps * 32, NT == 1 ? 3 : 2) k_few(const LinArgs p, int kw) {
   constexpr int kRow = NT * 8 + 1;   // padded against bank conflicts
+  constexpr int U = NT == 1 ? 4 : 2;
+  constexpr bool kAhead = NT > 1;
   __shared__ int s_part[kFewWarps][16 * kRow];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int groups = kFewWarps / kw, turn = warp % kw;
@@ -99,30 +174,32 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT <= 2 ? 3 : 2) k_few(const L
   const int8_t* x[NT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) x[j] = p.x + min(j * 8 + g, p.T - 1) * p.ldx + q * 16;
-  int acc[NT][4] = {};
-  auto step = [&](const uint4& a, const uint4& b, const uint4 (&v)[NT]) {
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      mma_s8(acc[j], a.x, b.x, a.y, b.y, v[j].x, v[j].y);
-      mma_s8(acc[j], a.z, b.z, a.w, b.w, v[j].z, v[j].w);
-    }
-  };
+  FewSums<NT> sums;
   const int whole = min(r1, p.K / 64);
-  int k = r0;
-  constexpr int U = 4;   // runs in flight
-  for (; k + U <= whole; k += U) {
-    uint4 a[U], b[U], v[U][NT];
+  const int last = r0 + (whole > r0 ? (whole - r0) / U * U : 0);   // turns of U whole runs end here
+  uint4 a[U], b[U];
+  auto fetch = [&](int k) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       a[u] = load_once(w0 + (k + u) * 64);
       b[u] = load_once(w1 + (k + u) * 64);
     }
+  };
+  int k = r0;
+  if (kAhead && k < last) fetch(k);
+  for (; k < last; k += U) {
+    if (!kAhead) fetch(k);
+    uint4 ca[U], cb[U], v[U][NT];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u) {
+      ca[u] = a[u];
+      cb[u] = b[u];
 #pragma unroll
       for (int j = 0; j < NT; ++j) v[u][j] = __ldg(reinterpret_cast<const uint4*>(x[j] + (k + u) * 64));
+    }
+    if (kAhead && k + U < last) fetch(k + U);
 #pragma unroll
-    for (int u = 0; u < U; ++u) step(a[u], b[u], v[u]);
+    for (int u = 0; u < U; ++u) sums.add(ca[u], cb[u], v[u], k - r0 + u);
   }
   for (; k < r1; ++k) {   // single runs, the last one perhaps not whole
     const int left = p.K - k * 64 - q * 16;
@@ -132,13 +209,14 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT <= 2 ? 3 : 2) k_few(const L
     uint4 v[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) v[j] = part(x[j]);
-    step(part(w0), part(w1), v);
+    sums.add(part(w0), part(w1), v, k - r0);
   }
+  if (NT > 1) sums.flush();
   // acc[j][0..3]: channels g, g, g + 8, g + 8; tokens 8 j + 2 q + 0, 1, 0, 1
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s_part[warp][(g + (i >> 1) * 8) * kRow + j * 8 + q * 2 + (i & 1)] = acc[j][i];
+    for (int i = 0; i < 4; ++i) s_part[warp][(g + (i >> 1) * 8) * kRow + j * 8 + q * 2 + (i & 1)] = sums.acc[j][i];
   __syncthreads();
   for (int i = threadIdx.x; i < groups * 16 * p.T; i += kFewWarps * 32) {
     const int c = i % (groups * 16), t = i / (groups * 16), grp = c >> 4;
@@ -157,7 +235,7 @@ cudaError_t launch_few_nt(const LinArgs& p, cudaStream_t s) {
   // the L1), up to eight where there are few
   const int groups = (p.N + 15) / 16, runs = (p.K + 63) / 64;
   int kw = 1;
-  while (kw < kFewWarps && groups * kw < sm_count() * 16 && runs >= 4 * kw) kw *= 2;
+  while (kw < kFewWarps && groups * kw < sm_count() * (NT == 1 ? 16 : 24) && runs >= 4 * kw) kw *= 2;
   const int per = kFewWarps / kw;
   k_few<O, NT><<<(groups + per - 1) / per, kFewWarps * 32, 0, s>>>(p, kw);
   return cudaGetLastError();
@@ -167,6 +245,7 @@ template <typename O>
 cudaError_t launch_few(const LinArgs& p, cudaStream_t s) {
   if (p.T <= 8) return launch_few_nt<O, 1>(p, s);
   if (p.T <= 16) return launch_few_nt<O, 2>(p, s);
+  if (p.T <= 24) return launch_few_nt<O, 3>(p, s);
   return launch_few_nt<O, 4>(p, s);
 }
 
@@ -178,13 +257,13 @@ cudaError_t launch_few(const LinArgs& p, cudaStream_t s) {
 //  * warp 0 fetches int8 weights by TMA into a ring of S8 stages, warp 2 the
 //    fp16 tokens into the operand ring of S stages;
 //  * the last 8 warps, in 4 groups that take a stage in turn, convert the
-//    weights to fp16 in the operand ring.  A byte b becomes the fp16 number
-//    1024 + (b + 128) by placing it in the low byte of 0x6400, and 1152 is
-//    subtracted: five operations for four values, stored in the K-major
-//    128-byte-swizzled layout the MMA reads;
-//  * warp 1 issues tcgen05.mma kind::f16 (fp32 in tensor memory, two
-//    accumulators of NT columns), 1024 columns of K into one accumulator,
-//    then the next 1024 into the other;
+//    weights to fp16 in the operand ring, in the K-major 128-byte-swizzled
+//    layout the MMA reads;
+//  * warp 1 issues tcgen05.mma kind::f16 (fp32 in tensor memory), up to 1024
+//    columns of K into one accumulator of NT columns, then as many into
+//    another.  An issue takes some 60 clocks, more than the MMA of few tokens
+//    itself, so up to 128 tokens warp 3 issues every other stage, into
+//    accumulators of its own (MMAs of two threads are not ordered);
 //  * warps 4.. add each finished accumulator to their int32 registers while
 //    the next one fills, and at the tile's end scale and store.
 // Two CTAs of a cluster make a pair (cta_group::2), each with its own 128
@@ -213,16 +292,21 @@ struct Tile {
   static constexpr int kRowsB = NT / 2;                   // tokens that a CTA holds
   static constexpr int A = kM * kBK * 2, B = kRowsB * kBK * 2;   // bytes of a stage's operands
   static constexpr int A8 = kM * kBK;                     // and of its int8 weights
-  static constexpr int S = 5;                             // operand stages
-  static constexpr int S8 = NT <= 64 ? 14 : NT == 128 ? 12 : 7;   // int8 stages
+  static constexpr int S = NT <= 128 ? 6 : 5;             // operand stages
+  static constexpr int S8 = NT == 32 ? 13 : NT == 64 ? 12 : NT == 128 ? 8 : 7;   // int8 stages
   static constexpr int kRing8 = S * (A + B);
   static constexpr int kOffBar = kRing8 + S8 * A8;
-  static constexpr int kSmem = kOffBar + 8 * (3 * S + 2 * S8 + 4) + 16 + 1024;
-  static constexpr uint32_t kCols = 2 * NT;
+  static constexpr int kSmem = kOffBar + 8 * (3 * S + 2 * S8 + 6) + 16 + 1024;
+  static constexpr int kIssuers = NT <= 128 ? 2 : 1;      // MMA warps
+  static constexpr int kWindow = kChunk * kIssuers;       // stages of a set of accumulators
+  static constexpr uint32_t kCols = 2 * kIssuers * NT;
   // D f32, A and B f16, N / 8 and M / 16
   static constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(NT >> 3) << 17) |
                                      (static_cast<uint32_t>(2 * kM >> 4) << 24);
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+  // a stage belongs to one issuer: one that ran ahead of the other could not
+  // tell a stage's next use from its use before last
+  static_assert(S % kIssuers == 0, "stages of an issuer");
   static_assert(kM * NT * 4 <= kRing8, "a CTA's int32 sums fit the operand ring");
 };
 
@@ -234,22 +318,6 @@ struct Tile {
 // still waiting for theirs would leave them waiting for good).
 constexpr int kRegsLaunch = 96, kRegsIssue = 32, kRegsAcc = 160, kRegsConv = 64;
 static_assert(128 * (kRegsIssue + 2 * kRegsAcc + 2 * kRegsConv) <= 640 * kRegsLaunch, "register split");
-
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
-  uint32_t d;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
-  return d;
-}
-
-// Four int8 values as two fp16 pairs.
-__device__ __forceinline__ void to_f16x4(uint32_t v, uint32_t& lo, uint32_t& hi) {
-  const uint32_t u = v ^ 0x80808080u;                       // b + 128
-  const __half2 k = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));   // 1152
-  uint32_t a = prmt(u, 0x64646464u, 0x4140), b = prmt(u, 0x64646464u, 0x4342);
-  const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), k), y = __hsub2(*reinterpret_cast<__half2*>(&b), k);
-  lo = *reinterpret_cast<const uint32_t*>(&x);
-  hi = *reinterpret_cast<const uint32_t*>(&y);
-}
 
 __device__ __forceinline__ void sts16(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
@@ -282,10 +350,7 @@ struct Weights {
     for (int i = 0; i < kN; ++i) {
       const int r = (tid >> 2) + i * (kGroupWarps * 8);
       uint32_t h[8];
-      to_f16x4(v[i].x, h[0], h[1]);
-      to_f16x4(v[i].y, h[2], h[3]);
-      to_f16x4(v[i].z, h[4], h[5]);
-      to_f16x4(v[i].w, h[6], h[7]);
+      to_f16x16(v[i], h);
       sts16(dst + r * 128 + ((j ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
       sts16(dst + r * 128 + (((j + 1) ^ (r & 7)) << 4), h[4], h[5], h[6], h[7]);
     }
@@ -409,8 +474,8 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
   const uint32_t base = saddr(smem);
   const uint32_t fullw = base + C::kOffBar, fullx = fullw + 8 * C::S, empty = fullx + 8 * C::S;
   const uint32_t full8 = empty + 8 * C::S, empty8 = full8 + 8 * C::S8;
-  const uint32_t dfull = empty8 + 8 * C::S8, dempty = dfull + 16;
-  int* s_misc = reinterpret_cast<int*>(smem + C::kOffBar + 8 * (3 * C::S + 2 * C::S8 + 4));   // tmem, abort
+  const uint32_t dfull = empty8 + 8 * C::S8, dempty = dfull + 16, fin = dempty + 16;
+  int* s_misc = reinterpret_cast<int*>(smem + C::kOffBar + 8 * (3 * C::S + 2 * C::S8 + 6));   // tmem, abort
   volatile int* abort = s_misc + 1;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // the compiler then knows that it is uniform
@@ -432,7 +497,8 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
       mbar_init(empty + 8 * i, 1);
     }
     for (int i = 0; i < C::S8; ++i) mbar_init(full8 + 8 * i, 1), mbar_init(empty8 + 8 * i, kGroupWarps);
-    for (int i = 0; i < 2; ++i) mbar_init(dfull + 8 * i, 1), mbar_init(dempty + 8 * i, 2 * C::EW);
+    for (int i = 0; i < 2; ++i) mbar_init(fin + 8 * i, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(dfull + 8 * i, C::kIssuers), mbar_init(dempty + 8 * i, 2 * C::EW);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     s_misc[1] = 0;
   }
@@ -511,26 +577,30 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
         for (int64_t g = 0; g < all && poll(fullx + 8 * r.stage, r.parity, abort); ++g, r.next())
           arrive_at(fullw + 8 * r.stage, leader);
       }
-    } else if (warp == 1) {
+    } else if (!side && (warp == 1 || (C::kIssuers == 2 && warp == 3))) {
       // ---- MMA issue: the whole warp in step, so that the operands stay in
       // uniform registers, and an elected thread for the instructions.  A
-      // barrier takes over 100 clocks to read, so the next stage's are read
+      // barrier takes over 100 clocks to read, so the next stage's is read
       // before this stage's MMAs are issued and looked at after
-      Ring<C::S> r;
-      Ring<2> d;
+      const uint32_t me = warp == 3;
       const uint16_t both = static_cast<uint16_t>(3u << leader);
+      Ring<C::S> r;
+      r.next(me);
+      Ring<2> d;
       bool ok = true, ready = false;
+      uint32_t g = 0;   // stage among all of the CTA's (its parity says whose it is)
       for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
         for (int k = 0; k < steps && ok; d.next()) {
           if (!d.first && !(ok = wait(dempty + 8 * d.stage, d.parity ^ 1))) break;
           tc_fence_after();
-          const uint32_t acc = tmem + d.stage * NT;
-          const int end = min(steps, k + kChunk);
-          for (uint32_t more = 0; k < end; ++k) {
+          const uint32_t acc = tmem + (d.stage * C::kIssuers + me) * NT;
+          const int end = min(steps, k + C::kWindow);
+          for (uint32_t more = 0; k < end; ++k, ++g) {
+            if (C::kIssuers == 2 && (g & 1) != me) continue;
             if (!ready && !(ok = wait(fullx + 8 * r.stage, r.parity) && wait(fullw + 8 * r.stage, r.parity))) break;
             tc_fence_after();
             const uint32_t stage = r.stage;
-            r.next();
+            r.next(C::kIssuers);
             ready = test_wait(fullx + 8 * r.stage, r.parity) & test_wait(fullw + 8 * r.stage, r.parity);
             if (elect_one()) {
               const uint64_t da = smem_desc(base + stage * (C::A + C::B)), db = da + (C::A >> 4);
@@ -545,7 +615,14 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
           __syncwarp();
         }
       }
-      if (*abort && lane == 0) drain(empty, C::S, r);
+      if (*abort) {   // the MMAs in flight end before the CTA does
+        if (elect_one()) {
+          volatile int none = 0;
+          commit_pair(fin + 8 * me, static_cast<uint16_t>(1u << leader));
+          poll(fin + 8 * me, 0, &none);
+        }
+        __syncwarp();
+      }
     }
     __syncwarp();
     if constexpr (kSplitRegs) {
@@ -558,22 +635,29 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
     const int q = warp & 3, half = (warp - kEpiWarp0) >> 2;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * C::ACC;
     Ring<2> d;
+    uint32_t g = 0;
     bool ok = true;
     for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
       int acc[C::ACC];
 #pragma unroll
       for (int i = 0; i < C::ACC; ++i) acc[i] = 0;
-      for (int k = 0; k < steps; k += kChunk, d.next()) {
+      for (int k = 0; k < steps; k += C::kWindow, d.next()) {
+        const int n = min(steps - k, C::kWindow);
         if (!(ok = warp_ok(lane != 0 || poll<100>(dfull + 8 * d.stage, d.parity, abort)))) break;
         tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < C::ACC; c += 16) {
-          uint32_t r[16];
-          tmem_ld16(lanes + d.stage * NT + c, r);
-          tmem_wait(r);
+        for (uint32_t m = 0; m < C::kIssuers; ++m) {
+          if (C::kIssuers == 2 && n == 1 && (g & 1) != m) continue;   // one stage: the other's accumulator is old
 #pragma unroll
-          for (int i = 0; i < 16; ++i) acc[c + i] += __float2int_rn(__uint_as_float(r[i]));
+          for (int c = 0; c < C::ACC; c += 16) {
+            uint32_t r[16];
+            tmem_ld16(lanes + (d.stage * C::kIssuers + m) * NT + c, r);
+            tmem_wait(r);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[c + i] += __float2int_rn(__uint_as_float(r[i]));
+          }
         }
+        g += n;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_at(dempty + 8 * d.stage, leader);
@@ -704,10 +788,7 @@ __global__ void __launch_bounds__(256) k_widen(const int8_t* x, int64_t ldx, int
     const int8_t* from = x + t * ldx + k;
     const uint4 v = k + 16 <= K ? __ldg(reinterpret_cast<const uint4*>(from)) : load_tail(from, K - k);
     uint32_t h[8];
-    to_f16x4(v.x, h[0], h[1]);
-    to_f16x4(v.y, h[2], h[3]);
-    to_f16x4(v.z, h[4], h[5]);
-    to_f16x4(v.w, h[6], h[7]);
+    to_f16x16(v, h);
     uint4* to = reinterpret_cast<uint4*>(out + t * kp + k);
     to[0] = make_uint4(h[0], h[1], h[2], h[3]);
     to[1] = make_uint4(h[4], h[5], h[6], h[7]);
@@ -745,7 +826,32 @@ cudaError_t map_tile(CUtensorMap* m, int size, const void* base, int64_t ld, int
 
 int padded_k(int K) { return (K + 63) & ~63; }
 
-constexpr int kMaxDev = 64;
+
+// Clusters of `size` CTAs of k_tc<O, NT> that the device holds at once (asked
+// once per device; size 4 or 8).
+template <typename O, int NT>
+int max_clusters(int dev, int size) {
+  static std::atomic<int> known[kMaxDev][2];
+  std::atomic<int>& k = known[dev][size == 8];
+  int n = k.load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(size);
+    cfg.blockDim = dim3(Tile<NT>::kThreads);
+    cfg.dynamicSmemBytes = Tile<NT>::kSmem;
+    cudaLaunchAttribute a{};
+    a.id = cudaLaunchAttributeClusterDimension;
+    a.val.clusterDim = {static_cast<unsigned>(size), 1, 1};
+    cfg.attrs = &a;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, k_tc<O, NT>, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();   // not fatal: K stays whole
+      n = -1;
+    }
+    k.store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
 
 template <typename O, int NT>
 cudaError_t launch_tc_nt(const LinArgs& p, void* ws, cudaStream_t s) {
@@ -777,8 +883,11 @@ cudaError_t launch_tc_nt(const LinArgs& p, void* ws, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int64_t tiles = static_cast<int64_t>((p.N + 2 * kM - 1) / (2 * kM)) * ((p.T + NT - 1) / NT);
   const int steps = (p.K + kBK - 1) / kBK;
+  // K is split while all the parts still run at once: clusters of 8 fit a
+  // processing cluster's SMs less often than their number says, and a second
+  // turn costs as much as the first
   int split = 1;
-  while (split < 4 && tiles * split * 4 <= sms && steps >= 4 * split) split *= 2;
+  while (split < 4 && tiles <= max_clusters<O, NT>(dev, 4 * split) && steps >= 8 * split) split *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * (split > 1 ? tiles * split : std::min<int64_t>(tiles, sms / 2))));
   cfg.blockDim = dim3(C::kThreads);
@@ -798,14 +907,15 @@ cudaError_t launch_tc_nt(const LinArgs& p, void* ws, cudaStream_t s) {
 
 template <typename O>
 cudaError_t launch_linear(const LinArgs& p, void* ws, cudaStream_t s) {
-  if (p.T <= kFewTokens) return launch_few<O>(p, s);
+  if (p.T <= kInt8Tokens || (p.T <= kFewTokens && p.N < kManyChannels)) return launch_few<O>(p, s);
+  if (p.T <= 32) return launch_tc_nt<O, 32>(p, ws, s);
   if (p.T <= 64) return launch_tc_nt<O, 64>(p, ws, s);
   if (p.T <= 128) return launch_tc_nt<O, 128>(p, ws, s);
   return launch_tc_nt<O, 256>(p, ws, s);
 }
 
 size_t linear_ws_bytes(int T, int K) {
-  return T <= kFewTokens ? 0 : static_cast<size_t>(T) * padded_k(K) * 2;
+  return T <= kInt8Tokens ? 0 : static_cast<size_t>(T) * padded_k(K) * 2;
 }
 
 }  // namespace
