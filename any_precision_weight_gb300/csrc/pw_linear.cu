@@ -144,9 +144,11 @@ struct FewSums {
 };
 
 constexpr int kFewWarps = 8;
-constexpr int kInt8Tokens = 8;
-constexpr int kFewTokens = 32;
-constexpr int kManyChannels = 40000;
+// k_few against k_thin, K = 4096, us: 16 tokens 6.5 and 18 at N = 4096, 30 and 37
+// at 28672, 126 and 122 at 131072; 32 tokens 10 and 18 at 4096, 27 and 26 at
+// 14336, 48 and 37 at 28672.
+constexpr int kFewTokens = 16;
+constexpr int kManyChannels = 14336;   // from which 17 to 32 tokens take k_thin
 
 // A group of kw warps owns 16 channels and shares out K in runs of 64 columns.
 // Lane (g, q) = (lane / 4, lane % 4) loads the 16 bytes at column 16 q of
@@ -224,7 +226,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 ? 3 : 2) k_few(const L
     if (n >= p.N) continue;
     int sum = 0;
     for (int j = 0; j < kw; ++j) sum += s_part[grp * kw + j][(c & 15) * kRow + t];
-    store_out<O>(p, t, n, sum, p.xs[t], p.ws[n], p.bias ? to_f32<O>(static_cast<const O*>(p.bias)[n]) : 0.f);
+    store_out<O>(p, t, n, sum, __ldg(p.xs + t), __ldg(p.ws + n), p.bias ? to_f32<O>(static_cast<const O*>(p.bias)[n]) : 0.f);
   }
 }
 
@@ -260,10 +262,7 @@ cudaError_t launch_few(const LinArgs& p, cudaStream_t s) {
 //    weights to fp16 in the operand ring, in the K-major 128-byte-swizzled
 //    layout the MMA reads;
 //  * warp 1 issues tcgen05.mma kind::f16 (fp32 in tensor memory), up to 1024
-//    columns of K into one accumulator of NT columns, then as many into
-//    another.  An issue takes some 60 clocks, more than the MMA of few tokens
-//    itself, so up to 128 tokens warp 3 issues every other stage, into
-//    accumulators of its own (MMAs of two threads are not ordered);
+//    columns of K into one accumulator, then as many into another;
 //  * warps 4.. add each finished accumulator to their int32 registers while
 //    the next one fills, and at the tile's end scale and store.
 // Two CTAs of a cluster make a pair (cta_group::2), each with its own 128
@@ -285,28 +284,23 @@ constexpr int kEpiWarp0 = 4;
 
 template <int NT>
 struct Tile {
-  static constexpr int EW = NT <= 64 ? 4 : 8;             // accumulating warps
+  static constexpr int EW = 8;                            // accumulating warps
   static constexpr int ACC = NT / (EW / 4);               // int32 sums of one of their threads
   static constexpr int kConvWarp0 = kEpiWarp0 + EW;
   static constexpr int kThreads = 32 * (kConvWarp0 + kConvWarps);
   static constexpr int kRowsB = NT / 2;                   // tokens that a CTA holds
   static constexpr int A = kM * kBK * 2, B = kRowsB * kBK * 2;   // bytes of a stage's operands
   static constexpr int A8 = kM * kBK;                     // and of its int8 weights
-  static constexpr int S = NT <= 128 ? 6 : 5;             // operand stages
-  static constexpr int S8 = NT == 32 ? 13 : NT == 64 ? 12 : NT == 128 ? 8 : 7;   // int8 stages
+  static constexpr int S = 5;                             // operand stages
+  static constexpr int S8 = 7;                            // int8 stages
   static constexpr int kRing8 = S * (A + B);
   static constexpr int kOffBar = kRing8 + S8 * A8;
   static constexpr int kSmem = kOffBar + 8 * (3 * S + 2 * S8 + 6) + 16 + 1024;
-  static constexpr int kIssuers = NT <= 128 ? 2 : 1;      // MMA warps
-  static constexpr int kWindow = kChunk * kIssuers;       // stages of a set of accumulators
-  static constexpr uint32_t kCols = 2 * kIssuers * NT;
+  static constexpr uint32_t kCols = 2 * NT;
   // D f32, A and B f16, N / 8 and M / 16
   static constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(NT >> 3) << 17) |
                                      (static_cast<uint32_t>(2 * kM >> 4) << 24);
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
-  // a stage belongs to one issuer: one that ran ahead of the other could not
-  // tell a stage's next use from its use before last
-  static_assert(S % kIssuers == 0, "stages of an issuer");
   static_assert(kM * NT * 4 <= kRing8, "a CTA's int32 sums fit the operand ring");
 };
 
@@ -330,17 +324,18 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
 }
 
 // A converting thread's part of a stage: 16 columns at 16 (tid % 4) of the
-// channels tid / 4 + 16 i.  Eight neighbouring threads read two rows of 64
+// channels tid / 4 + 8 WARPS i.  Eight neighbouring threads read two rows of 64
 // bytes (with the TMA's 64-byte swizzle) and write 16-byte pieces of two fp16
 // rows, each time to different banks.
+template <int ROWS, int WARPS>
 struct Weights {
-  static constexpr int kN = kM / (kGroupWarps * 8);
+  static constexpr int kN = ROWS / (WARPS * 8);
   uint4 v[kN];
 
   __device__ __forceinline__ void load(uint32_t src, int tid) {
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const int r = (tid >> 2) + i * (kGroupWarps * 8);
+      const int r = (tid >> 2) + i * (WARPS * 8);
       v[i] = lds16(src + r * 64 + (((tid & 3) ^ ((r >> 1) & 3)) << 4));
     }
   }
@@ -348,7 +343,7 @@ struct Weights {
     const int j = (tid & 3) * 2;
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const int r = (tid >> 2) + i * (kGroupWarps * 8);
+      const int r = (tid >> 2) + i * (WARPS * 8);
       uint32_t h[8];
       to_f16x16(v[i], h);
       sts16(dst + r * 128 + ((j ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
@@ -497,8 +492,8 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
       mbar_init(empty + 8 * i, 1);
     }
     for (int i = 0; i < C::S8; ++i) mbar_init(full8 + 8 * i, 1), mbar_init(empty8 + 8 * i, kGroupWarps);
-    for (int i = 0; i < 2; ++i) mbar_init(fin + 8 * i, 1);
-    for (int i = 0; i < 2; ++i) mbar_init(dfull + 8 * i, C::kIssuers), mbar_init(dempty + 8 * i, 2 * C::EW);
+    mbar_init(fin, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(dfull + 8 * i, 1), mbar_init(dempty + 8 * i, 2 * C::EW);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     s_misc[1] = 0;
   }
@@ -577,30 +572,26 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
         for (int64_t g = 0; g < all && poll(fullx + 8 * r.stage, r.parity, abort); ++g, r.next())
           arrive_at(fullw + 8 * r.stage, leader);
       }
-    } else if (!side && (warp == 1 || (C::kIssuers == 2 && warp == 3))) {
+    } else if (warp == 1) {
       // ---- MMA issue: the whole warp in step, so that the operands stay in
       // uniform registers, and an elected thread for the instructions.  A
       // barrier takes over 100 clocks to read, so the next stage's is read
       // before this stage's MMAs are issued and looked at after
-      const uint32_t me = warp == 3;
       const uint16_t both = static_cast<uint16_t>(3u << leader);
       Ring<C::S> r;
-      r.next(me);
       Ring<2> d;
       bool ok = true, ready = false;
-      uint32_t g = 0;   // stage among all of the CTA's (its parity says whose it is)
       for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
         for (int k = 0; k < steps && ok; d.next()) {
           if (!d.first && !(ok = wait(dempty + 8 * d.stage, d.parity ^ 1))) break;
           tc_fence_after();
-          const uint32_t acc = tmem + (d.stage * C::kIssuers + me) * NT;
-          const int end = min(steps, k + C::kWindow);
-          for (uint32_t more = 0; k < end; ++k, ++g) {
-            if (C::kIssuers == 2 && (g & 1) != me) continue;
+          const uint32_t acc = tmem + d.stage * NT;
+          const int end = min(steps, k + kChunk);
+          for (uint32_t more = 0; k < end; ++k) {
             if (!ready && !(ok = wait(fullx + 8 * r.stage, r.parity) && wait(fullw + 8 * r.stage, r.parity))) break;
             tc_fence_after();
             const uint32_t stage = r.stage;
-            r.next(C::kIssuers);
+            r.next();
             ready = test_wait(fullx + 8 * r.stage, r.parity) & test_wait(fullw + 8 * r.stage, r.parity);
             if (elect_one()) {
               const uint64_t da = smem_desc(base + stage * (C::A + C::B)), db = da + (C::A >> 4);
@@ -618,8 +609,8 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
       if (*abort) {   // the MMAs in flight end before the CTA does
         if (elect_one()) {
           volatile int none = 0;
-          commit_pair(fin + 8 * me, static_cast<uint16_t>(1u << leader));
-          poll(fin + 8 * me, 0, &none);
+          commit_pair(fin, static_cast<uint16_t>(1u << leader));
+          poll(fin, 0, &none);
         }
         __syncwarp();
       }
@@ -635,29 +626,22 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
     const int q = warp & 3, half = (warp - kEpiWarp0) >> 2;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * C::ACC;
     Ring<2> d;
-    uint32_t g = 0;
     bool ok = true;
     for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
       int acc[C::ACC];
 #pragma unroll
       for (int i = 0; i < C::ACC; ++i) acc[i] = 0;
-      for (int k = 0; k < steps; k += C::kWindow, d.next()) {
-        const int n = min(steps - k, C::kWindow);
+      for (int k = 0; k < steps; k += kChunk, d.next()) {
         if (!(ok = warp_ok(lane != 0 || poll<100>(dfull + 8 * d.stage, d.parity, abort)))) break;
         tc_fence_after();
 #pragma unroll
-        for (uint32_t m = 0; m < C::kIssuers; ++m) {
-          if (C::kIssuers == 2 && n == 1 && (g & 1) != m) continue;   // one stage: the other's accumulator is old
+        for (int c = 0; c < C::ACC; c += 16) {
+          uint32_t r[16];
+          tmem_ld16(lanes + d.stage * NT + c, r);
+          tmem_wait(r);
 #pragma unroll
-          for (int c = 0; c < C::ACC; c += 16) {
-            uint32_t r[16];
-            tmem_ld16(lanes + (d.stage * C::kIssuers + m) * NT + c, r);
-            tmem_wait(r);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[c + i] += __float2int_rn(__uint_as_float(r[i]));
-          }
+          for (int i = 0; i < 16; ++i) acc[c + i] += __float2int_rn(__uint_as_float(r[i]));
         }
-        g += n;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_at(dempty + 8 * d.stage, leader);
@@ -670,9 +654,9 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
         const int n = n0 + q * 32 + lane, ts = t0 + half * C::ACC;
         float xs[C::ACC / 32], ws = 0.f, bias = 0.f;
 #pragma unroll
-        for (int i = 0; i < C::ACC / 32; ++i) xs[i] = ts + i * 32 + lane < p.T ? p.xs[ts + i * 32 + lane] : 0.f;
+        for (int i = 0; i < C::ACC / 32; ++i) xs[i] = ts + i * 32 + lane < p.T ? __ldg(p.xs + ts + i * 32 + lane) : 0.f;
         if (n < p.N) {
-          ws = p.ws[n];
+          ws = __ldg(p.ws + n);
           if (p.bias) bias = to_f32<O>(static_cast<const O*>(p.bias)[n]);
         }
         O* out = static_cast<O*>(p.out) + ts * p.ldo + n;
@@ -706,7 +690,7 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
     const int64_t mine = static_cast<int64_t>(steps) * ((tiles - tile0 + tile_step - 1) / tile_step);
     for (int64_t g = group; g < mine; g += kGroups, r.next(kGroups), r8.next(kGroups)) {
       if (!wait(full8 + 8 * r8.stage, r8.parity)) break;
-      Weights w;
+      Weights<kM, kGroupWarps> w;
       w.load(base + C::kRing8 + r8.stage * C::A8, ctid);
       if (!r.first && !wait(empty + 8 * r.stage, r.parity ^ 1)) break;
       w.store(base + r.stage * (C::A + C::B), ctid);
@@ -737,7 +721,7 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const bool in = n + c < p.N;
-        ws[c] = in ? p.ws[n + c] : 0.f;
+        ws[c] = in ? __ldg(p.ws + n + c) : 0.f;
         bias[c] = in && p.bias ? to_f32<O>(static_cast<const O*>(p.bias)[n + c]) : 0.f;
       }
       constexpr int U = 4;                     // tokens whose loads are in flight together
@@ -748,7 +732,7 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
         for (int u = 0; u < U; ++u) {
           const int i = i0 + u * C::kThreads, t = t0 + i / (kM / 4);
           sum[u] = make_int4(0, 0, 0, 0);
-          xs[u] = i < end && t < p.T ? p.xs[t] : 0.f;
+          xs[u] = i < end && t < p.T ? __ldg(p.xs + t) : 0.f;
         }
         for (int r = 0; r < split; ++r) {
           int4 v[U];
@@ -776,6 +760,333 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
   cluster_sync();   // nothing of this CTA is read or signalled any more
   tc_fence_after();
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols));
+}
+
+// ---------------------------------------------------------------- up to 128 tokens
+
+// An MMA takes about 130 clocks however few columns it has, so with the
+// channels as its rows (k_tc) few tokens leave it mostly empty.  Here they are
+// its columns: one CTA, up to 128 tokens (M, rows past T hold anything) x 256
+// channels (N).  Roles and rings as in k_tc, without the pair: half the MMAs
+// for the same weights.  MT: tokens that a stage has room for; the MMA reads
+// 128 rows, the ones past MT from the weights behind them, into lanes that
+// nobody reads.  Bound by HBM, and by the conversion close behind.
+constexpr int kThinN = 256;
+template <int MT>
+struct Thin {
+  static constexpr int EW = 8, ACC = 128;
+  static constexpr int kConvWarp0 = kEpiWarp0 + EW;
+  static constexpr int kThreads = 32 * (kConvWarp0 + kConvWarps);
+  static constexpr int kGroups = 2, kGroupWarps = kConvWarps / kGroups;
+  static constexpr int X = MT * kBK * 2, W = kThinN * kBK * 2;   // bytes of a stage's operands
+  static constexpr int W8 = kThinN * kBK;                        // and of its int8 weights
+  static constexpr int S = MT == 32 ? 4 : 3;
+  static constexpr int S8 = MT == 64 ? 6 : 5;
+  static constexpr int kRing8 = S * (X + W);
+  static constexpr int kOffBar = kRing8 + S8 * W8;
+  static constexpr int kSmem = kOffBar + 8 * (3 * S + 2 * S8 + 5) + 16 + 1024;
+  static constexpr uint32_t kCols = 2 * kThinN;
+  static constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(kThinN >> 3) << 17) |
+                                     (static_cast<uint32_t>(kM >> 4) << 24);
+  static constexpr int kSumRow = MT + 1;                         // of a channel's int32 sums, padded
+  static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+  // a tile's int32 sums, and half of them once more, fit the rings
+  static_assert(kThinN * kSumRow * 4 + MT * (kThinN / 2 + 1) * 4 <= kOffBar, "sums");
+  static_assert(kM * kBK * 2 <= X + W, "the rows past MT are inside the stage");
+};
+
+__device__ __forceinline__ int ld_cluster1(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+
+template <typename O, int MT>
+__global__ void __launch_bounds__(Thin<MT>::kThreads, 1)
+k_thin(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_constant__ CUtensorMap mapx, int box,
+       int split) {
+  using C = Thin<MT>;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);
+  const uint32_t base = saddr(smem);
+  const uint32_t fullw = base + C::kOffBar, fullx = fullw + 8 * C::S, empty = fullx + 8 * C::S;
+  const uint32_t full8 = empty + 8 * C::S, empty8 = full8 + 8 * C::S8;
+  const uint32_t dfull = empty8 + 8 * C::S8, dempty = dfull + 16, fin = dempty + 16;
+  int* s_misc = reinterpret_cast<int*>(smem + C::kOffBar + 8 * (3 * C::S + 2 * C::S8 + 5));   // tmem, abort
+  volatile int* abort = s_misc + 1;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  uint32_t part;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(part));
+
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(s_misc)),
+                 "r"(C::kCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  if (tid == 0) {
+    for (int i = 0; i < C::S; ++i) {
+      mbar_init(fullw + 8 * i, C::kGroupWarps);
+      mbar_init(fullx + 8 * i, 1);
+      mbar_init(empty + 8 * i, 1);
+    }
+    for (int i = 0; i < C::S8; ++i) mbar_init(full8 + 8 * i, 1), mbar_init(empty8 + 8 * i, C::kGroupWarps);
+    for (int i = 0; i < 2; ++i) mbar_init(dfull + 8 * i, 1), mbar_init(dempty + 8 * i, C::EW);
+    mbar_init(fin, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    s_misc[1] = 0;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, static_cast<uint32_t>(s_misc[0]), 0);
+
+  auto warp_ok = [&](bool ok) {
+    ok = __all_sync(0xffffffffu, ok);
+    __syncwarp();
+    return ok;
+  };
+  auto wait = [&](uint32_t bar, uint32_t parity) { return warp_ok(lane != 0 || poll(bar, parity, abort)); };
+  auto drain = [&](uint32_t bars, uint32_t stages, const auto& r) {   // as in k_tc
+    volatile int none = 0;
+    for (uint32_t i = 0; i < stages; ++i) {
+      if (i < r.stage)
+        poll(bars + 8 * i, r.parity, &none);
+      else if (!r.first)
+        poll(bars + 8 * i, r.parity ^ 1, &none);
+    }
+  };
+
+  const int tiles = (p.N + kThinN - 1) / kThinN;
+  const int steps_all = (p.K + kBK - 1) / kBK;
+  const int s0 = static_cast<int>(static_cast<int64_t>(steps_all) * part / split);
+  const int s1 = static_cast<int>(static_cast<int64_t>(steps_all) * (part + 1) / split);
+  const int steps = s1 - s0;
+  const int tile0 = blockIdx.x / split, tile_step = gridDim.x / split;
+
+  if (warp < kEpiWarp0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    if (warp == 0 && lane == 0) {
+      // ---- int8 weights by TMA
+      Ring<C::S8> r;
+      bool ok = true;
+      for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
+        for (int k = s0; k < s1; ++k, r.next()) {
+          if (!r.first && !(ok = poll(empty8 + 8 * r.stage, r.parity ^ 1, abort))) break;
+          mbar_expect_tx(full8 + 8 * r.stage, C::W8);
+          tma_load_2d(base + C::kRing8 + r.stage * C::W8, &mapw, k * kBK, tile * kThinN, full8 + 8 * r.stage);
+        }
+      }
+      if (*abort) drain(full8, C::S8, r);
+    }
+    if (warp == 2 && lane == 0) {
+      // ---- fp16 tokens by TMA, once k_widen has written them
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      Ring<C::S> r;
+      bool ok = true;
+      for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
+        for (int k = s0; k < s1; ++k, r.next()) {
+          if (!r.first && !(ok = poll(empty + 8 * r.stage, r.parity ^ 1, abort))) break;
+          mbar_expect_tx(fullx + 8 * r.stage, box * kBK * 2);
+          tma_load_2d(base + r.stage * (C::X + C::W), &mapx, k * kBK, 0, fullx + 8 * r.stage);
+        }
+      }
+      if (*abort) drain(fullx, C::S, r);
+    }
+    if (warp == 1) {
+      // ---- MMA issue
+      Ring<C::S> r;
+      Ring<2> d;
+      bool ok = true, ready = false;
+      for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
+        for (int k = 0; k < steps && ok; d.next()) {
+          if (!d.first && !(ok = wait(dempty + 8 * d.stage, d.parity ^ 1))) break;
+          tc_fence_after();
+          const uint32_t acc = tmem + d.stage * kThinN;
+          const int end = min(steps, k + kChunk);
+          for (uint32_t more = 0; k < end; ++k) {
+            if (!ready && !(ok = wait(fullx + 8 * r.stage, r.parity) && wait(fullw + 8 * r.stage, r.parity))) break;
+            tc_fence_after();
+            const uint32_t stage = r.stage;
+            r.next();
+            ready = test_wait(fullx + 8 * r.stage, r.parity) & test_wait(fullw + 8 * r.stage, r.parity);
+            if (elect_one()) {
+              const uint64_t da = smem_desc(base + stage * (C::X + C::W)), db = da + (C::X >> 4);
+#pragma unroll
+              for (int kk = 0; kk < kBK / 16; ++kk) mma_f16(acc, da + kk * 2, db + kk * 2, C::kIdesc, more | kk);
+              mma_commit(empty + 8 * stage);
+            }
+            ready = __all_sync(0xffffffffu, ready);
+            more = 1;
+          }
+          if (ok && elect_one()) mma_commit(dfull + 8 * d.stage);
+          __syncwarp();
+        }
+      }
+      if (*abort) {   // the MMAs in flight end before the CTA does
+        if (elect_one()) {
+          volatile int none = 0;
+          mma_commit(fin);
+          poll(fin, 0, &none);
+        }
+        __syncwarp();
+      }
+    }
+    __syncwarp();
+    cta_barrier();
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
+  } else if (warp < C::kConvWarp0) {
+    // ---- accumulate and store: a token to a lane, 128 channels to a thread
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsAcc));
+    const int q = warp & 3, half = (warp - kEpiWarp0) >> 2;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * C::ACC;
+    const int t = q * 32 + lane;
+    const bool busy = q * 32 < p.T;
+    Ring<2> d;
+    bool ok = true;
+    for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
+      int acc[C::ACC];
+#pragma unroll
+      for (int i = 0; i < C::ACC; ++i) acc[i] = 0;
+      for (int k = 0; k < steps; k += kChunk, d.next()) {
+        if (!(ok = warp_ok(lane != 0 || poll<100>(dfull + 8 * d.stage, d.parity, abort)))) break;
+        tc_fence_after();
+        if (busy) {
+#pragma unroll
+          for (int c = 0; c < C::ACC; c += 16) {
+            uint32_t r[16];
+            tmem_ld16(lanes + d.stage * kThinN + c, r);
+            tmem_wait(r);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[c + i] += __float2int_rn(__uint_as_float(r[i]));
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(dempty + 8 * d.stage);
+      }
+      if (!ok) break;
+      if (!busy) continue;
+      if (split == 1) {
+        // lane l holds the scales of channels n + 4 l .. + 3 of this half
+        const int n = tile * kThinN + half * C::ACC;
+        float ws[4], bias[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const bool in = n + lane * 4 + c < p.N;
+          ws[c] = in ? __ldg(p.ws + n + lane * 4 + c) : 0.f;
+          bias[c] = in && p.bias ? to_f32<O>(static_cast<const O*>(p.bias)[n + lane * 4 + c]) : 0.f;
+        }
+        const float xs = t < p.T ? __ldg(p.xs + t) : 0.f;
+        O* out = static_cast<O*>(p.out) + t * p.ldo + n;
+        constexpr int E = 16 / sizeof(O);   // channels of a 16-byte store
+        const bool wide = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.ldo % E == 0;
+#pragma unroll
+        for (int i = 0; i < C::ACC; i += E) {
+          alignas(16) O v[E];
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const float w = __shfl_sync(0xffffffffu, ws[(i + e) % 4], (i + e) / 4);
+            const float b = __shfl_sync(0xffffffffu, bias[(i + e) % 4], (i + e) / 4);
+            v[e] = from_f32<O>(fmaf(static_cast<float>(acc[i + e]) * xs, w, b));
+          }
+          if (t < p.T) {
+            if (wide && n + i + E <= p.N) {
+              *reinterpret_cast<uint4*>(out + i) = *reinterpret_cast<const uint4*>(v);
+            } else {
+#pragma unroll
+              for (int e = 0; e < E; ++e)
+                if (n + i + e < p.N) out[i + e] = v[e];
+            }
+          }
+        }
+      } else if (t < MT) {
+        // every stage has been read: the rings take the sums, [channel][token]
+        int* sums = reinterpret_cast<int*>(smem);
+#pragma unroll
+        for (int i = 0; i < C::ACC; ++i) sums[(half * C::ACC + i) * C::kSumRow + t] = acc[i];
+      }
+    }
+    __syncwarp();
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
+    cta_barrier();
+  } else {
+    // ---- int8 to fp16
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
+    const int ctid = (tid - C::kConvWarp0 * 32) % (C::kGroupWarps * 32);
+    const int group = (warp - C::kConvWarp0) / C::kGroupWarps;
+    Ring<C::S> r;
+    Ring<C::S8> r8;
+    r.next(group);
+    r8.next(group);
+    const int64_t mine = static_cast<int64_t>(steps) * ((tiles - tile0 + tile_step - 1) / tile_step);
+    for (int64_t g = group; g < mine; g += C::kGroups, r.next(C::kGroups), r8.next(C::kGroups)) {
+      if (!wait(full8 + 8 * r8.stage, r8.parity)) break;
+      Weights<kThinN, C::kGroupWarps> w;
+      w.load(base + C::kRing8 + r8.stage * C::W8, ctid);
+      if (!r.first && !wait(empty + 8 * r.stage, r.parity ^ 1)) break;
+      w.store(base + r.stage * (C::X + C::W) + C::X, ctid);
+      proxy_fence_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(fullw + 8 * r.stage);
+        mbar_arrive(empty8 + 8 * r8.stage);   // not before the stores: the loads have then arrived for sure
+      }
+    }
+    __syncwarp();
+    cta_barrier();
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
+  }
+
+  __syncwarp();
+  if (split > 1) {
+    // the parts of one tile: each CTA adds its share of the channels, tokens
+    // side by side as they lie in the other CTAs (a warp's remote reads are then
+    // one line each), into [token][channel] behind the sums, and stores those
+    cluster_sync();
+    if (!*abort) {
+      const int share = kThinN / split, c0 = share * part;   // split is a power of two
+      int* rows = reinterpret_cast<int*>(smem) + kThinN * C::kSumRow;
+      constexpr int U = 4;   // with four parts each: 16 reads in flight together
+      for (int i0 = tid; i0 < share * MT; i0 += U * C::kThreads) {
+        int sum[U] = {};
+        for (int r0 = 0; r0 < split; r0 += 4) {
+          int v[U][4];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int i = min(i0 + u * C::kThreads, share * MT - 1);
+            const uint32_t at = base + ((c0 + i / MT) * C::kSumRow + i % MT) * 4;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[u][r] = r0 + r < split ? ld_cluster1(at, r0 + r) : 0;
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u) sum[u] += v[u][0] + v[u][1] + v[u][2] + v[u][3];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = i0 + u * C::kThreads;
+          if (i < share * MT) rows[(i % MT) * (share + 1) + i / MT] = sum[u];
+        }
+      }
+      __syncthreads();
+      const int n0 = tile0 * kThinN + c0;
+      static_assert(C::kThreads % (kThinN / 2) == 0, "a thread keeps its channel");
+      const int c = tid % share, n = n0 + c;
+      if (n < p.N) {
+        const float ws = __ldg(p.ws + n), bias = p.bias ? to_f32<O>(static_cast<const O*>(p.bias)[n]) : 0.f;
+#pragma unroll 4
+        for (int t = tid / share; t < p.T; t += C::kThreads / share)
+          store_out<O>(p, t, n, rows[t * (share + 1) + c], __ldg(p.xs + t), ws, bias);
+      }
+    }
+    cluster_sync();   // nothing of this CTA is read any more
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols));
 }
 
 // Tokens as fp16, [T][kp] with kp a multiple of 64, zero past K.
@@ -827,95 +1138,137 @@ cudaError_t map_tile(CUtensorMap* m, int size, const void* base, int64_t ld, int
 int padded_k(int K) { return (K + 63) & ~63; }
 
 
-// Clusters of `size` CTAs of k_tc<O, NT> that the device holds at once (asked
-// once per device; size 4 or 8).
-template <typename O, int NT>
-int max_clusters(int dev, int size) {
-  static std::atomic<int> known[kMaxDev][2];
-  std::atomic<int>& k = known[dev][size == 8];
-  int n = k.load(std::memory_order_relaxed);
-  if (n == 0) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(size);
-    cfg.blockDim = dim3(Tile<NT>::kThreads);
-    cfg.dynamicSmemBytes = Tile<NT>::kSmem;
-    cudaLaunchAttribute a{};
-    a.id = cudaLaunchAttributeClusterDimension;
-    a.val.clusterDim = {static_cast<unsigned>(size), 1, 1};
-    cfg.attrs = &a;
-    cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, k_tc<O, NT>, &cfg) != cudaSuccess || n < 1) {
-      cudaGetLastError();   // not fatal: K stays whole
-      n = -1;
-    }
-    k.store(n, std::memory_order_relaxed);
+// Clusters of `size` CTAs of a kernel that the device holds at once.
+template <typename K>
+int max_clusters(K* kernel, int threads, int smem, int size) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(size);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute a{};
+  a.id = cudaLaunchAttributeClusterDimension;
+  a.val.clusterDim = {static_cast<unsigned>(size), 1, 1};
+  cfg.attrs = &a;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();   // not fatal: K stays whole
+    n = 0;
   }
   return n;
 }
 
-template <typename O, int NT>
-cudaError_t launch_tc_nt(const LinArgs& p, void* ws, cudaStream_t s) {
-  using C = Tile<NT>;
-  static std::atomic<bool> ready[kMaxDev];
+// What a tensor-core kernel's launches need to know about a device, asked once.
+struct OnDevice {
+  std::atomic<bool> ready{false};
+  int clusters[4] = {};   // of 1, 2, 4 and 8 CTAs, at once
+};
+template <typename K>
+cudaError_t prepare(OnDevice* all, K* kernel, int threads, int smem, OnDevice** out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
-  if (!ready[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(k_tc<O, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  OnDevice& d = all[dev];
+  if (!d.ready.load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     cudaFuncAttributes at{};
-    if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, k_tc<O, NT>);
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, kernel);
     if (e != cudaSuccess) return e;
-    // the register split must fit what the CTA is launched with
-    if (NT == 256 && at.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
-    ready[dev].store(true, std::memory_order_release);
+    // the register split must be what the CTA is launched with
+    if (at.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
+    for (int i = 0; i < 4; ++i) d.clusters[i] = max_clusters(kernel, threads, smem, 1 << i);
+    d.ready.store(true, std::memory_order_release);
   }
-  CUtensorMap mapw, mapx;
+  *out = &d;
+  return cudaSuccess;
+}
+
+cudaError_t widen(const LinArgs& p, void* ws, cudaStream_t s) {
   const int kp = padded_k(p.K);
-  e = map_tile(&mapw, 1, p.w, p.ldw, p.N, p.K, kM);
-  if (e == cudaSuccess) e = map_tile(&mapx, 2, ws, kp * int64_t{2}, p.T, kp, C::kRowsB);
-  if (e != cudaSuccess) return e;
-  const int sms = sm_count();
   const int64_t chunks = static_cast<int64_t>(p.T) * (kp / 16);
-  k_widen<<<static_cast<unsigned>(std::min<int64_t>((chunks + 255) / 256, sms * 8)), 256, 0, s>>>(
+  k_widen<<<static_cast<unsigned>(std::min<int64_t>((chunks + 255) / 256, sm_count() * 8)), 256, 0, s>>>(
       p.x, p.ldx, p.T, p.K, kp, static_cast<__half*>(ws));
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  const int64_t tiles = static_cast<int64_t>((p.N + 2 * kM - 1) / (2 * kM)) * ((p.T + NT - 1) / NT);
-  const int steps = (p.K + kBK - 1) / kBK;
-  // K is split while all the parts still run at once: clusters of 8 fit a
-  // processing cluster's SMs less often than their number says, and a second
-  // turn costs as much as the first
-  int split = 1;
-  while (split < 4 && tiles <= max_clusters<O, NT>(dev, 4 * split) && steps >= 8 * split) split *= 2;
+  return cudaGetLastError();
+}
+
+// A launch in clusters that may start while k_widen runs: only its token loads
+// wait for k_widen, which itself started after everything before it had ended.
+template <typename... P, typename... A>
+cudaError_t launch_after_widen(void (*kernel)(P...), unsigned grid, int threads, int smem, int cluster, cudaStream_t s,
+                               A... args) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * (split > 1 ? tiles * split : std::min<int64_t>(tiles, sms / 2))));
-  cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute a[2]{};
   a[0].id = cudaLaunchAttributeClusterDimension;
-  a[0].val.clusterDim = {static_cast<unsigned>(2 * split), 1, 1};
-  // it may start while k_widen runs: only its token loads wait for k_widen,
-  // which itself started after everything before it had ended
+  a[0].val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
   a[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   a[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = a;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, k_tc<O, NT>, p, mapw, mapx, split);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Parts of K, up to 2^most: while all of them still run at once (clusters of 8
+// fit a processing cluster's SMs less often than their number says, and a
+// second turn costs as much as the first) and have eight stages or more each.
+int parts_of_k(const OnDevice& d, int64_t tiles, int steps, int first, int most) {
+  int i = 0;
+  while (i < most && tiles <= d.clusters[first + i + 1] && steps >= 16 << i) ++i;
+  return 1 << i;
+}
+
+template <typename O>
+cudaError_t launch_tc(const LinArgs& p, void* ws, cudaStream_t s) {
+  using C = Tile<256>;
+  static OnDevice all[kMaxDev];
+  OnDevice* d;
+  cudaError_t e = prepare(all, k_tc<O, 256>, C::kThreads, C::kSmem, &d);
+  CUtensorMap mapw, mapx;
+  const int kp = padded_k(p.K);
+  if (e == cudaSuccess) e = map_tile(&mapw, 1, p.w, p.ldw, p.N, p.K, kM);
+  if (e == cudaSuccess) e = map_tile(&mapx, 2, ws, kp * int64_t{2}, p.T, kp, C::kRowsB);
+  if (e == cudaSuccess) e = widen(p, ws, s);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = static_cast<int64_t>((p.N + 2 * kM - 1) / (2 * kM)) * ((p.T + 255) / 256);
+  const int split = parts_of_k(*d, tiles, (p.K + kBK - 1) / kBK, 1, 2);
+  const int64_t pairs = split > 1 ? tiles * split : std::min<int64_t>(tiles, sm_count() / 2);
+  return launch_after_widen(k_tc<O, 256>, static_cast<unsigned>(2 * pairs), C::kThreads, C::kSmem, 2 * split, s, p,
+                            mapw, mapx, split);
+}
+
+template <typename O, int MT>
+cudaError_t launch_thin(const LinArgs& p, void* ws, cudaStream_t s) {
+  using C = Thin<MT>;
+  static OnDevice all[kMaxDev];
+  OnDevice* d;
+  cudaError_t e = prepare(all, k_thin<O, MT>, C::kThreads, C::kSmem, &d);
+  CUtensorMap mapw, mapx;
+  const int kp = padded_k(p.K), box = (p.T + 7) / 8 * 8;
+  if (e == cudaSuccess) e = map_tile(&mapw, 1, p.w, p.ldw, p.N, p.K, kThinN);
+  if (e == cudaSuccess) e = map_tile(&mapx, 2, ws, kp * int64_t{2}, p.T, kp, box);
+  if (e == cudaSuccess) e = widen(p, ws, s);
+  if (e != cudaSuccess) return e;
+  const int tiles = (p.N + kThinN - 1) / kThinN;
+  const int split = parts_of_k(*d, tiles, (p.K + kBK - 1) / kBK, 0, 3);
+  return launch_after_widen(k_thin<O, MT>, static_cast<unsigned>(split > 1 ? tiles * split : std::min(tiles, sm_count())),
+                            C::kThreads, C::kSmem, split, s, p, mapw, mapx, box, split);
 }
 
 template <typename O>
 cudaError_t launch_linear(const LinArgs& p, void* ws, cudaStream_t s) {
-  if (p.T <= kInt8Tokens || (p.T <= kFewTokens && p.N < kManyChannels)) return launch_few<O>(p, s);
-  if (p.T <= 32) return launch_tc_nt<O, 32>(p, ws, s);
-  if (p.T <= 64) return launch_tc_nt<O, 64>(p, ws, s);
-  if (p.T <= 128) return launch_tc_nt<O, 128>(p, ws, s);
-  return launch_tc_nt<O, 256>(p, ws, s);
+  if (p.T <= kFewTokens || (p.T <= 32 && p.N < kManyChannels)) return launch_few<O>(p, s);
+  if (p.T <= 32) return launch_thin<O, 32>(p, ws, s);
+  if (p.T <= 64) return launch_thin<O, 64>(p, ws, s);
+  if (p.T <= 128) return launch_thin<O, 128>(p, ws, s);
+  return launch_tc<O>(p, ws, s);
 }
 
 size_t linear_ws_bytes(int T, int K) {
-  return T <= kInt8Tokens ? 0 : static_cast<size_t>(T) * padded_k(K) * 2;
+  return T <= kFewTokens ? 0 : static_cast<size_t>(T) * padded_k(K) * 2;
 }
 
 }  // namespace

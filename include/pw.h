@@ -591,7 +591,7 @@ int pw_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, c
 int pw_quant_i8(const void* x, int64_t ldx, int T, int K, int dtype, int8_t* q, int64_t ldq, float* scale,
                 pw_stream_t s);
 
-/* Bytes of device workspace that pw_linear_i8 needs: 0 up to 8 tokens, then
+/* Bytes of device workspace that pw_linear_i8 needs: 0 up to 16 tokens, then
  * the tokens as fp16.  0 for a bad shape. */
 size_t pw_linear_i8_workspace_bytes(int T, int K);
 

@@ -55,13 +55,13 @@ def _linear(**kw):
 
 
 def test_linear_workspace():
-    assert pw.pw_linear_i8_workspace_bytes(8, 4096) == 0
-    assert pw.pw_linear_i8_workspace_bytes(9, 100) == 9 * 128 * 2
+    assert pw.pw_linear_i8_workspace_bytes(16, 4096) == 0
+    assert pw.pw_linear_i8_workspace_bytes(17, 100) == 17 * 128 * 2
     assert pw.pw_linear_i8_workspace_bytes(-1, 100) == 0 and pw.pw_linear_i8_workspace_bytes(4, 0) == 0
-    assert _linear(T=9) == pw.PW_ENOMEM
-    assert _linear(T=9, sp=P, sb=9 * 128 - 1) == pw.PW_ENOMEM
-    assert _linear(T=9, sp=None, sb=1 << 20) == pw.PW_ENOMEM
-    assert _linear(T=9, sp=P + 16, sb=1 << 20) == pw.PW_EINVAL
+    assert _linear(T=17) == pw.PW_ENOMEM
+    assert _linear(T=17, sp=P, sb=17 * 128 - 1) == pw.PW_ENOMEM
+    assert _linear(T=17, sp=None, sb=1 << 20) == pw.PW_ENOMEM
+    assert _linear(T=17, sp=P + 16, sb=1 << 20) == pw.PW_EINVAL
 
 
 @pytest.mark.parametrize("kw", [
