@@ -96,35 +96,84 @@ __device__ __forceinline__ void block_reduce(float& a, float& b, float2* sh) {
   b = warp_max(v.y);
 }
 
-// Factors of a row's outputs, v = s * w: y = v * rstd; q = v * steps, rounded,
-// with v first times 2^100 where the row's largest value is so small that
-// 127 / max overflows.  Rows without a step (zeros, NaN, infinities) have q 0.
+// Factors of a row's outputs, v = s * w: y = v * rstd; q = 127 v / max, rounded,
+// with v and max first times `up` where max is so small or large that a factor
+// or product would leave fp32's range.  Rows without a step (zeros, NaN,
+// infinities) have q 0.
 struct RowScale {
-  float rstd, steps, scale;
-  bool tiny, none;
+  float rstd, scale, steps;
+  float amax, inv, up;
+  bool far, none;
 };
 template <bool NORM>
 __device__ __forceinline__ RowScale row_scale(float ss, float amax, int H, float eps) {
   RowScale f;
   f.rstd = NORM ? 1.f / sqrtf(ss / static_cast<float>(H) + eps) : 1.f;
-  f.tiny = amax < 0x1p-100f;
   f.none = !(amax > 0.f && amax < INFINITY);
-  f.steps = 127.f / (f.tiny ? amax * 0x1p100f : amax);
-  f.scale = amax * f.rstd / 127.f;
+  f.up = amax < 0x1p-100f ? 0x1p100f : amax > 0x1p100f ? 0x1p-100f : 1.f;
+  f.far = f.up != 1.f;
+  f.amax = amax * f.up;
+  if (NORM)
+    f.steps = 127.f / f.amax;
+  else
+    f.inv = __frcp_rn(f.amax);
+  f.scale = amax * f.rstd;   // times 1 / 127, by the thread that stores it
   return f;
 }
 
-// v * steps rounded to the nearest whole number (ties to even), in the low byte:
-// 1.5 * 2^23 is added, above which fp32 holds whole numbers only.
-__device__ __forceinline__ uint32_t to_step(const RowScale& f, float v) {
-  return __float_as_uint(fmaf(v, f.steps, 12582912.f));
+// Two fp32 numbers in one operation.
+__device__ __forceinline__ uint64_t pair2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
-template <int VE>
+// The steps of two values rounded to the nearest whole number (ties to even), in
+// the low bytes: 1.5 * 2^23 is added, above which fp32 holds whole numbers only.
+// Where v is an input itself (not NORM), ties are common (16-bit inputs have few
+// digits), so the quotient 127 v / max is brought to within a rounding: 127 v is
+// exact for 16-bit inputs, and one correction by the remainder makes a quotient
+// that is a half come out as a half.
+template <bool NORM>
+__device__ __forceinline__ void to_steps(const RowScale& f, float va, float vb, uint32_t& a, uint32_t& b) {
+  const uint64_t magic = pair2(12582912.f, 12582912.f), v = pair2(va, vb);
+  uint64_t r;
+  if (NORM) {
+    r = fma2(v, pair2(f.steps, f.steps), magic);
+  } else {
+    const uint64_t inv = pair2(f.inv, f.inv), t = mul2(v, pair2(127.f, 127.f)), q = mul2(t, inv);
+    r = add2(fma2(fma2(q, pair2(-f.amax, -f.amax), t), inv, q), magic);
+  }
+  a = static_cast<uint32_t>(r);
+  b = static_cast<uint32_t>(r >> 32);
+}
+
+template <int VE, bool NORM>
 __device__ __forceinline__ void store_q(int8_t* row, int e0, int H, const float (&v)[VE], const RowScale& f) {
   uint32_t b[VE];
+  auto at = [&](int i) { return f.far ? v[i] * f.up : v[i]; };
+  if constexpr (VE == 1) {
+    const float v0 = at(0), t = v0 * 127.f, q = t * f.inv;
+    b[0] = __float_as_uint(NORM ? fmaf(v0, f.steps, 12582912.f) : fmaf(fmaf(-q, f.amax, t), f.inv, q) + 12582912.f);
+  } else {
 #pragma unroll
-  for (int i = 0; i < VE; ++i) b[i] = to_step(f, f.tiny ? v[i] * 0x1p100f : v[i]);
+    for (int i = 0; i < VE; i += 2) to_steps<NORM>(f, at(i), at(i + 1), b[i], b[i + 1]);
+  }
   if (f.none) {
 #pragma unroll
     for (int i = 0; i < VE; ++i) b[i] = 0;
@@ -177,8 +226,8 @@ __device__ __forceinline__ void finish_row(const RowArgs& p, int64_t row, float 
   }
   if (p.q) {
 #pragma unroll
-    for (int c = 0; c < VPT; ++c) store_q<VE>(p.q + row * p.ldq, at(c), H, v[c], f);
-    if (threadIdx.x == 0) p.scale[row] = f.scale;
+    for (int c = 0; c < VPT; ++c) store_q<VE, NORM>(p.q + row * p.ldq, at(c), H, v[c], f);
+    if (threadIdx.x == 0) p.scale[row] = f.scale / 127.f;
   }
 }
 
@@ -315,9 +364,9 @@ __global__ void __launch_bounds__(1024, 1) k_rows_long(const RowArgs p) {
       v[i] = s[i] * f.rstd;
     }
     if (p.y) store_chunk<T, VE>(static_cast<T*>(p.y) + row * p.ldy, e0, H, v);
-    if (p.q) store_q<VE>(p.q + row * p.ldq, e0, H, s, f);
+    if (p.q) store_q<VE, NORM>(p.q + row * p.ldq, e0, H, s, f);
   }
-  if (p.q && threadIdx.x == 0) p.scale[row] = f.scale;
+  if (p.q && threadIdx.x == 0) p.scale[row] = f.scale / 127.f;
 }
 
 template <typename T, int VE, int VPT, bool NORM>
