@@ -15,6 +15,7 @@ never call it.
 Modules:
   apl    -- bit-plane pack/unpack, child LUTs, dequantisation
   moe    -- routing, permutation, expert MLP, combine, whole layer
+  operators -- norm, row quantiser, int8 product, log probabilities
 
 Parity status: every function here is pinned by tests/test_oracle_*.py
 (hand-derived golden fixtures, closed forms, invariants, brute force and
