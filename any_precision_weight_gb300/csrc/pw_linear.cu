@@ -18,6 +18,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <cmath>
 #include <atomic>
 
 #include "pw_rows.cuh"
@@ -144,8 +145,9 @@ struct FewSums {
 };
 
 constexpr int kFewWarps = 8;
-// k_few against k_thin, K = 4096, us: 16 tokens 6.5 and 18 at N = 4096, 30 and 37
-// at 28672, 126 and 122 at 131072; 32 tokens 10 and 18 at 4096, 27 and 26 at
+constexpr int few_ctas(bool ahead) { return ahead ? 2 : 3; }   // of an SM
+// k_few against k_thin, K = 4096, us: 16 tokens 6.7 and 18 at N = 4096, 28 and 37
+// at 28672, 115 and 122 at 131072; 32 tokens 10 and 18 at 4096, 26 and 26 at
 // 14336, 48 and 37 at 28672.
 constexpr int kFewTokens = 16;
 constexpr int kManyChannels = 14336;   // from which 17 to 32 tokens take k_thin
@@ -155,15 +157,20 @@ constexpr int kManyChannels = 14336;   // from which 17 to 32 tokens take k_thin
 // channels g and g + 8, and of token g of every 8: the operand registers of its
 // products, with the columns of K in an order of their own that both operands
 // share.  So the weights go from memory to the tensor cores through registers
-// alone, 64 bytes of a channel at a time.  NT: groups of 8 tokens.  One group
-// has the registers for three CTAs of an SM, and their other warps' loads are
-// in flight while one multiplies (28672 x 4096, one token: 22.5 us; 26 us with
-// the next U runs loaded ahead by two CTAs); more groups load ahead.
-template <typename O, int NT>
-__global__ void __launch_bounds__(kFewWarps * 32, NT == 1 ? 3 : 2) k_few(const LinArgs p, int kw) {
+// alone, 64 bytes of a channel at a time (128 at a time, in loads of 32 bytes,
+// was no faster).  NT: groups of 8 tokens.  The loads in flight come from three
+// CTAs of an SM, whose other warps load while one multiplies, or from two that
+// fetch their next U runs ahead (AHEAD).  One token, 28672 x 4096: 21.7 us,
+// 80 % of the copy rate, and 25.2 with AHEAD; what is left there is the launch
+// and the ramps, 131072 channels run at 93 %.  16 tokens, 131072 x 4096: 115 us,
+// 69 %; the conversions of weights and tokens to fp16 (20 instructions for each
+// 16 bytes) and the products take half of the issue slots and the warps wait
+// for operands in the other half.  Two groups of channels to a warp, so that
+// a token is converted for 32, came to 113 us, with the small sizes slower.
+template <typename O, int NT, bool AHEAD>
+__global__ void __launch_bounds__(kFewWarps * 32, few_ctas(AHEAD)) k_few(const LinArgs p, int kw) {
   constexpr int kRow = NT * 8 + 1;   // padded against bank conflicts
   constexpr int U = NT == 1 ? 4 : 2;
-  constexpr bool kAhead = NT > 1;
   __shared__ int s_part[kFewWarps][16 * kRow];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int groups = kFewWarps / kw, turn = warp % kw;
@@ -188,9 +195,9 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 ? 3 : 2) k_few(const L
     }
   };
   int k = r0;
-  if (kAhead && k < last) fetch(k);
+  if (AHEAD && k < last) fetch(k);
   for (; k < last; k += U) {
-    if (!kAhead) fetch(k);
+    if (!AHEAD) fetch(k);
     uint4 ca[U], cb[U], v[U][NT];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -199,7 +206,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 ? 3 : 2) k_few(const L
 #pragma unroll
       for (int j = 0; j < NT; ++j) v[u][j] = __ldg(reinterpret_cast<const uint4*>(x[j] + (k + u) * 64));
     }
-    if (kAhead && k + U < last) fetch(k + U);
+    if (AHEAD && k + U < last) fetch(k + U);
 #pragma unroll
     for (int u = 0; u < U; ++u) sums.add(ca[u], cb[u], v[u], k - r0 + u);
   }
@@ -230,25 +237,35 @@ __global__ void __launch_bounds__(kFewWarps * 32, NT == 1 ? 3 : 2) k_few(const L
   }
 }
 
-template <typename O, int NT>
+// How many warps share a group's K: the count that leaves the least of the last
+// wave of CTAs idle, each doubling charged 6 % for its shorter loops and longer
+// joins, each warp with two runs or more.  T = 1, N = 131072, K = 4096: 94.5 us
+// with one warp (2.2 waves), 84.7 with four (9.0 waves, 6.3 TB/s, 93 % of the
+// copy rate); at 28672 two of 1, 2, 4, 8: 26.9, 21.7, 22.0, 24.0.
+template <typename O, int NT, bool AHEAD>
 cudaError_t launch_few_nt(const LinArgs& p, cudaStream_t s) {
-  // enough warps to fill the GPU, each with two runs or more: one to 16
-  // channels where there are many (the CTA's warps then share the tokens in
-  // the L1), up to eight where there are few
-  const int groups = (p.N + 15) / 16, runs = (p.K + 63) / 64;
+  const int groups = (p.N + 15) / 16, runs = (p.K + 63) / 64, slots = sm_count() * few_ctas(AHEAD);
   int kw = 1;
-  while (kw < kFewWarps && groups * kw < sm_count() * (NT == 1 ? 16 : 24) && runs >= 4 * kw) kw *= 2;
+  float least = 0.f;
+  for (int n = 1, i = 0; n <= kFewWarps && (n == 1 || runs >= 2 * n); n *= 2, ++i) {
+    const float waves = static_cast<float>(groups) * n / (kFewWarps * slots);
+    const float cost = std::ceil(waves) / waves * (1.f + 0.06f * i);
+    if (n == 1 || cost < least) kw = n, least = cost;
+  }
   const int per = kFewWarps / kw;
-  k_few<O, NT><<<(groups + per - 1) / per, kFewWarps * 32, 0, s>>>(p, kw);
+  k_few<O, NT, AHEAD><<<(groups + per - 1) / per, kFewWarps * 32, 0, s>>>(p, kw);
   return cudaGetLastError();
 }
 
 template <typename O>
 cudaError_t launch_few(const LinArgs& p, cudaStream_t s) {
-  if (p.T <= 8) return launch_few_nt<O, 1>(p, s);
-  if (p.T <= 16) return launch_few_nt<O, 2>(p, s);
-  if (p.T <= 24) return launch_few_nt<O, 3>(p, s);
-  return launch_few_nt<O, 4>(p, s);
+  if (p.T <= 8) return launch_few_nt<O, 1, false>(p, s);
+  // 16 tokens, K = 4096, two CTAs loading ahead against three, us: N = 4096 6.7
+  // and 7.4, 8192 10.6 and 12.6, 14336 17.6 and 15.7, 131072 118.6 and 115
+  if (p.T <= 16)
+    return (p.N + 15) / 16 <= 4 * sm_count() ? launch_few_nt<O, 2, true>(p, s) : launch_few_nt<O, 2, false>(p, s);
+  if (p.T <= 24) return launch_few_nt<O, 3, true>(p, s);
+  return launch_few_nt<O, 4, true>(p, s);
 }
 
 // ---------------------------------------------------------------- tensor cores
