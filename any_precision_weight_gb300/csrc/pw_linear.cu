@@ -5,9 +5,9 @@
 //
 // the sum exact in int32 (K <= 131071: 128 * 128 * K < 2^31).
 //
-// Up to 32 tokens: k_few, tensor-core products fed from registers, the weights
-// streamed once.  More tokens: k_tc on the 5th-generation tensor
-// cores.  This GPU's int8 tensor rate is a small part of its 16-bit rate, and
+// Few tokens: k_few, tensor-core products fed from registers, the weights
+// streamed once.  Up to 128 and more: k_thin and k_tc on the 5th-generation
+// tensor cores.  This GPU's int8 tensor rate is a small part of its 16-bit rate, and
 // tcgen05 has no int8 kind here, so that work runs in fp16: int8 values are
 // exact in fp16, their products (at most 2^14) are exact in fp32, and so are
 // sums of up to 1024 of them (2^24).  Every 1024 terms the fp32 accumulator
@@ -20,6 +20,7 @@
 #include <algorithm>
 #include <cmath>
 #include <atomic>
+#include <mutex>
 
 #include "pw_rows.cuh"
 #include "pw_tc.cuh"
@@ -291,6 +292,14 @@ cudaError_t launch_few(const LinArgs& p, cudaStream_t s) {
 // here too made 1025 of its clocks for the 512 of a 128 x 256 x 64 step.
 // Where there are few tiles a cluster of CTAs splits K and adds the parts
 // through distributed shared memory; whole numbers, so in any order.
+//
+// 28672 x 4096 weights: 1024, 2048, 4096 tokens in 149, 292 and 573 us (1617 to
+// 1678 TFLOP/s, 86 to 89 % of the 16-bit library product in isolation, and near
+// its rate in a long run: the power limit is in reach).  2048 x 4096 x 14336:
+// 177 us, 1360 TFLOP/s, because 128 tiles are 1.7 turns of 76 pairs; 333 x 5003 x
+// 1411: 19 us, a chain of k_widen, 23 stages, the joins and the stores.  One CTA
+// to a tile, converting the tokens too, took 238 us of the 177; tiles of 128
+// channels to a pair of issuers, or two stages to a barrier, gained nothing.
 constexpr int kM = 128;
 constexpr int kBK = 64;         // K columns of a stage: a 128-byte row of fp16
 constexpr int kConvWarps = 8;
@@ -299,8 +308,8 @@ constexpr int kGroupWarps = kConvWarps / kGroups;
 constexpr int kChunk = 1024 / kBK;   // stages that fp32 adds exactly: 2^24 / 2^14 products
 constexpr int kEpiWarp0 = 4;
 
-template <int NT>
 struct Tile {
+  static constexpr int NT = 256;
   static constexpr int EW = 8;                            // accumulating warps
   static constexpr int ACC = NT / (EW / 4);               // int32 sums of one of their threads
   static constexpr int kConvWarp0 = kEpiWarp0 + EW;
@@ -321,7 +330,7 @@ struct Tile {
   static_assert(kM * NT * 4 <= kRing8, "a CTA's int32 sums fit the operand ring");
 };
 
-// Registers by role for NT = 256, whose accumulating threads hold 128 sums:
+// Registers by role; the accumulating threads hold 128 sums:
 // 640 threads are launched with kRegsLaunch each; 128 * (32 + 2 * 160 + 2 * 64)
 // = 640 * 96 = 61440.  Every role returns to kRegsLaunch at its end: the
 // accumulating warps give theirs back before a CTA barrier, the others take
@@ -477,10 +486,11 @@ struct Ring {
   }
 };
 
-template <typename O, int NT>
-__global__ void __launch_bounds__(Tile<NT>::kThreads, 1)
+template <typename O>
+__global__ void __launch_bounds__(Tile::kThreads, 1)
 k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_constant__ CUtensorMap mapx, int split) {
-  using C = Tile<NT>;
+  using C = Tile;
+  constexpr int NT = C::NT;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);
   const uint32_t base = saddr(smem);
@@ -549,9 +559,8 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
   const int tile0 = blockIdx.x / (2 * split), tile_step = gridDim.x / (2 * split);
   auto channel0 = [&](int tile) { return ((tile % ntn) * 2 + static_cast<int>(side)) * kM; };
 
-  constexpr bool kSplitRegs = NT == 256;
   if (warp < kEpiWarp0) {
-    if constexpr (kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
     if (warp == 0 && lane == 0) {
       // ---- int8 weights by TMA
       Ring<C::S8> r;
@@ -633,13 +642,11 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
       }
     }
     __syncwarp();
-    if constexpr (kSplitRegs) {
-      cta_barrier();
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
-    }
+    cta_barrier();
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
   } else if (warp < C::kConvWarp0) {
     // ---- accumulate and store
-    if constexpr (kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsAcc));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsAcc));
     const int q = warp & 3, half = (warp - kEpiWarp0) >> 2;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * C::ACC;
     Ring<2> d;
@@ -691,13 +698,11 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
       }
     }
     __syncwarp();
-    if constexpr (kSplitRegs) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
-      cta_barrier();
-    }
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
+    cta_barrier();
   } else {
     // ---- int8 to fp16
-    if constexpr (kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsConv));
     const int ctid = (tid - C::kConvWarp0 * 32) % (kGroupWarps * 32);
     const int group = (warp - C::kConvWarp0) / kGroupWarps;
     Ring<C::S> r;
@@ -719,10 +724,8 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
       }
     }
     __syncwarp();
-    if constexpr (kSplitRegs) {
-      cta_barrier();
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
-    }
+    cta_barrier();
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
   }
 
   __syncwarp();
@@ -787,7 +790,12 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
 // channels (N).  Roles and rings as in k_tc, without the pair: half the MMAs
 // for the same weights.  MT: tokens that a stage has room for; the MMA reads
 // 128 rows, the ones past MT from the weights behind them, into lanes that
-// nobody reads.  Bound by HBM, and by the conversion close behind.
+// nobody reads.  What bounds it is the shared-memory data pipe: a stage of 256
+// channels x 64 columns goes in by TMA (16 KB), out for conversion, in again as
+// fp16 (32 KB) and out to the MMA, 750 of its clocks with the tokens, and with
+// the barriers' latencies about 1100 were taken.  28672 x 4096 weights: 37, 42
+// and 44 us for 32, 64 and 128 tokens (43 % of the copy rate at 64); k_tc takes
+// 57 for 129 to 256.
 constexpr int kThinN = 256;
 template <int MT>
 struct Thin {
@@ -1188,6 +1196,10 @@ cudaError_t prepare(OnDevice* all, K* kernel, int threads, int smem, OnDevice** 
   if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
   OnDevice& d = all[dev];
   if (!d.ready.load(std::memory_order_acquire)) {
+    static std::mutex asking;
+    const std::lock_guard<std::mutex> lock(asking);
+    *out = &d;
+    if (d.ready.load(std::memory_order_relaxed)) return cudaSuccess;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     cudaFuncAttributes at{};
     if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, kernel);
@@ -1240,10 +1252,10 @@ int parts_of_k(const OnDevice& d, int64_t tiles, int steps, int first, int most)
 
 template <typename O>
 cudaError_t launch_tc(const LinArgs& p, void* ws, cudaStream_t s) {
-  using C = Tile<256>;
+  using C = Tile;
   static OnDevice all[kMaxDev];
   OnDevice* d;
-  cudaError_t e = prepare(all, k_tc<O, 256>, C::kThreads, C::kSmem, &d);
+  cudaError_t e = prepare(all, k_tc<O>, C::kThreads, C::kSmem, &d);
   CUtensorMap mapw, mapx;
   const int kp = padded_k(p.K);
   if (e == cudaSuccess) e = map_tile(&mapw, 1, p.w, p.ldw, p.N, p.K, kM);
@@ -1253,7 +1265,7 @@ cudaError_t launch_tc(const LinArgs& p, void* ws, cudaStream_t s) {
   const int64_t tiles = static_cast<int64_t>((p.N + 2 * kM - 1) / (2 * kM)) * ((p.T + 255) / 256);
   const int split = parts_of_k(*d, tiles, (p.K + kBK - 1) / kBK, 1, 2);
   const int64_t pairs = split > 1 ? tiles * split : std::min<int64_t>(tiles, sm_count() / 2);
-  return launch_after_widen(k_tc<O, 256>, static_cast<unsigned>(2 * pairs), C::kThreads, C::kSmem, 2 * split, s, p,
+  return launch_after_widen(k_tc<O>, static_cast<unsigned>(2 * pairs), C::kThreads, C::kSmem, 2 * split, s, p,
                             mapw, mapx, split);
 }
 
@@ -1314,9 +1326,9 @@ int pw_linear_i8(const int8_t* x, int64_t ldx, const float* x_scale, const int8_
                  const float* w_scale, const void* bias, int T, int N, int K, int out_dtype, void* out, int64_t ldo,
                  void* workspace, size_t ws_bytes, pw_stream_t s) {
   pw::NvtxCall nvtx_range("pw_linear_i8");
-  if (T < 0 || N < 1 || K < 1 || K > PW_MAX_K_I8)
-    return pw::failf(PW_EINVAL, "pw_linear_i8: need T >= 0, N >= 1, 1 <= K <= %d (T %d, N %d, K %d)", PW_MAX_K_I8, T,
-                     N, K);
+  if (T < 0 || T > PW_MAX_VOCAB || N < 1 || N > PW_MAX_VOCAB || K < 1 || K > PW_MAX_K_I8)
+    return pw::failf(PW_EINVAL, "pw_linear_i8: need 0 <= T <= %d, 1 <= N <= %d, 1 <= K <= %d (T %d, N %d, K %d)",
+                     PW_MAX_VOCAB, PW_MAX_VOCAB, PW_MAX_K_I8, T, N, K);
   if (!pw::dtype_ok(out_dtype)) return pw::failf(PW_EINVAL, "pw_linear_i8: unknown out_dtype %d", out_dtype);
   if (T == 0) return PW_OK;
   if (!x || !x_scale || !w || !w_scale || !out) return pw::failf(PW_EINVAL, "pw_linear_i8: null x, w, scales or out");

@@ -430,7 +430,8 @@ int pw_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, c
                 int T, int H, int dtype, void* sum_out, int64_t lds, void* y, int64_t ldy, int8_t* q, int64_t ldq,
                 float* scale, pw_stream_t s) {
   pw::NvtxCall nvtx_range("pw_rms_norm");
-  if (T < 0 || H < 1) return pw::failf(PW_EINVAL, "pw_rms_norm: need T >= 0 and H >= 1 (T %d, H %d)", T, H);
+  if (T < 0 || H < 1 || H > PW_MAX_VOCAB)
+    return pw::failf(PW_EINVAL, "pw_rms_norm: need T >= 0 and 1 <= H <= %d (T %d, H %d)", PW_MAX_VOCAB, T, H);
   if (!pw::dtype_ok(dtype)) return pw::failf(PW_EINVAL, "pw_rms_norm: unknown dtype %d", dtype);
   if (!(eps >= 0.f)) return pw::failf(PW_EINVAL, "pw_rms_norm: eps must not be negative or NaN");
   if (T == 0) return PW_OK;
@@ -450,7 +451,8 @@ int pw_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, c
 int pw_quant_i8(const void* x, int64_t ldx, int T, int K, int dtype, int8_t* q, int64_t ldq, float* scale,
                 pw_stream_t s) {
   pw::NvtxCall nvtx_range("pw_quant_i8");
-  if (T < 0 || K < 1) return pw::failf(PW_EINVAL, "pw_quant_i8: need T >= 0 and K >= 1 (T %d, K %d)", T, K);
+  if (T < 0 || K < 1 || K > PW_MAX_VOCAB)
+    return pw::failf(PW_EINVAL, "pw_quant_i8: need T >= 0 and 1 <= K <= %d (T %d, K %d)", PW_MAX_VOCAB, T, K);
   if (!pw::dtype_ok(dtype)) return pw::failf(PW_EINVAL, "pw_quant_i8: unknown dtype %d", dtype);
   if (T == 0) return PW_OK;
   if (!x || !q || !scale) return pw::failf(PW_EINVAL, "pw_quant_i8: null x, q or scale");

@@ -557,7 +557,8 @@ int pw_profile_attach(void* const* events, int n_events);
 
 #define PW_MAX_K_I8 131071   /* longest row of pw_linear_i8: its int32 sums cannot overflow */
 #define PW_MAX_TOP  32       /* most alternatives of pw_logprobs */
-#define PW_MAX_VOCAB (1 << 30)  /* longest row of pw_logprobs */
+#define PW_MAX_VOCAB (1 << 30)  /* longest row of pw_logprobs, pw_rms_norm and
+                                   pw_quant_i8; most rows and channels of pw_linear_i8 */
 
 /*
  * pw_rms_norm -- root-mean-square norm of rows, with the residual's addition.

@@ -19,7 +19,7 @@ def _norm(**kw):
     dict(T=-1), dict(H=0), dict(dt=3), dict(dt=-1), dict(eps=-1e-6), dict(eps=float("nan")), dict(x=None),
     dict(w=None), dict(y=None), dict(q=P, ldq=64), dict(ldx=63), dict(r=P, ldr=63), dict(sum=P, lds=63),
     dict(ldy=63), dict(q=P, ldq=63, scale=P), dict(x=P + 1), dict(dt=pw.PW_F32, y=P + 2), dict(w=P + 1),
-    dict(q=P, ldq=64, scale=P + 2)])
+    dict(q=P, ldq=64, scale=P + 2), dict(H=(1 << 30) + 1, ldx=1 << 31, ldy=1 << 31)])
 def test_norm_refuses(kw):
     assert _norm(**kw) == pw.PW_EINVAL
     assert b"pw_rms_norm" in pw.lib().pw_last_error()
@@ -27,7 +27,7 @@ def test_norm_refuses(kw):
 
 @pytest.mark.parametrize("kw", [
     dict(T=-1), dict(K=0), dict(dt=9), dict(x=None), dict(q=None), dict(scale=None), dict(ldx=31), dict(ldq=31),
-    dict(x=P + 1), dict(scale=P + 1)])
+    dict(x=P + 1), dict(scale=P + 1), dict(K=(1 << 30) + 1, ldx=1 << 31, ldq=1 << 31)])
 def test_quant_refuses(kw):
     a = dict(x=P, ldx=32, T=2, K=32, dt=pw.PW_F16, q=P, ldq=32, scale=P)
     a.update(kw)
@@ -40,7 +40,7 @@ def test_quant_refuses(kw):
     dict(T=-1), dict(N=0), dict(K=0), dict(K=pw.MAX_K_I8 + 1, ldx=1 << 20, ldw=1 << 20), dict(dt=3), dict(x=None),
     dict(xs=None), dict(w=None), dict(ws=None), dict(out=None), dict(ldx=48), dict(ldw=48), dict(ldo=7),
     dict(x=P + 8), dict(w=P + 8), dict(ldx=72), dict(ldw=72), dict(out=P + 1), dict(bias=P + 1), dict(xs=P + 2),
-    dict(ws=P + 1)])
+    dict(ws=P + 1), dict(N=(1 << 30) + 1, ldo=1 << 31), dict(T=(1 << 30) + 1, sp=P, sb=1 << 62)])
 def test_linear_refuses(kw):
     assert _linear(**kw) == pw.PW_EINVAL
     assert b"pw_linear_i8" in pw.lib().pw_last_error()
