@@ -19,7 +19,9 @@
 //
 // Bound by HBM for many rows of 32-bit logits; 16-bit logits are near the
 // issue rate, hence the paired arithmetic (f32x2, and 16-bit pairs for maxima
-// and comparisons).
+// and comparisons).  2048 x 131072: fp16 without alternatives 88 us, 6.1 TB/s,
+// 90 % of the copy rate; bf16 with 20 of them 112 us, 4.8 TB/s, 70 %.  One row of
+// 131072 fp32, 5 alternatives: 6.6 us of latencies.
 
 #include <cmath>
 
@@ -577,7 +579,9 @@ __global__ void __launch_bounds__(kThreads, 4) k_logprobs(const LogArgs p, int s
 
 template <typename T, bool TOP>
 cudaError_t launch_top(const LogArgs& p, int T_, cudaStream_t s) {
-  // as many CTAs to a row as give every SM one, each with some 2048 elements
+  // a row is split until every SM has a CTA, each with 2048 elements or more;
+  // until every SM has two was slower (33 x 50001 fp16, 32 alternatives: 7.8 and
+  // 9.6 us; 256 x 32000: 10.7 and 12.9)
   const int sms = sm_count();
   int split = 1;
   while (split < kMaxCluster && static_cast<int64_t>(T_) * split < sms && p.V >= 4096 * split) split *= 2;
