@@ -178,6 +178,28 @@ def test_quant(T, K, dt):
     check_q(q, s, f64(x), 2 * U)
 
 
+@pytest.mark.parametrize("T,K", [(3, 1411), (4, 4096), (2, 14336), (500, 512), (2, 70000)])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_quant_of_16_bit_rows_rounds_as_the_quotient_does(T, K, dt):
+    # In whole numbers, halves to even.  No tolerance: a quotient 127 a / b of
+    # numbers of 11 digits that is no half lies q 2^-19 or more from one, and the
+    # kernel's, rounded once from a factor of twice fp32's digits, within q 2^-23.
+    rng = gen(T, K, dt, "halves")
+    x = rng.normal(0, 5, (T, K))
+    x[np.abs(x) < 2.0 ** -6] = 0
+    x[0, :K // 2] = rng.integers(-254, 255, K // 2) / 2     # every quotient a whole number or a half
+    x[0, 0], x[0, K // 2:] = 127, 0
+    x = place(x, DT[dt])
+    q, _ = pw.pw_quant_i8(x)
+    n = np.round(f64(x) * 2 ** 24).astype(np.int64)         # exact: 2^-24 divides every value
+    a = np.abs(n)
+    den = 2 * a.max(1, keepdims=True)
+    num = 254 * a + den // 2
+    want = num // den
+    want -= (num % den == 0) & (want % 2 == 1)
+    assert (q.cpu().numpy() == np.sign(n) * want).all()
+
+
 def test_quant_extremes():
     x = torch.zeros(6, 64, device="cuda")
     x[0, 3], x[0, 4] = 1e-38, -0.5e-38          # 127 / max overflows fp32
