@@ -272,7 +272,7 @@ cudaError_t launch_few(const LinArgs& p, cudaStream_t s) {
 // ---------------------------------------------------------------- tensor cores
 
 // k_widen writes the tokens as fp16 into the workspace; then one CTA per SM
-// takes tiles of 256 channels (M, the weights) x NT tokens (N) with another.
+// takes tiles of 256 channels (M, the weights) x up to NT tokens (N) with another.
 // Warps by role:
 //  * warp 0 fetches int8 weights by TMA into a ring of S8 stages, warp 2 the
 //    fp16 tokens into the operand ring of S stages;
@@ -287,19 +287,22 @@ cudaError_t launch_few(const LinArgs& p, cudaStream_t s) {
 // channels and half of the tokens, so a stage of 256 tokens brings 24 KB to an
 // SM instead of 40 (at 40 the L2 was the bound, about 9.6 TB/s), and one issue
 // serves two SMs.  The even CTA issues the MMAs for both.
-// What else bounds it is the shared-memory data pipe (128 bytes a clock), which the
-// tensor cores' operand reads share with the conversion: converting the tokens
-// here too made 1025 of its clocks for the 512 of a 128 x 256 x 64 step.
+// What bounds it at 256 tokens are two things alike: those 24 KB at the L2's rate
+// (790 clocks a stage) and the shared-memory data pipe (128 bytes a clock), which
+// the tensor cores' operand reads (48 KB) share with the conversion (24 KB) and
+// the copies (24 KB): 768 of its clocks for 512 of MMA.  Converting the tokens
+// here too made 1025.
 // Where there are few tiles a cluster of CTAs splits K and adds the parts
 // through distributed shared memory; whole numbers, so in any order.
 //
-// 28672 x 4096 weights: 1024, 2048, 4096 tokens in 149, 292 and 573 us (1617 to
+// 28672 x 4096 weights: 1024, 2048, 4096 tokens in 149, 290 and 573 us (1617 to
 // 1678 TFLOP/s, 86 to 89 % of the 16-bit library product in isolation, and near
 // its rate in a long run: the power limit is in reach).  2048 x 4096 x 14336:
-// 177 us, 1360 TFLOP/s, because 128 tiles are 1.7 turns of 76 pairs; 333 x 5003 x
-// 1411: 19 us, a chain of k_widen, 23 stages, the joins and the stores.  One CTA
-// to a tile, converting the tokens too, took 238 us of the 177; tiles of 128
-// channels to a pair of issuers, or two stages to a barrier, gained nothing.
+// 177 us, 1360 TFLOP/s, 128 tiles in two turns of 76 pairs.  333 x 5003 x 1411:
+// 19 us, a chain of k_widen, 23 stages, the joins and the stores.  One CTA to a
+// tile, converting the tokens too, took 238 us of the 177; two issuers, or two
+// stages to a barrier, gained nothing; the last two turns' tiles cut into equal
+// runs of K gave 171, and 160 instead of 153 at 1024 x 28672 x 4096.
 constexpr int kM = 128;
 constexpr int kBK = 64;         // K columns of a stage: a 128-byte row of fp16
 constexpr int kConvWarps = 8;
@@ -324,8 +327,9 @@ struct Tile {
   static constexpr int kSmem = kOffBar + 8 * (3 * S + 2 * S8 + 6) + 16 + 1024;
   static constexpr uint32_t kCols = 2 * NT;
   // D f32, A and B f16, N / 8 and M / 16
-  static constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(NT >> 3) << 17) |
-                                     (static_cast<uint32_t>(2 * kM >> 4) << 24);
+  __host__ __device__ static constexpr uint32_t idesc(int n) {
+    return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(2 * kM >> 4) << 24);
+  }
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
   static_assert(kM * NT * 4 <= kRing8, "a CTA's int32 sums fit the operand ring");
 };
@@ -488,7 +492,8 @@ struct Ring {
 
 template <typename O>
 __global__ void __launch_bounds__(Tile::kThreads, 1)
-k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_constant__ CUtensorMap mapx, int split) {
+k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_constant__ CUtensorMap mapx, int nt,
+     int split) {
   using C = Tile;
   constexpr int NT = C::NT;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -550,7 +555,7 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
     }
   };
 
-  const int ntn = (p.N + 2 * kM - 1) / (2 * kM), ntt = (p.T + NT - 1) / NT;
+  const int ntn = (p.N + 2 * kM - 1) / (2 * kM), ntt = (p.T + nt - 1) / nt;
   const int tiles = ntn * ntt;
   const int steps_all = (p.K + kBK - 1) / kBK;
   const int s0 = static_cast<int>(static_cast<int64_t>(steps_all) * part / split);
@@ -581,10 +586,10 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
       Ring<C::S> r;
       bool ok = true;
       for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
-        const int t0 = (tile / ntn) * NT + static_cast<int>(side) * C::kRowsB;
+        const int t0 = (tile / ntn) * nt + static_cast<int>(side) * (nt / 2);
         for (int k = s0; k < s1; ++k, r.next()) {
           if (!r.first && !(ok = poll(empty + 8 * r.stage, r.parity ^ 1, abort))) break;
-          mbar_expect_tx(fullx + 8 * r.stage, C::B);
+          mbar_expect_tx(fullx + 8 * r.stage, nt / 2 * kBK * 2);
           tma_load_2d(base + r.stage * (C::A + C::B) + C::A, &mapx, k * kBK, t0, fullx + 8 * r.stage);
         }
       }
@@ -605,6 +610,7 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
       // before this stage's MMAs are issued and looked at after
       const uint16_t both = static_cast<uint16_t>(3u << leader);
       Ring<C::S> r;
+      const uint32_t idesc = C::idesc(nt);
       Ring<2> d;
       bool ok = true, ready = false;
       for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
@@ -622,7 +628,7 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
             if (elect_one()) {
               const uint64_t da = smem_desc(base + stage * (C::A + C::B)), db = da + (C::A >> 4);
 #pragma unroll
-              for (int kk = 0; kk < kBK / 16; ++kk) mma_pair(acc, da + kk * 2, db + kk * 2, C::kIdesc, more | kk);
+              for (int kk = 0; kk < kBK / 16; ++kk) mma_pair(acc, da + kk * 2, db + kk * 2, idesc, more | kk);
               commit_pair(empty + 8 * stage, both);
             }
             ready = __all_sync(0xffffffffu, ready);
@@ -671,14 +677,14 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
         if (lane == 0) arrive_at(dempty + 8 * d.stage, leader);
       }
       if (!ok) break;
-      const int n0 = channel0(tile), t0 = (tile / ntn) * NT;
+      const int n0 = channel0(tile), t0 = (tile / ntn) * nt, t1 = min(p.T, t0 + nt);
       if (split == 1) {
         // the token scales are read ahead and passed around the warp: a load
         // beside each store would wait for the store (they might be the same memory)
         const int n = n0 + q * 32 + lane, ts = t0 + half * C::ACC;
         float xs[C::ACC / 32], ws = 0.f, bias = 0.f;
 #pragma unroll
-        for (int i = 0; i < C::ACC / 32; ++i) xs[i] = ts + i * 32 + lane < p.T ? __ldg(p.xs + ts + i * 32 + lane) : 0.f;
+        for (int i = 0; i < C::ACC / 32; ++i) xs[i] = ts + i * 32 + lane < t1 ? __ldg(p.xs + ts + i * 32 + lane) : 0.f;
         if (n < p.N) {
           ws = __ldg(p.ws + n);
           if (p.bias) bias = to_f32<O>(static_cast<const O*>(p.bias)[n]);
@@ -687,7 +693,7 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
 #pragma unroll
         for (int i = 0; i < C::ACC; ++i) {
           const float x = __shfl_sync(0xffffffffu, xs[i / 32], i % 32);
-          if (n < p.N && ts + i < p.T) *out = from_f32<O>(fmaf(static_cast<float>(acc[i]) * x, ws, bias));
+          if (n < p.N && ts + i < t1) *out = from_f32<O>(fmaf(static_cast<float>(acc[i]) * x, ws, bias));
           out += p.ldo;
         }
       } else {
@@ -733,8 +739,8 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
     // the parts of one tile: each CTA adds and stores its share of the tokens
     cluster_sync();
     if (!*abort) {
-      const int n0 = channel0(tile0), t0 = (tile0 / ntn) * NT;
-      const int j0 = NT * part / split, j1 = NT * (part + 1) / split;
+      const int n0 = channel0(tile0), t0 = (tile0 / ntn) * nt;
+      const int j0 = nt * part / split, j1 = nt * (part + 1) / split;
       const int end = j1 * (kM / 4);
       const int n = n0 + tid % (kM / 4) * 4;   // four channels, the same for all of the thread's tokens
       float ws[4], bias[4];
@@ -1257,16 +1263,20 @@ cudaError_t launch_tc(const LinArgs& p, void* ws, cudaStream_t s) {
   OnDevice* d;
   cudaError_t e = prepare(all, k_tc<O>, C::kThreads, C::kSmem, &d);
   CUtensorMap mapw, mapx;
+  // tokens of a tile, about the same for all and a multiple of the 32 that a
+  // pair's MMA takes: 333 are 192 and 141, not 256 and 77 (300 x 4096 x 4096: 22.0
+  // and 23.6 us; 260 x 28672 x 4096: 74.4 and 77.1)
+  const int ntt = (p.T + C::NT - 1) / C::NT, nt = ((p.T + ntt - 1) / ntt + 31) / 32 * 32;
   const int kp = padded_k(p.K);
   if (e == cudaSuccess) e = map_tile(&mapw, 1, p.w, p.ldw, p.N, p.K, kM);
-  if (e == cudaSuccess) e = map_tile(&mapx, 2, ws, kp * int64_t{2}, p.T, kp, C::kRowsB);
+  if (e == cudaSuccess) e = map_tile(&mapx, 2, ws, kp * int64_t{2}, p.T, kp, nt / 2);
   if (e == cudaSuccess) e = widen(p, ws, s);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = static_cast<int64_t>((p.N + 2 * kM - 1) / (2 * kM)) * ((p.T + 255) / 256);
+  const int64_t tiles = static_cast<int64_t>((p.N + 2 * kM - 1) / (2 * kM)) * ntt;
   const int split = parts_of_k(*d, tiles, (p.K + kBK - 1) / kBK, 1, 2);
   const int64_t pairs = split > 1 ? tiles * split : std::min<int64_t>(tiles, sm_count() / 2);
   return launch_after_widen(k_tc<O>, static_cast<unsigned>(2 * pairs), C::kThreads, C::kSmem, 2 * split, s, p,
-                            mapw, mapx, split);
+                            mapw, mapx, nt, split);
 }
 
 template <typename O, int MT>
