@@ -147,9 +147,9 @@ struct FewSums {
 
 constexpr int kFewWarps = 8;
 constexpr int few_ctas(bool ahead) { return ahead ? 2 : 3; }   // of an SM
-// k_few against k_thin, K = 4096, us: 16 tokens 6.7 and 18 at N = 4096, 28 and 37
-// at 28672, 115 and 122 at 131072; 32 tokens 10 and 18 at 4096, 26 and 26 at
-// 14336, 48 and 37 at 28672.
+// k_few against k_thin, K = 4096, us: 16 tokens 6.7 and 18 at N = 4096, 28 and 36
+// at 28672, 115 and 118 at 131072; 32 tokens 10 and 18 at 4096, 26 and 25 at
+// 14336, 48 and 36 at 28672.
 constexpr int kFewTokens = 16;
 constexpr int kManyChannels = 14336;   // from which 17 to 32 tokens take k_thin
 
@@ -362,17 +362,19 @@ struct Weights {
   static constexpr int kN = ROWS / (WARPS * 8);
   uint4 v[kN];
 
-  __device__ __forceinline__ void load(uint32_t src, int tid) {
+  __device__ __forceinline__ void load(uint32_t src, int tid, int rows = ROWS) {
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
+      if (i * (WARPS * 8) >= rows) break;
       const int r = (tid >> 2) + i * (WARPS * 8);
       v[i] = lds16(src + r * 64 + (((tid & 3) ^ ((r >> 1) & 3)) << 4));
     }
   }
-  __device__ __forceinline__ void store(uint32_t dst, int tid) const {
+  __device__ __forceinline__ void store(uint32_t dst, int tid, int rows = ROWS) const {
     const int j = (tid & 3) * 2;
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
+      if (i * (WARPS * 8) >= rows) break;
       const int r = (tid >> 2) + i * (WARPS * 8);
       uint32_t h[8];
       to_f16x16(v[i], h);
@@ -792,16 +794,16 @@ k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_con
 
 // An MMA takes about 130 clocks however few columns it has, so with the
 // channels as its rows (k_tc) few tokens leave it mostly empty.  Here they are
-// its columns: one CTA, up to 128 tokens (M, rows past T hold anything) x 256
-// channels (N).  Roles and rings as in k_tc, without the pair: half the MMAs
+// its columns: one CTA, up to 128 tokens (M, rows past T hold anything) x 128 to
+// 256 channels (N).  Roles and rings as in k_tc, without the pair: half the MMAs
 // for the same weights.  MT: tokens that a stage has room for; the MMA reads
 // 128 rows, the ones past MT from the weights behind them, into lanes that
-// nobody reads.  What bounds it is the shared-memory data pipe: a stage of 256
-// channels x 64 columns goes in by TMA (16 KB), out for conversion, in again as
-// fp16 (32 KB) and out to the MMA, 750 of its clocks with the tokens, and with
-// the barriers' latencies about 1100 were taken.  28672 x 4096 weights: 37, 42
-// and 44 us for 32, 64 and 128 tokens (43 % of the copy rate at 64); k_tc takes
-// 57 for 129 to 256.
+// nobody reads.  A stage of 256 channels x 64 columns goes into shared memory by
+// TMA (16 KB), out for conversion, in again as fp16 (32 KB) and out to the MMA,
+// about 1000 clocks of its data pipe with the tokens, and 1100 are taken; at 192
+// channels it is 1050, so the chain of barriers and conversions counts too.
+// 28672 x 4096 weights: 36, 39 and 42 us for 32, 64 and 128 tokens (46 % of the
+// copy rate at 64); k_tc takes 53 for 129 to 160.
 constexpr int kThinN = 256;
 template <int MT>
 struct Thin {
@@ -817,8 +819,9 @@ struct Thin {
   static constexpr int kOffBar = kRing8 + S8 * W8;
   static constexpr int kSmem = kOffBar + 8 * (3 * S + 2 * S8 + 5) + 16 + 1024;
   static constexpr uint32_t kCols = 2 * kThinN;
-  static constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(kThinN >> 3) << 17) |
-                                     (static_cast<uint32_t>(kM >> 4) << 24);
+  __host__ __device__ static constexpr uint32_t idesc(int n) {
+    return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(kM >> 4) << 24);
+  }
   static constexpr int kSumRow = MT + 1;                         // of a channel's int32 sums, padded
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
   // a tile's int32 sums, and half of them once more, fit the rings
@@ -837,7 +840,7 @@ __device__ __forceinline__ int ld_cluster1(uint32_t addr, uint32_t rank) {
 template <typename O, int MT>
 __global__ void __launch_bounds__(Thin<MT>::kThreads, 1)
 k_thin(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_constant__ CUtensorMap mapx, int box,
-       int split) {
+       int nw, int split) {
   using C = Thin<MT>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);
@@ -890,7 +893,7 @@ k_thin(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_c
     }
   };
 
-  const int tiles = (p.N + kThinN - 1) / kThinN;
+  const int tiles = (p.N + nw - 1) / nw;
   const int steps_all = (p.K + kBK - 1) / kBK;
   const int s0 = static_cast<int>(static_cast<int64_t>(steps_all) * part / split);
   const int s1 = static_cast<int>(static_cast<int64_t>(steps_all) * (part + 1) / split);
@@ -906,8 +909,8 @@ k_thin(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_c
       for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
         for (int k = s0; k < s1; ++k, r.next()) {
           if (!r.first && !(ok = poll(empty8 + 8 * r.stage, r.parity ^ 1, abort))) break;
-          mbar_expect_tx(full8 + 8 * r.stage, C::W8);
-          tma_load_2d(base + C::kRing8 + r.stage * C::W8, &mapw, k * kBK, tile * kThinN, full8 + 8 * r.stage);
+          mbar_expect_tx(full8 + 8 * r.stage, nw * kBK);
+          tma_load_2d(base + C::kRing8 + r.stage * C::W8, &mapw, k * kBK, tile * nw, full8 + 8 * r.stage);
         }
       }
       if (*abort) drain(full8, C::S8, r);
@@ -928,6 +931,7 @@ k_thin(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_c
     }
     if (warp == 1) {
       // ---- MMA issue
+      const uint32_t idesc = C::idesc(nw);
       Ring<C::S> r;
       Ring<2> d;
       bool ok = true, ready = false;
@@ -946,7 +950,7 @@ k_thin(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_c
             if (elect_one()) {
               const uint64_t da = smem_desc(base + stage * (C::X + C::W)), db = da + (C::X >> 4);
 #pragma unroll
-              for (int kk = 0; kk < kBK / 16; ++kk) mma_f16(acc, da + kk * 2, db + kk * 2, C::kIdesc, more | kk);
+              for (int kk = 0; kk < kBK / 16; ++kk) mma_f16(acc, da + kk * 2, db + kk * 2, idesc, more | kk);
               mma_commit(empty + 8 * stage);
             }
             ready = __all_sync(0xffffffffu, ready);
@@ -1002,11 +1006,11 @@ k_thin(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_c
       if (!busy) continue;
       if (split == 1) {
         // lane l holds the scales of channels n + 4 l .. + 3 of this half
-        const int n = tile * kThinN + half * C::ACC;
+        const int n = tile * nw + half * C::ACC, end = min(p.N, (tile + 1) * nw);
         float ws[4], bias[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const bool in = n + lane * 4 + c < p.N;
+          const bool in = n + lane * 4 + c < end;
           ws[c] = in ? __ldg(p.ws + n + lane * 4 + c) : 0.f;
           bias[c] = in && p.bias ? to_f32<O>(static_cast<const O*>(p.bias)[n + lane * 4 + c]) : 0.f;
         }
@@ -1024,12 +1028,12 @@ k_thin(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_c
             v[e] = from_f32<O>(fmaf(static_cast<float>(acc[i + e]) * xs, w, b));
           }
           if (t < p.T) {
-            if (wide && n + i + E <= p.N) {
+            if (wide && n + i + E <= end) {
               *reinterpret_cast<uint4*>(out + i) = *reinterpret_cast<const uint4*>(v);
             } else {
 #pragma unroll
               for (int e = 0; e < E; ++e)
-                if (n + i + e < p.N) out[i + e] = v[e];
+                if (n + i + e < end) out[i + e] = v[e];
             }
           }
         }
@@ -1056,9 +1060,9 @@ k_thin(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_c
     for (int64_t g = group; g < mine; g += C::kGroups, r.next(C::kGroups), r8.next(C::kGroups)) {
       if (!wait(full8 + 8 * r8.stage, r8.parity)) break;
       Weights<kThinN, C::kGroupWarps> w;
-      w.load(base + C::kRing8 + r8.stage * C::W8, ctid);
+      w.load(base + C::kRing8 + r8.stage * C::W8, ctid, nw);
       if (!r.first && !wait(empty + 8 * r.stage, r.parity ^ 1)) break;
-      w.store(base + r.stage * (C::X + C::W) + C::X, ctid);
+      w.store(base + r.stage * (C::X + C::W) + C::X, ctid, nw);
       proxy_fence_smem();
       __syncwarp();
       if (lane == 0) {
@@ -1078,7 +1082,7 @@ k_thin(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_c
     // one line each), into [token][channel] behind the sums, and stores those
     cluster_sync();
     if (!*abort) {
-      const int share = kThinN / split, c0 = share * part;   // split is a power of two
+      const int share = nw / split, c0 = share * part;   // nw is a multiple of 32, split at most 8
       int* rows = reinterpret_cast<int*>(smem) + kThinN * C::kSumRow;
       constexpr int U = 4;   // with four parts each: 16 reads in flight together
       for (int i0 = tid; i0 < share * MT; i0 += U * C::kThreads) {
@@ -1102,13 +1106,11 @@ k_thin(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_c
         }
       }
       __syncthreads();
-      const int n0 = tile0 * kThinN + c0;
-      static_assert(C::kThreads % (kThinN / 2) == 0, "a thread keeps its channel");
-      const int c = tid % share, n = n0 + c;
-      if (n < p.N) {
+      const int c = tid % share, n = tile0 * nw + c0 + c, t_step = C::kThreads / share;   // a thread keeps its channel
+      if (n < p.N && tid < t_step * share) {
         const float ws = __ldg(p.ws + n), bias = p.bias ? to_f32<O>(static_cast<const O*>(p.bias)[n]) : 0.f;
 #pragma unroll 4
-        for (int t = tid / share; t < p.T; t += C::kThreads / share)
+        for (int t = tid / share; t < p.T; t += t_step)
           store_out<O>(p, t, n, rows[t * (share + 1) + c], __ldg(p.xs + t), ws, bias);
       }
     }
@@ -1285,16 +1287,29 @@ cudaError_t launch_thin(const LinArgs& p, void* ws, cudaStream_t s) {
   static OnDevice all[kMaxDev];
   OnDevice* d;
   cudaError_t e = prepare(all, k_thin<O, MT>, C::kThreads, C::kSmem, &d);
+  if (e != cudaSuccess) return e;
+  const int kp = padded_k(p.K), steps = (p.K + kBK - 1) / kBK, box = (p.T + 7) / 8 * 8;
+  // channels of a tile: what gives the SMs the least to do in turn, a stage's
+  // time being some constant and a part that grows with them.  64 x 28672 x 4096:
+  // 42.1 us with 256 (112 tiles), 39.0 with 192 (150), 58 with 128 (two turns);
+  // 32 x 131072 x 4096: 124, 137 and, with the 224 of the rule, 118; 128 x 4096 x
+  // 14336: 43.3, 39.4 and, K split over more CTAs with 128, 34.8
+  int nw = kThinN, split = 1;
+  float least = 0.f;
+  for (int n = kThinN; n >= kThinN / 2; n -= 32) {
+    const int tiles = (p.N + n - 1) / n, parts = parts_of_k(*d, tiles, steps, 0, 3);
+    const int turns = (tiles + sm_count() - 1) / sm_count();   // one where K is split
+    const float cost = static_cast<float>(turns * (n + 64)) / parts;
+    if (n == kThinN || cost < least) nw = n, split = parts, least = cost;
+  }
   CUtensorMap mapw, mapx;
-  const int kp = padded_k(p.K), box = (p.T + 7) / 8 * 8;
-  if (e == cudaSuccess) e = map_tile(&mapw, 1, p.w, p.ldw, p.N, p.K, kThinN);
+  e = map_tile(&mapw, 1, p.w, p.ldw, p.N, p.K, nw);
   if (e == cudaSuccess) e = map_tile(&mapx, 2, ws, kp * int64_t{2}, p.T, kp, box);
   if (e == cudaSuccess) e = widen(p, ws, s);
   if (e != cudaSuccess) return e;
-  const int tiles = (p.N + kThinN - 1) / kThinN;
-  const int split = parts_of_k(*d, tiles, (p.K + kBK - 1) / kBK, 0, 3);
+  const int tiles = (p.N + nw - 1) / nw;
   return launch_after_widen(k_thin<O, MT>, static_cast<unsigned>(split > 1 ? tiles * split : std::min(tiles, sm_count())),
-                            C::kThreads, C::kSmem, split, s, p, mapw, mapx, box, split);
+                            C::kThreads, C::kSmem, split, s, p, mapw, mapx, box, nw, split);
 }
 
 template <typename O>

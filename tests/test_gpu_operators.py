@@ -271,6 +271,19 @@ def test_linear_sums_are_exact(T, K):
     assert np.array_equal(f64(got), acc.astype(np.float32).astype(np.float64))
 
 
+@pytest.mark.parametrize("T", [3, 13, 20, 50, 100, 131, 300, 520])
+@pytest.mark.parametrize("N,K", [(20011, 200), (14337, 1040), (9001, 2100), (30000, 70)])
+def test_linear_many_channels(T, N, K):
+    # tiles of every width and token count; sums below 2^20, exact in fp32
+    rng = gen(T, N, K)
+    x, w = [torch.as_tensor(rng.integers(-16, 17, (n, (K + 15) // 16 * 16), dtype=np.int8)).cuda()[:, :K] for n in (T, N)]
+    one = torch.ones(max(T, N), device="cuda")
+    out = torch.full((T, N + 3), -7.0, device="cuda")
+    pw.pw_linear_i8(x, one[:T], w, one[:N], out=out[:, 1:N + 1])
+    assert torch.equal(out[:, 1:N + 1].double(), x.double() @ w.double().T)
+    assert (out[:, 0] == -7).all() and (out[:, N + 1:] == -7).all()
+
+
 def test_linear_bf16_and_wide_rows():
     rng = gen(44)
     x, xs, w, ws, b = _linear_case(37, 333, 4096, "bf16", True)
