@@ -1170,7 +1170,6 @@ cudaError_t map_tile(CUtensorMap* m, int size, const void* base, int64_t ld, int
 
 int padded_k(int K) { return (K + 63) & ~63; }
 
-
 // Clusters of `size` CTAs of a kernel that the device holds at once.
 template <typename K>
 int max_clusters(K* kernel, int threads, int smem, int size) {
