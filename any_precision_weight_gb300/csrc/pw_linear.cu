@@ -332,6 +332,8 @@ struct Tile {
   }
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
   static_assert(kM * NT * 4 <= kRing8, "a CTA's int32 sums fit the operand ring");
+  // a parity tells a stage's last use from the one before, not from earlier ones
+  static_assert(kGroups <= S && kGroups <= S8, "no group is a lap ahead of another");
 };
 
 // Registers by role; the accumulating threads hold 128 sums:
@@ -827,6 +829,7 @@ struct Thin {
   // a tile's int32 sums, and half of them once more, fit the rings
   static_assert(kThinN * kSumRow * 4 + MT * (kThinN / 2 + 1) * 4 <= kOffBar, "sums");
   static_assert(kM * kBK * 2 <= X + W, "the rows past MT are inside the stage");
+  static_assert(kGroups <= S && kGroups <= S8, "no group is a lap ahead of another");   // as in Tile
 };
 
 __device__ __forceinline__ int ld_cluster1(uint32_t addr, uint32_t rank) {
