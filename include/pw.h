@@ -547,9 +547,9 @@ int pw_profile_attach(void* const* events, int n_events);
  * PW_BF16 or PW_F32; a matrix is rows of consecutive elements whose starts are
  * `ld*` elements apart (ld >= the row's length, 64-bit), so padded and sliced
  * matrices need no copy.  Work is enqueued on `s` and nothing waits; nothing
- * is kept between calls, so calls on several streams may overlap.  T = 0 is a no-op.  A call may be captured into a CUDA
- * graph.  Results do not depend on what else runs: a call repeated on the same
- * inputs gives the same bits.
+ * is kept between calls, so calls on several streams may overlap.  T = 0 is a
+ * no-op.  A call may be captured into a CUDA graph.  Results do not depend on
+ * what else runs: a call repeated on the same inputs gives the same bits.
  */
 #define PW_F16  0
 #define PW_BF16 1

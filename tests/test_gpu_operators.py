@@ -272,7 +272,7 @@ def test_linear_sums_are_exact(T, K):
 
 
 @pytest.mark.parametrize("T", [3, 13, 20, 50, 100, 131, 300, 520])
-@pytest.mark.parametrize("N,K", [(20011, 200), (14337, 1040), (9001, 2100), (30000, 70)])
+@pytest.mark.parametrize("N,K", [(20011, 200), (14337, 1040), (9001, 2100), (30000, 70), (77, 1), (300, 3), (1, 65)])
 def test_linear_many_channels(T, N, K):
     # tiles of every width and token count; sums below 2^20, exact in fp32
     rng = gen(T, N, K)
