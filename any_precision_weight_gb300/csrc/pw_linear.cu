@@ -21,6 +21,7 @@
 #include <cmath>
 #include <atomic>
 #include <mutex>
+#include <type_traits>
 
 #include "pw_rows.cuh"
 #include "pw_tc.cuh"
@@ -111,129 +112,170 @@ __device__ __forceinline__ void to_f16x16(const uint4& v, uint32_t (&h)[8]) {
   to_f16x4(v.w, h[6], h[7]);
 }
 
-// The sums of 16 channels x 8 NT tokens in a warp's registers.  Up to 8 tokens
-// in int8 (256 products a clock and SM, the weights need 190 at the memory's
-// rate); above, where int8 would be the bound, in fp16, whose fp32 sums move to
-// int32 every 1024 columns (run `n` of 16 ends one).
-template <int NT>
+// The sums of 16 G channels x 8 NT tokens of a warp, in the end in row c of
+// sums[kRow] for channel c.  Up to 8 tokens in int8 (256 products a clock and SM,
+// the weights need 190 at the memory's rate); above, where int8 would be the
+// bound, in fp16, whose fp32 sums go to int32 every 1024 columns (run `n` of 16
+// ends one): to registers, or to shared memory where registers are short (32
+// tokens, 8192 x 4096: 15.5 us, 17.3 with registers; 16 tokens, 4096 x 4096: 6.9
+// and 6.7).
+template <int NT, int G>
 struct FewSums {
-  int acc[NT][4] = {};
-  float part[NT][4] = {};
-  __device__ __forceinline__ void add(const uint4& a, const uint4& b, const uint4 (&x)[NT], int n) {
+  using D = std::conditional_t<NT == 1, int, float>;
+  static constexpr int kRow = NT * 8 + 1;   // padded against bank conflicts
+  static constexpr bool kShared = NT > 2 || G > 1;
+  D part[G][NT][4] = {};
+  int acc[G][NT][4] = {};   // where sums go to registers
+  int* s = nullptr;         // of the lane's first channel and token
+
+  __device__ __forceinline__ void place(int* sums, int lane) { s = sums + (lane >> 2) * kRow + (lane & 3) * 2; }
+  __device__ __forceinline__ FewSums(int* sums, int lane) {
+    if constexpr (kShared) {
+      place(sums, lane);
+      for (int i = lane; i < 16 * G * kRow; i += 32) sums[i] = 0;
+      __syncwarp();
+    }
+  }
+  // w: channels g and g + 8 of every 16
+  __device__ __forceinline__ void add(const uint4 (&w)[2 * G], const uint4 (&x)[NT], int n) {
     if constexpr (NT == 1) {
-      mma_s8(acc[0], a.x, b.x, a.y, b.y, x[0].x, x[0].y);
-      mma_s8(acc[0], a.z, b.z, a.w, b.w, x[0].z, x[0].w);
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        const uint4 &a = w[2 * h], &b = w[2 * h + 1];
+        mma_s8(part[h][0], a.x, b.x, a.y, b.y, x[0].x, x[0].y);
+        mma_s8(part[h][0], a.z, b.z, a.w, b.w, x[0].z, x[0].w);
+      }
     } else {
-      uint32_t ha[8], hb[8];
-      to_f16x16(a, ha);
-      to_f16x16(b, hb);
+      uint32_t hw[2 * G][8];
+#pragma unroll
+      for (int i = 0; i < 2 * G; ++i) to_f16x16(w[i], hw[i]);
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         uint32_t hx[8];
         to_f16x16(x[j], hx);
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) mma_f16_16816(part[j], ha[i], hb[i], ha[i + 1], hb[i + 1], hx[i], hx[i + 1]);
+        for (int h = 0; h < G; ++h)
+#pragma unroll
+          for (int i = 0; i < 8; i += 2)
+            mma_f16_16816(part[h][j], hw[2 * h][i], hw[2 * h + 1][i], hw[2 * h][i + 1], hw[2 * h + 1][i + 1], hx[i],
+                          hx[i + 1]);
       }
       if (n % 16 == 15) flush();
     }
   }
+  // part[h][j][0..3]: channels g, g, g + 8, g + 8 of 16; tokens 8 j + 2 q + 0, 1, 0, 1
+  template <typename F>
+  __device__ __forceinline__ void each(F&& f) {
+#pragma unroll
+    for (int h = 0; h < G; ++h)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f(h, j, i, (h * 16 + (i >> 1) * 8) * kRow + j * 8 + (i & 1));
+  }
   __device__ __forceinline__ void flush() {
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[j][i] += __float2int_rn(part[j][i]), part[j][i] = 0.f;
+    each([&](int h, int j, int i, int at) {
+      (kShared ? s[at] : acc[h][j][i]) += static_cast<int>(part[h][j][i]);
+      part[h][j][i] = 0;
+    });
+  }
+  __device__ __forceinline__ void finish(int* sums, int lane) {
+    if constexpr (NT > 1) flush();
+    if constexpr (!kShared) {
+      place(sums, lane);
+      each([&](int h, int j, int i, int at) { s[at] = NT > 1 ? acc[h][j][i] : static_cast<int>(part[h][j][i]); });
+    }
   }
 };
 
 constexpr int kFewWarps = 8;
 constexpr int few_ctas(bool ahead) { return ahead ? 2 : 3; }   // of an SM
+constexpr int few_groups(int nt, bool ahead) { return nt > 1 && !ahead ? 2 : 1; }   // of 16 channels, a warp's
 // k_few against k_thin, K = 4096, us: 16 tokens 6.7 and 18 at N = 4096, 28 and 36
-// at 28672, 115 and 118 at 131072; 32 tokens 10 and 18 at 4096, 26 and 25 at
-// 14336, 48 and 36 at 28672.
+// at 28672, 108 and 118 at 131072; 24 tokens 22 and 25 at 14336, 37 and 35 at 28672;
+// 32 tokens 9 and 18 at 4096, 25 and 25 at 14336, 38 and 33 at 20000, 44 and 36 at
+// 28672.
 constexpr int kFewTokens = 16;
-constexpr int kManyChannels = 14336;   // from which 17 to 32 tokens take k_thin
+constexpr int kManyChannels = 16384;   // from which 17 to 32 tokens take k_thin
 
-// A group of kw warps owns 16 channels and shares out K in runs of 64 columns.
+// A group of kw warps owns 16 G channels and shares out K in runs of 64 columns.
 // Lane (g, q) = (lane / 4, lane % 4) loads the 16 bytes at column 16 q of
-// channels g and g + 8, and of token g of every 8: the operand registers of its
-// products, with the columns of K in an order of their own that both operands
-// share.  So the weights go from memory to the tensor cores through registers
-// alone, 64 bytes of a channel at a time (128 at a time, in loads of 32 bytes,
-// was no faster).  NT: groups of 8 tokens.  The loads in flight come from three
-// CTAs of an SM, whose other warps load while one multiplies, or from two that
-// fetch their next U runs ahead (AHEAD).  One token, 28672 x 4096: 21.7 us,
-// 80 % of the copy rate, and 25.2 with AHEAD; what is left there is the launch
-// and the ramps, 131072 channels run at 93 %.  16 tokens, 131072 x 4096: 115 us,
-// 69 %; the conversions of weights and tokens to fp16 (20 instructions for each
-// 16 bytes) and the products take half of the issue slots and the warps wait
-// for operands in the other half.  Two groups of channels to a warp, so that
-// a token is converted for 32, came to 113 us, with the small sizes slower.
+// channels g and g + 8 of every 16, and of token g of every 8: the operand
+// registers of its products, with the columns of K in an order of their own that
+// both operands share.  So the weights go from memory to the tensor cores through
+// registers alone, 64 bytes of a channel at a time (128 at a time, in loads of 32
+// bytes, was no faster).  NT: groups of 8 tokens.  The loads in flight come from
+// three CTAs of an SM, whose other warps load while one multiplies, or from two
+// that fetch their next U runs ahead (AHEAD).  One token, 28672 x 4096: 22 us,
+// 79 % of the copy rate, and 25 with AHEAD; what is left there is the launch and
+// the ramps, 131072 channels run at 92 %.  16 tokens, 131072 x 4096: 108 us, 74 %,
+// with a token converted for 32 channels (G = 2; 116 with 16): the conversions to
+// fp16 (20 instructions for each 16 bytes) and the products take half of the issue
+// slots, and the warps wait for operands in the other half.
 template <typename O, int NT, bool AHEAD>
 __global__ void __launch_bounds__(kFewWarps * 32, few_ctas(AHEAD)) k_few(const LinArgs p, int kw) {
-  constexpr int kRow = NT * 8 + 1;   // padded against bank conflicts
-  constexpr int U = NT == 1 ? 4 : 2;
-  __shared__ int s_part[kFewWarps][16 * kRow];
+  constexpr int G = few_groups(NT, AHEAD), kChannels = 16 * G;
+  constexpr int U = NT == 1 ? 4 : AHEAD ? 2 : 1;
+  using Sums = FewSums<NT, G>;
+  __shared__ int s_part[kFewWarps][kChannels * Sums::kRow];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int groups = kFewWarps / kw, turn = warp % kw;
-  const int n0 = (blockIdx.x * groups + warp / kw) * 16;
+  const int n0 = (blockIdx.x * groups + warp / kw) * kChannels;
   const int runs = (p.K + 63) / 64;
   const int r0 = static_cast<int>(static_cast<int64_t>(runs) * turn / kw);
   const int r1 = static_cast<int>(static_cast<int64_t>(runs) * (turn + 1) / kw);
-  const int8_t* w0 = p.w + min(n0 + g, p.N - 1) * p.ldw + q * 16;
-  const int8_t* w1 = p.w + min(n0 + g + 8, p.N - 1) * p.ldw + q * 16;
+  const int8_t* w[2 * G];
+#pragma unroll
+  for (int i = 0; i < 2 * G; ++i) w[i] = p.w + min(n0 + g + 8 * i, p.N - 1) * p.ldw + q * 16;
   const int8_t* x[NT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) x[j] = p.x + min(j * 8 + g, p.T - 1) * p.ldx + q * 16;
-  FewSums<NT> sums;
+  Sums sums(s_part[warp], lane);
   const int whole = min(r1, p.K / 64);
   const int last = r0 + (whole > r0 ? (whole - r0) / U * U : 0);   // turns of U whole runs end here
-  uint4 a[U], b[U];
+  uint4 a[U][2 * G];
   auto fetch = [&](int k) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      a[u] = load_once(w0 + (k + u) * 64);
-      b[u] = load_once(w1 + (k + u) * 64);
-    }
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < 2 * G; ++i) a[u][i] = load_once(w[i] + (k + u) * 64);
   };
   int k = r0;
   if (AHEAD && k < last) fetch(k);
   for (; k < last; k += U) {
     if (!AHEAD) fetch(k);
-    uint4 ca[U], cb[U], v[U][NT];
+    uint4 c[U][2 * G], v[U][NT];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      ca[u] = a[u];
-      cb[u] = b[u];
+#pragma unroll
+      for (int i = 0; i < 2 * G; ++i) c[u][i] = a[u][i];
 #pragma unroll
       for (int j = 0; j < NT; ++j) v[u][j] = __ldg(reinterpret_cast<const uint4*>(x[j] + (k + u) * 64));
     }
     if (AHEAD && k + U < last) fetch(k + U);
 #pragma unroll
-    for (int u = 0; u < U; ++u) sums.add(ca[u], cb[u], v[u], k - r0 + u);
+    for (int u = 0; u < U; ++u) sums.add(c[u], v[u], k - r0 + u);
   }
   for (; k < r1; ++k) {   // single runs, the last one perhaps not whole
     const int left = p.K - k * 64 - q * 16;
     auto part = [&](const int8_t* from) {
       return left >= 16 ? __ldg(reinterpret_cast<const uint4*>(from + k * 64)) : load_tail(from + k * 64, left);
     };
-    uint4 v[NT];
+    uint4 c[2 * G], v[NT];
+#pragma unroll
+    for (int i = 0; i < 2 * G; ++i) c[i] = part(w[i]);
 #pragma unroll
     for (int j = 0; j < NT; ++j) v[j] = part(x[j]);
-    sums.add(part(w0), part(w1), v, k - r0);
+    sums.add(c, v, k - r0);
   }
-  if (NT > 1) sums.flush();
-  // acc[j][0..3]: channels g, g, g + 8, g + 8; tokens 8 j + 2 q + 0, 1, 0, 1
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s_part[warp][(g + (i >> 1) * 8) * kRow + j * 8 + q * 2 + (i & 1)] = sums.acc[j][i];
+  sums.finish(s_part[warp], lane);
   __syncthreads();
-  for (int i = threadIdx.x; i < groups * 16 * p.T; i += kFewWarps * 32) {
-    const int c = i % (groups * 16), t = i / (groups * 16), grp = c >> 4;
-    const int n = blockIdx.x * groups * 16 + c;
+  for (int i = threadIdx.x; i < groups * kChannels * p.T; i += kFewWarps * 32) {
+    const int c = i % (groups * kChannels), t = i / (groups * kChannels), grp = c / kChannels;
+    const int n = blockIdx.x * groups * kChannels + c;
     if (n >= p.N) continue;
     int sum = 0;
-    for (int j = 0; j < kw; ++j) sum += s_part[grp * kw + j][(c & 15) * kRow + t];
+    for (int j = 0; j < kw; ++j) sum += s_part[grp * kw + j][c % kChannels * Sums::kRow + t];
     store_out<O>(p, t, n, sum, __ldg(p.xs + t), __ldg(p.ws + n), p.bias ? to_f32<O>(static_cast<const O*>(p.bias)[n]) : 0.f);
   }
 }
@@ -241,11 +283,12 @@ __global__ void __launch_bounds__(kFewWarps * 32, few_ctas(AHEAD)) k_few(const L
 // How many warps share a group's K: the count that leaves the least of the last
 // wave of CTAs idle, each doubling charged 6 % for its shorter loops and longer
 // joins, each warp with two runs or more.  T = 1, N = 131072, K = 4096: 94.5 us
-// with one warp (2.2 waves), 84.7 with four (9.0 waves, 6.3 TB/s, 93 % of the
-// copy rate); at 28672 two of 1, 2, 4, 8: 26.9, 21.7, 22.0, 24.0.
+// with one warp (2.2 waves), 84.7 with four (9.0 waves); at 28672 with 1, 2, 4 and
+// 8: 26.9, 21.7, 22.0 and 24.0.
 template <typename O, int NT, bool AHEAD>
 cudaError_t launch_few_nt(const LinArgs& p, cudaStream_t s) {
-  const int groups = (p.N + 15) / 16, runs = (p.K + 63) / 64, slots = sm_count() * few_ctas(AHEAD);
+  constexpr int kChannels = 16 * few_groups(NT, AHEAD);
+  const int groups = (p.N + kChannels - 1) / kChannels, runs = (p.K + 63) / 64, slots = sm_count() * few_ctas(AHEAD);
   int kw = 1;
   float least = 0.f;
   for (int n = 1, i = 0; n <= kFewWarps && (n == 1 || runs >= 2 * n); n *= 2, ++i) {
@@ -261,8 +304,9 @@ cudaError_t launch_few_nt(const LinArgs& p, cudaStream_t s) {
 template <typename O>
 cudaError_t launch_few(const LinArgs& p, cudaStream_t s) {
   if (p.T <= 8) return launch_few_nt<O, 1, false>(p, s);
-  // 16 tokens, K = 4096, two CTAs loading ahead against three, us: N = 4096 6.7
-  // and 7.4, 8192 10.6 and 12.6, 14336 17.6 and 15.7, 131072 118.6 and 115
+  // 16 tokens, K = 4096, loading ahead against three CTAs and 32 channels to a
+  // warp, us: N = 4096 6.7 and 9.7, 8192 10.7 and 11.8, 14336 17.6 and 15.4, 131072
+  // 119 and 108
   if (p.T <= 16)
     return (p.N + 15) / 16 <= 4 * sm_count() ? launch_few_nt<O, 2, true>(p, s) : launch_few_nt<O, 2, false>(p, s);
   if (p.T <= 24) return launch_few_nt<O, 3, true>(p, s);
