@@ -5,8 +5,8 @@
 //
 // the sum exact in int32 (K <= 131071: 128 * 128 * K < 2^31).
 //
-// Few tokens: k_few, tensor-core products fed from registers, the weights
-// streamed once.  Up to 128 and more: k_thin and k_tc on the 5th-generation
+// Few tokens, or little to do: k_few, tensor-core products fed from registers,
+// the weights streamed once (for each block of tokens).  Up to 128 and more: k_thin and k_tc on the 5th-generation
 // tensor cores.  This GPU's int8 tensor rate is a small part of its 16-bit rate, and
 // tcgen05 has no int8 kind here, so that work runs in fp16: int8 values are
 // exact in fp16, their products (at most 2^14) are exact in fp32, and so are
@@ -198,7 +198,8 @@ constexpr int few_groups(int nt, bool ahead) { return nt > 1 && !ahead ? 2 : 1; 
 constexpr int kFewTokens = 16;
 constexpr int kManyChannels = 16384;   // from which 17 to 32 tokens take k_thin
 
-// A group of kw warps owns 16 G channels and shares out K in runs of 64 columns.
+// A group of kw warps owns 16 G channels and up to 8 NT tokens (blockIdx.y) and
+// shares out K in runs of 64 columns.
 // Lane (g, q) = (lane / 4, lane % 4) loads the 16 bytes at column 16 q of
 // channels g and g + 8 of every 16, and of token g of every 8: the operand
 // registers of its products, with the columns of K in an order of their own that
@@ -221,6 +222,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, few_ctas(AHEAD)) k_few(const L
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int groups = kFewWarps / kw, turn = warp % kw;
   const int n0 = (blockIdx.x * groups + warp / kw) * kChannels;
+  const int t0 = blockIdx.y * (NT * 8), T = min(p.T - t0, NT * 8);
   const int runs = (p.K + 63) / 64;
   const int r0 = static_cast<int>(static_cast<int64_t>(runs) * turn / kw);
   const int r1 = static_cast<int>(static_cast<int64_t>(runs) * (turn + 1) / kw);
@@ -229,7 +231,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, few_ctas(AHEAD)) k_few(const L
   for (int i = 0; i < 2 * G; ++i) w[i] = p.w + min(n0 + g + 8 * i, p.N - 1) * p.ldw + q * 16;
   const int8_t* x[NT];
 #pragma unroll
-  for (int j = 0; j < NT; ++j) x[j] = p.x + min(j * 8 + g, p.T - 1) * p.ldx + q * 16;
+  for (int j = 0; j < NT; ++j) x[j] = p.x + (t0 + min(j * 8 + g, T - 1)) * p.ldx + q * 16;
   Sums sums(s_part[warp], lane);
   const int whole = min(r1, p.K / 64);
   const int last = r0 + (whole > r0 ? (whole - r0) / U * U : 0);   // turns of U whole runs end here
@@ -270,13 +272,14 @@ __global__ void __launch_bounds__(kFewWarps * 32, few_ctas(AHEAD)) k_few(const L
   }
   sums.finish(s_part[warp], lane);
   __syncthreads();
-  for (int i = threadIdx.x; i < groups * kChannels * p.T; i += kFewWarps * 32) {
+  for (int i = threadIdx.x; i < groups * kChannels * T; i += kFewWarps * 32) {
     const int c = i % (groups * kChannels), t = i / (groups * kChannels), grp = c / kChannels;
     const int n = blockIdx.x * groups * kChannels + c;
     if (n >= p.N) continue;
     int sum = 0;
     for (int j = 0; j < kw; ++j) sum += s_part[grp * kw + j][c % kChannels * Sums::kRow + t];
-    store_out<O>(p, t, n, sum, __ldg(p.xs + t), __ldg(p.ws + n), p.bias ? to_f32<O>(static_cast<const O*>(p.bias)[n]) : 0.f);
+    store_out<O>(p, t0 + t, n, sum, __ldg(p.xs + t0 + t), __ldg(p.ws + n),
+                 p.bias ? to_f32<O>(static_cast<const O*>(p.bias)[n]) : 0.f);
   }
 }
 
@@ -289,21 +292,21 @@ template <typename O, int NT, bool AHEAD>
 cudaError_t launch_few_nt(const LinArgs& p, cudaStream_t s) {
   constexpr int kChannels = 16 * few_groups(NT, AHEAD);
   const int groups = (p.N + kChannels - 1) / kChannels, runs = (p.K + 63) / 64, slots = sm_count() * few_ctas(AHEAD);
+  const int token_blocks = (p.T + NT * 8 - 1) / (NT * 8);
   int kw = 1;
   float least = 0.f;
   for (int n = 1, i = 0; n <= kFewWarps && (n == 1 || runs >= 2 * n); n *= 2, ++i) {
-    const float waves = static_cast<float>(groups) * n / (kFewWarps * slots);
+    const float waves = static_cast<float>(groups) * token_blocks * n / (kFewWarps * slots);
     const float cost = std::ceil(waves) / waves * (1.f + 0.06f * i);
     if (n == 1 || cost < least) kw = n, least = cost;
   }
   const int per = kFewWarps / kw;
-  k_few<O, NT, AHEAD><<<(groups + per - 1) / per, kFewWarps * 32, 0, s>>>(p, kw);
+  k_few<O, NT, AHEAD><<<dim3((groups + per - 1) / per, token_blocks), kFewWarps * 32, 0, s>>>(p, kw);
   return cudaGetLastError();
 }
 
 template <typename O>
 cudaError_t launch_few(const LinArgs& p, cudaStream_t s) {
-  if (p.T <= 8) return launch_few_nt<O, 1, false>(p, s);
   // 16 tokens, K = 4096, loading ahead against three CTAs and 32 channels to a
   // warp, us: N = 4096 6.7 and 9.7, 8192 10.7 and 11.8, 14336 17.6 and 15.4, 131072
   // 119 and 108
@@ -1360,7 +1363,17 @@ cudaError_t launch_thin(const LinArgs& p, void* ws, cudaStream_t s) {
 
 template <typename O>
 cudaError_t launch_linear(const LinArgs& p, void* ws, cudaStream_t s) {
+  // Few tokens, or little to do (k_few in blocks of tokens): in blocks of 8 as long
+  // as one wave of CTAs holds them, N = 60, K = 4096: 64 tokens 3.7 us and 13.6 by
+  // the tensor-core kernels, 256 tokens 3.8 and 18; 16 x 3600 in two blocks 7.5 and
+  // 6.6 in one.  Then in blocks of 32, K = 4096: 64 x 2048 9.4 and 16.7, 64 x 4096
+  // 15.6 and 17.9, 2048 x 60 10.4 and 22.6, 64 x 8192 26.9 and 22.1; K = 14336:
+  // 64 x 2048 21.7 and 24.2, 64 x 4096 41 and 33; K = 2048: 128 x 4096 16.8 and 17.0.
+  const int64_t blocks = int64_t{(p.N + 15) / 16} * ((p.T + 7) / 8);
+  if (p.T <= 8 || blocks <= sm_count() * (p.T <= kFewTokens ? 2 : 3)) return launch_few_nt<O, 1, false>(p, s);
   if (p.T <= kFewTokens || (p.T <= 32 && p.N < kManyChannels)) return launch_few<O>(p, s);
+  if (p.T > 32 && (blocks <= sm_count() * 7 || (blocks <= 4096 && blocks * p.K <= 1 << 23)))
+    return launch_few_nt<O, 4, true>(p, s);
   if (p.T <= 32) return launch_thin<O, 32>(p, ws, s);
   if (p.T <= 64) return launch_thin<O, 64>(p, ws, s);
   if (p.T <= 128) return launch_thin<O, 128>(p, ws, s);

@@ -284,6 +284,23 @@ def test_linear_many_channels(T, N, K):
     assert (out[:, 0] == -7).all() and (out[:, N + 1:] == -7).all()
 
 
+@pytest.mark.parametrize("T,N,K", [(17, 60, 2048), (33, 60, 9000), (64, 520, 1411), (250, 130, 16384), (1000, 57, 70),
+                                   (40, 4096, 2100), (70, 1300, 16384), (5000, 40, 300), (100, 3000, 16384),
+                                   (64, 4100, 131071), (40, 20011, 5000), (130, 20011, 5000), (300, 1030, 131071),
+                                   (300, 2000, 16384)])
+def test_linear_sums_are_exact_in_every_kernel(T, N, K):
+    """Small and large work by token blocks, few and many tiles, K whole and
+    split: the fp32 of the exact sum."""
+    rng = gen(T, N, K, "kernels")
+    x, w = _i8(rng, T, K), _i8(rng, N, K)
+    x[0], w[0], w[N // 2, ::2] = -128, -128, 127
+    one = torch.ones(max(T, N), device="cuda")
+    out = torch.empty(T, N, device="cuda")
+    pw.pw_linear_i8(x, one[:T], w, one[:N], out=out)
+    # sums below 2^31 are exact in 64 bits
+    assert torch.equal(out, (x.double() @ w.double().T).float())
+
+
 def test_linear_bf16_and_wide_rows():
     rng = gen(44)
     x, xs, w, ws, b = _linear_case(37, 333, 4096, "bf16", True)
