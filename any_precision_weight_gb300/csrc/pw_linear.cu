@@ -358,6 +358,18 @@ constexpr int kGroupWarps = kConvWarps / kGroups;
 constexpr int kChunk = 1024 / kBK;   // stages that fp32 adds exactly: 2^24 / 2^14 products
 constexpr int kEpiWarp0 = 4;
 
+// Whether the converting groups, which take the stages in turn, can wait by
+// parity.  A parity tells a stage's last use from the one before, not from
+// earlier ones, and loads land in any order: at step s a group must know by
+// itself that the load of step s - S8 has landed.  It does where that step was its
+// own (S8 a multiple of the groups), or where a product that it has waited for was
+// at or behind it: the one of s - groups - S, which its last step waited for, or,
+// where a step waits for its operand stage first, the one of s - S.  The operand
+// ring's uses end in order, as the products do.
+constexpr bool parities_suffice(int groups, int S, int S8, bool operand_first) {
+  return groups <= S && groups <= S8 && (S8 % groups == 0 || S8 >= S + (operand_first ? 0 : groups));
+}
+
 struct Tile {
   static constexpr int NT = 256;
   static constexpr int EW = 8;                            // accumulating warps
@@ -368,7 +380,7 @@ struct Tile {
   static constexpr int A = kM * kBK * 2, B = kRowsB * kBK * 2;   // bytes of a stage's operands
   static constexpr int A8 = kM * kBK;                     // and of its int8 weights
   static constexpr int S = 5;                             // operand stages
-  static constexpr int S8 = 7;                            // int8 stages
+  static constexpr int S8 = 8;                            // int8 stages
   static constexpr int kRing8 = S * (A + B);
   static constexpr int kOffBar = kRing8 + S8 * A8;
   static constexpr int kSmem = kOffBar + 8 * (3 * S + 2 * S8 + 6) + 16 + 1024;
@@ -379,8 +391,7 @@ struct Tile {
   }
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
   static_assert(kM * NT * 4 <= kRing8, "a CTA's int32 sums fit the operand ring");
-  // a parity tells a stage's last use from the one before, not from earlier ones
-  static_assert(kGroups <= S && kGroups <= S8, "no group is a lap ahead of another");
+  static_assert(parities_suffice(kGroups, S, S8, false), "no group is a lap ahead of another");
 };
 
 // Registers by role; the accumulating threads hold 128 sums:
@@ -864,6 +875,11 @@ struct Thin {
   static constexpr int W8 = kThinN * kBK;                        // and of its int8 weights
   static constexpr int S = MT == 32 ? 4 : 3;
   static constexpr int S8 = MT == 64 ? 6 : 5;
+  // whether a converting group waits for its operand stage before the weights: what
+  // 4 and 5 stages need (parities_suffice).  32 x 28672 and 32 x 131072 x 4096: 36 and
+  // 120 us; weights first with 3 and 6 stages 38 and 141, with 4 and 4 49 and 181.  64
+  // rows, whose 6 stages are a multiple of the groups: 39 us, and 41 operand first
+  static constexpr bool kOperandFirst = MT == 32;
   static constexpr int kRing8 = S * (X + W);
   static constexpr int kOffBar = kRing8 + S8 * W8;
   static constexpr int kSmem = kOffBar + 8 * (3 * S + 2 * S8 + 5) + 16 + 1024;
@@ -876,7 +892,7 @@ struct Thin {
   // a tile's int32 sums, and half of them once more, fit the rings
   static_assert(kThinN * kSumRow * 4 + MT * (kThinN / 2 + 1) * 4 <= kOffBar, "sums");
   static_assert(kM * kBK * 2 <= X + W, "the rows past MT are inside the stage");
-  static_assert(kGroups <= S && kGroups <= S8, "no group is a lap ahead of another");   // as in Tile
+  static_assert(parities_suffice(kGroups, S, S8, kOperandFirst), "no group is a lap ahead of another");
 };
 
 __device__ __forceinline__ int ld_cluster1(uint32_t addr, uint32_t rank) {
@@ -1108,10 +1124,11 @@ k_thin(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_c
     r8.next(group);
     const int64_t mine = static_cast<int64_t>(steps) * ((tiles - tile0 + tile_step - 1) / tile_step);
     for (int64_t g = group; g < mine; g += C::kGroups, r.next(C::kGroups), r8.next(C::kGroups)) {
+      if (C::kOperandFirst && !r.first && !wait(empty + 8 * r.stage, r.parity ^ 1)) break;
       if (!wait(full8 + 8 * r8.stage, r8.parity)) break;
       Weights<kThinN, C::kGroupWarps> w;
       w.load(base + C::kRing8 + r8.stage * C::W8, ctid, nw);
-      if (!r.first && !wait(empty + 8 * r.stage, r.parity ^ 1)) break;
+      if (!C::kOperandFirst && !r.first && !wait(empty + 8 * r.stage, r.parity ^ 1)) break;
       w.store(base + r.stage * (C::X + C::W) + C::X, ctid, nw);
       proxy_fence_smem();
       __syncwarp();
