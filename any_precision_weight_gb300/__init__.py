@@ -512,6 +512,10 @@ class PagedMoE:
 
 # ----------------------------------------------------------------------------- operators around the layer
 
+# Each call runs on `stream` (default: the current one).  Outputs and workspaces
+# that it makes itself are that stream's memory; one that is used on another
+# stream than its own has to be ordered, and recorded, by the caller.
+
 _torch_mod = None
 _codes = {}
 
@@ -569,11 +573,21 @@ def _vec(t, name: str, dtype, n: int):
     return t.data_ptr()
 
 
-def rows_i8(T: int, K: int, device="cuda"):
+def _empty(torch, stream, shape, dtype, device):
+    """Uninitialised memory of the stream that a call writes it on: a block of
+    another stream's pool may still be in use there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def rows_i8(T: int, K: int, device="cuda", stream=None):
     """An uninitialised int8 matrix [T][K] whose rows start on 16-byte
-    boundaries, as pw_linear_i8 wants them (a view of a padded one)."""
+    boundaries, as pw_linear_i8 wants them (a view of a padded one), in memory
+    of the given stream or the current one."""
     torch = _torch()
-    return torch.empty((T, (K + 15) // 16 * 16), dtype=torch.int8, device=device)[:, :K]
+    return _empty(torch, stream, (T, (K + 15) // 16 * 16), torch.int8, device)[:, :K]
 
 
 def _norm(torch, what, x, shape, weight, eps, residual, sum_out, y, q, scale, stream):
@@ -601,9 +615,9 @@ def pw_rms_norm(x, weight, eps: float = 1e-6, residual=None, out=None, sum_out=N
     torch = _torch()
     shape = _matrix(x, "x")
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        out = _empty(torch, stream, shape, x.dtype, x.device)
     if residual is not None and sum_out is None:
-        sum_out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        sum_out = _empty(torch, stream, shape, x.dtype, x.device)
     _norm(torch, "pw_rms_norm", x, shape, weight, eps, residual, sum_out, out, None, None, stream)
     return out if residual is None else (out, sum_out)
 
@@ -616,11 +630,11 @@ def pw_rms_norm_i8(x, weight, eps: float = 1e-6, residual=None, q=None, scale=No
     torch = _torch()
     shape = _matrix(x, "x")
     if q is None:
-        q = rows_i8(*shape, x.device)
+        q = rows_i8(*shape, x.device, stream)
     if scale is None:
-        scale = torch.empty(shape[0], dtype=torch.float32, device=x.device)
+        scale = _empty(torch, stream, (shape[0],), torch.float32, x.device)
     if residual is not None and sum_out is None:
-        sum_out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        sum_out = _empty(torch, stream, shape, x.dtype, x.device)
     _norm(torch, "pw_rms_norm_i8", x, shape, weight, eps, residual, sum_out, out, q, scale, stream)
     return (q, scale) if residual is None else (q, scale, sum_out)
 
@@ -631,9 +645,9 @@ def pw_quant_i8(x, q=None, scale=None, stream=None):
     shape = _matrix(x, "x")
     T, K = shape
     if q is None:
-        q = rows_i8(T, K, x.device)
+        q = rows_i8(T, K, x.device, stream)
     if scale is None:
-        scale = torch.empty(T, dtype=torch.float32, device=x.device)
+        scale = _empty(torch, stream, (T,), torch.float32, x.device)
     _check(lib().pw_quant_i8(x.data_ptr(), _rows(x, "x", x.dtype, shape), T, K, _code(x.dtype), q.data_ptr(),
                              _rows(q, "q", torch.int8, shape), _vec(scale, "scale", torch.float32, T),
                              _raw_stream(torch, stream, x)), "pw_quant_i8")
@@ -650,18 +664,15 @@ def pw_linear_i8(x, x_scale, w, w_scale, bias=None, out=None, out_dtype=None, ws
     T, K = _matrix(x, "x")
     N = _matrix(w, "w")[0]
     if out is None:
-        out = torch.empty((T, N), dtype=out_dtype or torch.float16, device=x.device)
+        out = _empty(torch, stream, (T, N), out_dtype or torch.float16, x.device)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"pw_linear_i8: out is {out.dtype}, not {out_dtype}")
     dt, f32, i8 = out.dtype, torch.float32, torch.int8
     L = lib()
     if ws is None:
         need = L.pw_linear_i8_workspace_bytes(T, K)
-        if need and stream is None:
-            ws = torch.empty(need, dtype=torch.uint8, device=x.device)
-        elif need:
-            with torch.cuda.stream(stream):   # the allocator's memory belongs to the call's stream
-                ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+        if need:
+            ws = _empty(torch, stream, (need,), torch.uint8, x.device)
     _check(L.pw_linear_i8(x.data_ptr(), _rows(x, "x", i8, (T, K)), _vec(x_scale, "x_scale", f32, T),
                           w.data_ptr(), _rows(w, "w", i8, (N, K)), _vec(w_scale, "w_scale", f32, N),
                           None if bias is None else _vec(bias, "bias", dt, N), T, N, K, _code(dt),
@@ -701,7 +712,7 @@ def pw_logprobs(logits, ids=None, top: int = 0, out=None, stream=None):
     f32, i32 = torch.float32, torch.int32
     if out is None:
         dev = logits.device
-        new = lambda dt, *shape: torch.empty(shape, dtype=dt, device=dev)
+        new = lambda dt, *shape: _empty(torch, stream, shape, dt, dev)
         out = (None if ids is None else new(f32, T), None if ids is None else new(i32, T), new(f32, T),
                new(i32, T, top), new(f32, T, top))
     lp, rank, ent, ti, tl = out
