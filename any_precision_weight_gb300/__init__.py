@@ -512,20 +512,23 @@ class PagedMoE:
 
 # ----------------------------------------------------------------------------- operators around the layer
 
-# Each call runs on `stream` (default: the current one).  Outputs and workspaces
+# Each call runs on `stream` (default: the current one) of the current device, which
+# holds every operand; anything else is refused before a launch.  Outputs and workspaces
 # that it makes itself are that stream's memory; one that is used on another
 # stream than its own has to be ordered, and recorded, by the caller.
 
 _torch_mod = None
 _codes = {}
+_devices = 1   # GPUs of the process, once torch is known
 
 
 def _torch():
     """torch, imported at the first call that needs it (and the C ABI's codes
     of its element types)."""
-    global _torch_mod
+    global _torch_mod, _devices
     if _torch_mod is None:
         import torch
+        _devices = torch.cuda.device_count()
         _codes.update({torch.float16: PW_F16, torch.bfloat16: PW_BF16, torch.float32: PW_F32})
         _torch_mod = torch
     return _torch_mod
@@ -539,20 +542,36 @@ def _code(dtype) -> int:
         raise TypeError(f"{dtype}: float16, bfloat16 or float32 is needed") from None
 
 
-def _raw_stream(torch, stream, t):
-    """The given stream, or the current one of t's device (looked up without
-    building a Stream object, which costs more than a launch)."""
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+def _place(torch, t, name: str, stream):
+    """(device index, raw stream) of a call whose first operand is t: on the current
+    device, where the library launches, and the given stream or the current one
+    (looked up without building a Stream object, which costs more than a launch).
+    None for the index where there is one GPU: every CUDA tensor is on it, and to
+    ask each for its index costs 0.4 us a call."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: a CUDA tensor is needed, got one on {t.device}")
+    dev = None
+    if _devices > 1:
+        dev, now = t.get_device(), torch._C._cuda_getDevice()
+        if dev != now:
+            raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{now}")
+        if stream is not None and stream.device_index != dev:
+            raise ValueError(f"{name}: on {t.device}, but the stream is one of cuda:{stream.device_index}")
+    return dev, torch._C._cuda_getCurrentRawStream(dev or 0) if stream is None else stream.cuda_stream
 
 
-def _rows(t, name: str, dtype, shape):
-    """Row stride of a CUDA matrix whose rows are consecutive elements."""
+def _away(t, dev) -> bool:
+    """Whether t is not on the call's device (dev None: the only GPU)."""
+    return not t.is_cuda or (dev is not None and t.get_device() != dev)
+
+
+def _rows(t, name: str, dtype, shape, dev):
+    """Row stride of a matrix on the call's device whose rows are consecutive elements."""
     if t.dtype is not dtype:
         raise TypeError(f"{name}: {dtype} is needed, got {t.dtype}")
-    if t.shape != shape or not t.is_cuda:
-        raise ValueError(f"{name}: a CUDA matrix of shape {tuple(shape)} is needed, got {tuple(t.shape)} on {t.device}")
+    if t.shape != shape or not t.is_cuda or (dev is not None and t.get_device() != dev):
+        raise ValueError(f"{name}: a matrix of shape {tuple(shape)} on the call's GPU is needed, "
+                         f"got {tuple(t.shape)} on {t.device}")
     ld, one = t.stride()
     if one != 1 and shape[1] > 1:
         raise ValueError(f"{name}: the elements of a row must be consecutive")
@@ -567,9 +586,10 @@ def _matrix(t, name: str):
     return t.shape
 
 
-def _vec(t, name: str, dtype, n: int):
-    if t.dtype is not dtype or not t.is_cuda or t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name}: a contiguous CUDA vector of {n} {dtype} is needed")
+def _vec(t, name: str, dtype, n: int, dev):
+    if (t.dtype is not dtype or not t.is_cuda or t.shape != (n,) or not t.is_contiguous()
+            or (dev is not None and t.get_device() != dev)):
+        raise ValueError(f"{name}: a contiguous vector of {n} {dtype} on the call's GPU is needed")
     return t.data_ptr()
 
 
@@ -590,22 +610,22 @@ def rows_i8(T: int, K: int, device="cuda", stream=None):
     return _empty(torch, stream, (T, (K + 15) // 16 * 16), torch.int8, device)[:, :K]
 
 
-def _norm(torch, what, x, shape, weight, eps, residual, sum_out, y, q, scale, stream):
+def _norm(torch, dev, raw, what, x, shape, weight, eps, residual, sum_out, y, q, scale):
     dt = x.dtype
     pr = ps = py = pq = pc = None
     lr = ls = ly = lq = 0
-    lx = _rows(x, "x", dt, shape)
+    lx = _rows(x, "x", dt, shape, dev)
     if residual is not None:
-        lr, pr = _rows(residual, "residual", dt, shape), residual.data_ptr()
+        lr, pr = _rows(residual, "residual", dt, shape, dev), residual.data_ptr()
     if sum_out is not None:
-        ls, ps = _rows(sum_out, "sum_out", dt, shape), sum_out.data_ptr()
+        ls, ps = _rows(sum_out, "sum_out", dt, shape, dev), sum_out.data_ptr()
     if y is not None:
-        ly, py = _rows(y, "out", dt, shape), y.data_ptr()
+        ly, py = _rows(y, "out", dt, shape, dev), y.data_ptr()
     if q is not None:
-        lq, pq = _rows(q, "q", torch.int8, shape), q.data_ptr()
-        pc = _vec(scale, "scale", torch.float32, shape[0])
-    _check(lib().pw_rms_norm(x.data_ptr(), lx, pr, lr, _vec(weight, "weight", dt, shape[1]), eps, shape[0], shape[1],
-                             _code(dt), ps, ls, py, ly, pq, lq, pc, _raw_stream(torch, stream, x)), what)
+        lq, pq = _rows(q, "q", torch.int8, shape, dev), q.data_ptr()
+        pc = _vec(scale, "scale", torch.float32, shape[0], dev)
+    _check(lib().pw_rms_norm(x.data_ptr(), lx, pr, lr, _vec(weight, "weight", dt, shape[1], dev), eps, shape[0],
+                             shape[1], _code(dt), ps, ls, py, ly, pq, lq, pc, raw), what)
 
 
 def pw_rms_norm(x, weight, eps: float = 1e-6, residual=None, out=None, sum_out=None, stream=None):
@@ -613,12 +633,12 @@ def pw_rms_norm(x, weight, eps: float = 1e-6, residual=None, out=None, sum_out=N
     (out, sum_out) with a residual; sum_out (the new residual stream) may be
     the residual itself."""
     torch = _torch()
-    shape = _matrix(x, "x")
+    shape, (dev, raw) = _matrix(x, "x"), _place(torch, x, "x", stream)
     if out is None:
         out = _empty(torch, stream, shape, x.dtype, x.device)
     if residual is not None and sum_out is None:
         sum_out = _empty(torch, stream, shape, x.dtype, x.device)
-    _norm(torch, "pw_rms_norm", x, shape, weight, eps, residual, sum_out, out, None, None, stream)
+    _norm(torch, dev, raw, "pw_rms_norm", x, shape, weight, eps, residual, sum_out, out, None, None)
     return out if residual is None else (out, sum_out)
 
 
@@ -628,29 +648,29 @@ def pw_rms_norm_i8(x, weight, eps: float = 1e-6, residual=None, q=None, scale=No
     pw_linear_i8.  ``out`` also receives the unquantised norm if given.
     Returns (q, scale), or (q, scale, sum_out) with a residual."""
     torch = _torch()
-    shape = _matrix(x, "x")
+    shape, (dev, raw) = _matrix(x, "x"), _place(torch, x, "x", stream)
     if q is None:
         q = rows_i8(*shape, x.device, stream)
     if scale is None:
         scale = _empty(torch, stream, (shape[0],), torch.float32, x.device)
     if residual is not None and sum_out is None:
         sum_out = _empty(torch, stream, shape, x.dtype, x.device)
-    _norm(torch, "pw_rms_norm_i8", x, shape, weight, eps, residual, sum_out, out, q, scale, stream)
+    _norm(torch, dev, raw, "pw_rms_norm_i8", x, shape, weight, eps, residual, sum_out, out, q, scale)
     return (q, scale) if residual is None else (q, scale, sum_out)
 
 
 def pw_quant_i8(x, q=None, scale=None, stream=None):
     """(q, scale): the rows of x as int8 with one scale per row."""
     torch = _torch()
-    shape = _matrix(x, "x")
+    shape, (dev, raw) = _matrix(x, "x"), _place(torch, x, "x", stream)
     T, K = shape
     if q is None:
         q = rows_i8(T, K, x.device, stream)
     if scale is None:
         scale = _empty(torch, stream, (T,), torch.float32, x.device)
-    _check(lib().pw_quant_i8(x.data_ptr(), _rows(x, "x", x.dtype, shape), T, K, _code(x.dtype), q.data_ptr(),
-                             _rows(q, "q", torch.int8, shape), _vec(scale, "scale", torch.float32, T),
-                             _raw_stream(torch, stream, x)), "pw_quant_i8")
+    _check(lib().pw_quant_i8(x.data_ptr(), _rows(x, "x", x.dtype, shape, dev), T, K, _code(x.dtype), q.data_ptr(),
+                             _rows(q, "q", torch.int8, shape, dev), _vec(scale, "scale", torch.float32, T, dev),
+                             raw), "pw_quant_i8")
     return q, scale
 
 
@@ -662,7 +682,7 @@ def pw_linear_i8(x, x_scale, w, w_scale, bias=None, out=None, out_dtype=None, ws
     it is needed and not given)."""
     torch = _torch()
     T, K = _matrix(x, "x")
-    N = _matrix(w, "w")[0]
+    N, (dev, raw) = _matrix(w, "w")[0], _place(torch, x, "x", stream)
     if out is None:
         out = _empty(torch, stream, (T, N), out_dtype or torch.float16, x.device)
     elif out_dtype is not None and out.dtype != out_dtype:
@@ -673,11 +693,13 @@ def pw_linear_i8(x, x_scale, w, w_scale, bias=None, out=None, out_dtype=None, ws
         need = L.pw_linear_i8_workspace_bytes(T, K)
         if need:
             ws = _empty(torch, stream, (need,), torch.uint8, x.device)
-    _check(L.pw_linear_i8(x.data_ptr(), _rows(x, "x", i8, (T, K)), _vec(x_scale, "x_scale", f32, T),
-                          w.data_ptr(), _rows(w, "w", i8, (N, K)), _vec(w_scale, "w_scale", f32, N),
-                          None if bias is None else _vec(bias, "bias", dt, N), T, N, K, _code(dt),
-                          out.data_ptr(), _rows(out, "out", dt, (T, N)), None if ws is None else ws.data_ptr(),
-                          0 if ws is None else ws.numel(), _raw_stream(torch, stream, x)), "pw_linear_i8")
+    elif ws.dtype is not torch.uint8 or not ws.is_contiguous() or _away(ws, dev):
+        raise ValueError(f"ws: a contiguous uint8 tensor on the call's GPU is needed, got {ws.dtype} on {ws.device}")
+    _check(L.pw_linear_i8(x.data_ptr(), _rows(x, "x", i8, (T, K), dev), _vec(x_scale, "x_scale", f32, T, dev),
+                          w.data_ptr(), _rows(w, "w", i8, (N, K), dev), _vec(w_scale, "w_scale", f32, N, dev),
+                          None if bias is None else _vec(bias, "bias", dt, N, dev), T, N, K, _code(dt),
+                          out.data_ptr(), _rows(out, "out", dt, (T, N), dev), None if ws is None else ws.data_ptr(),
+                          0 if ws is None else ws.numel(), raw), "pw_linear_i8")
     return out
 
 
@@ -708,27 +730,26 @@ def pw_logprobs(logits, ids=None, top: int = 0, out=None, stream=None):
     None.  out: a LogProbs (or tuple) of tensors to write into; its entries may
     be None for what is not wanted."""
     torch = _torch()
-    T, V = _matrix(logits, "logits")
+    (T, V), (dev, raw) = _matrix(logits, "logits"), _place(torch, logits, "logits", stream)
     f32, i32 = torch.float32, torch.int32
     if out is None:
-        dev = logits.device
-        new = lambda dt, *shape: _empty(torch, stream, shape, dt, dev)
+        new = lambda dt, *shape: _empty(torch, stream, shape, dt, logits.device)
         out = (None if ids is None else new(f32, T), None if ids is None else new(i32, T), new(f32, T),
                new(i32, T, top), new(f32, T, top))
     lp, rank, ent, ti, tl = out
     pid, ids64 = None, 0
     if ids is not None:
         ids64 = 1 if ids.dtype is torch.int64 else 0
-        pid = _vec(ids, "ids", torch.int64 if ids64 else i32, T)
+        pid = _vec(ids, "ids", torch.int64 if ids64 else i32, T, dev)
     if top:
         for name, t, dt in (("top_ids", ti, i32), ("top_logprobs", tl, f32)):
-            if t.shape != (T, top) or t.dtype is not dt or not t.is_contiguous() or not t.is_cuda:
-                raise ValueError(f"{name}: a contiguous CUDA matrix [{T}][{top}] of {dt} is needed")
-    _check(lib().pw_logprobs(logits.data_ptr(), _rows(logits, "logits", logits.dtype, (T, V)), _code(logits.dtype),
-                             T, V, pid, ids64, top,
-                             None if lp is None else _vec(lp, "logprob", f32, T),
-                             None if rank is None else _vec(rank, "rank", i32, T),
-                             None if ent is None else _vec(ent, "entropy", f32, T),
+            if t.shape != (T, top) or t.dtype is not dt or not t.is_contiguous() or _away(t, dev):
+                raise ValueError(f"{name}: a contiguous matrix [{T}][{top}] of {dt} on the call's GPU is needed")
+    _check(lib().pw_logprobs(logits.data_ptr(), _rows(logits, "logits", logits.dtype, (T, V), dev),
+                             _code(logits.dtype), T, V, pid, ids64, top,
+                             None if lp is None else _vec(lp, "logprob", f32, T, dev),
+                             None if rank is None else _vec(rank, "rank", i32, T, dev),
+                             None if ent is None else _vec(ent, "entropy", f32, T, dev),
                              ti.data_ptr() if top else None, tl.data_ptr() if top else None,
-                             _raw_stream(torch, stream, logits)), "pw_logprobs")
+                             raw), "pw_logprobs")
     return LogProbs(lp, rank, ent, ti, tl)

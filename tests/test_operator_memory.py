@@ -15,7 +15,8 @@ class Shape:
     """What the binding asks of a CUDA tensor, without memory."""
 
     def __init__(self, shape, dtype, index=0, ld=None, contiguous=True):
-        self.shape, self.dtype, self.device = torch.Size(shape), dtype, torch.device("cuda", index)
+        self.shape, self.dtype = torch.Size(shape), dtype
+        self.device = torch.device("cuda", index) if index >= 0 else torch.device("cpu")
         self.index, self.is_cuda, self.contiguous = index, index >= 0, contiguous
         self.strides = (ld or self.shape[-1], 1)[-len(shape):]
 
