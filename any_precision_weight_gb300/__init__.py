@@ -743,7 +743,7 @@ def pw_logprobs(logits, ids=None, top: int = 0, out=None, stream=None):
         pid = _vec(ids, "ids", torch.int64 if ids64 else i32, T, dev)
     if top:
         for name, t, dt in (("top_ids", ti, i32), ("top_logprobs", tl, f32)):
-            if t.shape != (T, top) or t.dtype is not dt or not t.is_contiguous() or _away(t, dev):
+            if t is None or t.shape != (T, top) or t.dtype is not dt or not t.is_contiguous() or _away(t, dev):
                 raise ValueError(f"{name}: a contiguous matrix [{T}][{top}] of {dt} on the call's GPU is needed")
     _check(lib().pw_logprobs(logits.data_ptr(), _rows(logits, "logits", logits.dtype, (T, V), dev),
                              _code(logits.dtype), T, V, pid, ids64, top,

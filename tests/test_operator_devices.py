@@ -105,3 +105,10 @@ def test_a_workspace_of_another_form_is_refused(ws, library):
     with pytest.raises(ValueError):
         linear(ws=ws)
     assert not library.called
+
+
+@pytest.mark.parametrize("name", ["top_ids", "top_logprobs"])
+def test_alternatives_without_their_outputs_are_refused(name, library):
+    with pytest.raises(ValueError):
+        logprobs(**{name: None})
+    assert not library.called
