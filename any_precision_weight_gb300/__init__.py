@@ -149,6 +149,15 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _empty(torch, stream, shape, dtype, device):
+    """Uninitialised memory of the stream that a call writes it on: a block of
+    another stream's pool may still be in use there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 # ----------------------------------------------------------------------------- format
 
 def pw_plane_bytes(R: int, K: int) -> int:
@@ -252,8 +261,12 @@ class PagedMoE:
         self._t = h
         self._keep = {}
 
-    def _alloc(self, nbytes: int, name: str):
+    def _alloc(self, nbytes: int, name: str, stream=None):
+        """Device memory of the given stream, or of the current one."""
         import torch
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self._alloc(nbytes, name)
         if self.guards is None:
             return torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         return self.guards.alloc(nbytes, self.device, name)
@@ -432,9 +445,9 @@ class PagedMoE:
         n = T * top_k * self.H * 4
         return ws[off:off + n].view(torch.float32).view(T * top_k, self.H)
 
-    def workspace(self, T: int, top_k: int):
+    def workspace(self, T: int, top_k: int, stream=None):
         nb = lib().pw_workspace_bytes(T, self.E, top_k, self.H, self.I)
-        return self._alloc(max(nb, 256), f"workspace T={T}")
+        return self._alloc(max(nb, 256), f"workspace T={T}", stream)
 
     def pw_moe_forward(self, layer, x, logits, top_k, renorm, residual=None, out=None, ws=None,
                        routing=False, stream=None):
@@ -445,15 +458,15 @@ class PagedMoE:
         assert x.dtype == torch.float16 and logits.dtype == torch.float32
         assert x.is_contiguous() and logits.is_contiguous()
         if out is None:
-            out = torch.empty_like(x)
+            out = _empty(torch, stream, x.shape, x.dtype, x.device)
         if ws is None:
-            ws = self.workspace(T, top_k)
+            ws = self.workspace(T, top_k, stream)
         ri = rw = ro = rp = None
         if routing:
-            ri = torch.empty((T, top_k), dtype=torch.int32, device=x.device)
-            rw = torch.empty((T, top_k), dtype=torch.float32, device=x.device)
-            ro = torch.empty((self.E + 1,), dtype=torch.int32, device=x.device)
-            rp = torch.empty((T * top_k,), dtype=torch.int32, device=x.device)
+            ri = _empty(torch, stream, (T, top_k), torch.int32, x.device)
+            rw = _empty(torch, stream, (T, top_k), torch.float32, x.device)
+            ro = _empty(torch, stream, (self.E + 1,), torch.int32, x.device)
+            rp = _empty(torch, stream, (T * top_k,), torch.int32, x.device)
         _check(lib().pw_moe_forward(self._t, layer, _ptr(x), _ptr(logits), T, top_k, int(renorm),
                                     _ptr(residual), _ptr(out), _ptr(ri), _ptr(rw), _ptr(ro), _ptr(rp),
                                     _ptr(ws), ws.numel(), _stream(stream)), "pw_moe_forward")
@@ -464,7 +477,7 @@ class PagedMoE:
         """Host (pinned) inputs and output; synchronises the stream."""
         T = x_host.shape[0]
         if ws is None:
-            ws = self.workspace(T, top_k)
+            ws = self.workspace(T, top_k, stream)
         _check(lib().pw_moe_forward_host(self._t, layer, _ptr(x_host), _ptr(logits_host), T, top_k,
                                          int(renorm), _ptr(residual_host), _ptr(out_host), _ptr(ws),
                                          ws.numel(), _stream(stream)), "pw_moe_forward_host")
@@ -478,7 +491,7 @@ class PagedMoE:
         import torch
         assert x.dtype == torch.float16 and logits.dtype == torch.float32
         if out is None:
-            out = torch.empty_like(x)
+            out = _empty(torch, stream, x.shape, x.dtype, x.device)
         _check(lib().pw_moe_forward_noalloc(self._t, layer, _ptr(x), _ptr(logits), x.shape[0], top_k,
                                             int(renorm), _ptr(residual), _ptr(out), _stream(stream)),
                "pw_moe_forward_noalloc")
@@ -591,15 +604,6 @@ def _vec(t, name: str, dtype, n: int, dev):
             or (dev is not None and t.get_device() != dev)):
         raise ValueError(f"{name}: a contiguous vector of {n} {dtype} on the call's GPU is needed")
     return t.data_ptr()
-
-
-def _empty(torch, stream, shape, dtype, device):
-    """Uninitialised memory of the stream that a call writes it on: a block of
-    another stream's pool may still be in use there."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def rows_i8(T: int, K: int, device="cuda", stream=None):

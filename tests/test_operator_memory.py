@@ -1,4 +1,4 @@
-"""Whose memory the operators' outputs and workspaces are: with `stream` given they
+"""Whose memory the layer's and the operators' outputs and workspaces are: with `stream` given they
 come from that stream's pool, since a block freed on another stream may still be
 in use by work queued there.  On the CPU, with tensors that only have a shape."""
 import contextlib
@@ -102,4 +102,30 @@ def test_what_a_call_makes_is_its_streams_memory(call, n, made):
     assert made == [stream] * n
     made.clear()
     call(None)
+    assert made == [None] * n
+
+
+@pytest.fixture
+def layer(made, monkeypatch):
+    monkeypatch.setattr(torch, "empty_like", lambda x: torch.empty(x.shape, x.dtype, x.device))
+    monkeypatch.setattr(torch.cuda, "current_stream", Stream)
+    m = object.__new__(pw.PagedMoE)
+    m.L, m.E, m.H, m.I, m.device, m.guards, m._t = 1, 8, 64, 128, DEV, None, None
+    return m
+
+
+LOGITS = Shape((40, 8), torch.float32)
+FORWARDS = [(lambda m, s: m.pw_moe_forward(0, X, LOGITS, 2, True, stream=s), 2),
+            (lambda m, s: m.pw_moe_forward(0, X, LOGITS, 2, True, routing=True, stream=s), 6),
+            (lambda m, s: m.pw_moe_forward_host(0, X, LOGITS, 2, True, X, stream=s), 1),
+            (lambda m, s: m.pw_moe_forward_noalloc(0, X, LOGITS, 2, True, stream=s), 1)]
+
+
+@pytest.mark.parametrize("call,n", FORWARDS)
+def test_what_a_forward_makes_is_its_streams_memory(call, n, layer, made):
+    stream = Stream()
+    call(layer, stream)
+    assert made == [stream] * n
+    made.clear()
+    call(layer, None)
     assert made == [None] * n
