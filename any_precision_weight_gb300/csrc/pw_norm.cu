@@ -111,7 +111,8 @@ template <bool NORM>
 __device__ __forceinline__ RowScale row_scale(float ss, float amax, int H, float eps) {
   RowScale f;
   const float whole = amax;
-  f.rstd = NORM ? 1.f / sqrtf(ss / static_cast<float>(H) + eps) : 1.f;
+  const float ms = ss / static_cast<float>(H) + eps;
+  f.rstd = !NORM ? 1.f : ms == 0.f ? 0.f : 1.f / sqrtf(ms);   // zeros without eps stay zeros
   f.none = !(amax > 0.f && amax < INFINITY);
   f.up = amax < 0x1p-100f ? 0x1p100f : amax > 0x1p100f ? 0x1p-100f : 1.f;
   f.far = f.up != 1.f;
