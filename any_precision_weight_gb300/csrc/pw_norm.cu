@@ -17,6 +17,7 @@
 // inputs either way, 60).  One row of 4096: 2.1 us.
 
 #include <algorithm>
+#include <type_traits>
 
 #include "pw_rows.cuh"
 
@@ -96,6 +97,16 @@ __device__ __forceinline__ void block_reduce(float& a, float& b, float2* sh) {
   }
   b = warp_max(v.y);
 }
+
+// Squares of bf16 and fp32 rows leave fp32's range from 2^64 up, and below 2^-75
+// where eps does not cover them.  Such rows take s times a power of two: y, q and
+// y / max|y| do not change with it, and the sum of squares and eps take its square.
+// fp16 rows (below 2^18 with a residual, no square under 2^-48) have no need of it.
+constexpr float kLargeSum = 0x1p100f, kSmallSum = 0x1p-90f;   // of squares
+constexpr float kDown = 0x1p-80f, kUp = 0x1p70f;
+template <typename T, bool NORM> constexpr bool kRange = NORM && !std::is_same_v<T, __half>;
+__device__ __forceinline__ bool too_large(float ss) { return !(ss <= kLargeSum); }   // and NaN
+__device__ __forceinline__ bool too_small(float ss, float eps) { return ss < kSmallSum && eps < kSmallSum; }
 
 // Factors of a row's outputs, v = s * w: y = v * rstd; q = 127 v / max, rounded,
 // with v and max first times `up` where max is so small or large that a factor
@@ -187,16 +198,42 @@ __device__ __forceinline__ void store_q(int8_t* row, int e0, int H, const float 
   }
 }
 
+// Rows and two steps of a grid stay below 2^32.  A row's number is held in what
+// takes fewer registers: with chunks of one element the compiler keeps 64-bit sums.
+template <int VE> using RowIndex = std::conditional_t<VE == 1, int64_t, uint32_t>;
+
 // A thread's chunks of a row, chunk c at element at(c): from v = x + residual
-// to the row's outputs.  g(c, i) is the weight of element i of chunk c.
+// to the row's outputs.  weight(c, g) gives the weights of chunk c; `own` is a slot of
+// shared memory of the thread's own (where kRange).
 template <typename T, int VE, int VPT, bool NORM, typename At, typename Weight>
-__device__ __forceinline__ void finish_row(const RowArgs& p, int64_t row, float (&v)[VPT][VE], float2* sh, At&& at,
-                                           Weight&& weight) {
+__device__ __forceinline__ void finish_row(const RowArgs& p, RowIndex<VE> row, float (&v)[VPT][VE], float2* sh, float* own,
+                                           At&& at, Weight&& weight) {
   const int H = p.H;
-  float ss = 0.f, amax = 0.f;
+  float ss = 0.f, amax = 0.f, eps = p.eps;
   if (p.sum) {
 #pragma unroll
     for (int c = 0; c < VPT; ++c) store_chunk<T, VE>(static_cast<T*>(p.sum) + row * p.lds, at(c), H, v[c]);
+  }
+  // f(v) for all of the thread's values
+  auto each = [&](auto&& f) {
+#pragma unroll
+    for (int c = 0; c < VPT; ++c)
+#pragma unroll
+      for (int i = 0; i < VE; ++i) f(v[c][i]);
+  };
+  // A thread whose own squares leave the range keeps v and their sum in another unit;
+  // a large one adds nothing to the CTA's sum and makes the largest element infinite.
+  bool down = false, up = false;
+  if constexpr (kRange<T, NORM>) {
+    each([&](float x) { ss = fmaf(x, x, ss); });
+    down = too_large(ss), up = too_small(ss, eps);
+    if (down || up) {
+      const float u = up ? kUp : kDown;
+      float sum = 0.f;
+      each([&](float& x) { x *= u, sum = fmaf(x, x, sum); });
+      *own = sum;   // no register for what hardly any row needs
+      if (down) ss = 0.f;
+    }
   }
 #pragma unroll
   for (int c = 0; c < VPT; ++c) {
@@ -204,12 +241,30 @@ __device__ __forceinline__ void finish_row(const RowArgs& p, int64_t row, float 
     if (NORM) weight(c, g);
 #pragma unroll
     for (int i = 0; i < VE; ++i) {
-      if (NORM) ss = fmaf(v[c][i], v[c][i], ss), v[c][i] *= g[i];
+      if (NORM && !kRange<T, NORM>) ss = fmaf(v[c][i], v[c][i], ss);
+      if (NORM) v[c][i] *= g[i];
       amax = max_nan(amax, fabsf(v[c][i]));
     }
   }
+  if (down) amax = INFINITY;
+  if (up) amax /= kUp;
   block_reduce<NORM>(ss, amax, sh);
-  const RowScale f = row_scale<NORM>(ss, amax, H, p.eps);
+  if constexpr (kRange<T, NORM>) {
+    // (an infinite weight does not make a row large)
+    const bool large = !(amax < INFINITY) && __syncthreads_or(down), small = !large && too_small(ss, eps);
+    if (up && !small) each([&](float& x) { x /= kUp; });
+    if (large || small) {   // the row in one unit; where it is small, kUp is every thread's
+      const float u = large ? kDown : kUp;
+      if (large && !down) each([&](float& x) { x *= kDown; });
+      float sum = down || small ? *own : 0.f;
+      amax = 0.f, eps *= u, eps *= u;
+      each([&](float x) { amax = max_nan(amax, fabsf(x)); });
+      __syncthreads();   // sh has been read
+      block_reduce<NORM>(sum, amax, sh);
+      ss = large ? fmaf(ss * kDown, kDown, sum) : sum;
+    }
+  }
+  const RowScale f = row_scale<NORM>(ss, amax, H, eps);
   if (p.y) {
 #pragma unroll
     for (int c = 0; c < VPT; ++c) {
@@ -230,7 +285,8 @@ __device__ __forceinline__ void finish_row(const RowArgs& p, int64_t row, float 
 template <typename T, int VE, int VPT, bool NORM>
 __global__ void __launch_bounds__(1024, 1) k_rows(const RowArgs p) {
   __shared__ float2 sh[32];
-  const int64_t row = blockIdx.x;
+  __shared__ float own[kRange<T, NORM> ? 1024 : 1];
+  const RowIndex<VE> row = blockIdx.x;
   const int H = p.H;
   const T* x = static_cast<const T*>(p.x) + row * p.ldx;
   const T* r = p.r ? static_cast<const T*>(p.r) + row * p.ldr : nullptr;
@@ -247,7 +303,7 @@ __global__ void __launch_bounds__(1024, 1) k_rows(const RowArgs p) {
       for (int i = 0; i < VE; ++i) v[c][i] += rv[i];
     }
   }
-  finish_row<T, VE, VPT, NORM>(p, row, v, sh, at, [&](int c, float(&g)[VE]) {
+  finish_row<T, VE, VPT, NORM>(p, row, v, sh, own + (kRange<T, NORM> ? threadIdx.x : 0), at, [&](int c, float(&g)[VE]) {
     load_chunk<T, VE>(static_cast<const T*>(p.w), at(c), H, g);
   });
 }
@@ -269,29 +325,42 @@ template <typename T> struct Raw<T, 1> {
 // Many rows: persistent CTAs.  The weight stays in registers, and the loads of
 // the next row (RES: with its residual) or of the next two are in flight while
 // this one is reduced and stored.  Whole chunks only.
+// Where rows may leave the range a thread's weights stay in shared memory: what such
+// rows need would spill registers of loads in flight, and a spill waits for its load (8192 x 4096 bf16, residual and int8 out: 39.8 and
+// 50 us; no residual: 25.3 and 36).
 template <typename T, int VE, int VPT, bool NORM, bool RES>
 __global__ void __launch_bounds__(1024, 1) k_rows_many(const RowArgs p, int T_) {
   using R = Raw<T, VE>;
+  using Row = RowIndex<VE>;
+  constexpr bool kShared = kRange<T, NORM>;
   __shared__ float2 sh[2][32];
+  extern __shared__ __align__(16) unsigned char of_thread[];   // kRange: a float for each thread, and its chunks
   const int H = p.H;
   auto at = [&](int c) { return static_cast<int>(threadIdx.x + c * blockDim.x) * VE; };
-  R w[VPT], x[VPT], r[VPT];   // r: the residual, or the row after next
-  auto fetch = [&](R(&to)[VPT], const void* from, int64_t ld, int64_t row) {
+  R x[VPT], r[VPT];   // r: the residual, or the row after next
+  R w[VPT];
+  float* const own = reinterpret_cast<float*>(of_thread) + threadIdx.x;
+  R* const ws = reinterpret_cast<R*>(of_thread + blockDim.x * sizeof(float)) + threadIdx.x;
+  auto fetch = [&](R(&to)[VPT], const void* from, int64_t ld, Row row) {
 #pragma unroll
     for (int c = 0; c < VPT; ++c)
       if (at(c) < H) to[c].load(static_cast<const T*>(from) + row * ld + at(c));
   };
 #pragma unroll
   for (int c = 0; c < VPT; ++c) x[c].zero(), r[c].zero(), w[c].zero();
-  const int64_t step = gridDim.x;
-  int64_t row = blockIdx.x;
+  const Row step = gridDim.x, rows = T_;
+  Row row = blockIdx.x;
   fetch(x, p.x, p.ldx, row);
   if (RES)
     fetch(r, p.r, p.ldr, row);
-  else if (row + step < T_)
+  else if (row + step < rows)
     fetch(r, p.x, p.ldx, row + step);
   if (NORM) fetch(w, p.w, 0, 0);
-  for (int turn = 0; row < T_; row += step, turn ^= 1) {
+  if (kShared) {
+#pragma unroll
+    for (int c = 0; c < VPT; ++c) ws[c * blockDim.x] = w[c];
+  }
+  for (int turn = 0; row < rows; row += step, turn ^= 1) {
     float v[VPT][VE];
 #pragma unroll
     for (int c = 0; c < VPT; ++c) {
@@ -306,14 +375,17 @@ __global__ void __launch_bounds__(1024, 1) k_rows_many(const RowArgs p, int T_) 
       }
     }
     if (RES) {
-      if (row + step < T_) {
+      if (row + step < rows) {
         fetch(x, p.x, p.ldx, row + step);
         fetch(r, p.r, p.ldr, row + step);
       }
-    } else if (row + 2 * step < T_) {
+    } else if (row + 2 * step < rows) {
       fetch(r, p.x, p.ldx, row + 2 * step);
     }
-    finish_row<T, VE, VPT, NORM>(p, row, v, sh[turn], at, [&](int c, float(&g)[VE]) { w[c].unpack(g); });
+    finish_row<T, VE, VPT, NORM>(p, row, v, sh[turn], own, at, [&](int c, float(&g)[VE]) {
+      const R k = kShared ? ws[c * blockDim.x] : w[c];
+      k.unpack(g);
+    });
   }
 }
 
@@ -336,41 +408,62 @@ __global__ void __launch_bounds__(1024, 1) k_rows_long(const RowArgs p) {
     }
     if (NORM) load_chunk<T, VE>(w, e0, H, g);
   };
-  float ss = 0.f, amax = 0.f;
-  for (int64_t e = static_cast<int64_t>(threadIdx.x) * VE; e < H; e += step) {
-    float s[VE], g[VE];
-    load(static_cast<int>(e), s, g);
+  float ss, amax, unit = 1.f, eps = p.eps;
+  auto pass = [&](auto scaled) {
+    ss = 0.f, amax = 0.f;
+    for (int64_t e = static_cast<int64_t>(threadIdx.x) * VE; e < H; e += step) {
+      float s[VE], g[VE];
+      load(static_cast<int>(e), s, g);
 #pragma unroll
-    for (int i = 0; i < VE; ++i) {
-      ss = fmaf(s[i], s[i], ss);
-      amax = max_nan(amax, fabsf(NORM ? s[i] * g[i] : s[i]));
+      for (int i = 0; i < VE; ++i) {
+        if (scaled) s[i] *= unit;
+        ss = fmaf(s[i], s[i], ss);
+        amax = max_nan(amax, fabsf(NORM ? s[i] * g[i] : s[i]));
+      }
     }
+    block_reduce<NORM>(ss, amax, sh);
+  };
+  pass(std::false_type{});
+  if (kRange<T, NORM> && (too_large(ss) || too_small(ss, eps))) {
+    unit = too_large(ss) ? kDown : kUp;
+    eps *= unit, eps *= unit;
+    __syncthreads();   // sh has been read
+    pass(std::true_type{});
   }
-  block_reduce<NORM>(ss, amax, sh);
-  const RowScale f = row_scale<NORM>(ss, amax, H, p.eps);
-  for (int64_t e = static_cast<int64_t>(threadIdx.x) * VE; e < H; e += step) {
-    const int e0 = static_cast<int>(e);
-    float s[VE], g[VE], v[VE];
-    load(e0, s, g);
-    if (p.sum) store_chunk<T, VE>(static_cast<T*>(p.sum) + row * p.lds, e0, H, s);
+  const RowScale f = row_scale<NORM>(ss, amax, H, eps);
+  auto finish = [&](auto scaled) {
+    for (int64_t e = static_cast<int64_t>(threadIdx.x) * VE; e < H; e += step) {
+      const int e0 = static_cast<int>(e);
+      float s[VE], g[VE], v[VE];
+      load(e0, s, g);
+      if (p.sum) store_chunk<T, VE>(static_cast<T*>(p.sum) + row * p.lds, e0, H, s);
 #pragma unroll
-    for (int i = 0; i < VE; ++i) {
-      if (NORM) s[i] *= g[i];
-      v[i] = s[i] * f.rstd;
+      for (int i = 0; i < VE; ++i) {
+        if (scaled) s[i] *= unit;
+        if (NORM) s[i] *= g[i];
+        v[i] = s[i] * f.rstd;
+      }
+      if (p.y) store_chunk<T, VE>(static_cast<T*>(p.y) + row * p.ldy, e0, H, v);
+      if (p.q) store_q<VE, NORM>(p.q + row * p.ldq, e0, H, s, f);
     }
-    if (p.y) store_chunk<T, VE>(static_cast<T*>(p.y) + row * p.ldy, e0, H, v);
-    if (p.q) store_q<VE, NORM>(p.q + row * p.ldq, e0, H, s, f);
-  }
+  };
+  if (unit == 1.f)
+    finish(std::false_type{});
+  else
+    finish(std::true_type{});
   if (p.q && threadIdx.x == 0) p.scale[row] = f.scale / 127.f;
 }
 
 template <typename T, int VE, int VPT, bool NORM>
 void launch_many(const RowArgs& p, int T_, int threads, cudaStream_t s) {
   const int grid = std::min(T_, sm_count() * std::min(32, 1024 / threads));
+  constexpr size_t kThread = !kRange<T, NORM> ? 0 : sizeof(float) + VPT * sizeof(Raw<T, VE>);
+  static_assert(1024 * kThread + sizeof(float2) * 64 <= 48 * 1024, "shared memory");
+  const size_t smem = threads * kThread;
   if (p.r)
-    k_rows_many<T, VE, VPT, NORM, true><<<grid, threads, 0, s>>>(p, T_);
+    k_rows_many<T, VE, VPT, NORM, true><<<grid, threads, smem, s>>>(p, T_);
   else
-    k_rows_many<T, VE, VPT, NORM, false><<<grid, threads, 0, s>>>(p, T_);
+    k_rows_many<T, VE, VPT, NORM, false><<<grid, threads, smem, s>>>(p, T_);
 }
 
 // Few rows take the shortest way through a row, one chunk a thread; many are

@@ -568,7 +568,9 @@ int pw_profile_attach(void* const* events, int n_events);
  *                fp32 s (not from the rounded sum_out)
  *   scale[t]   = max|y[t]| / 127;  q[t] = y[t] / scale[t], rounded to the
  *                nearest whole number (ties to even), y unrounded
- * A row of zeros has y 0, scale 0 and q 0, with eps 0 too.
+ * A row of zeros has y 0, scale 0 and q 0, with eps 0 too.  Squares may leave
+ * fp32's range, s may not: rows of any size up to its ends have their y and scale
+ * (elements 2^-100 below the row's largest may come out as 0).
  * x, residual, weight [H], sum_out and y have element type dtype; q is int8,
  * scale fp32 [T].  residual, sum_out, y and q (with scale) may each be NULL,
  * y and q not both.  A row with a NaN or an infinity gives non-finite y and

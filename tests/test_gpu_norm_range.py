@@ -32,3 +32,67 @@ def test_rows_of_zeros_without_eps(T, H, dt, res):
         assert (y[t] == 0).all() and s[t] == 0 and (q[t] == 0).all()
     assert (y[1] == 1.5).all() and (q[1] == 127).all()
     assert abs(s[1].item() * 127 - 1.5) <= 1.5 * 4 * U
+
+
+def _row(kind, rng, H):
+    n = rng.normal(0, 1, H)
+    return {"large": n * 1e20, "largest": np.clip(n, -3, 3) * 1e38, "sum": n * 1e15, "small": n * 1e-25, "smaller": n * 1e-35,
+            "one_large": np.where(np.arange(H) == H // 2, 1e25, n), "one_normal": np.where(np.arange(H) == H // 3, 1.0, n * 1e-25),
+            "normal": n, "one_small": np.where(np.arange(H) == H - 1, 1e-30, 0.0)}[kind]
+
+
+KINDS = ["large", "largest", "sum", "small", "smaller", "one_large", "one_normal", "normal", "one_small"]
+
+
+@pytest.mark.parametrize("T,H", SHAPES)
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+@pytest.mark.parametrize("res", [False, True])
+def test_rows_whose_squares_leave_the_range(T, H, dt, eps, res):
+    rng = np.random.default_rng([T, H])
+    T = max(T, len(KINDS))
+    a = np.stack([_row(KINDS[t % len(KINDS)], rng, H) for t in range(T)])
+    x = torch.as_tensor(a).to(DT[dt]).cuda()
+    r = torch.as_tensor(a[:, ::-1] * 0.5).to(DT[dt]).cuda() if res else None
+    w = torch.as_tensor(rng.normal(1, 0.1, H)).to(DT[dt]).cuda()
+    # the sum as the kernel has it: fp32, one rounding
+    s = (x.float() + (r.float() if res else 0.0)).double().cpu().numpy()
+    out = torch.empty_like(x)
+    got = pw.pw_rms_norm_i8(x, w, eps, residual=r, out=out)
+    rel = 64 * U
+    if res:
+        assert torch.equal(got[2], torch.as_tensor(s).to(torch.float32).to(DT[dt]).cuda())
+        # the residual stream updated in place
+        out2, s2 = pw.pw_rms_norm(x, w, eps, residual=r, sum_out=r)
+        assert torch.equal(out2.view(torch.uint8), out.view(torch.uint8)) and torch.equal(s2, got[2])
+    # a sum that fp32 does not hold is an infinity, and has no scale
+    inf = np.isinf(s)
+    none, keep = inf.any(1), ~inf.any(1)
+    q, sc = f64(got[0]), f64(got[1])
+    assert np.isnan(f64(out)[inf]).all() and (f64(out)[none][~inf[none]] == 0).all()
+    assert np.isnan(sc[none]).all() and (q[none] == 0).all()
+    out, q, sc, (_, y) = f64(out)[keep], q[keep], sc[keep], ops.rms_norm(s[keep], f64(w), eps)
+    # elements 2^-100 and more below the largest may be lost
+    tiny = np.abs(y).max(1, keepdims=True) * 2.0 ** -100 + 1e-38
+    assert (np.abs(out - y) <= np.abs(y) * (rel + ROUND[dt]) + tiny).all()
+    steps, scale = ops.quant_i8(y)
+    assert (np.abs(sc - scale) <= scale * (rel + 2 * U) + 1e-43).all()
+    assert (np.abs(q - steps) <= 0.5 + 127 * (rel + 4 * U)).all()
+
+
+@pytest.mark.parametrize("T,H", SHAPES)
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_a_weight_that_is_no_number_spoils_its_own_element_only(T, H, dt, bad):
+    rng = np.random.default_rng([T, H, 3])
+    x = torch.as_tensor(rng.normal(0, 2, (T, H))).to(DT[dt]).cuda()
+    w = torch.as_tensor(rng.normal(1, 0.1, H)).to(DT[dt]).cuda()
+    at = H // 2
+    w[at] = bad
+    y = f64(pw.pw_rms_norm(x, w, 1e-6))
+    q, s = pw.pw_rms_norm_i8(x, w, 1e-6)
+    assert not np.isfinite(y[:, at]).any() and not torch.isfinite(s).any() and (q == 0).all()
+    w[at] = 0
+    ref = ops.rms_norm(f64(x), f64(w), 1e-6)[1]
+    keep = np.arange(H) != at
+    assert (np.abs(y - ref)[:, keep] <= (np.abs(ref) * (64 * U + ROUND[dt]) + 2.0 ** -25)[:, keep]).all()
