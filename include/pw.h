@@ -573,9 +573,10 @@ int pw_profile_attach(void* const* events, int n_events);
  * (elements 2^-100 below the row's largest may come out as 0).
  * x, residual, weight [H], sum_out and y have element type dtype; q is int8,
  * scale fp32 [T].  residual, sum_out, y and q (with scale) may each be NULL,
- * y and q not both.  A row with a NaN or an infinity gives non-finite y and
- * scale.  Rows on 16-byte boundaries (q: 8, or 4 for PW_F32) are read 16 bytes
- * at a time, others element by element.
+ * y and q not both.  A row with a NaN has y NaN; one with an infinity has y NaN
+ * there and 0 elsewhere; either has scale NaN and q 0.
+ * Rows on 16-byte boundaries (q: 8, or 4 for PW_F32) are read 16 bytes at a time,
+ * others element by element.
  * Errors: PW_EINVAL (shapes, strides, null or misaligned pointers, dtype, eps
  * negative or NaN), PW_ECUDA.
  */

@@ -96,3 +96,20 @@ def test_a_weight_that_is_no_number_spoils_its_own_element_only(T, H, dt, bad):
     ref = ops.rms_norm(f64(x), f64(w), 1e-6)[1]
     keep = np.arange(H) != at
     assert (np.abs(y - ref)[:, keep] <= (np.abs(ref) * (64 * U + ROUND[dt]) + 2.0 ** -25)[:, keep]).all()
+
+
+@pytest.mark.parametrize("T,H", SHAPES)
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+def test_rows_with_infinities_and_nan(T, H, dt):
+    """As the formula gives: 0 beside an infinity (a finite number by an infinite root),
+    NaN at it; a NaN is everywhere.  No scale, and q 0."""
+    rng = np.random.default_rng([T, H, 5])
+    x = torch.as_tensor(rng.normal(0, 2, (T, H))).to(DT[dt]).cuda()
+    w = torch.as_tensor(rng.normal(1, 0.1, H)).to(DT[dt]).cuda()
+    x[0, H // 2], x[1, 0], x[2, H - 1] = float("inf"), float("nan"), -float("inf")
+    y = pw.pw_rms_norm(x, w, 1e-6)
+    q, s = pw.pw_rms_norm_i8(x, w, 1e-6)
+    for t, at in ((0, H // 2), (2, H - 1)):
+        assert torch.isnan(y[t, at]) and (y[t, :at] == 0).all() and (y[t, at + 1:] == 0).all()
+    assert torch.isnan(y[1]).all() and torch.isnan(s[:3]).all() and (q[:3] == 0).all()
+    assert torch.isfinite(y[3:]).all() and torch.isfinite(s[3:]).all()
