@@ -94,6 +94,7 @@ _SIGS = {
                           _vp]),
     "pw_linear_i8_workspace_bytes": (_sz, [_i, _i]),
     "pw_linear_i8_status": (_i, [_vp, _pi]),
+    "pw_debug_linear_timeout": (_i, [_vp]),
     "pw_logprobs": (_i, [_vp, _i64, _i, _i, _i, _vp, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp]),
 }
 
@@ -712,10 +713,15 @@ def pw_linear_i8_workspace_bytes(T: int, K: int) -> int:
 
 
 def pw_linear_i8_status(stream=None) -> int:
-    """Status bits that pw_linear_i8 calls ordered before `stream`'s work have raised."""
+    """Status bits that pw_linear_i8 calls have raised since the previous status call,
+    those ordered before `stream`'s work included."""
     st = _i()
     _check(lib().pw_linear_i8_status(_stream(stream), ctypes.byref(st)), "pw_linear_i8_status")
     return st.value
+
+
+def pw_debug_linear_timeout(stream=None):
+    return _check(lib().pw_debug_linear_timeout(_stream(stream)), "pw_debug_linear_timeout")
 
 
 class LogProbs(NamedTuple):

@@ -42,8 +42,9 @@ struct LinArgs {
   int T, N, K;
 };
 
-// PW_STATUS_* bits of the tensor-core kernel's bounded waits (pw_linear_i8_status).
-__device__ int g_linear_status;
+// Bounded waits of the tensor-core kernels that gave up (pw_linear_i8_status).
+__device__ uint32_t g_linear_timeouts;
+__global__ void k_count_timeout() { atomicAdd(&g_linear_timeouts, 1u); }
 
 template <typename O>
 __device__ __forceinline__ void store_out(const LinArgs& p, int t, int n, int acc, float xs, float ws, float bias) {
@@ -499,7 +500,7 @@ __device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, volatile int
   for (int n = 0; !test_wait(bar, parity); ++n) {
     if (*abort) return false;
     if (n == kPolls) {
-      atomicOr(&g_linear_status, PW_STATUS_TIMEOUT);
+      atomicAdd(&g_linear_timeouts, 1u);
       *abort = 1;
       return false;
     }
@@ -1457,12 +1458,28 @@ int pw_linear_i8_status(pw_stream_t s, int* status) {
   pw::NvtxCall nvtx_range("pw_linear_i8_status");
   if (!status) return pw::failf(PW_EINVAL, "pw_linear_i8_status: null status");
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(s);
-  int v = 0;
-  cudaError_t e = cudaMemcpyFromSymbolAsync(&v, pw::g_linear_status, sizeof v, 0, cudaMemcpyDeviceToHost, st);
+  uint32_t now = 0;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && (dev < 0 || dev >= pw::kMaxDev)) e = cudaErrorInvalidDevice;
+  if (e == cudaSuccess)
+    e = cudaMemcpyFromSymbolAsync(&now, pw::g_linear_timeouts, sizeof now, 0, cudaMemcpyDeviceToHost, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e != cudaSuccess) return pw::failf(PW_ECUDA, "pw_linear_i8_status: %s", cudaGetErrorString(e));
-  *status = v;
+  // the count up to which an earlier call has told; another thread may tell meanwhile
+  static std::atomic<uint32_t> told[pw::kMaxDev];
+  uint32_t before = told[dev].load();
+  bool more = false;
+  while ((more = static_cast<int32_t>(now - before) > 0) && !told[dev].compare_exchange_weak(before, now)) {
+  }
+  *status = more ? PW_STATUS_TIMEOUT : 0;
   return PW_OK;
+}
+
+int pw_debug_linear_timeout(pw_stream_t s) {
+  pw::NvtxCall nvtx_range("pw_debug_linear_timeout");
+  pw::k_count_timeout<<<1, 1, 0, reinterpret_cast<cudaStream_t>(s)>>>();
+  return pw::launch_status(cudaGetLastError(), "pw_debug_linear_timeout");
 }
 
 }  // extern "C"

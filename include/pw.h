@@ -621,11 +621,20 @@ int pw_linear_i8(const int8_t* x, int64_t ldx, const float* x_scale, const int8_
 
 /*
  * pw_linear_i8_status -- the PW_STATUS_* bits that pw_linear_i8 calls on the
- * current device have raised so far (0, or PW_STATUS_TIMEOUT when a bounded
- * device-side wait gave up: that call's outputs are not valid).  Covers the
- * work ordered before this call on `s`; synchronises `s`.
+ * current device have raised since the previous pw_linear_i8_status there (0, or
+ * PW_STATUS_TIMEOUT when a bounded device-side wait gave up: that call's outputs
+ * are not valid).  Covers the work ordered before this call on `s`; synchronises
+ * `s`.  The device counts the waits that gave up, and of several threads that ask
+ * at once one is told: a program that asks from several threads shares the answer.
  */
 int pw_linear_i8_status(pw_stream_t s, int* status);
+
+/*
+ * pw_debug_linear_timeout -- test hook for pw_linear_i8_status: counts, in the order
+ * of `s`, a wait as one that gave up.  No wait does.
+ * Errors: PW_ECUDA.
+ */
+int pw_debug_linear_timeout(pw_stream_t s);
 
 /*
  * pw_logprobs -- what a row of logits says about a token, and its alternatives.
