@@ -1,6 +1,8 @@
 """The operators' outputs against the fp64 oracle by a comparison that a NaN cannot
 pass: norms with what the int8 call writes beside its rows, 16-bit products, and
 the norms and products of a decode step.  Tolerances as in test_gpu_operators.py."""
+import itertools
+
 import numpy as np
 import pytest
 import torch
@@ -16,41 +18,40 @@ pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("T,H", NORMS + [(305, 8), (700, 256), (999, 513), (457, 4096), (310, 8191), (305, 14336)])
-@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
-@pytest.mark.parametrize("res", [False, True])
-def test_norms_and_what_they_write_beside(T, H, dt, res):
-    rng = gen(T, H, dt, res, "values")
-    x = place(rng.standard_normal((T, H), np.float32) * 2, DT[dt])
-    w = torch.as_tensor(rng.normal(1, 0.3, H)).to(DT[dt]).cuda()
-    r = place(rng.standard_normal((T, H), np.float32) * 3, DT[dt]) if res else None
-    s, y = ops.rms_norm(f64(x), f64(w), 1e-5, f64(r) if res else None)
-    # the sum's own rounding moves elements beside which it is large
-    extra = np.abs(f64(w)) * 4 * U if res else 0.0
-    a = pw.pw_rms_norm(x, w, 1e-5, residual=r)
-    out = torch.full_like(x, float("nan"))
-    b = pw.pw_rms_norm_i8(x, w, 1e-5, residual=r, out=out)
-    assert_values(f64(a[0] if res else a), y, dt, 64 * U, extra)
-    assert_values(f64(out), y, dt, 64 * U, extra)
-    check_q(b[0], b[1], y, 72 * U)
-    if res:
-        assert_values(f64(a[1]), s, dt, U)
-        assert_values(f64(b[2]), s, dt, U)
+def test_norms_and_what_they_write_beside(T, H):
+    for dt, res in itertools.product(["f16", "bf16", "f32"], [False, True]):
+        rng = gen(T, H, dt, res, "values")
+        x = place(rng.standard_normal((T, H), np.float32) * 2, DT[dt])
+        w = torch.as_tensor(rng.normal(1, 0.3, H)).to(DT[dt]).cuda()
+        r = place(rng.standard_normal((T, H), np.float32) * 3, DT[dt]) if res else None
+        s, y = ops.rms_norm(f64(x), f64(w), 1e-5, f64(r) if res else None)
+        # the sum's own rounding moves elements beside which it is large
+        extra = np.abs(f64(w)) * 4 * U if res else 0.0
+        a = pw.pw_rms_norm(x, w, 1e-5, residual=r)
+        out = torch.full_like(x, float("nan"))
+        b = pw.pw_rms_norm_i8(x, w, 1e-5, residual=r, out=out)
+        assert_values(f64(a[0] if res else a), y, dt, 64 * U, extra)
+        assert_values(f64(out), y, dt, 64 * U, extra)
+        check_q(b[0], b[1], y, 72 * U)
+        if res:
+            assert_values(f64(a[1]), s, dt, U)
+            assert_values(f64(b[2]), s, dt, U)
 
 
 @pytest.mark.parametrize("T,N,K", [(1, 60, 2048), (12, 333, 1411), (24, 20001, 512), (37, 333, 4096), (100, 1411, 1411),
                                    (128, 20001, 1040), (300, 1000, 3000)])
-@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
-def test_products(T, N, K, dt):
-    x, xs, w, ws, b = _linear_case(T, N, K, dt, True, seed=1)
-    out = torch.full((T, N), float("nan"), dtype=DT[dt], device="cuda")
-    pw.pw_linear_i8(x, xs, w, ws, bias=b, out=out)
-    acc, ref = ops.linear_i8(f64(x), f64(xs), f64(w), f64(ws), f64(b))
-    prod = np.abs(acc * f64(xs)[:, None] * f64(ws)[None, :])
-    if dt == "f16":   # beyond its range there is nothing to compare
-        far = np.abs(ref) > 65504.0
-        ref[far], prod[far] = 0.0, 0.0
-        out[torch.as_tensor(far).cuda()] = 0.0
-    assert_values(f64(out), ref, dt, U, extra=prod * 3 * U)
+def test_products(T, N, K):
+    for dt in ("f16", "bf16", "f32"):
+        x, xs, w, ws, b = _linear_case(T, N, K, dt, True, seed=1)
+        out = torch.full((T, N), float("nan"), dtype=DT[dt], device="cuda")
+        pw.pw_linear_i8(x, xs, w, ws, bias=b, out=out)
+        acc, ref = ops.linear_i8(f64(x), f64(xs), f64(w), f64(ws), f64(b))
+        prod = np.abs(acc * f64(xs)[:, None] * f64(ws)[None, :])
+        if dt == "f16":   # beyond its range there is nothing to compare
+            far = np.abs(ref) > 65504.0
+            ref[far], prod[far] = 0.0, 0.0
+            out[torch.as_tensor(far).cuda()] = 0.0
+        assert_values(f64(out), ref, dt, U, extra=prod * 3 * U)
 
 
 @pytest.mark.parametrize("batch", [1, 20, 100])
