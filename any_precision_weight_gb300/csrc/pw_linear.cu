@@ -6,13 +6,13 @@
 // the sum exact in int32 (K <= 131071: 128 * 128 * K < 2^31).
 //
 // Few tokens, or little to do: k_few, tensor-core products fed from registers,
-// the weights streamed once (for each block of tokens).  Up to 128 and more: k_thin and k_tc on the 5th-generation
-// tensor cores.  This GPU's int8 tensor rate is a small part of its 16-bit rate, and
-// tcgen05 has no int8 kind here, so that work runs in fp16: int8 values are
-// exact in fp16, their products (at most 2^14) are exact in fp32, and so are
-// sums of up to 1024 of them (2^24).  Every 1024 terms the fp32 accumulator
-// moves from tensor memory into int32 registers, so the sum is the
-// whole-number one at any K.
+// the weights streamed once (for each block of tokens).  Otherwise k_thin up to 128
+// tokens and k_tc above, on the 5th-generation tensor cores.  This GPU's int8 tensor
+// rate is a small part of its 16-bit rate, and tcgen05 has no int8 kind here, so
+// that work runs in fp16: int8 values are exact in fp16, their products (at most
+// 2^14) are exact in fp32, and so are sums of up to 1024 of them (2^24).  Every 1024
+// terms the fp32 accumulator moves from tensor memory into int32 registers, so the
+// sum is the whole-number one at any K.
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -343,11 +343,11 @@ cudaError_t launch_few(const LinArgs& p, cudaStream_t s) {
 // Where there are few tiles a cluster of CTAs splits K and adds the parts
 // through distributed shared memory; whole numbers, so in any order.
 //
-// 28672 x 4096 weights: 1024, 2048, 4096 tokens in 149, 290 and 573 us (1617 to
+// 28672 x 4096 weights: 1024, 2048, 4096 tokens in 148, 290 and 573 us (1617 to
 // 1678 TFLOP/s, 86 to 89 % of the 16-bit library product in isolation, and near
 // its rate in a long run: the power limit is in reach).  2048 x 4096 x 14336:
 // 177 us, 1360 TFLOP/s, 128 tiles in two turns of 76 pairs.  333 x 5003 x 1411:
-// 19 us, a chain of k_widen, 23 stages, the joins and the stores.  One CTA to a
+// 18 us, a chain of k_widen, 23 stages, the joins and the stores.  One CTA to a
 // tile, converting the tokens too, took 238 us of the 177; two issuers, or two
 // stages to a barrier, gained nothing; the last two turns' tiles cut into equal
 // runs of K gave 171, and 160 instead of 153 at 1024 x 28672 x 4096.
@@ -1359,7 +1359,7 @@ cudaError_t launch_thin(const LinArgs& p, void* ws, cudaStream_t s) {
   // channels of a tile: what gives the SMs the least to do in turn, a stage's
   // time being some constant and a part that grows with them.  64 x 28672 x 4096:
   // 42.1 us with 256 (112 tiles), 39.0 with 192 (150), 58 with 128 (two turns);
-  // 32 x 131072 x 4096: 124, 137 and, with the 224 of the rule, 118; 128 x 4096 x
+  // 32 x 131072 x 4096: 125, 135 and, with the 224 of the rule, 119; 128 x 4096 x
   // 14336: 43.3, 39.4 and, K split over more CTAs with 128, 34.8
   int nw = kThinN, split = 1;
   float least = 0.f;
@@ -1398,6 +1398,8 @@ cudaError_t launch_linear(const LinArgs& p, void* ws, cudaStream_t s) {
   return launch_tc<O>(p, ws, s);
 }
 
+// By the tokens alone, so that one workspace serves a model's products of any N; the
+// calls above kFewTokens that k_few takes leave it untouched.
 size_t linear_ws_bytes(int T, int K) {
   return T <= kFewTokens ? 0 : static_cast<size_t>(T) * padded_k(K) * 2;
 }

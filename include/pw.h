@@ -547,7 +547,8 @@ int pw_profile_attach(void* const* events, int n_events);
  * PW_BF16 or PW_F32; a matrix is rows of consecutive elements whose starts are
  * `ld*` elements apart (ld >= the row's length, 64-bit), so padded and sliced
  * matrices need no copy.  Work is enqueued on `s` and nothing waits; nothing
- * is kept between calls, so calls on several streams may overlap.  T = 0 is a
+ * is kept between calls but the count of waits that gave up (pw_linear_i8_status),
+ * so calls on several streams may overlap.  Operands lie on the current device.  T = 0 is a
  * no-op.  A call may be captured into a CUDA graph.  Results do not depend on
  * what else runs: a call repeated on the same inputs gives the same bits.
  */
@@ -595,8 +596,10 @@ int pw_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, c
 int pw_quant_i8(const void* x, int64_t ldx, int T, int K, int dtype, int8_t* q, int64_t ldq, float* scale,
                 pw_stream_t s);
 
-/* Bytes of device workspace that pw_linear_i8 needs: 0 up to 16 tokens, then
- * the tokens as fp16.  0 for a bad shape. */
+/* Bytes of device workspace that pw_linear_i8 asks for: 0 up to 16 tokens, then room
+ * for the tokens as fp16.  The figure is one for every N: calls with few channels do
+ * not touch the workspace, and are refused without it all the same.  0 for a bad
+ * shape. */
 size_t pw_linear_i8_workspace_bytes(int T, int K);
 
 /*
