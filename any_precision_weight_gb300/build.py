@@ -19,6 +19,7 @@ CHECK_LIB = os.path.join(HERE, "libpw_check.so")
 
 SOURCES = ["pw_runtime.cpp", "pw_planner.cpp", "pw_kernels.cu", "pw_decode.cu", "pw_prefill.cu", "pw_static.cu",
            "pw_norm.cu", "pw_linear.cu", "pw_logprobs.cu"]
+UNCHECKED = {"pw_norm.cu", "pw_linear.cu", "pw_logprobs.cu"}   # no PW_CHECK code: one object for both libraries
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -65,12 +66,11 @@ def build(verbose: bool = False) -> str:
     """libpw.so, and libpw_check.so: the same sources with PW_CHECK defined
     (device-side bounds checks that report PW_STATUS_BOUNDS)."""
     os.makedirs(BUILD, exist_ok=True)
-    jobs = [(s, c) for c in (False, True) for s in SOURCES]
+    jobs = [(s, c) for c in (False, True) for s in SOURCES if not (c and s in UNCHECKED)]
     with ThreadPoolExecutor(max_workers=len(jobs)) as ex:
-        objs = list(ex.map(_compile, jobs))
-    n = len(SOURCES)
-    _link(objs[:n], LIB)
-    _link(objs[n:], CHECK_LIB)
+        objs = dict(zip(jobs, ex.map(_compile, jobs)))
+    _link([objs[s, False] for s in SOURCES], LIB)
+    _link([objs[s, s not in UNCHECKED] for s in SOURCES], CHECK_LIB)
     if verbose:
         for s in SOURCES:
             p = os.path.join(BUILD, os.path.splitext(s)[0] + ".ptxas.txt")
