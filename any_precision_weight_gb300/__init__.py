@@ -42,6 +42,8 @@ MAX_BITS = 8
 PW_F16, PW_BF16, PW_F32 = 0, 1, 2
 MAX_K_I8 = 131071
 MAX_TOP = 32
+MAX_GROUPS = 512
+F8_BLOCK = 128   # columns, and rows of weights, that share a scale
 
 _lib = None
 
@@ -96,6 +98,15 @@ _SIGS = {
     "pw_linear_i8_status": (_i, [_vp, _pi]),
     "pw_debug_linear_timeout": (_i, [_vp]),
     "pw_logprobs": (_i, [_vp, _i64, _i, _i, _i, _vp, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "pw_route_workspace_bytes": (_sz, [_i, _i, _i]),
+    "pw_route": (_i, [_vp, _i64, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "pw_quant_f8": (_i, [_vp, _i64, _i64, _vp, _i, _i, _i, _i, _vp, _i64, _vp, _i64, _vp]),
+    "pw_silu_quant_f8": (_i, [_vp, _i64, _i, _i, _i, _vp, _i64, _vp, _i64, _vp]),
+    "pw_quant_f8_blocks": (_i, [_vp, _i64, _i, _i, _i, _vp, _i64, _vp, _i64, _vp]),
+    "pw_linear_f8": (_i, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i, _i, _i, _i, _vp, _i64, _vp]),
+    "pw_grouped_linear_f8": (_i, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i, _i, _i, _i,
+                                  _i, _vp, _i64, _vp]),
+    "pw_combine": (_i, [_vp, _i64, _i64, _i, _vp, _vp, _vp, _i64, _i, _i, _i, _i, _vp, _i64, _vp]),
 }
 
 
@@ -763,3 +774,205 @@ def pw_logprobs(logits, ids=None, top: int = 0, out=None, stream=None):
                              ti.data_ptr() if top else None, tl.data_ptr() if top else None,
                              raw), "pw_logprobs")
     return LogProbs(lp, rank, ent, ti, tl)
+
+
+# ----------------------------------------------------------------------------- expert layers in 8-bit floating point
+
+# The conventions are those of the operators above.  8-bit numbers are
+# torch.float8_e4m3fn; scales are float32, one for every 128 columns.
+
+def f8_blocks(n: int) -> int:
+    """Scales of n columns (or of n rows of weights)."""
+    return (n + F8_BLOCK - 1) // F8_BLOCK
+
+
+def rows_f8(*shape, device="cuda", stream=None):
+    """An uninitialised e4m3 tensor [..][K] whose rows start on 16-byte
+    boundaries, as pw_linear_f8 wants them (a view of a padded one), in memory
+    of the given stream or the current one."""
+    torch = _torch()
+    K = shape[-1]
+    return _empty(torch, stream, (*shape[:-1], (K + 15) // 16 * 16), torch.float8_e4m3fn, device)[..., :K]
+
+
+def _stack(t, name: str, dtype, shape, dev):
+    """(row stride, stride of the first axis) of [E][rows][columns] on the call's
+    device whose rows are consecutive elements."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: {dtype} is needed, got {t.dtype}")
+    if t.shape != shape or _away(t, dev):
+        raise ValueError(f"{name}: a tensor of shape {tuple(shape)} on the call's GPU is needed, "
+                         f"got {tuple(t.shape)} on {t.device}")
+    group, ld, one = t.stride()
+    if one != 1 and shape[2] > 1:
+        raise ValueError(f"{name}: the elements of a row must be consecutive")
+    # an axis of one has no stride of its own
+    return ld if shape[1] > 1 else (shape[2] + 15) // 16 * 16, group if shape[0] > 1 else 0
+
+
+class Routing(NamedTuple):
+    """What pw_route returns."""
+    idx: object
+    weight: object
+    offsets: object
+    perm: object
+    inv: object
+
+
+def pw_route_workspace_bytes(T: int, E: int, k: int) -> int:
+    return lib().pw_route_workspace_bytes(T, E, k)
+
+
+def pw_route(logits, top_k: int, renorm: bool = False, out=None, ws=None, stream=None):
+    """A Routing of logits [T][E] float32: the top_k experts of every token and their
+    softmax weights [T][top_k] (renorm: over the chosen ones), offsets [E + 1] of the
+    routed pairs in expert order, the pair id t * top_k + j at each place (perm) and
+    the place of each pair (inv).  out: a Routing (or tuple) to write into.  ws: a
+    uint8 workspace of pw_route_workspace_bytes bytes (allocated here where it is
+    needed and not given)."""
+    torch = _torch()
+    (T, E), (dev, raw) = _matrix(logits, "logits"), _place(torch, logits, "logits", stream)
+    f32, i32, P = torch.float32, torch.int32, T * top_k
+    if out is None:
+        new = lambda dt, *shape: _empty(torch, stream, shape, dt, logits.device)
+        out = (new(i32, T, top_k), new(f32, T, top_k), new(i32, E + 1), new(i32, P), new(i32, P))
+    idx, weight, offsets, perm, inv = out
+    for name, t, dt in (("idx", idx, i32), ("weight", weight, f32)):
+        if t.shape != (T, top_k) or t.dtype is not dt or not t.is_contiguous() or _away(t, dev):
+            raise ValueError(f"{name}: a contiguous matrix [{T}][{top_k}] of {dt} on the call's GPU is needed")
+    L = lib()
+    if ws is None:
+        need = L.pw_route_workspace_bytes(T, E, top_k)
+        if need:
+            ws = _empty(torch, stream, (need,), torch.uint8, logits.device)
+    elif ws.dtype is not torch.uint8 or not ws.is_contiguous() or _away(ws, dev):
+        raise ValueError(f"ws: a contiguous uint8 tensor on the call's GPU is needed, got {ws.dtype} on {ws.device}")
+    _check(L.pw_route(logits.data_ptr(), _rows(logits, "logits", f32, (T, E), dev), T, E, top_k, int(renorm),
+                      idx.data_ptr(), weight.data_ptr(), _vec(offsets, "offsets", i32, E + 1, dev),
+                      _vec(perm, "perm", i32, P, dev), _vec(inv, "inv", i32, P, dev),
+                      None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), raw), "pw_route")
+    return Routing(idx, weight, offsets, perm, inv)
+
+
+def _quant_f8(torch, stream, dev, x, T, K, scale_rows, q, scale):
+    """(q, its address and row stride, scale, its address and row stride) of a
+    quantiser, made where they are not given."""
+    shape = (scale_rows, f8_blocks(K))
+    if q is None:
+        q = rows_f8(T, K, device=x.device, stream=stream)
+    if scale is None:
+        scale = _empty(torch, stream, shape, torch.float32, x.device)
+    return (q, scale, q.data_ptr(), _rows(q, "q", torch.float8_e4m3fn, (T, K), dev), scale.data_ptr(),
+            _rows(scale, "scale", torch.float32, shape, dev))
+
+
+def pw_quant_f8(x, rows=None, per: int = 1, q=None, scale=None, stream=None):
+    """(q, scale): the rows of x as e4m3 with a scale for every 128 columns.  rows
+    (int32): row t is x[rows[t] // per], so that a Routing's perm with per = top_k
+    gives the tokens in expert order."""
+    torch = _torch()
+    (n, K), (dev, raw) = _matrix(x, "x"), _place(torch, x, "x", stream)
+    T, pr = n, None
+    if rows is not None:
+        T = rows.shape[0]
+        pr = _vec(rows, "rows", torch.int32, T, dev)
+    q, scale, pq, lq, ps, ls = _quant_f8(torch, stream, dev, x, T, K, T, q, scale)
+    _check(lib().pw_quant_f8(x.data_ptr(), _rows(x, "x", x.dtype, (n, K), dev), n, pr, per, T, K, _code(x.dtype), pq, lq,
+                             ps, ls, raw), "pw_quant_f8")
+    return q, scale
+
+
+def pw_silu_quant_f8(x, q=None, scale=None, stream=None):
+    """(q, scale) of silu(gate) * up, x [T][2 K] with the gate columns first."""
+    torch = _torch()
+    (T, K2), (dev, raw) = _matrix(x, "x"), _place(torch, x, "x", stream)
+    if K2 % 2:
+        raise ValueError(f"x: gate and up columns are needed, got {K2}")
+    q, scale, pq, lq, ps, ls = _quant_f8(torch, stream, dev, x, T, K2 // 2, T, q, scale)
+    _check(lib().pw_silu_quant_f8(x.data_ptr(), _rows(x, "x", x.dtype, (T, K2), dev), T, K2 // 2, _code(x.dtype), pq, lq,
+                                  ps, ls, raw), "pw_silu_quant_f8")
+    return q, scale
+
+
+def pw_quant_f8_blocks(w, q=None, scale=None, stream=None):
+    """(q, scale): weights [N][K] as e4m3 with a scale for each block of 128 x 128."""
+    torch = _torch()
+    (N, K), (dev, raw) = _matrix(w, "w"), _place(torch, w, "w", stream)
+    q, scale, pq, lq, ps, ls = _quant_f8(torch, stream, dev, w, N, K, f8_blocks(N), q, scale)
+    _check(lib().pw_quant_f8_blocks(w.data_ptr(), _rows(w, "w", w.dtype, (N, K), dev), N, K, _code(w.dtype), pq, lq, ps,
+                                    ls, raw), "pw_quant_f8_blocks")
+    return q, scale
+
+
+def _f8_out(torch, stream, what, x, shape, out, out_dtype):
+    if out is None:
+        return _empty(torch, stream, shape, out_dtype or torch.float16, x.device)
+    if out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"{what}: out is {out.dtype}, not {out_dtype}")
+    return out
+
+
+def pw_linear_f8(x, x_scale, w, w_scale, bias=None, out=None, out_dtype=None, stream=None):
+    """out [T][N] = x . w^T (+ bias), x [T][K] and w [N][K] e4m3 with 16-byte
+    aligned rows (rows_f8), x_scale [T][ceil(K / 128)] and w_scale [ceil(N / 128)]
+    [ceil(K / 128)], as pw_quant_f8 and pw_quant_f8_blocks write them.  out has type
+    out_dtype (default float16) where it is not given."""
+    torch = _torch()
+    T, K = _matrix(x, "x")
+    N, (dev, raw) = _matrix(w, "w")[0], _place(torch, x, "x", stream)
+    out = _f8_out(torch, stream, "pw_linear_f8", x, (T, N), out, out_dtype)
+    dt, f32, f8, kb = out.dtype, torch.float32, torch.float8_e4m3fn, f8_blocks(K)
+    _check(lib().pw_linear_f8(x.data_ptr(), _rows(x, "x", f8, (T, K), dev), x_scale.data_ptr(),
+                              _rows(x_scale, "x_scale", f32, (T, kb), dev), w.data_ptr(), _rows(w, "w", f8, (N, K), dev),
+                              w_scale.data_ptr(), _rows(w_scale, "w_scale", f32, (f8_blocks(N), kb), dev),
+                              None if bias is None else _vec(bias, "bias", dt, N, dev), T, N, K, _code(dt),
+                              out.data_ptr(), _rows(out, "out", dt, (T, N), dev), raw), "pw_linear_f8")
+    return out
+
+
+def pw_grouped_linear_f8(x, x_scale, w, w_scale, offsets, bias=None, out=None, out_dtype=None, stream=None):
+    """pw_linear_f8 of rows sorted by expert: rows [offsets[e], offsets[e + 1]) of x
+    with w[e], w_scale[e] and bias[e]; w [E][N][K], w_scale [E][ceil(N / 128)][ceil(K /
+    128)], bias [E][N], offsets [E + 1] int32 on the GPU (pw_route).  Rows outside every
+    range are left as they are."""
+    torch = _torch()
+    T, K = _matrix(x, "x")
+    if w.dim() != 3:
+        raise ValueError(f"w: weights [E][N][K] are needed, got {w.dim()} dimensions")
+    (E, N, _), (dev, raw) = w.shape, _place(torch, x, "x", stream)
+    out = _f8_out(torch, stream, "pw_grouped_linear_f8", x, (T, N), out, out_dtype)
+    dt, f32, f8, kb = out.dtype, torch.float32, torch.float8_e4m3fn, f8_blocks(K)
+    ldw, gw = _stack(w, "w", f8, (E, N, K), dev)
+    ldws, gws = _stack(w_scale, "w_scale", f32, (E, f8_blocks(N), kb), dev)
+    if bias is not None and (bias.dtype is not dt or bias.shape != (E, N) or not bias.is_contiguous() or _away(bias, dev)):
+        raise ValueError(f"bias: a contiguous matrix [{E}][{N}] of {dt} on the call's GPU is needed")
+    _check(lib().pw_grouped_linear_f8(x.data_ptr(), _rows(x, "x", f8, (T, K), dev), x_scale.data_ptr(),
+                                      _rows(x_scale, "x_scale", f32, (T, kb), dev), w.data_ptr(), ldw, gw,
+                                      w_scale.data_ptr(), ldws, gws,
+                                      _vec(offsets, "offsets", torch.int32, E + 1, dev),
+                                      None if bias is None else bias.data_ptr(), T, E, N, K, _code(dt), out.data_ptr(),
+                                      _rows(out, "out", dt, (T, N), dev), raw), "pw_grouped_linear_f8")
+    return out
+
+
+def pw_combine(y, weight, inv, residual=None, out=None, out_dtype=None, stream=None):
+    """out [T][H] = residual + sum_j weight[t][j] * y[inv[t][j]]: y [rows][H] in expert
+    order, weight [T][k] and inv ([T * k] or [T][k]) of a Routing.  out has type
+    out_dtype (default: the residual's, or y's) where it is not given."""
+    torch = _torch()
+    R, H = _matrix(y, "y")
+    (T, k), (dev, raw) = _matrix(weight, "weight"), _place(torch, y, "y", stream)
+    if out_dtype is None and out is None:
+        out_dtype = y.dtype if residual is None else residual.dtype
+    out = _f8_out(torch, stream, "pw_combine", y, (T, H), out, out_dtype)
+    dt, pr, lr = out.dtype, None, 0
+    if residual is not None:
+        lr, pr = _rows(residual, "residual", dt, (T, H), dev), residual.data_ptr()
+    if weight.dtype is not torch.float32 or not weight.is_contiguous() or _away(weight, dev):
+        raise ValueError(f"weight: a contiguous float32 matrix [{T}][{k}] on the call's GPU is needed")
+    if inv.dtype is not torch.int32 or inv.numel() != T * k or not inv.is_contiguous() or _away(inv, dev):
+        raise ValueError(f"inv: {T * k} consecutive int32 on the call's GPU are needed")
+    _check(lib().pw_combine(y.data_ptr(), _rows(y, "y", y.dtype, (R, H), dev), R, _code(y.dtype), weight.data_ptr(),
+                            inv.data_ptr(), pr, lr, T, k, H, _code(dt), out.data_ptr(), _rows(out, "out", dt, (T, H), dev),
+                            raw), "pw_combine")
+    return out

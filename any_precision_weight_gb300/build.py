@@ -18,8 +18,8 @@ LIB = os.path.join(HERE, "libpw.so")
 CHECK_LIB = os.path.join(HERE, "libpw_check.so")
 
 SOURCES = ["pw_runtime.cpp", "pw_planner.cpp", "pw_kernels.cu", "pw_decode.cu", "pw_prefill.cu", "pw_static.cu",
-           "pw_norm.cu", "pw_linear.cu", "pw_logprobs.cu"]
-UNCHECKED = {"pw_norm.cu", "pw_linear.cu", "pw_logprobs.cu"}   # no PW_CHECK code: one object for both libraries
+           "pw_norm.cu", "pw_linear.cu", "pw_logprobs.cu", "pw_f8.cu", "pw_f8_rows.cu", "pw_router.cu"]
+UNCHECKED = {"pw_norm.cu", "pw_linear.cu", "pw_logprobs.cu", "pw_f8.cu", "pw_f8_rows.cu", "pw_router.cu"}   # no PW_CHECK code: one object for both libraries
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

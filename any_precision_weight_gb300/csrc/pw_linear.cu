@@ -445,28 +445,6 @@ struct Weights {
   }
 };
 
-// 16 consecutive fp32 columns of this thread's TMEM lane (after tmem_wait).
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
-// The loads issued so far have arrived; r cannot be used before.
-__device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-               :
-               : "memory");
-}
-
-__device__ __forceinline__ void cta_barrier() { asm volatile("bar.sync 0;" ::: "memory"); }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 __device__ __forceinline__ int4 ld_cluster(uint32_t addr, uint32_t rank) {
   uint32_t a;
   int4 v;
@@ -476,19 +454,6 @@ __device__ __forceinline__ int4 ld_cluster(uint32_t addr, uint32_t rank) {
                : "r"(a)
                : "memory");
   return v;
-}
-
-// Whether the phase of the given parity has ended; never waits.
-__device__ __forceinline__ bool test_wait(uint32_t bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return done;
 }
 
 // Polls up to kPolls times (about a second; PAUSE ns between two) for the phase
@@ -509,19 +474,7 @@ __device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, volatile int
   return true;
 }
 
-// Arrives at the barrier that has this address in CTA `rank` of the cluster.
-// What it reports is shared memory of the arriving CTA, which only the tensor
-// cores read, behind the proxy fence; a release at cluster scope would also wait
-// for everything else in flight (it cost 1000 to 2600 clocks here).
-__device__ __forceinline__ void arrive_at(uint32_t bar, uint32_t rank) {
-  asm volatile(
-      "{\n\t.reg .b32 a;\n\t"
-      "mapa.shared::cluster.u32 a, %0, %1;\n\t"
-      "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar), "r"(rank)
-      : "memory");
-}
-
-// MMA of a pair of CTAs, and a commit that arrives in both (mask: their ranks).
+// MMA of a pair of CTAs.
 __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -529,30 +482,6 @@ __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uin
       "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
-__device__ __forceinline__ void commit_pair(uint32_t bar, uint16_t mask) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-      "h"(mask)
-      : "memory");
-}
-
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
-  return p;
-}
-
-// A position in a ring of S stages, and the parity of its current use.
-template <int S>
-struct Ring {
-  uint32_t stage = 0, parity = 0;
-  bool first = true;   // no stage has been used before
-  __device__ __forceinline__ void next(uint32_t n = 1) {
-    stage += n;
-    if (stage >= S) stage -= S, parity ^= 1, first = false;
-  }
-};
-
 template <typename O>
 __global__ void __launch_bounds__(Tile::kThreads, 1)
 k_tc(const LinArgs p, const __grid_constant__ CUtensorMap mapw, const __grid_constant__ CUtensorMap mapx, int nt,
@@ -1207,19 +1136,6 @@ __global__ void __launch_bounds__(256) k_widen(const int8_t* x, int64_t ldx, int
   }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-  static std::atomic<void*> fn{nullptr};
-  void* f = fn.load(std::memory_order_acquire);
-  if (!f) {
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return nullptr;
-    fn.store(f, std::memory_order_release);
-  }
-  return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-}
-
 // Boxes of kBK columns x box rows of an int8 (size 1) or fp16 (2) matrix of
 // stride ld bytes; columns and rows past its ends read as zero.
 cudaError_t map_tile(CUtensorMap* m, int size, const void* base, int64_t ld, int rows, int cols, int box) {
@@ -1237,26 +1153,6 @@ cudaError_t map_tile(CUtensorMap* m, int size, const void* base, int64_t ld, int
 }
 
 int padded_k(int K) { return (K + 63) & ~63; }
-
-// Clusters of `size` CTAs of a kernel that the device holds at once.
-template <typename K>
-int max_clusters(K* kernel, int threads, int smem, int size) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(size);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cudaLaunchAttribute a{};
-  a.id = cudaLaunchAttributeClusterDimension;
-  a.val.clusterDim = {static_cast<unsigned>(size), 1, 1};
-  cfg.attrs = &a;
-  cfg.numAttrs = 1;
-  int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
-    cudaGetLastError();   // not fatal: K stays whole
-    n = 0;
-  }
-  return n;
-}
 
 // What a tensor-core kernel's launches need to know about a device, asked once.
 struct OnDevice {

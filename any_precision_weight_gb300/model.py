@@ -1,4 +1,5 @@
-"""Loading quantised MoE blocks into a PagedMoE page table.
+"""Loading quantised MoE blocks into a PagedMoE page table, and expert layers with
+8-bit floating point weights.
 
 Marshalling only: the packing is pw_pack (C++), the registration is
 pw_block_register; this module moves arrays into pinned host memory and
@@ -6,9 +7,12 @@ hands the pointers over.
 """
 from __future__ import annotations
 
+from typing import NamedTuple
+
 import numpy as np
 
-from . import KIND_DOWN, KIND_GATE_UP, PagedMoE, pw_lut_bytes, pw_pack, pw_tile_planes
+from . import (KIND_DOWN, KIND_GATE_UP, PagedMoE, _torch, f8_blocks, pw_combine, pw_grouped_linear_f8, pw_lut_bytes,
+               pw_pack, pw_quant_f8, pw_quant_f8_blocks, pw_route, pw_silu_quant_f8, pw_tile_planes, rows_f8)
 
 
 class HostStore:
@@ -79,3 +83,59 @@ def load_expert_layer(moe: PagedMoE, layer: int, blocks, bits, n_bits: int = 8, 
             na = None if alloc_planes is None else alloc_planes(e, kind)
             moe.register(layer, e, kind, planes, luts, int(bits[e][kind]), n_bits=n_bits,
                          b_min=b_min, alloc_planes=na, stream=stream, per_plane=per_plane)
+
+
+class F8Stages(NamedTuple):
+    """What the stages of an F8Experts forward wrote, rows in expert order."""
+    routing: object
+    q: object           # tokens as e4m3
+    scale: object
+    up: object          # gate and up rows' product
+    act: object         # silu(gate) * up as e4m3
+    act_scale: object
+    y: object           # down rows' product
+
+
+class F8Experts:
+    """An expert layer whose weights are e4m3 with a scale for each block of 128 x
+    128, as fp8 checkpoints hold them: the counterpart of a PagedMoE layer.
+
+    gate_up [E][2 I][H] (gate rows, then up rows) and down [E][H][I]: e4m3 with their
+    scales [E][blocks of rows][blocks of columns] float32 and rows on 16-byte
+    boundaries, or 16- or 32-bit weights, which are then quantised here.
+    """
+
+    def __init__(self, gate_up, down, gate_up_scale=None, down_scale=None):
+        self.E, two_i, self.H = gate_up.shape
+        self.I = two_i // 2
+        if two_i % 2 or tuple(down.shape) != (self.E, self.H, self.I):
+            raise ValueError(f"weights [E][2 I][H] and [E][H][I] are needed, got {tuple(gate_up.shape)} and {tuple(down.shape)}")
+        self.gate_up, self.gate_up_scale = self._weights(gate_up, gate_up_scale)
+        self.down, self.down_scale = self._weights(down, down_scale)
+
+    @staticmethod
+    def _weights(w, scale):
+        torch = _torch()
+        if w.dtype is torch.float8_e4m3fn:
+            if scale is None:
+                raise ValueError("e4m3 weights need their scales")
+            return w, scale
+        E, N, K = w.shape
+        q = rows_f8(E, N, K, device=w.device)
+        scale = torch.empty(E, f8_blocks(N), f8_blocks(K), dtype=torch.float32, device=w.device)
+        for e in range(E):
+            pw_quant_f8_blocks(w[e], q=q[e], scale=scale[e])
+        return q, scale
+
+    def forward(self, x, logits, top_k: int, renorm: bool, residual=None, out=None, stream=None, trace: bool = False):
+        """residual + the weighted sum of the top_k experts of every token: x [T][H] of
+        16 or 32 bits, logits [T][E] float32.  Six launches (seven for a large batch's
+        routing) on the stream, which nothing waits for; can be captured into a CUDA
+        graph.  trace: returns (out, F8Stages)."""
+        r = pw_route(logits, top_k, renorm, stream=stream)
+        q, s = pw_quant_f8(x, rows=r.perm, per=top_k, stream=stream)
+        up = pw_grouped_linear_f8(q, s, self.gate_up, self.gate_up_scale, r.offsets, out_dtype=x.dtype, stream=stream)
+        a, sa = pw_silu_quant_f8(up, stream=stream)
+        y = pw_grouped_linear_f8(a, sa, self.down, self.down_scale, r.offsets, out_dtype=x.dtype, stream=stream)
+        out = pw_combine(y, r.weight, r.inv, residual=residual, out=out, out_dtype=x.dtype, stream=stream)
+        return (out, F8Stages(r, q, s, up, a, sa, y)) if trace else out

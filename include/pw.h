@@ -661,6 +661,117 @@ int pw_logprobs(const void* logits, int64_t ld, int dtype, int T, int V, const v
                 float* logprob, int32_t* rank, float* entropy, int32_t* top_ids, float* top_logprobs,
                 pw_stream_t s);
 
+/* ------------------------------------------------------------------ expert layers in 8-bit floating point */
+
+/*
+ * Weights as fp8 checkpoints hold them (e4m3, one fp32 scale for each block of
+ * 128 x 128) for dense products and for experts, next to the bit-plane experts of
+ * pw_moe_forward: the routing, the quantisers of rows and weights, the products and
+ * the experts' weighted sum.  Runtime additions of this library.
+ *
+ * The conventions are those of the operators above.  An e4m3 number is a byte; the
+ * largest is 448.  A row of K columns has ceil(K / 128) scales; a block at the end of
+ * a row (or of the weights' rows) may be short.  A number stands for its e4m3 value
+ * times its scale.
+ */
+#define PW_MAX_GROUPS 512   /* most experts of pw_route and pw_grouped_linear_f8, most slots of pw_combine */
+
+/* Bytes of device workspace that pw_route asks for: 0 for a small batch, else room for
+ * a count per expert and part of the batch.  0 for a bad shape. */
+size_t pw_route_workspace_bytes(int T, int E, int k);
+
+/*
+ * pw_route -- the routing of pw_moe_forward on its own: top-k experts of every token,
+ * and the routed pairs in expert order.
+ *   logits  [T][E] fp32
+ *   idx, weight  [T][k] int32, fp32: experts in descending logit order (ties to the
+ *                lower index) and their softmax weights over all E; renorm: over the k
+ *   offsets [E+1] int32: the places [offsets[e], offsets[e+1]) are expert e's
+ *   perm    [T*k] int32: pair id t*k + j at each place, in (expert, token) order
+ *   inv     [T*k] int32: the place of each pair id
+ *   workspace  pw_route_workspace_bytes(T, E, k) bytes, 4-byte aligned, or NULL where
+ *           that is 0; it may hold anything, and must not be shared by two calls in
+ *           flight at once
+ * A NaN logit counts as -inf.  A row of nothing else than -inf has weights 0; where
+ * +inf is among the logits, the weight is theirs alone.  T = 0 writes offsets (zeros).
+ * Errors: PW_EINVAL (shapes, T * k above PW_MAX_VOCAB, strides, null or misaligned
+ * pointers), PW_ENOMEM (workspace too small), PW_ECUDA.
+ */
+int pw_route(const float* logits, int64_t ld, int T, int E, int k, int renorm, int32_t* idx, float* weight,
+             int32_t* offsets, int32_t* perm, int32_t* inv, void* workspace, size_t ws_bytes, pw_stream_t s);
+
+/*
+ * pw_quant_f8 -- rows to e4m3 with one scale for each 128 columns:
+ *   scale[t][b] = max|x[t][128 b ..]| / 448;  q = x * 448 / max, rounded once (ties to
+ *   even)
+ * rows: NULL, or T int32 numbers, and row t is then x[rows[t] / per]: with pw_route's
+ * perm (or that of pw_moe_forward) and per = k, the tokens in expert order.  A row
+ * outside [0, x_rows) has q 0 and scales 0, and nothing is read for it.  x_rows: rows
+ * of x (T or more where rows is NULL).
+ * A block of zeros has scale 0 and q 0; one with a NaN or an infinity has that scale
+ * and q 0.
+ * pw_silu_quant_f8 -- the same of silu(gate) * up in fp32, x [T][2 K] with the gate
+ * columns first: what lies between an expert's two products.
+ * pw_quant_f8_blocks -- the same with one scale for each 128 rows x 128 columns:
+ * weights, scale [ceil(N / 128)][ceil(K / 128)].
+ * q [T][K] has any stride; pw_linear_f8 wants its rows on 16-byte boundaries.
+ * Errors: PW_EINVAL (shapes, strides, null or misaligned pointers, dtype), PW_ECUDA.
+ */
+int pw_quant_f8(const void* x, int64_t ldx, int64_t x_rows, const int32_t* rows, int per, int T, int K, int dtype,
+                uint8_t* q, int64_t ldq, float* scale, int64_t lds, pw_stream_t s);
+int pw_silu_quant_f8(const void* x, int64_t ldx, int T, int K, int dtype, uint8_t* q, int64_t ldq, float* scale,
+                     int64_t lds, pw_stream_t s);
+int pw_quant_f8_blocks(const void* w, int64_t ldw, int N, int K, int dtype, uint8_t* q, int64_t ldq, float* scale,
+                       int64_t lds, pw_stream_t s);
+
+/*
+ * pw_linear_f8 -- product of e4m3 rows with e4m3 weights:
+ *   out[t][n] = sum_b x_scale[t][b] * w_scale[n / 128][b] * sum_{k in b} x[t][k] * w[n][k]
+ *               + bias[n],  b the blocks of 128 columns
+ * Sums are fp32; out is rounded once to out_dtype.
+ *   x  [T][K] with x_scale [T][ceil(K / 128)]: as pw_quant_f8 writes them
+ *   w  [N][K] with w_scale [ceil(N / 128)][ceil(K / 128)]
+ *   bias [N] of out_dtype or NULL;  out [T][N] of out_dtype
+ * Rows of x and w start on 16-byte boundaries (pointers and ldx, ldw multiples of
+ * 16); K itself is any number, and bytes past K are never used.  out and the scales
+ * have any stride.
+ * Errors: PW_EINVAL (shapes, strides, null or misaligned pointers, dtype), PW_ECUDA.
+ */
+int pw_linear_f8(const uint8_t* x, int64_t ldx, const float* x_scale, int64_t ldxs, const uint8_t* w, int64_t ldw,
+                 const float* w_scale, int64_t ldws, const void* bias, int T, int N, int K, int out_dtype, void* out,
+                 int64_t ldo, pw_stream_t s);
+
+/*
+ * pw_grouped_linear_f8 -- pw_linear_f8 of rows sorted by expert, each expert's with its
+ * own weights: rows [offsets[e], offsets[e+1]) of x and out with w[e] [N][K],
+ * w_scale[e] and bias[e] [N] (consecutive; or NULL).
+ *   offsets  device [E+1] int32, ascending, as pw_route writes them: read by the
+ *            kernels, so that nothing waits for the host; experts may have no rows
+ *   group_w, group_ws  elements from one expert's weights (a multiple of 16) and
+ *            scales to the next one's
+ * T is the number of rows of x and out.  Rows outside every range are left as they
+ * are; an offset outside [0, T], or below the one before it, is cut to where no other
+ * row is touched.
+ * Errors: as pw_linear_f8.
+ */
+int pw_grouped_linear_f8(const uint8_t* x, int64_t ldx, const float* x_scale, int64_t ldxs, const uint8_t* w,
+                         int64_t ldw, int64_t group_w, const float* w_scale, int64_t ldws, int64_t group_ws,
+                         const int32_t* offsets, const void* bias, int T, int E, int N, int K, int out_dtype, void* out,
+                         int64_t ldo, pw_stream_t s);
+
+/*
+ * pw_combine -- the experts' weighted sum:
+ *   out[t] = residual[t] + sum_j weight[t][j] * y[inv[t][j]],  rounded once
+ *   y [y_rows][H] of dtype;  weight, inv [T][k] as pw_route writes them;  residual [T][H]
+ *   of out_dtype or NULL (may be out itself)
+ * The sum is fp32, in the order of the slots.  A slot of weight 0, or whose place is
+ * outside [0, y_rows), adds nothing, and nothing is read for it.
+ * Errors: PW_EINVAL (shapes, strides, null or misaligned pointers, dtypes), PW_ECUDA.
+ */
+int pw_combine(const void* y, int64_t ldy, int64_t y_rows, int dtype, const float* weight, const int32_t* inv,
+               const void* residual, int64_t ldr, int T, int k, int H, int out_dtype, void* out, int64_t ldo,
+               pw_stream_t s);
+
 #ifdef __cplusplus
 }
 #endif
