@@ -106,6 +106,8 @@ _SIGS = {
     "pw_linear_f8": (_i, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i, _i, _i, _i, _vp, _i64, _vp]),
     "pw_grouped_linear_f8": (_i, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i, _i, _i, _i,
                                   _i, _vp, _i64, _vp]),
+    "pw_linear_f8_status": (_i, [_vp, _pi]),
+    "pw_debug_linear_f8_timeout": (_i, [_vp]),
     "pw_combine": (_i, [_vp, _i64, _i64, _i, _vp, _vp, _vp, _i64, _i, _i, _i, _i, _vp, _i64, _vp]),
 }
 
@@ -953,6 +955,18 @@ def pw_grouped_linear_f8(x, x_scale, w, w_scale, offsets, bias=None, out=None, o
                                       None if bias is None else bias.data_ptr(), T, E, N, K, _code(dt), out.data_ptr(),
                                       _rows(out, "out", dt, (T, N), dev), raw), "pw_grouped_linear_f8")
     return out
+
+
+def pw_linear_f8_status(stream=None) -> int:
+    """Status bits that pw_linear_f8 and pw_grouped_linear_f8 calls have raised since the
+    previous status call, those ordered before `stream`'s work included."""
+    st = _i()
+    _check(lib().pw_linear_f8_status(_stream(stream), ctypes.byref(st)), "pw_linear_f8_status")
+    return st.value
+
+
+def pw_debug_linear_f8_timeout(stream=None):
+    return _check(lib().pw_debug_linear_f8_timeout(_stream(stream)), "pw_debug_linear_f8_timeout")
 
 
 def pw_combine(y, weight, inv, residual=None, out=None, out_dtype=None, stream=None):

@@ -11,6 +11,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <mutex>
 
@@ -217,9 +218,520 @@ cudaError_t launch_few(const F8Args& p, int turns, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+// ---------------------------------------------------------------- tensor cores
+
+// Pairs of CTAs (cta_group::2), one CTA to an SM, take tiles of 256 channels (M, 128 to a
+// CTA: one block of the weights' scales) x up to 256 rows (N) with tcgen05.mma
+// kind::f8f6f4.  Each block of 128 columns of K goes into an accumulator of its own in
+// tensor memory, of two that take turns, and from there scaled into fp32 registers.
+// Warps by role:
+//  * warp 0 fetches weights and rows by TMA into a ring of S stages (128 columns each);
+//  * warp 1 issues the MMAs (in the even CTA, for both; in the odd one it reports its
+//    loads to the even one);
+//  * warps 2 and 3 write the products of both scales for each block into a ring of SS;
+//  * warps 4.. scale each finished accumulator into their sums while the next one
+//    fills, and at the tile's end store.
+// Where there are few tiles a cluster of pairs splits K and adds the parts through
+// distributed shared memory, in the order of the parts.
+constexpr int kM = 128;
+constexpr int kEpiWarp0 = 4;
+
+struct Tc {
+  static constexpr int NT = 256;
+  static constexpr int EW = 8;                            // accumulating warps
+  static constexpr int ACC = NT / (EW / 4);               // sums of one of their threads
+  static constexpr int kThreads = 32 * (kEpiWarp0 + EW);
+  static constexpr int A = kM * kB, X = NT / 2 * kB;      // bytes of a stage's operands
+  static constexpr int S = 6, SS = 8;
+  static constexpr int kOffScale = S * (A + X);
+  static constexpr int kOffBar = kOffScale + SS * NT * 4;
+  static constexpr int kBars = 2 * S + 2 * SS + 5;
+  static constexpr int kOffMisc = kOffBar + 8 * kBars;    // tmem, abort, first tile of each group
+  static constexpr int kSmem = kOffMisc + 16 + 4 * (PW_MAX_GROUPS + 1) + 1024;
+  static constexpr uint32_t kCols = 2 * NT;
+  // D f32, A and B e4m3, N / 8 and M / 16
+  __host__ __device__ static constexpr uint32_t idesc(int n) {
+    return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(2 * kM >> 4) << 24);
+  }
+  static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+  static_assert(kM * NT * 4 <= kOffScale, "a CTA's sums fit the operand ring");
+};
+
+// Registers by role: 384 threads are launched with kRegsLaunch each, and the
+// accumulating ones hold 128 sums.  Every role returns to kRegsLaunch at its end, the
+// accumulating warps before a CTA barrier and the others after it.
+constexpr int kRegsLaunch = 168, kRegsIssue = 56, kRegsAcc = 224;
+static_assert(128 * (kRegsIssue + 2 * kRegsAcc) <= Tc::kThreads * kRegsLaunch, "register split");
+
+// Bounded waits of the kernel that gave up (pw_linear_f8_status).
+__device__ uint32_t g_f8_timeouts;
+__global__ void k_count_timeout() { atomicAdd(&g_f8_timeouts, 1u); }
+
+// Polls up to kPolls times (about a second) for the phase of the given parity; false,
+// and the abort flag, when they run out or another thread has raised it.
+constexpr int kPolls = 1 << 23;
+__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, volatile int* abort) {
+  for (int n = 0; !test_wait(bar, parity); ++n) {
+    if (*abort) return false;
+    if (n == kPolls) {
+      atomicAdd(&g_f8_timeouts, 1u);
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+// MMA of a pair of CTAs: 32 columns of K.
+__device__ __forceinline__ void mma_f8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t s) {
+  asm("{\n\t.reg .b64 t;\n\tmov.b64 t, {%1, %2};\n\tfma.rn.f32x2 %0, t, %3, %0;\n\t}" : "+l"(acc) : "r"(lo), "r"(hi), "l"(s));
+}
+__device__ __forceinline__ void lds_2x64(uint32_t a, uint64_t& x, uint64_t& y) {
+  asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "r"(a) : "memory");
+}
+__device__ __forceinline__ float2 halves(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+
+// Tensor maps: the weights in boxes of 128 rows, the rows in boxes of 128, 64, 32 and 16.
+struct Maps {
+  CUtensorMap w;
+  CUtensorMap x[4];
+};
+
+// Tiles of a group of `rows` rows: about the same number of rows for all, a multiple of
+// the 32 that a pair's MMA takes.
+struct Split {
+  int tiles, nt;
+  __device__ __forceinline__ explicit Split(int rows) {
+    tiles = (rows + Tc::NT - 1) / Tc::NT;
+    nt = tiles ? ((rows + tiles - 1) / tiles + 31) / 32 * 32 : 0;
+  }
+};
+
+// A tile: its group, rows [t0, t1) of a tile of nt, and its 256 channels from n0 on.
+struct Tile {
+  int e, nt, t0, t1, n0;
+};
+
+// The tiles in order of the groups, `start` the first of each; within a group bands of
+// kBand row tiles, so that pairs at work share operands in the L2.
+constexpr int kBand = 8;
+struct Tiles {
+  const int* start;
+  int ntn, e = 0;
+  __device__ __forceinline__ Tile at(const F8Args& p, int tile) {
+    while (tile >= start[e + 1]) ++e;
+    const Rows r = rows_of(p, e);
+    const Split s(r.end - r.begin);
+    const int local = tile - start[e], band = local / (kBand * ntn), rest = local - band * kBand * ntn;
+    const int width = min(kBand, s.tiles - band * kBand), tt = band * kBand + rest % width;
+    const int t0 = r.begin + tt * s.nt;
+    return {e, s.nt, t0, min(r.end, t0 + s.nt), rest / width * 2 * kM};
+  }
+};
+
+template <typename O>
+__global__ void __launch_bounds__(Tc::kThreads, 1)
+k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, int split) {
+  using C = Tc;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);
+  const uint32_t base = saddr(smem);
+  const uint32_t full = base + C::kOffBar, empty = full + 8 * C::S;
+  const uint32_t sfull = empty + 8 * C::S, sempty = sfull + 8 * C::SS;
+  const uint32_t dfull = sempty + 8 * C::SS, dempty = dfull + 16, fin = dempty + 16;
+  int* s_misc = reinterpret_cast<int*>(smem + C::kOffMisc);   // tmem, abort
+  int* s_start = s_misc + 4;
+  volatile int* abort = s_misc + 1;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // the compiler then knows that it is uniform
+  // the CTA's place: in its pair, and among the parts of K
+  uint32_t rank;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  const uint32_t side = rank & 1, part = rank >> 1, leader = rank - side;
+  const int ntn = (p.N + 2 * kM - 1) / (2 * kM);
+
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(s_misc)),
+                 "r"(C::kCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  if (tid == 0) {
+    for (int i = 0; i < C::S; ++i) {
+      mbar_init(full + 8 * i, side ? 1 : 2);   // the CTA's loads, and the odd CTA's report
+      mbar_init(empty + 8 * i, 1);
+    }
+    for (int i = 0; i < C::SS; ++i) mbar_init(sfull + 8 * i, 2), mbar_init(sempty + 8 * i, C::EW);
+    for (int i = 0; i < 2; ++i) mbar_init(dfull + 8 * i, 1), mbar_init(dempty + 8 * i, 2 * C::EW);
+    mbar_init(fin, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    s_misc[1] = 0;
+  }
+  if (warp == 2) {   // the first tile of each group
+    int before = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
+      int n = 0;
+      if (e0 + lane < p.E) {
+        const Rows r = rows_of(p, e0 + lane);
+        n = Split(r.end - r.begin).tiles * ntn;
+      }
+      int sum = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
+      }
+      if (e0 + lane < p.E) s_start[e0 + lane] = before + sum - n;
+      before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (lane == 0) s_start[p.E] = before;
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // the other CTA's barriers and tensor memory
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, static_cast<uint32_t>(s_misc[0]), 0);
+
+  // a warp waits through one thread: polls of all its lanes would keep the
+  // other warps' barrier operations waiting
+  auto wait = [&](uint32_t bar, uint32_t parity) {
+    const bool ok = __all_sync(0xffffffffu, lane != 0 || poll(bar, parity, abort));
+    __syncwarp();
+    return ok;
+  };
+
+  const int tiles = s_start[p.E];
+  const int steps_all = (p.K + kB - 1) / kB;
+  const int s0 = static_cast<int>(static_cast<int64_t>(steps_all) * part / split);
+  const int s1 = static_cast<int>(static_cast<int64_t>(steps_all) * (part + 1) / split);
+  const int tile0 = blockIdx.x / (2 * split), tile_step = gridDim.x / (2 * split);
+  Tiles order{s_start, ntn};
+
+  if (warp < kEpiWarp0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    if (warp == 0 && lane == 0) {
+      // ---- operands by TMA
+      Ring<C::S> r;
+      bool ok = true;
+      for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
+        const Tile t = order.at(p, tile);
+        const int half = t.nt / 2, n0 = t.n0 + static_cast<int>(side) * kM, t0 = t.t0 + static_cast<int>(side) * half;
+        for (int k = s0; k < s1; ++k, r.next()) {
+          if (!r.first && !(ok = poll(empty + 8 * r.stage, r.parity ^ 1, abort))) break;
+          const uint32_t bar = full + 8 * r.stage, to = base + r.stage * (C::A + C::X);
+          mbar_expect_tx(bar, C::A + half * kB);
+          tma_load_3d(to, &maps.w, k * kB, n0, p.gw ? t.e : 0, bar);
+          int at = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (half & (128 >> i)) {
+              tma_load_2d(to + C::A + at * kB, &maps.x[i], k * kB, t0 + at, bar);
+              at += 128 >> i;
+            }
+        }
+      }
+      if (*abort) {   // what is in flight still ends before the CTA does
+        volatile int none = 0;
+        for (uint32_t i = 0; i < C::S; ++i) {
+          if (i < r.stage)
+            poll(full + 8 * i, r.parity, &none);
+          else if (!r.first)
+            poll(full + 8 * i, r.parity ^ 1, &none);
+        }
+      }
+    }
+    if (warp == 1 && side) {
+      // ---- the odd CTA's loads are reported to the even one
+      if (lane == 0) {
+        Ring<C::S> r;
+        const int64_t all = static_cast<int64_t>(s1 - s0) * (tiles > tile0 ? (tiles - tile0 + tile_step - 1) / tile_step : 0);
+        for (int64_t g = 0; g < all && poll(full + 8 * r.stage, r.parity, abort); ++g, r.next())
+          arrive_at(full + 8 * r.stage, leader);
+      }
+    } else if (warp == 1) {
+      // ---- MMA issue: the whole warp in step, so that the operands stay in uniform
+      // registers, and an elected thread for the instructions
+      const uint16_t both = static_cast<uint16_t>(3u << leader);
+      Ring<C::S> r;
+      Ring<2> d;
+      bool ok = true;
+      for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
+        const uint32_t idesc = C::idesc(order.at(p, tile).nt);
+        for (int k = s0; k < s1; ++k, r.next(), d.next()) {
+          if (!d.first && !(ok = wait(dempty + 8 * d.stage, d.parity ^ 1))) break;
+          if (!(ok = wait(full + 8 * r.stage, r.parity))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t da = smem_desc(base + r.stage * (C::A + C::X)), db = da + (C::A >> 4);
+#pragma unroll
+            for (int kk = 0; kk < kB / 32; ++kk)
+              mma_f8_pair(tmem + d.stage * C::NT, da + kk * 2, db + kk * 2, idesc, kk);
+            commit_pair(empty + 8 * r.stage, both);
+            commit_pair(dfull + 8 * d.stage, both);
+          }
+          __syncwarp();
+        }
+      }
+      if (*abort) {   // the MMAs in flight end before the CTA does
+        if (elect_one()) {
+          volatile int none = 0;
+          commit_pair(fin, static_cast<uint16_t>(1u << leader));
+          poll(fin, 0, &none);
+        }
+        __syncwarp();
+      }
+    }
+    if (warp >= 2) {
+      // ---- products of the scales: four rows to a lane, four blocks at a time
+      const int col = (warp - 2) * 128 + lane * 4;
+      Ring<C::SS> r;
+      bool ok = true;
+      for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
+        const Tile t = order.at(p, tile);
+        const int nb = min(t.n0 / kB + static_cast<int>(side), (p.N - 1) / kB);
+        const float* ws = p.ws + t.e * p.gws + nb * p.ldws;
+        for (int k0 = s0; k0 < s1 && ok; k0 += 4) {
+          float v[4][4], w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[j] = k0 + j < s1 ? __ldg(ws + k0 + j) : 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = t.t0 + col + i;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              v[i][j] = row < t.t1 && k0 + j < s1 ? __ldg(p.xs + row * p.ldxs + k0 + j) : 0.f;
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (k0 + j >= s1) break;
+            if (!r.first && !(ok = wait(sempty + 8 * r.stage, r.parity ^ 1))) break;
+            *reinterpret_cast<float4*>(smem + C::kOffScale + (r.stage * C::NT + col) * 4) =
+                make_float4(v[0][j] * w[j], v[1][j] * w[j], v[2][j] * w[j], v[3][j] * w[j]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sfull + 8 * r.stage);
+            r.next();
+          }
+        }
+      }
+    }
+    __syncwarp();
+    cta_barrier();
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
+  } else {
+    // ---- scale, accumulate and store: a channel to a lane, nt / 2 rows to a thread
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsAcc));
+    const int q = warp & 3, h = (warp - kEpiWarp0) >> 2;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    Ring<2> d;
+    Ring<C::SS> r;
+    bool ok = true;
+    for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
+      const Tile t = order.at(p, tile);
+      const int half = t.nt / 2;
+      uint64_t acc[C::ACC / 2];
+#pragma unroll
+      for (int i = 0; i < C::ACC / 2; ++i) acc[i] = 0;
+      for (int k = s0; k < s1; ++k, d.next(), r.next()) {
+        if (!(ok = wait(sfull + 8 * r.stage, r.parity) && wait(dfull + 8 * d.stage, d.parity))) break;
+        tc_fence_after();
+        const uint32_t from = lanes + d.stage * C::NT + h * half;
+        const uint32_t sc = base + C::kOffScale + (r.stage * C::NT + h * half) * 4;
+        uint32_t v[2][16];
+        tmem_ld16(from, v[0]);
+#pragma unroll
+        for (int c = 0; c < C::ACC; c += 16) {
+          if (c >= half) break;
+          uint32_t(&now)[16] = v[c / 16 % 2];
+          tmem_wait(now);
+          if (c + 16 < half) {
+            tmem_ld16(from + c + 16, v[(c / 16 + 1) % 2]);
+          } else {   // all of it is in registers
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_at(dempty + 8 * d.stage, leader);
+          }
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            uint64_t sa, sb;
+            lds_2x64(sc + (c + i) * 4, sa, sb);
+            fma2(acc[(c + i) / 2], now[i], now[i + 1], sa);
+            fma2(acc[(c + i) / 2 + 1], now[i + 2], now[i + 3], sb);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sempty + 8 * r.stage);
+      }
+      if (!ok) break;
+      if (split == 1) {
+        const int n = t.n0 + static_cast<int>(side) * kM + q * 32 + lane, ts = t.t0 + h * half;
+        float bias = 0.f;
+        if (p.bias && n < p.N) bias = to_f32<O>(static_cast<const O*>(p.bias)[static_cast<int64_t>(t.e) * p.N + n]);
+        O* out = static_cast<O*>(p.out) + ts * p.ldo + n;
+#pragma unroll
+        for (int i = 0; i < C::ACC; ++i) {
+          const float2 f = halves(acc[i / 2]);
+          if (n < p.N && i < half && ts + i < t.t1) *out = from_f32<O>((i & 1 ? f.y : f.x) + bias);
+          out += p.ldo;
+        }
+      } else {
+        // every stage of the ring has been read: its space takes the sums
+        float* sums = reinterpret_cast<float*>(smem);
+#pragma unroll
+        for (int i = 0; i < C::ACC; ++i) {
+          const float2 f = halves(acc[i / 2]);
+          if (i < half) sums[(h * half + i) * kM + q * 32 + lane] = i & 1 ? f.y : f.x;
+        }
+      }
+    }
+    __syncwarp();
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
+    cta_barrier();
+  }
+
+  __syncwarp();
+  if (split > 1) {
+    // the parts of one tile: each CTA adds and stores its share of the rows
+    cluster_sync();
+    if (!*abort && tile0 < tiles) {
+      const Tile t = order.at(p, tile0);
+      const int j0 = t.nt * part / split, j1 = t.nt * (part + 1) / split;
+      const int n = t.n0 + static_cast<int>(side) * kM + tid % (kM / 4) * 4;   // four channels, the thread's for all rows
+      float bias[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        bias[c] = p.bias && n + c < p.N ? to_f32<O>(static_cast<const O*>(p.bias)[static_cast<int64_t>(t.e) * p.N + n + c]) : 0.f;
+      for (int i = j0 * (kM / 4) + tid; i < j1 * (kM / 4); i += C::kThreads) {
+        const int row = t.t0 + i / (kM / 4);
+        if (row >= t.t1) break;
+        float sum[4] = {};
+        for (int s = 0; s < split; ++s) {
+          const float4 v = ld_cluster(base + i * 16, s * 2 + side);
+          sum[0] += v.x, sum[1] += v.y, sum[2] += v.z, sum[3] += v.w;
+        }
+        O* out = static_cast<O*>(p.out) + row * p.ldo + n;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (n + c < p.N) out[c] = from_f32<O>(sum[c] + bias[c]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // nothing of this CTA is read or signalled any more
+  tc_fence_after();
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols));
+}
+
+// Boxes of 128 columns x `box` rows of e4m3 rows [groups][rows][cols]; columns and rows
+// past the ends read as zero.
+cudaError_t map_rows(CUtensorMap* m, const void* base, int64_t ld, int64_t group, int groups, int rows, int cols, int box) {
+  const auto encode = encoder();
+  if (!encode) return cudaErrorNotSupported;
+  const cuuint32_t rank = groups ? 3 : 2;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(groups)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld), static_cast<cuuint64_t>(group)};
+  const cuuint32_t boxes[3] = {kB, static_cast<cuuint32_t>(box), 1}, es[3] = {1, 1, 1};
+  const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims, strides, boxes, es,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// What the kernel's launches need to know about a device, asked once.
+struct OnDevice {
+  std::atomic<bool> ready{false};
+  int clusters[4] = {};   // of 1, 2, 4 and 8 CTAs, at once
+};
+template <typename K>
+cudaError_t prepare(OnDevice* all, K* kernel, OnDevice** out) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
+  OnDevice& d = all[dev];
+  *out = &d;
+  if (d.ready.load(std::memory_order_acquire)) return cudaSuccess;
+  static std::mutex asking;
+  const std::lock_guard<std::mutex> lock(asking);
+  if (d.ready.load(std::memory_order_relaxed)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Tc::kSmem);
+  cudaFuncAttributes at{};
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, kernel);
+  if (e != cudaSuccess) return e;
+  // the register split must be what the CTA is launched with
+  if (at.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
+  for (int i = 0; i < 4; ++i) d.clusters[i] = max_clusters(kernel, Tc::kThreads, Tc::kSmem, 1 << i);
+  d.ready.store(true, std::memory_order_release);
+  return cudaSuccess;
+}
+
+// Parts of K, 1, 2 or 4: while all of them still run at once and have four blocks or
+// more each.
+int parts_of_k(const OnDevice& d, int64_t tiles, int steps) {
+  int i = 0;
+  while (i < 2 && tiles <= d.clusters[i + 2] && steps >= 8 << i) ++i;
+  return 1 << i;
+}
+
+template <typename O>
+cudaError_t launch_tc(const F8Args& p, cudaStream_t s) {
+  static OnDevice all[kMaxDev];
+  OnDevice* d;
+  cudaError_t e = prepare(all, k_tc_f8<O>, &d);
+  Maps maps;
+  if (e == cudaSuccess) e = map_rows(&maps.w, p.w, p.ldw, p.gw ? p.gw : p.ldw, p.gw ? p.E : 1, p.N, p.K, kM);
+  for (int i = 0; i < 4 && e == cudaSuccess; ++i) e = map_rows(&maps.x[i], p.x, p.ldx, 0, 0, p.T, p.K, 128 >> i);
+  if (e != cudaSuccess) return e;
+  // every tile that a product of T rows has; of rows in groups there may be as many more as groups
+  const int64_t ntn = (p.N + 2 * kM - 1) / (2 * kM), tiles = ntn * ((p.T + Tc::NT - 1) / Tc::NT);
+  const int split = p.offsets ? 1 : parts_of_k(*d, tiles, (p.K + kB - 1) / kB);
+  const int64_t most = p.offsets ? ntn * std::min<int64_t>(p.T, (p.T + Tc::NT - 1) / Tc::NT + p.E) : tiles;
+  const int64_t pairs = split > 1 ? tiles * split : std::min<int64_t>(most, sm_count() / 2);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+  cfg.blockDim = dim3(Tc::kThreads);
+  cfg.dynamicSmemBytes = Tc::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute a{};
+  a.id = cudaLaunchAttributeClusterDimension;
+  a.val.clusterDim = {static_cast<unsigned>(2 * split), 1, 1};
+  cfg.attrs = &a;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_tc_f8<O>, p, maps, split);
+}
+
 template <typename O>
 cudaError_t launch_f8(const F8Args& p, cudaStream_t s) {
   const int64_t rows = p.offsets ? (p.T + p.E - 1) / p.E : p.T;   // of a group, about
+  if (rows > 16) return launch_tc<O>(p, s);
   const int nt = rows <= 8 ? 1 : 2;
   const int turns = static_cast<int>(std::min<int64_t>((rows + nt * 8 - 1) / (nt * 8), 65535 / p.E));
   return nt == 1 ? launch_few<O, 1>(p, turns, s) : launch_few<O, 2>(p, turns, s);
@@ -239,6 +751,8 @@ int linear_f8(const char* what, const F8Args& p, int out_dtype, pw_stream_t s) {
   if (!aligned(p.x, 16) || !aligned(p.w, 16) || p.ldx % 16 || p.ldw % 16 || p.gw % 16)
     return failf(PW_EINVAL, "%s: rows of x and w must start on 16-byte boundaries", what);
   if (p.E > 1 && (p.gw < 0 || p.gws < 0)) return failf(PW_EINVAL, "%s: a group stride is negative", what);
+  if (((static_cast<int64_t>(p.T) + 255) / 256 + p.E) * ((static_cast<int64_t>(p.N) + 255) / 256) > PW_MAX_VOCAB)
+    return failf(PW_EINVAL, "%s: an output of %d x %d is too large", what, p.T, p.N);
   const size_t es = dtype_bytes(out_dtype);
   if (!aligned(p.out, es) || !aligned(p.bias, es) || !aligned(p.xs, 4) || !aligned(p.ws, 4) || !aligned(p.offsets, 4))
     return failf(PW_EINVAL, "%s: misaligned pointer", what);
@@ -273,6 +787,34 @@ int pw_grouped_linear_f8(const uint8_t* x, int64_t ldx, const float* x_scale, in
                        pw::F8Args{x, w, x_scale, w_scale, bias, offsets, out, ldx, ldxs, ldw, ldws, ldo, group_w,
                                   group_ws, T, N, K, E},
                        out_dtype, s);
+}
+
+int pw_linear_f8_status(pw_stream_t s, int* status) {
+  pw::NvtxCall nvtx_range("pw_linear_f8_status");
+  if (!status) return pw::failf(PW_EINVAL, "pw_linear_f8_status: null status");
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(s);
+  uint32_t now = 0;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && (dev < 0 || dev >= pw::kMaxDev)) e = cudaErrorInvalidDevice;
+  if (e == cudaSuccess)
+    e = cudaMemcpyFromSymbolAsync(&now, pw::g_f8_timeouts, sizeof now, 0, cudaMemcpyDeviceToHost, st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  if (e != cudaSuccess) return pw::failf(PW_ECUDA, "pw_linear_f8_status: %s", cudaGetErrorString(e));
+  // the count up to which an earlier call has told; another thread may tell meanwhile
+  static std::atomic<uint32_t> told[pw::kMaxDev];
+  uint32_t before = told[dev].load();
+  bool more = false;
+  while ((more = static_cast<int32_t>(now - before) > 0) && !told[dev].compare_exchange_weak(before, now)) {
+  }
+  *status = more ? PW_STATUS_TIMEOUT : 0;
+  return PW_OK;
+}
+
+int pw_debug_linear_f8_timeout(pw_stream_t s) {
+  pw::NvtxCall nvtx_range("pw_debug_linear_f8_timeout");
+  pw::k_count_timeout<<<1, 1, 0, reinterpret_cast<cudaStream_t>(s)>>>();
+  return pw::launch_status(cudaGetLastError(), "pw_debug_linear_f8_timeout");
 }
 
 }  // extern "C"

@@ -760,6 +760,22 @@ int pw_grouped_linear_f8(const uint8_t* x, int64_t ldx, const float* x_scale, in
                          int64_t ldo, pw_stream_t s);
 
 /*
+ * pw_linear_f8_status -- the PW_STATUS_* bits that pw_linear_f8 and pw_grouped_linear_f8
+ * calls on the current device have raised since the previous call of it there (0, or
+ * PW_STATUS_TIMEOUT when a bounded device-side wait gave up: that call's outputs are not
+ * valid).  Covers the work ordered before it on `s`; synchronises `s`.  The device counts
+ * the waits that gave up, and of several threads that ask at once one is told.
+ */
+int pw_linear_f8_status(pw_stream_t s, int* status);
+
+/*
+ * pw_debug_linear_f8_timeout -- test hook for pw_linear_f8_status: counts, in the order
+ * of `s`, a wait as one that gave up.  No wait does.
+ * Errors: PW_ECUDA.
+ */
+int pw_debug_linear_f8_timeout(pw_stream_t s);
+
+/*
  * pw_combine -- the experts' weighted sum:
  *   out[t] = residual[t] + sum_j weight[t][j] * y[inv[t][j]],  rounded once
  *   y [y_rows][H] of dtype;  weight, inv [T][k] as pw_route writes them;  residual [T][H]
