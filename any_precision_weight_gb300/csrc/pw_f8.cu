@@ -260,18 +260,31 @@ struct Tc {
 // Registers by role: 384 threads are launched with kRegsLaunch each, and the
 // accumulating ones hold 128 sums.  Every role returns to kRegsLaunch at its end, the
 // accumulating warps before a CTA barrier and the others after it.
-constexpr int kRegsLaunch = 168, kRegsIssue = 56, kRegsAcc = 224;
+constexpr int kRegsLaunch = 168, kRegsIssue = 72, kRegsAcc = 216;
 static_assert(128 * (kRegsIssue + 2 * kRegsAcc) <= Tc::kThreads * kRegsLaunch, "register split");
 
 // Bounded waits of the kernel that gave up (pw_linear_f8_status).
 __device__ uint32_t g_f8_timeouts;
 __global__ void k_count_timeout() { atomicAdd(&g_f8_timeouts, 1u); }
 
-// Polls up to kPolls times (about a second) for the phase of the given parity; false,
-// and the abort flag, when they run out or another thread has raised it.
-constexpr int kPolls = 1 << 23;
+// Whether the phase of the given parity has ended; waits for it up to 2 us.
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 2000;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done;
+}
+
+// Waits up to kPolls times (at most a few seconds) for the phase of the given parity;
+// false, and the abort flag, when they run out or another thread has raised it.
+constexpr int kPolls = 1 << 20;
 __device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, volatile int* abort) {
-  for (int n = 0; !test_wait(bar, parity); ++n) {
+  for (int n = 0; !try_wait(bar, parity); ++n) {
     if (*abort) return false;
     if (n == kPolls) {
       atomicAdd(&g_f8_timeouts, 1u);
@@ -358,6 +371,28 @@ struct Tiles {
   }
 };
 
+// The first tile of each group, and behind them the number of tiles, by one warp.
+__device__ __forceinline__ void first_tiles(const F8Args& p, int ntn, int* start) {
+  const int lane = threadIdx.x & 31;
+  int before = 0;
+  for (int e0 = 0; e0 < p.E; e0 += 32) {
+    int n = 0;
+    if (e0 + lane < p.E) {
+      const Rows r = rows_of(p, e0 + lane);
+      n = Split(r.end - r.begin).tiles * ntn;
+    }
+    int sum = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    if (e0 + lane < p.E) start[e0 + lane] = before + sum - n;
+    before += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  if (lane == 0) start[p.E] = before;
+}
+
 template <typename O>
 __global__ void __launch_bounds__(Tc::kThreads, 1)
 k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, int split) {
@@ -395,25 +430,7 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, int split) {
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     s_misc[1] = 0;
   }
-  if (warp == 2) {   // the first tile of each group
-    int before = 0;
-    for (int e0 = 0; e0 < p.E; e0 += 32) {
-      int n = 0;
-      if (e0 + lane < p.E) {
-        const Rows r = rows_of(p, e0 + lane);
-        n = Split(r.end - r.begin).tiles * ntn;
-      }
-      int sum = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += v;
-      }
-      if (e0 + lane < p.E) s_start[e0 + lane] = before + sum - n;
-      before += __shfl_sync(0xffffffffu, sum, 31);
-    }
-    if (lane == 0) s_start[p.E] = before;
-  }
+  if (warp == 2) first_tiles(p, ntn, s_start);
   tc_fence_before();
   __syncthreads();
   cluster_sync();   // the other CTA's barriers and tensor memory
@@ -564,27 +581,29 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, int split) {
         tc_fence_after();
         const uint32_t from = lanes + d.stage * C::NT + h * half;
         const uint32_t sc = base + C::kOffScale + (r.stage * C::NT + h * half) * 4;
+        // the next 16 sums and their scales are on their way while these are added
         uint32_t v[2][16];
-        tmem_ld16(from, v[0]);
+        uint64_t f[2][8];
+        auto fetch = [&](int c) {
+          tmem_ld16(from + c, v[c / 16 % 2]);
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) lds_2x64(sc + (c + i * 2) * 4, f[c / 16 % 2][i], f[c / 16 % 2][i + 1]);
+        };
+        fetch(0);
 #pragma unroll
         for (int c = 0; c < C::ACC; c += 16) {
           if (c >= half) break;
           uint32_t(&now)[16] = v[c / 16 % 2];
           tmem_wait(now);
           if (c + 16 < half) {
-            tmem_ld16(from + c + 16, v[(c / 16 + 1) % 2]);
+            fetch(c + 16);
           } else {   // all of it is in registers
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_at(dempty + 8 * d.stage, leader);
           }
 #pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            uint64_t sa, sb;
-            lds_2x64(sc + (c + i) * 4, sa, sb);
-            fma2(acc[(c + i) / 2], now[i], now[i + 1], sa);
-            fma2(acc[(c + i) / 2 + 1], now[i + 2], now[i + 3], sb);
-          }
+          for (int i = 0; i < 16; i += 2) fma2(acc[(c + i) / 2], now[i], now[i + 1], f[c / 16 % 2][i / 2]);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(sempty + 8 * r.stage);
@@ -650,6 +669,266 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, int split) {
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols));
 }
 
+// ---------------------------------------------------------------- many rows
+
+// As k_tc_f8 with the operands' parts exchanged: the rows are the MMA's M (256 to a pair,
+// 128 to a CTA) and the channels its N (256).  A lane of tensor memory is then a row, so a
+// block's sums take one factor to a thread, which the thread reads for itself.
+struct Wide {
+  static constexpr int NT = 256, EW = 8, ACC = NT / (EW / 4);
+  static constexpr int kThreads = 32 * (kEpiWarp0 + EW);
+  static constexpr int X = kM * kB, W = NT / 2 * kB;      // bytes of a stage's operands
+  static constexpr int S = 6;
+  static constexpr int kOffOut = S * (X + W);
+  static constexpr int kOutWarp = 32 * 128;               // a warp's part of the stores: 32 rows x 128 bytes
+  static constexpr int kOffBar = kOffOut + EW * kOutWarp;
+  static constexpr int kBars = 2 * S + 5;
+  static constexpr int kOffMisc = kOffBar + 8 * kBars;
+  static constexpr int kSmem = kOffMisc + 16 + 4 * (PW_MAX_GROUPS + 1);
+  static constexpr uint32_t kCols = 2 * NT;
+  static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+};
+static_assert(Wide::kThreads == Tc::kThreads, "one register split");
+
+// 32 consecutive fp32 columns of this thread's TMEM lane (after tmem_wait32).
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
+template <typename O>
+__global__ void __launch_bounds__(Wide::kThreads, 1)
+k_wide_f8(const F8Args p, const __grid_constant__ CUtensorMap mapx, const __grid_constant__ CUtensorMap mapw) {
+  using C = Wide;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const uint32_t base = saddr(smem);
+  if (base % 1024) {   // the swizzled tiles would lie wrong (the array is aligned, so it never is)
+    if (threadIdx.x == 0) atomicAdd(&g_f8_timeouts, 1u);
+    return;
+  }
+  const uint32_t full = base + C::kOffBar, empty = full + 8 * C::S;
+  const uint32_t dfull = empty + 8 * C::S, dempty = dfull + 16, fin = dempty + 16;
+  int* s_misc = reinterpret_cast<int*>(smem + C::kOffMisc);   // tmem, abort
+  int* s_start = s_misc + 4;
+  volatile int* abort = s_misc + 1;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  uint32_t side;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(side));
+  const int ntn = (p.N + C::NT - 1) / C::NT;
+
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(s_misc)),
+                 "r"(C::kCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  if (tid == 0) {
+    for (int i = 0; i < C::S; ++i) {
+      mbar_init(full + 8 * i, side ? 1 : 2);   // the CTA's loads, and the odd CTA's report
+      mbar_init(empty + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) mbar_init(dfull + 8 * i, 1), mbar_init(dempty + 8 * i, 2 * C::EW);
+    mbar_init(fin, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    s_misc[1] = 0;
+  }
+  if (warp == 2) first_tiles(p, ntn, s_start);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, static_cast<uint32_t>(s_misc[0]), 0);
+  auto wait = [&](uint32_t bar, uint32_t parity) {   // as in k_tc_f8
+    const bool ok = __all_sync(0xffffffffu, lane != 0 || poll(bar, parity, abort));
+    __syncwarp();
+    return ok;
+  };
+  const int tiles = s_start[p.E], steps = (p.K + kB - 1) / kB;
+  const int tile0 = blockIdx.x / 2, tile_step = gridDim.x / 2;
+  Tiles order{s_start, ntn};
+
+  if (warp < kEpiWarp0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    if (warp == 0 && lane == 0) {
+      // ---- operands by TMA
+      Ring<C::S> r;
+      bool ok = true;
+      for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
+        const Tile t = order.at(p, tile);
+        for (int k = 0; k < steps; ++k, r.next()) {
+          if (!r.first && !(ok = poll(empty + 8 * r.stage, r.parity ^ 1, abort))) break;
+          const uint32_t bar = full + 8 * r.stage, to = base + r.stage * (C::X + C::W);
+          mbar_expect_tx(bar, C::X + C::W);
+          tma_load_2d(to, &mapx, k * kB, t.t0 + static_cast<int>(side) * kM, bar);
+          tma_load_3d(to + C::X, &mapw, k * kB, t.n0 + static_cast<int>(side) * kM, p.gw ? t.e : 0, bar);
+        }
+      }
+      if (*abort) {   // what is in flight still ends before the CTA does
+        volatile int none = 0;
+        for (uint32_t i = 0; i < C::S; ++i) {
+          if (i < r.stage)
+            poll(full + 8 * i, r.parity, &none);
+          else if (!r.first)
+            poll(full + 8 * i, r.parity ^ 1, &none);
+        }
+      }
+    }
+    if (warp == 1 && side) {
+      // ---- the odd CTA's loads are reported to the even one
+      if (lane == 0) {
+        Ring<C::S> r;
+        const int64_t all = static_cast<int64_t>(steps) * (tiles > tile0 ? (tiles - tile0 + tile_step - 1) / tile_step : 0);
+        for (int64_t g = 0; g < all && poll(full + 8 * r.stage, r.parity, abort); ++g, r.next())
+          arrive_at(full + 8 * r.stage, 0);
+      }
+    } else if (warp == 1) {
+      // ---- MMA issue
+      Ring<C::S> r;
+      Ring<2> d;
+      bool ok = true;
+      for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
+        for (int k = 0; k < steps; ++k, r.next(), d.next()) {
+          if (!d.first && !(ok = wait(dempty + 8 * d.stage, d.parity ^ 1))) break;
+          if (!(ok = wait(full + 8 * r.stage, r.parity))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t da = smem_desc(base + r.stage * (C::X + C::W)), db = da + (C::X >> 4);
+#pragma unroll
+            for (int kk = 0; kk < kB / 32; ++kk)
+              mma_f8_pair(tmem + d.stage * C::NT, da + kk * 2, db + kk * 2, Tc::idesc(C::NT), kk);
+            commit_pair(empty + 8 * r.stage, 3);
+            commit_pair(dfull + 8 * d.stage, 3);
+          }
+          __syncwarp();
+        }
+      }
+      if (*abort) {   // the MMAs in flight end before the CTA does
+        if (elect_one()) {
+          volatile int none = 0;
+          commit_pair(fin, 1);
+          poll(fin, 0, &none);
+        }
+        __syncwarp();
+      }
+    }
+    __syncwarp();
+    cta_barrier();
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
+  } else {
+    // ---- scale, accumulate and store: a row to a lane, 128 channels to a thread
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsAcc));
+    const int q = warp & 3, h = (warp - kEpiWarp0) >> 2;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * C::ACC;
+    unsigned char* stage = smem + C::kOffOut + (warp - kEpiWarp0) * C::kOutWarp;
+    Ring<2> d;
+    bool ok = true, ready = false;
+    for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
+      const Tile t = order.at(p, tile);
+      const int row0 = t.t0 + static_cast<int>(side) * kM + q * 32;   // of the warp
+      const int n0 = t.n0 + h * C::ACC;
+      const float* xs = p.xs + min(row0 + lane, t.t1 - 1) * p.ldxs;
+      const float* ws = p.ws + t.e * p.gws + min(n0, p.N - 1) / kB * p.ldws;
+      float x_next = __ldg(xs), w_next = __ldg(ws);
+      uint64_t acc[C::ACC / 2];
+#pragma unroll
+      for (int i = 0; i < C::ACC / 2; ++i) acc[i] = 0;
+      for (int k = 0; k < steps; ++k, d.next()) {
+        const float f = x_next * w_next;
+        if (k + 1 < steps) x_next = __ldg(xs + k + 1), w_next = __ldg(ws + k + 1);
+        uint64_t f2;
+        asm("mov.b64 %0, {%1, %1};" : "=l"(f2) : "f"(f));
+        if (!ready && !(ok = wait(dfull + 8 * d.stage, d.parity))) break;
+        tc_fence_after();
+        const uint32_t from = lanes + d.stage * C::NT;
+        uint32_t v[2][32];
+        tmem_ld32(from, v[0]);
+#pragma unroll
+        for (int c = 0; c < C::ACC / 32; ++c) {
+          uint32_t(&now)[32] = v[c % 2];
+          tmem_wait32(now);
+          if (c + 1 < C::ACC / 32) {
+            tmem_ld32(from + (c + 1) * 32, v[(c + 1) % 2]);
+          } else {   // all of it is in registers
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              arrive_at(dempty + 8 * d.stage, 0);
+              // a barrier takes over 100 clocks to read: the next one's while this is added
+              ready = test_wait(dfull + 8 * (d.stage ^ 1), d.parity ^ d.stage);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) fma2(acc[c * 16 + i / 2], now[i], now[i + 1], f2);
+        }
+        ready = __shfl_sync(0xffffffffu, ready, 0);
+      }
+      if (!ok) break;
+      // 128 bytes of each of the warp's rows at a time, through shared memory
+      constexpr int N = 128 / sizeof(O), V = 16 / sizeof(O);   // channels of a turn, of 16 bytes
+      const bool wide = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.ldo % V == 0;
+      const O* bias = p.bias ? static_cast<const O*>(p.bias) + static_cast<int64_t>(t.e) * p.N : nullptr;
+      auto value = [&](int i) {
+        const float2 f = halves(acc[i / 2]);
+        return from_f32<O>((i & 1 ? f.y : f.x) + (bias && n0 + i < p.N ? to_f32<O>(__ldg(bias + n0 + i)) : 0.f));
+      };
+#pragma unroll
+      for (int c = 0; c < C::ACC; c += N) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {   // the row's 16-byte pieces, each row's in another order
+          alignas(16) O o[V];
+#pragma unroll
+          for (int e = 0; e < V; ++e) o[e] = value(c + i * V + e);
+          *reinterpret_cast<uint4*>(stage + lane * 128 + ((i ^ (lane & 7)) << 4)) = *reinterpret_cast<const uint4*>(o);
+        }
+        __syncwarp();
+        const int n = n0 + c + (lane & 7) * V;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = i * 4 + (lane >> 3), row = row0 + r;
+          uint4 raw = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+          if (row >= t.t1) continue;
+          O* out = static_cast<O*>(p.out) + row * p.ldo + n;
+          if (wide && n + V <= p.N) {
+            *reinterpret_cast<uint4*>(out) = raw;
+          } else {
+            const O* v = reinterpret_cast<const O*>(&raw);
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+              if (n + e < p.N) out[e] = v[e];
+          }
+        }
+        __syncwarp();
+      }
+    }
+    __syncwarp();
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
+    cta_barrier();
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // nothing of this CTA is read or signalled any more
+  tc_fence_after();
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols));
+}
+
 // Boxes of 128 columns x `box` rows of e4m3 rows [groups][rows][cols]; columns and rows
 // past the ends read as zero.
 cudaError_t map_rows(CUtensorMap* m, const void* base, int64_t ld, int64_t group, int groups, int rows, int cols, int box) {
@@ -671,7 +950,7 @@ struct OnDevice {
   int clusters[4] = {};   // of 1, 2, 4 and 8 CTAs, at once
 };
 template <typename K>
-cudaError_t prepare(OnDevice* all, K* kernel, OnDevice** out) {
+cudaError_t prepare(OnDevice* all, K* kernel, int smem, OnDevice** out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -682,13 +961,13 @@ cudaError_t prepare(OnDevice* all, K* kernel, OnDevice** out) {
   static std::mutex asking;
   const std::lock_guard<std::mutex> lock(asking);
   if (d.ready.load(std::memory_order_relaxed)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Tc::kSmem);
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   cudaFuncAttributes at{};
   if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, kernel);
   if (e != cudaSuccess) return e;
   // the register split must be what the CTA is launched with
   if (at.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
-  for (int i = 0; i < 4; ++i) d.clusters[i] = max_clusters(kernel, Tc::kThreads, Tc::kSmem, 1 << i);
+  for (int i = 0; i < 4; ++i) d.clusters[i] = max_clusters(kernel, Tc::kThreads, smem, 1 << i);
   d.ready.store(true, std::memory_order_release);
   return cudaSuccess;
 }
@@ -701,36 +980,59 @@ int parts_of_k(const OnDevice& d, int64_t tiles, int steps) {
   return 1 << i;
 }
 
+template <typename... P, typename... A>
+cudaError_t launch_clusters(void (*kernel)(P...), int64_t grid, int smem, int cluster, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(Tc::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute a{};
+  a.id = cudaLaunchAttributeClusterDimension;
+  a.val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
+  cfg.attrs = &a;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Tiles of 256 x 256 that a product has; of rows in groups there may be as many more
+// as groups, in each of which the last one may be short.
+int64_t most_tiles(const F8Args& p) {
+  const int64_t ntn = (p.N + 2 * kM - 1) / (2 * kM), ntt = (p.T + Tc::NT - 1) / Tc::NT;
+  return ntn * (p.offsets ? std::min<int64_t>(p.T, ntt + p.E) : ntt);
+}
+
 template <typename O>
 cudaError_t launch_tc(const F8Args& p, cudaStream_t s) {
   static OnDevice all[kMaxDev];
   OnDevice* d;
-  cudaError_t e = prepare(all, k_tc_f8<O>, &d);
+  cudaError_t e = prepare(all, k_tc_f8<O>, Tc::kSmem, &d);
   Maps maps;
   if (e == cudaSuccess) e = map_rows(&maps.w, p.w, p.ldw, p.gw ? p.gw : p.ldw, p.gw ? p.E : 1, p.N, p.K, kM);
   for (int i = 0; i < 4 && e == cudaSuccess; ++i) e = map_rows(&maps.x[i], p.x, p.ldx, 0, 0, p.T, p.K, 128 >> i);
   if (e != cudaSuccess) return e;
-  // every tile that a product of T rows has; of rows in groups there may be as many more as groups
-  const int64_t ntn = (p.N + 2 * kM - 1) / (2 * kM), tiles = ntn * ((p.T + Tc::NT - 1) / Tc::NT);
+  const int64_t tiles = most_tiles(p);
   const int split = p.offsets ? 1 : parts_of_k(*d, tiles, (p.K + kB - 1) / kB);
-  const int64_t most = p.offsets ? ntn * std::min<int64_t>(p.T, (p.T + Tc::NT - 1) / Tc::NT + p.E) : tiles;
-  const int64_t pairs = split > 1 ? tiles * split : std::min<int64_t>(most, sm_count() / 2);
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
-  cfg.blockDim = dim3(Tc::kThreads);
-  cfg.dynamicSmemBytes = Tc::kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute a{};
-  a.id = cudaLaunchAttributeClusterDimension;
-  a.val.clusterDim = {static_cast<unsigned>(2 * split), 1, 1};
-  cfg.attrs = &a;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_tc_f8<O>, p, maps, split);
+  const int64_t pairs = split > 1 ? tiles * split : std::min<int64_t>(tiles, sm_count() / 2);
+  return launch_clusters(k_tc_f8<O>, 2 * pairs, Tc::kSmem, 2 * split, s, p, maps, split);
+}
+
+template <typename O>
+cudaError_t launch_wide(const F8Args& p, cudaStream_t s) {
+  static OnDevice all[kMaxDev];
+  OnDevice* d;
+  cudaError_t e = prepare(all, k_wide_f8<O>, Wide::kSmem, &d);
+  CUtensorMap mapx, mapw;
+  if (e == cudaSuccess) e = map_rows(&mapx, p.x, p.ldx, 0, 0, p.T, p.K, kM);
+  if (e == cudaSuccess) e = map_rows(&mapw, p.w, p.ldw, p.gw ? p.gw : p.ldw, p.gw ? p.E : 1, p.N, p.K, kM);
+  if (e != cudaSuccess) return e;
+  return launch_clusters(k_wide_f8<O>, 2 * std::min<int64_t>(most_tiles(p), sm_count() / 2), Wide::kSmem, 2, s, p, mapx, mapw);
 }
 
 template <typename O>
 cudaError_t launch_f8(const F8Args& p, cudaStream_t s) {
   const int64_t rows = p.offsets ? (p.T + p.E - 1) / p.E : p.T;   // of a group, about
+  if (rows > 256) return launch_wide<O>(p, s);
   if (rows > 16) return launch_tc<O>(p, s);
   const int nt = rows <= 8 ? 1 : 2;
   const int turns = static_cast<int>(std::min<int64_t>((rows + nt * 8 - 1) / (nt * 8), 65535 / p.E));
