@@ -14,6 +14,7 @@
 #include <atomic>
 #include <cmath>
 #include <mutex>
+#include <type_traits>
 
 #include "pw_rows.cuh"
 #include "pw_tc.cuh"
@@ -672,16 +673,19 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, int split) {
 // ---------------------------------------------------------------- many rows
 
 // As k_tc_f8 with the operands' parts exchanged: the rows are the MMA's M (256 to a pair,
-// 128 to a CTA) and the channels its N (256).  A lane of tensor memory is then a row, so a
-// block's sums take one factor to a thread, which the thread reads for itself.
+// 128 to a CTA) and the channels its N (256).  A lane of tensor memory is then a row, so
+// the sums of 128 channels (a block of the weights' scales) take one factor to a thread,
+// which fetches its scales for itself, kAhead blocks ahead.
 struct Wide {
   static constexpr int NT = 256, EW = 8, ACC = NT / (EW / 4);
   static constexpr int kThreads = 32 * (kEpiWarp0 + EW);
   static constexpr int X = kM * kB, W = NT / 2 * kB;      // bytes of a stage's operands
-  static constexpr int S = 6;
+  static constexpr int S = 5;
   static constexpr int kOffOut = S * (X + W);
-  static constexpr int kOutWarp = 32 * 128;               // a warp's part of the stores: 32 rows x 128 bytes
-  static constexpr int kOffBar = kOffOut + EW * kOutWarp;
+  static constexpr int kPiece = 32 * 128;                 // a warp stores 32 rows x 128 bytes at a time
+  static constexpr int kAhead = 4;                        // blocks
+  static constexpr int kOffScale = kOffOut + EW * kPiece; // [kAhead][row's, weights'][thread]
+  static constexpr int kOffBar = kOffScale + kAhead * 2 * EW * 32 * 4;
   static constexpr int kBars = 2 * S + 5;
   static constexpr int kOffMisc = kOffBar + 8 * kBars;
   static constexpr int kSmem = kOffMisc + 16 + 4 * (PW_MAX_GROUPS + 1);
@@ -713,9 +717,27 @@ __device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
                : "memory");
 }
 
+// Four bytes into shared memory, asynchronously.
+__device__ __forceinline__ void copy4(uint32_t to, const float* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ float lds4(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(src)
+               : "memory");
+}
+
 template <typename O>
 __global__ void __launch_bounds__(Wide::kThreads, 1)
-k_wide_f8(const F8Args p, const __grid_constant__ CUtensorMap mapx, const __grid_constant__ CUtensorMap mapw) {
+k_wide_f8(const F8Args p, const __grid_constant__ CUtensorMap mapx, const __grid_constant__ CUtensorMap mapw,
+          const __grid_constant__ CUtensorMap mapo, int bulk) {
   using C = Wide;
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t base = saddr(smem);
@@ -799,24 +821,29 @@ k_wide_f8(const F8Args p, const __grid_constant__ CUtensorMap mapx, const __grid
           arrive_at(full + 8 * r.stage, 0);
       }
     } else if (warp == 1) {
-      // ---- MMA issue
+      // ---- MMA issue: the whole warp in step, so that the operands stay in uniform
+      // registers, and an elected thread for the instructions.  A barrier takes over 100
+      // clocks to read, so the next block's are read before this block's MMAs are issued
       Ring<C::S> r;
       Ring<2> d;
-      bool ok = true;
+      bool ok = true, ready = false;
       for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
-        for (int k = 0; k < steps; ++k, r.next(), d.next()) {
-          if (!d.first && !(ok = wait(dempty + 8 * d.stage, d.parity ^ 1))) break;
-          if (!(ok = wait(full + 8 * r.stage, r.parity))) break;
+        for (int k = 0; k < steps; ++k) {
+          if (!ready && !(ok = wait(full + 8 * r.stage, r.parity) && (d.first || wait(dempty + 8 * d.stage, d.parity ^ 1))))
+            break;
           tc_fence_after();
+          const uint32_t acc = tmem + d.stage * C::NT, at = base + r.stage * (C::X + C::W);
+          const uint32_t done = dfull + 8 * d.stage, free = empty + 8 * r.stage;
+          d.next(), r.next();
+          ready = test_wait(full + 8 * r.stage, r.parity) & (d.first || test_wait(dempty + 8 * d.stage, d.parity ^ 1));
           if (elect_one()) {
-            const uint64_t da = smem_desc(base + r.stage * (C::X + C::W)), db = da + (C::X >> 4);
+            const uint64_t da = smem_desc(at), db = da + (C::X >> 4);
 #pragma unroll
-            for (int kk = 0; kk < kB / 32; ++kk)
-              mma_f8_pair(tmem + d.stage * C::NT, da + kk * 2, db + kk * 2, Tc::idesc(C::NT), kk);
-            commit_pair(empty + 8 * r.stage, 3);
-            commit_pair(dfull + 8 * d.stage, 3);
+            for (int kk = 0; kk < kB / 32; ++kk) mma_f8_pair(acc, da + kk * 2, db + kk * 2, Tc::idesc(C::NT), kk);
+            commit_pair(free, 3);
+            commit_pair(done, 3);
           }
-          __syncwarp();
+          ready = __all_sync(0xffffffffu, ready);
         }
       }
       if (*abort) {   // the MMAs in flight end before the CTA does
@@ -836,87 +863,116 @@ k_wide_f8(const F8Args p, const __grid_constant__ CUtensorMap mapx, const __grid
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsAcc));
     const int q = warp & 3, h = (warp - kEpiWarp0) >> 2;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * C::ACC;
-    unsigned char* stage = smem + C::kOffOut + (warp - kEpiWarp0) * C::kOutWarp;
+    unsigned char* stage = smem + C::kOffOut + (warp - kEpiWarp0) * C::kPiece;
+    const uint32_t slots = base + C::kOffScale + (tid - kEpiWarp0 * 32) * 4;
+    constexpr uint32_t kSlot = C::EW * 32 * 4;
+    const float *xs = nullptr, *ws = nullptr;
+    // a block's scales of this thread into its place
+    auto fetch = [&](int k) {
+      if (k < steps) {
+        const uint32_t at = slots + k % C::kAhead * 2 * kSlot;
+        copy4(at, xs + k);
+        copy4(at + kSlot, ws + k);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    // the tile's rows and channels, and its first scales
+    auto begin = [&](const Tile& t) {
+      xs = p.xs + min(t.t0 + static_cast<int>(side) * kM + q * 32 + lane, t.t1 - 1) * p.ldxs;
+      ws = p.ws + t.e * p.gws + min(t.n0 + h * C::ACC, p.N - 1) / kB * p.ldws;
+#pragma unroll
+      for (int k = 0; k < C::kAhead - 1; ++k) fetch(k);
+    };
     Ring<2> d;
     bool ok = true, ready = false;
-    for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
-      const Tile t = order.at(p, tile);
-      const int row0 = t.t0 + static_cast<int>(side) * kM + q * 32;   // of the warp
-      const int n0 = t.n0 + h * C::ACC;
-      const float* xs = p.xs + min(row0 + lane, t.t1 - 1) * p.ldxs;
-      const float* ws = p.ws + t.e * p.gws + min(n0, p.N - 1) / kB * p.ldws;
-      float x_next = __ldg(xs), w_next = __ldg(ws);
-      uint64_t acc[C::ACC / 2];
+    Tile t{};
+    if (tile0 < tiles) begin(t = order.at(p, tile0));
+    for (int tile = tile0; tile < tiles; tile += tile_step) {
+      float acc[C::ACC];
 #pragma unroll
-      for (int i = 0; i < C::ACC / 2; ++i) acc[i] = 0;
-      for (int k = 0; k < steps; ++k, d.next()) {
-        const float f = x_next * w_next;
-        if (k + 1 < steps) x_next = __ldg(xs + k + 1), w_next = __ldg(ws + k + 1);
-        uint64_t f2;
-        asm("mov.b64 %0, {%1, %1};" : "=l"(f2) : "f"(f));
+      for (int i = 0; i < C::ACC; ++i) acc[i] = 0.f;
+      for (int k = 0; k < steps; ++k) {
+        fetch(k + C::kAhead - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(C::kAhead - 1) : "memory");
+        const uint32_t at = slots + k % C::kAhead * 2 * kSlot;
+        const float f = lds4(at) * lds4(at + kSlot);
         if (!ready && !(ok = wait(dfull + 8 * d.stage, d.parity))) break;
         tc_fence_after();
-        const uint32_t from = lanes + d.stage * C::NT;
-        uint32_t v[2][32];
-        tmem_ld32(from, v[0]);
+        const uint32_t from = lanes + d.stage * C::NT, free = dempty + 8 * d.stage;
+        d.next();
+        uint32_t v[32];
+        // (two warps share the FMA pipe, so that one's loads are behind the other's sums)
 #pragma unroll
-        for (int c = 0; c < C::ACC / 32; ++c) {
-          uint32_t(&now)[32] = v[c % 2];
-          tmem_wait32(now);
-          if (c + 1 < C::ACC / 32) {
-            tmem_ld32(from + (c + 1) * 32, v[(c + 1) % 2]);
-          } else {   // all of it is in registers
+        for (int c = 0; c < C::ACC; c += 32) {
+          tmem_ld32(from + c, v);
+          tmem_wait32(v);
+          if (c + 32 == C::ACC) {   // all of it is in registers
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-              arrive_at(dempty + 8 * d.stage, 0);
+              arrive_at(free, 0);
               // a barrier takes over 100 clocks to read: the next one's while this is added
-              ready = test_wait(dfull + 8 * (d.stage ^ 1), d.parity ^ d.stage);
+              ready = test_wait(dfull + 8 * d.stage, d.parity);
             }
           }
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) fma2(acc[c * 16 + i / 2], now[i], now[i + 1], f2);
+          for (int i = 0; i < 32; ++i) acc[c + i] = fmaf(__uint_as_float(v[i]), f, acc[c + i]);
         }
         ready = __shfl_sync(0xffffffffu, ready, 0);
       }
       if (!ok) break;
-      // 128 bytes of each of the warp's rows at a time, through shared memory
+      const int row0 = t.t0 + static_cast<int>(side) * kM + q * 32, t1 = t.t1, n0 = t.n0 + h * C::ACC, e = t.e;
+      if (tile + tile_step < tiles) begin(t = order.at(p, tile + tile_step));
+      // 128 bytes of each of the warp's rows at a time, through shared memory: by TMA where
+      // all of the rows are the group's, else row by row
       constexpr int N = 128 / sizeof(O), V = 16 / sizeof(O);   // channels of a turn, of 16 bytes
-      const bool wide = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.ldo % V == 0;
-      const O* bias = p.bias ? static_cast<const O*>(p.bias) + static_cast<int64_t>(t.e) * p.N : nullptr;
-      auto value = [&](int i) {
-        const float2 f = halves(acc[i / 2]);
-        return from_f32<O>((i & 1 ? f.y : f.x) + (bias && n0 + i < p.N ? to_f32<O>(__ldg(bias + n0 + i)) : 0.f));
-      };
+      if (p.bias) {
+        const O* bias = static_cast<const O*>(p.bias) + static_cast<int64_t>(e) * p.N + n0;
+#pragma unroll
+        for (int i = 0; i < C::ACC; ++i)
+          if (n0 + i < p.N) acc[i] += to_f32<O>(__ldg(bias + i));
+      }
+      const bool whole = bulk && row0 + 32 <= t1;
 #pragma unroll
       for (int c = 0; c < C::ACC; c += N) {
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // of the last turn
+        __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {   // the row's 16-byte pieces, each row's in another order
+        for (int i = 0; i < 8; ++i) {   // with the TMA's 128-byte swizzle
           alignas(16) O o[V];
 #pragma unroll
-          for (int e = 0; e < V; ++e) o[e] = value(c + i * V + e);
+          for (int e = 0; e < V; ++e) o[e] = from_f32<O>(acc[c + i * V + e]);
           *reinterpret_cast<uint4*>(stage + lane * 128 + ((i ^ (lane & 7)) << 4)) = *reinterpret_cast<const uint4*>(o);
         }
-        __syncwarp();
-        const int n = n0 + c + (lane & 7) * V;
+        if (whole) {
+          proxy_fence_smem();
+          __syncwarp();
+          if (lane == 0 && n0 + c < p.N) {
+            tma_store_2d(&mapo, n0 + c, row0, saddr(stage));
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+        } else {
+          __syncwarp();
+          const int n = n0 + c + (lane & 7) * V;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = i * 4 + (lane >> 3), row = row0 + r;
-          uint4 raw = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
-          if (row >= t.t1) continue;
-          O* out = static_cast<O*>(p.out) + row * p.ldo + n;
-          if (wide && n + V <= p.N) {
-            *reinterpret_cast<uint4*>(out) = raw;
-          } else {
-            const O* v = reinterpret_cast<const O*>(&raw);
+          for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + (lane >> 3), row = row0 + r;
+            const uint4 raw = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+            if (row >= t1) continue;
+            O* out = static_cast<O*>(p.out) + row * p.ldo + n;
+            if (bulk && n + V <= p.N) {
+              *reinterpret_cast<uint4*>(out) = raw;
+            } else {
+              const O* v = reinterpret_cast<const O*>(&raw);
 #pragma unroll
-            for (int e = 0; e < V; ++e)
-              if (n + e < p.N) out[e] = v[e];
+              for (int e = 0; e < V; ++e)
+                if (n + e < p.N) out[e] = v[e];
+            }
           }
         }
-        __syncwarp();
       }
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     __syncwarp();
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
     cta_barrier();
@@ -929,19 +985,24 @@ k_wide_f8(const F8Args p, const __grid_constant__ CUtensorMap mapx, const __grid
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols));
 }
 
-// Boxes of 128 columns x `box` rows of e4m3 rows [groups][rows][cols]; columns and rows
-// past the ends read as zero.
-cudaError_t map_rows(CUtensorMap* m, const void* base, int64_t ld, int64_t group, int groups, int rows, int cols, int box) {
+// Boxes of `cols_box` columns (128 bytes) x `box` rows of a tensor [groups][rows][cols]
+// (groups 0: a matrix) with strides in bytes; columns and rows past the ends read as zero,
+// and are not written.
+cudaError_t map_tile(CUtensorMap* m, CUtensorMapDataType type, const void* base, int64_t ld, int64_t group, int groups,
+                     int rows, int cols, int box, int cols_box) {
   const auto encode = encoder();
   if (!encode) return cudaErrorNotSupported;
-  const cuuint32_t rank = groups ? 3 : 2;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(groups)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld), static_cast<cuuint64_t>(group)};
-  const cuuint32_t boxes[3] = {kB, static_cast<cuuint32_t>(box), 1}, es[3] = {1, 1, 1};
-  const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims, strides, boxes, es,
+  const cuuint32_t boxes[3] = {static_cast<cuuint32_t>(cols_box), static_cast<cuuint32_t>(box), 1}, es[3] = {1, 1, 1};
+  const CUresult r = encode(m, type, groups ? 3 : 2, const_cast<void*>(base), dims, strides, boxes, es,
                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+// e4m3 rows in boxes of 128 columns, [groups][rows][cols].
+cudaError_t map_rows(CUtensorMap* m, const void* base, int64_t ld, int64_t group, int groups, int rows, int cols, int box) {
+  return map_tile(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, ld, group, groups, rows, cols, box, kB);
 }
 
 // What the kernel's launches need to know about a device, asked once.
@@ -1022,11 +1083,17 @@ cudaError_t launch_wide(const F8Args& p, cudaStream_t s) {
   static OnDevice all[kMaxDev];
   OnDevice* d;
   cudaError_t e = prepare(all, k_wide_f8<O>, Wide::kSmem, &d);
-  CUtensorMap mapx, mapw;
+  CUtensorMap mapx, mapw, mapo{};
+  // stores by TMA, and of 16 bytes
+  const bool bulk = aligned(p.out, 16) && p.ldo * sizeof(O) % 16 == 0;
   if (e == cudaSuccess) e = map_rows(&mapx, p.x, p.ldx, 0, 0, p.T, p.K, kM);
   if (e == cudaSuccess) e = map_rows(&mapw, p.w, p.ldw, p.gw ? p.gw : p.ldw, p.gw ? p.E : 1, p.N, p.K, kM);
+  if (e == cudaSuccess && bulk)
+    e = map_tile(&mapo, std::is_same_v<O, float> ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, p.out,
+                 p.ldo * sizeof(O), 0, 0, p.T, p.N, 32, 128 / sizeof(O));
   if (e != cudaSuccess) return e;
-  return launch_clusters(k_wide_f8<O>, 2 * std::min<int64_t>(most_tiles(p), sm_count() / 2), Wide::kSmem, 2, s, p, mapx, mapw);
+  return launch_clusters(k_wide_f8<O>, 2 * std::min<int64_t>(most_tiles(p), sm_count() / 2), Wide::kSmem, 2, s, p, mapx, mapw,
+                         mapo, static_cast<int>(bulk));
 }
 
 template <typename O>
