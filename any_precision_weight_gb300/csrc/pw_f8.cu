@@ -268,24 +268,12 @@ static_assert(128 * (kRegsIssue + 2 * kRegsAcc) <= Tc::kThreads * kRegsLaunch, "
 __device__ uint32_t g_f8_timeouts;
 __global__ void k_count_timeout() { atomicAdd(&g_f8_timeouts, 1u); }
 
-// Whether the phase of the given parity has ended; waits for it up to 2 us.
-__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 2000;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return done;
-}
-
-// Waits up to kPolls times (at most a few seconds) for the phase of the given parity;
-// false, and the abort flag, when they run out or another thread has raised it.
-constexpr int kPolls = 1 << 20;
+// Polls up to kPolls times (about a second) for the phase of the given parity; false,
+// and the abort flag, when they run out or another thread has raised it.  (test_wait:
+// a thread that try_wait has put to sleep wakes up some hundred clocks late.)
+constexpr int kPolls = 1 << 23;
 __device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, volatile int* abort) {
-  for (int n = 0; !try_wait(bar, parity); ++n) {
+  for (int n = 0; !test_wait(bar, parity); ++n) {
     if (*abort) return false;
     if (n == kPolls) {
       atomicAdd(&g_f8_timeouts, 1u);
@@ -823,19 +811,19 @@ k_wide_f8(const F8Args p, const __grid_constant__ CUtensorMap mapx, const __grid
     } else if (warp == 1) {
       // ---- MMA issue: the whole warp in step, so that the operands stay in uniform
       // registers, and an elected thread for the instructions.  A barrier takes over 100
-      // clocks to read, so the next block's are read before this block's MMAs are issued
+      // clocks to read, so the next stage's is read before this one's MMAs are issued
       Ring<C::S> r;
       Ring<2> d;
-      bool ok = true, ready = false;
+      bool ok = true, loaded = false;
       for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
         for (int k = 0; k < steps; ++k) {
-          if (!ready && !(ok = wait(full + 8 * r.stage, r.parity) && (d.first || wait(dempty + 8 * d.stage, d.parity ^ 1))))
-            break;
+          if (!loaded && !(ok = wait(full + 8 * r.stage, r.parity))) break;
+          if (!d.first && !(ok = wait(dempty + 8 * d.stage, d.parity ^ 1))) break;
           tc_fence_after();
           const uint32_t acc = tmem + d.stage * C::NT, at = base + r.stage * (C::X + C::W);
           const uint32_t done = dfull + 8 * d.stage, free = empty + 8 * r.stage;
           d.next(), r.next();
-          ready = test_wait(full + 8 * r.stage, r.parity) & (d.first || test_wait(dempty + 8 * d.stage, d.parity ^ 1));
+          loaded = test_wait(full + 8 * r.stage, r.parity);
           if (elect_one()) {
             const uint64_t da = smem_desc(at), db = da + (C::X >> 4);
 #pragma unroll
@@ -843,7 +831,7 @@ k_wide_f8(const F8Args p, const __grid_constant__ CUtensorMap mapx, const __grid
             commit_pair(free, 3);
             commit_pair(done, 3);
           }
-          ready = __all_sync(0xffffffffu, ready);
+          loaded = __all_sync(0xffffffffu, loaded);
         }
       }
       if (*abort) {   // the MMAs in flight end before the CTA does
