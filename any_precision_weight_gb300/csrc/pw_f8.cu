@@ -662,8 +662,10 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, int split) {
 
 // As k_tc_f8 with the operands' parts exchanged: the rows are the MMA's M (256 to a pair,
 // 128 to a CTA) and the channels its N (256).  A lane of tensor memory is then a row, so
-// the sums of 128 channels (a block of the weights' scales) take one factor to a thread,
-// which fetches its scales for itself, kAhead blocks ahead.
+// the sums of 128 channels (a block of the weights' scales) take one factor to a thread.
+// Warps 2 and 3 write those into a ring of SS and report them with the loads of the block:
+// an MMA that has ended says that its block's factors are there, and one that starts, that
+// those of two blocks before have been read.
 struct Wide {
   static constexpr int NT = 256, EW = 8, ACC = NT / (EW / 4);
   static constexpr int kThreads = 32 * (kEpiWarp0 + EW);
@@ -671,14 +673,15 @@ struct Wide {
   static constexpr int S = 5;
   static constexpr int kOffOut = S * (X + W);
   static constexpr int kPiece = 32 * 128;                 // a warp stores 32 rows x 128 bytes at a time
-  static constexpr int kAhead = 4;                        // blocks
-  static constexpr int kOffScale = kOffOut + EW * kPiece; // [kAhead][row's, weights'][thread]
-  static constexpr int kOffBar = kOffScale + kAhead * 2 * EW * 32 * 4;
+  static constexpr int SS = 8;
+  static constexpr int kOffScale = kOffOut + EW * kPiece; // [SS][half of the channels][row]
+  static constexpr int kOffBar = kOffScale + SS * 2 * kM * 4;
   static constexpr int kBars = 2 * S + 5;
   static constexpr int kOffMisc = kOffBar + 8 * kBars;
   static constexpr int kSmem = kOffMisc + 16 + 4 * (PW_MAX_GROUPS + 1);
   static constexpr uint32_t kCols = 2 * NT;
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+  static_assert(SS >= S + 2, "the factors of a block that may be fetched have been read");
 };
 static_assert(Wide::kThreads == Tc::kThreads, "one register split");
 
@@ -705,10 +708,6 @@ __device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
                : "memory");
 }
 
-// Four bytes into shared memory, asynchronously.
-__device__ __forceinline__ void copy4(uint32_t to, const float* from) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
-}
 __device__ __forceinline__ float lds4(uint32_t a) {
   float v;
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
@@ -751,7 +750,7 @@ k_wide_f8(const F8Args p, const __grid_constant__ CUtensorMap mapx, const __grid
   }
   if (tid == 0) {
     for (int i = 0; i < C::S; ++i) {
-      mbar_init(full + 8 * i, side ? 1 : 2);   // the CTA's loads, and the odd CTA's report
+      mbar_init(full + 8 * i, side ? 3 : 4);   // the CTA's loads and factors, and the odd CTA's report
       mbar_init(empty + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) mbar_init(dfull + 8 * i, 1), mbar_init(dempty + 8 * i, 2 * C::EW);
@@ -797,6 +796,41 @@ k_wide_f8(const F8Args p, const __grid_constant__ CUtensorMap mapx, const __grid
             poll(full + 8 * i, r.parity, &none);
           else if (!r.first)
             poll(full + 8 * i, r.parity ^ 1, &none);
+        }
+      }
+    }
+    if (warp >= 2) {
+      // ---- factors: four rows to a lane, half of the channels to a warp, four blocks at a time
+      Ring<C::S> r;
+      uint32_t slot = 0;
+      bool ok = true;
+      for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
+        const Tile t = order.at(p, tile);
+        const float* ws = p.ws + t.e * p.gws + min(t.n0 / kB + warp - 2, (p.N - 1) / kB) * p.ldws;
+        const float* xs[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          xs[i] = p.xs + min(t.t0 + static_cast<int>(side) * kM + lane * 4 + i, t.t1 - 1) * p.ldxs;
+        for (int k0 = 0; k0 < steps && ok; k0 += 4) {
+          float v[4][4], w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int k = min(k0 + j, steps - 1);
+            w[j] = __ldg(ws + k);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i][j] = __ldg(xs[i] + k);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (k0 + j >= steps) break;
+            if (!r.first && !(ok = wait(empty + 8 * r.stage, r.parity ^ 1))) break;
+            *reinterpret_cast<float4*>(smem + C::kOffScale + ((slot * 2 + warp - 2) * kM + lane * 4) * 4) =
+                make_float4(v[0][j] * w[j], v[1][j] * w[j], v[2][j] * w[j], v[3][j] * w[j]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full + 8 * r.stage);
+            r.next();
+            slot = (slot + 1) % C::SS;
+          }
         }
       }
     }
@@ -852,42 +886,21 @@ k_wide_f8(const F8Args p, const __grid_constant__ CUtensorMap mapx, const __grid
     const int q = warp & 3, h = (warp - kEpiWarp0) >> 2;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * C::ACC;
     unsigned char* stage = smem + C::kOffOut + (warp - kEpiWarp0) * C::kPiece;
-    const uint32_t slots = base + C::kOffScale + (tid - kEpiWarp0 * 32) * 4;
-    constexpr uint32_t kSlot = C::EW * 32 * 4;
-    const float *xs = nullptr, *ws = nullptr;
-    // a block's scales of this thread into its place
-    auto fetch = [&](int k) {
-      if (k < steps) {
-        const uint32_t at = slots + k % C::kAhead * 2 * kSlot;
-        copy4(at, xs + k);
-        copy4(at + kSlot, ws + k);
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    // the tile's rows and channels, and its first scales
-    auto begin = [&](const Tile& t) {
-      xs = p.xs + min(t.t0 + static_cast<int>(side) * kM + q * 32 + lane, t.t1 - 1) * p.ldxs;
-      ws = p.ws + t.e * p.gws + min(t.n0 + h * C::ACC, p.N - 1) / kB * p.ldws;
-#pragma unroll
-      for (int k = 0; k < C::kAhead - 1; ++k) fetch(k);
-    };
+    const uint32_t factors = base + C::kOffScale + (h * kM + q * 32 + lane) * 4;
+    uint32_t slot = 0;
     Ring<2> d;
     bool ok = true, ready = false;
-    Tile t{};
-    if (tile0 < tiles) begin(t = order.at(p, tile0));
     for (int tile = tile0; tile < tiles; tile += tile_step) {
       float acc[C::ACC];
 #pragma unroll
       for (int i = 0; i < C::ACC; ++i) acc[i] = 0.f;
       for (int k = 0; k < steps; ++k) {
-        fetch(k + C::kAhead - 1);
-        asm volatile("cp.async.wait_group %0;" ::"n"(C::kAhead - 1) : "memory");
-        const uint32_t at = slots + k % C::kAhead * 2 * kSlot;
-        const float f = lds4(at) * lds4(at + kSlot);
         if (!ready && !(ok = wait(dfull + 8 * d.stage, d.parity))) break;
         tc_fence_after();
         const uint32_t from = lanes + d.stage * C::NT, free = dempty + 8 * d.stage;
+        const float f = lds4(factors + slot * (2 * kM * 4));
         d.next();
+        slot = (slot + 1) % C::SS;
         uint32_t v[32];
         // (two warps share the FMA pipe, so that one's loads are behind the other's sums)
 #pragma unroll
@@ -909,18 +922,18 @@ k_wide_f8(const F8Args p, const __grid_constant__ CUtensorMap mapx, const __grid
         ready = __shfl_sync(0xffffffffu, ready, 0);
       }
       if (!ok) break;
-      const int row0 = t.t0 + static_cast<int>(side) * kM + q * 32, t1 = t.t1, n0 = t.n0 + h * C::ACC, e = t.e;
-      if (tile + tile_step < tiles) begin(t = order.at(p, tile + tile_step));
+      const Tile t = order.at(p, tile);
+      const int row0 = t.t0 + static_cast<int>(side) * kM + q * 32, n0 = t.n0 + h * C::ACC;
       // 128 bytes of each of the warp's rows at a time, through shared memory: by TMA where
       // all of the rows are the group's, else row by row
       constexpr int N = 128 / sizeof(O), V = 16 / sizeof(O);   // channels of a turn, of 16 bytes
       if (p.bias) {
-        const O* bias = static_cast<const O*>(p.bias) + static_cast<int64_t>(e) * p.N + n0;
+        const O* bias = static_cast<const O*>(p.bias) + static_cast<int64_t>(t.e) * p.N + n0;
 #pragma unroll
         for (int i = 0; i < C::ACC; ++i)
           if (n0 + i < p.N) acc[i] += to_f32<O>(__ldg(bias + i));
       }
-      const bool whole = bulk && row0 + 32 <= t1;
+      const bool whole = bulk && row0 + 32 <= t.t1;
 #pragma unroll
       for (int c = 0; c < C::ACC; c += N) {
         if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // of the last turn
@@ -946,7 +959,7 @@ k_wide_f8(const F8Args p, const __grid_constant__ CUtensorMap mapx, const __grid
           for (int i = 0; i < 8; ++i) {
             const int r = i * 4 + (lane >> 3), row = row0 + r;
             const uint4 raw = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
-            if (row >= t1) continue;
+            if (row >= t.t1) continue;
             O* out = static_cast<O*>(p.out) + row * p.ldo + n;
             if (bulk && n + V <= p.N) {
               *reinterpret_cast<uint4*>(out) = raw;
