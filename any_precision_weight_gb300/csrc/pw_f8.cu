@@ -764,11 +764,9 @@ k_wide_f8(const F8Args p, const __grid_constant__ CUtensorMap mapx, const __grid
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, static_cast<uint32_t>(s_misc[0]), 0);
-  auto wait = [&](uint32_t bar, uint32_t parity) {   // as in k_tc_f8
-    const bool ok = __all_sync(0xffffffffu, lane != 0 || poll(bar, parity, abort));
-    __syncwarp();
-    return ok;
-  };
+  // (a look at a barrier takes 41 clocks by the whole warp, and 96 by one thread that
+  // tells the others)
+  auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, poll(bar, parity, abort)); };
   const int tiles = s_start[p.E], steps = (p.K + kB - 1) / kB;
   const int tile0 = blockIdx.x / 2, tile_step = gridDim.x / 2;
   Tiles order{s_start, ntn};
@@ -844,28 +842,26 @@ k_wide_f8(const F8Args p, const __grid_constant__ CUtensorMap mapx, const __grid
       }
     } else if (warp == 1) {
       // ---- MMA issue: the whole warp in step, so that the operands stay in uniform
-      // registers, and an elected thread for the instructions.  A barrier takes over 100
-      // clocks to read, so the next stage's is read before this one's MMAs are issued
+      // registers, and an elected thread for the instructions
       Ring<C::S> r;
       Ring<2> d;
-      bool ok = true, loaded = false;
+      bool ok = true;
       for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
         for (int k = 0; k < steps; ++k) {
-          if (!loaded && !(ok = wait(full + 8 * r.stage, r.parity))) break;
+          if (!(ok = wait(full + 8 * r.stage, r.parity))) break;
           if (!d.first && !(ok = wait(dempty + 8 * d.stage, d.parity ^ 1))) break;
           tc_fence_after();
           const uint32_t acc = tmem + d.stage * C::NT, at = base + r.stage * (C::X + C::W);
           const uint32_t done = dfull + 8 * d.stage, free = empty + 8 * r.stage;
           d.next(), r.next();
-          loaded = test_wait(full + 8 * r.stage, r.parity);
           if (elect_one()) {
             const uint64_t da = smem_desc(at), db = da + (C::X >> 4);
 #pragma unroll
             for (int kk = 0; kk < kB / 32; ++kk) mma_f8_pair(acc, da + kk * 2, db + kk * 2, Tc::idesc(C::NT), kk);
-            commit_pair(free, 3);
             commit_pair(done, 3);
+            commit_pair(free, 3);
           }
-          loaded = __all_sync(0xffffffffu, loaded);
+          __syncwarp();
         }
       }
       if (*abort) {   // the MMAs in flight end before the CTA does
@@ -889,13 +885,13 @@ k_wide_f8(const F8Args p, const __grid_constant__ CUtensorMap mapx, const __grid
     const uint32_t factors = base + C::kOffScale + (h * kM + q * 32 + lane) * 4;
     uint32_t slot = 0;
     Ring<2> d;
-    bool ok = true, ready = false;
+    bool ok = true;
     for (int tile = tile0; tile < tiles; tile += tile_step) {
       float acc[C::ACC];
 #pragma unroll
       for (int i = 0; i < C::ACC; ++i) acc[i] = 0.f;
       for (int k = 0; k < steps; ++k) {
-        if (!ready && !(ok = wait(dfull + 8 * d.stage, d.parity))) break;
+        if (!(ok = wait(dfull + 8 * d.stage, d.parity))) break;
         tc_fence_after();
         const uint32_t from = lanes + d.stage * C::NT, free = dempty + 8 * d.stage;
         const float f = lds4(factors + slot * (2 * kM * 4));
@@ -911,15 +907,13 @@ k_wide_f8(const F8Args p, const __grid_constant__ CUtensorMap mapx, const __grid
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-              arrive_at(free, 0);
-              // a barrier takes over 100 clocks to read: the next one's while this is added
-              ready = test_wait(dfull + 8 * d.stage, d.parity);
+              if (side) arrive_at(free, 0);
+              else mbar_arrive(free);
             }
           }
 #pragma unroll
           for (int i = 0; i < 32; ++i) acc[c + i] = fmaf(__uint_as_float(v[i]), f, acc[c + i]);
         }
-        ready = __shfl_sync(0xffffffffu, ready, 0);
       }
       if (!ok) break;
       const Tile t = order.at(p, tile);
