@@ -221,41 +221,53 @@ cudaError_t launch_few(const F8Args& p, int turns, cudaStream_t s) {
 
 // ---------------------------------------------------------------- tensor cores
 
-// Pairs of CTAs (cta_group::2), one CTA to an SM, take tiles of 256 channels (M, 128 to a
-// CTA: one block of the weights' scales) x up to 256 rows (N) with tcgen05.mma
-// kind::f8f6f4.  Each block of 128 columns of K goes into an accumulator of its own in
-// tensor memory, of two that take turns, and from there scaled into fp32 registers.
+// One CTA to an SM takes tiles of 128 rows (M) x up to 256 channels (N), a pair of CTAs
+// (cta_group::2) tiles of 256 rows, with tcgen05.mma kind::f8f6f4.  Each block of 128
+// columns of K goes into an accumulator of its own in tensor memory, of two or four that
+// take turns, and from there scaled into fp32 registers.  A lane of tensor memory is a row,
+// so 64 channels (half a block of the weights' scales) take one factor to a thread.
 // Warps by role:
-//  * warp 0 fetches weights and rows by TMA into a ring of S stages (128 columns each);
-//  * warp 1 issues the MMAs (in the even CTA, for both; in the odd one it reports its
-//    loads to the even one);
-//  * warps 2 and 3 write the products of both scales for each block into a ring of SS;
-//  * warps 4.. scale each finished accumulator into their sums while the next one
-//    fills, and at the tile's end store.
-// Where there are few tiles a cluster of pairs splits K and adds the parts through
-// distributed shared memory, in the order of the parts.
-constexpr int kM = 128;
+//  * warp 0 fetches rows and weights by TMA into a ring of stages (128 columns each);
+//  * warp 1 issues the MMAs (of a pair in the even CTA, for both; in the odd one it
+//    reports its loads to the even one);
+//  * warps 2 and 3 write a block's scales into a ring of SS and report them with the loads
+//    of the block: an MMA that has ended says that its block's scales are there, and one
+//    that starts, that those of the block that had its accumulator before have been read;
+//  * warps 4.. scale each finished accumulator into their sums while the next ones fill,
+//    and at the tile's end store.
+// Where there are few tiles a cluster splits K and adds the parts through distributed
+// shared memory, in the order of the parts.
+constexpr int kM = 128;          // rows of a CTA
 constexpr int kEpiWarp0 = 4;
 
 struct Tc {
-  static constexpr int NT = 256;
+  static constexpr int NT = 256;                          // most channels of a tile
   static constexpr int EW = 8;                            // accumulating warps
   static constexpr int ACC = NT / (EW / 4);               // sums of one of their threads
   static constexpr int kThreads = 32 * (kEpiWarp0 + EW);
-  static constexpr int A = kM * kB, X = NT / 2 * kB;      // bytes of a stage's operands
-  static constexpr int S = 6, SS = 8;
-  static constexpr int kOffScale = S * (A + X);
-  static constexpr int kOffBar = kOffScale + SS * NT * 4;
-  static constexpr int kBars = 2 * S + 2 * SS + 5;
+  static constexpr int kRing = 184 * 1024;                // bytes of the stages
+  static constexpr int S = 8;                             // most of them
+  static constexpr int D = 4;                             // most accumulators
+  static constexpr int kPiece = 32 * 128;                 // what a warp stores at a time: 32 rows x 32 channels
+  static constexpr int SS = 12;
+  static constexpr int kScale = kM + 4;                   // floats: the rows', and one for each 64 channels
+  static constexpr int kOffOut = kRing;
+  static constexpr int kOffScale = kOffOut + EW * kPiece;
+  static constexpr int kOffBar = kOffScale + SS * kScale * 4;
+  static constexpr int kBars = 2 * S + 2 * D + 1;
   static constexpr int kOffMisc = kOffBar + 8 * kBars;    // tmem, abort, first tile of each group
-  static constexpr int kSmem = kOffMisc + 16 + 4 * (PW_MAX_GROUPS + 1) + 1024;
-  static constexpr uint32_t kCols = 2 * NT;
-  // D f32, A and B e4m3, N / 8 and M / 16
-  __host__ __device__ static constexpr uint32_t idesc(int n) {
-    return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(2 * kM >> 4) << 24);
-  }
-  static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
-  static_assert(kM * NT * 4 <= kOffScale, "a CTA's sums fit the operand ring");
+  static constexpr int kSmem = kOffMisc + 16 + 4 * (PW_MAX_GROUPS + 1);
+  static constexpr uint32_t kCols = 512;                  // of tensor memory
+  static constexpr int kSumRow = NT + 1;                  // of a row's sums in the ring, padded
+  static_assert(kOffBar % 8 == 0 && kSmem <= 227 * 1024, "shared memory of a CTA");
+  static_assert(SS >= S + D, "the scales of a block that may be fetched have been read");
+  static_assert(kM * kSumRow * 4 <= kRing, "a CTA's sums fit the ring");
+};
+
+// What a launch chose: channels of a tile (a multiple of 64) and parts of K; and what
+// follows: bytes of a stage's rows and of the stage, stages, accumulators.
+struct Plan {
+  int nw, split, x_bytes, stage, stages, accs;
 };
 
 // Registers by role: 384 threads are launched with kRegsLaunch each, and the
@@ -290,400 +302,56 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
-
-// MMA of a pair of CTAs: 32 columns of K.
-__device__ __forceinline__ void mma_f8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
-
-__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t s) {
-  asm("{\n\t.reg .b64 t;\n\tmov.b64 t, {%1, %2};\n\tfma.rn.f32x2 %0, t, %3, %0;\n\t}" : "+l"(acc) : "r"(lo), "r"(hi), "l"(s));
-}
-__device__ __forceinline__ void lds_2x64(uint32_t a, uint64_t& x, uint64_t& y) {
-  asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "r"(a) : "memory");
-}
-__device__ __forceinline__ float2 halves(uint64_t v) {
-  float2 f;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
-  return f;
-}
-__device__ __forceinline__ float4 ld_cluster(uint32_t addr, uint32_t rank) {
-  uint32_t a;
-  float4 v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(a)
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(src)
                : "memory");
-  return v;
 }
 
-// Tensor maps: the weights in boxes of 128 rows, the rows in boxes of 128, 64, 32 and 16.
-struct Maps {
-  CUtensorMap w;
-  CUtensorMap x[4];
-};
-
-// Tiles of a group of `rows` rows: about the same number of rows for all, a multiple of
-// the 32 that a pair's MMA takes.
-struct Split {
-  int tiles, nt;
-  __device__ __forceinline__ explicit Split(int rows) {
-    tiles = (rows + Tc::NT - 1) / Tc::NT;
-    nt = tiles ? ((rows + tiles - 1) / tiles + 31) / 32 * 32 : 0;
+// What a CTA alone and a pair do differently.
+template <int CTAS> struct Cta;
+template <> struct Cta<1> {
+  static __device__ __forceinline__ void alloc(uint32_t to) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(to), "r"(Tc::kCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-};
-
-// A tile: its group, rows [t0, t1) of a tile of nt, and its 256 channels from n0 on.
-struct Tile {
-  int e, nt, t0, t1, n0;
-};
-
-// The tiles in order of the groups, `start` the first of each; within a group bands of
-// kBand row tiles, so that pairs at work share operands in the L2.
-constexpr int kBand = 8;
-struct Tiles {
-  const int* start;
-  int ntn, e = 0;
-  __device__ __forceinline__ Tile at(const F8Args& p, int tile) {
-    while (tile >= start[e + 1]) ++e;
-    const Rows r = rows_of(p, e);
-    const Split s(r.end - r.begin);
-    const int local = tile - start[e], band = local / (kBand * ntn), rest = local - band * kBand * ntn;
-    const int width = min(kBand, s.tiles - band * kBand), tt = band * kBand + rest % width;
-    const int t0 = r.begin + tt * s.nt;
-    return {e, s.nt, t0, min(r.end, t0 + s.nt), rest / width * 2 * kM};
+  static __device__ __forceinline__ void dealloc(uint32_t tmem) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(Tc::kCols));
   }
-};
-
-// The first tile of each group, and behind them the number of tiles, by one warp.
-__device__ __forceinline__ void first_tiles(const F8Args& p, int ntn, int* start) {
-  const int lane = threadIdx.x & 31;
-  int before = 0;
-  for (int e0 = 0; e0 < p.E; e0 += 32) {
-    int n = 0;
-    if (e0 + lane < p.E) {
-      const Rows r = rows_of(p, e0 + lane);
-      n = Split(r.end - r.begin).tiles * ntn;
-    }
-    int sum = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += v;
-    }
-    if (e0 + lane < p.E) start[e0 + lane] = before + sum - n;
-    before += __shfl_sync(0xffffffffu, sum, 31);
+  // 32 columns of K
+  static __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
   }
-  if (lane == 0) start[p.E] = before;
-}
-
-template <typename O>
-__global__ void __launch_bounds__(Tc::kThreads, 1)
-k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, int split) {
-  using C = Tc;
-  extern __shared__ __align__(1024) unsigned char smem_raw[];
-  unsigned char* smem = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);
-  const uint32_t base = saddr(smem);
-  const uint32_t full = base + C::kOffBar, empty = full + 8 * C::S;
-  const uint32_t sfull = empty + 8 * C::S, sempty = sfull + 8 * C::SS;
-  const uint32_t dfull = sempty + 8 * C::SS, dempty = dfull + 16, fin = dempty + 16;
-  int* s_misc = reinterpret_cast<int*>(smem + C::kOffMisc);   // tmem, abort
-  int* s_start = s_misc + 4;
-  volatile int* abort = s_misc + 1;
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // the compiler then knows that it is uniform
-  // the CTA's place: in its pair, and among the parts of K
-  uint32_t rank;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-  const uint32_t side = rank & 1, part = rank >> 1, leader = rank - side;
-  const int ntn = (p.N + 2 * kM - 1) / (2 * kM);
-
-  if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(s_misc)),
-                 "r"(C::kCols));
+  static __device__ __forceinline__ void commit(uint32_t bar, uint32_t) { mma_commit(bar); }
+};
+template <> struct Cta<2> {
+  static __device__ __forceinline__ void alloc(uint32_t to) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(to), "r"(Tc::kCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
   }
-  if (tid == 0) {
-    for (int i = 0; i < C::S; ++i) {
-      mbar_init(full + 8 * i, side ? 1 : 2);   // the CTA's loads, and the odd CTA's report
-      mbar_init(empty + 8 * i, 1);
-    }
-    for (int i = 0; i < C::SS; ++i) mbar_init(sfull + 8 * i, 2), mbar_init(sempty + 8 * i, C::EW);
-    for (int i = 0; i < 2; ++i) mbar_init(dfull + 8 * i, 1), mbar_init(dempty + 8 * i, 2 * C::EW);
-    mbar_init(fin, 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    s_misc[1] = 0;
+  static __device__ __forceinline__ void dealloc(uint32_t tmem) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(Tc::kCols));
   }
-  if (warp == 2) first_tiles(p, ntn, s_start);
-  tc_fence_before();
-  __syncthreads();
-  cluster_sync();   // the other CTA's barriers and tensor memory
-  tc_fence_after();
-  const uint32_t tmem = __shfl_sync(0xffffffffu, static_cast<uint32_t>(s_misc[0]), 0);
-
-  // a warp waits through one thread: polls of all its lanes would keep the
-  // other warps' barrier operations waiting
-  auto wait = [&](uint32_t bar, uint32_t parity) {
-    const bool ok = __all_sync(0xffffffffu, lane != 0 || poll(bar, parity, abort));
-    __syncwarp();
-    return ok;
-  };
-
-  const int tiles = s_start[p.E];
-  const int steps_all = (p.K + kB - 1) / kB;
-  const int s0 = static_cast<int>(static_cast<int64_t>(steps_all) * part / split);
-  const int s1 = static_cast<int>(static_cast<int64_t>(steps_all) * (part + 1) / split);
-  const int tile0 = blockIdx.x / (2 * split), tile_step = gridDim.x / (2 * split);
-  Tiles order{s_start, ntn};
-
-  if (warp < kEpiWarp0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-    if (warp == 0 && lane == 0) {
-      // ---- operands by TMA
-      Ring<C::S> r;
-      bool ok = true;
-      for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
-        const Tile t = order.at(p, tile);
-        const int half = t.nt / 2, n0 = t.n0 + static_cast<int>(side) * kM, t0 = t.t0 + static_cast<int>(side) * half;
-        for (int k = s0; k < s1; ++k, r.next()) {
-          if (!r.first && !(ok = poll(empty + 8 * r.stage, r.parity ^ 1, abort))) break;
-          const uint32_t bar = full + 8 * r.stage, to = base + r.stage * (C::A + C::X);
-          mbar_expect_tx(bar, C::A + half * kB);
-          tma_load_3d(to, &maps.w, k * kB, n0, p.gw ? t.e : 0, bar);
-          int at = 0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (half & (128 >> i)) {
-              tma_load_2d(to + C::A + at * kB, &maps.x[i], k * kB, t0 + at, bar);
-              at += 128 >> i;
-            }
-        }
-      }
-      if (*abort) {   // what is in flight still ends before the CTA does
-        volatile int none = 0;
-        for (uint32_t i = 0; i < C::S; ++i) {
-          if (i < r.stage)
-            poll(full + 8 * i, r.parity, &none);
-          else if (!r.first)
-            poll(full + 8 * i, r.parity ^ 1, &none);
-        }
-      }
-    }
-    if (warp == 1 && side) {
-      // ---- the odd CTA's loads are reported to the even one
-      if (lane == 0) {
-        Ring<C::S> r;
-        const int64_t all = static_cast<int64_t>(s1 - s0) * (tiles > tile0 ? (tiles - tile0 + tile_step - 1) / tile_step : 0);
-        for (int64_t g = 0; g < all && poll(full + 8 * r.stage, r.parity, abort); ++g, r.next())
-          arrive_at(full + 8 * r.stage, leader);
-      }
-    } else if (warp == 1) {
-      // ---- MMA issue: the whole warp in step, so that the operands stay in uniform
-      // registers, and an elected thread for the instructions
-      const uint16_t both = static_cast<uint16_t>(3u << leader);
-      Ring<C::S> r;
-      Ring<2> d;
-      bool ok = true;
-      for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
-        const uint32_t idesc = C::idesc(order.at(p, tile).nt);
-        for (int k = s0; k < s1; ++k, r.next(), d.next()) {
-          if (!d.first && !(ok = wait(dempty + 8 * d.stage, d.parity ^ 1))) break;
-          if (!(ok = wait(full + 8 * r.stage, r.parity))) break;
-          tc_fence_after();
-          if (elect_one()) {
-            const uint64_t da = smem_desc(base + r.stage * (C::A + C::X)), db = da + (C::A >> 4);
-#pragma unroll
-            for (int kk = 0; kk < kB / 32; ++kk)
-              mma_f8_pair(tmem + d.stage * C::NT, da + kk * 2, db + kk * 2, idesc, kk);
-            commit_pair(empty + 8 * r.stage, both);
-            commit_pair(dfull + 8 * d.stage, both);
-          }
-          __syncwarp();
-        }
-      }
-      if (*abort) {   // the MMAs in flight end before the CTA does
-        if (elect_one()) {
-          volatile int none = 0;
-          commit_pair(fin, static_cast<uint16_t>(1u << leader));
-          poll(fin, 0, &none);
-        }
-        __syncwarp();
-      }
-    }
-    if (warp >= 2) {
-      // ---- products of the scales: four rows to a lane, four blocks at a time
-      const int col = (warp - 2) * 128 + lane * 4;
-      Ring<C::SS> r;
-      bool ok = true;
-      for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
-        const Tile t = order.at(p, tile);
-        const int nb = min(t.n0 / kB + static_cast<int>(side), (p.N - 1) / kB);
-        const float* ws = p.ws + t.e * p.gws + nb * p.ldws;
-        for (int k0 = s0; k0 < s1 && ok; k0 += 4) {
-          float v[4][4], w[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) w[j] = k0 + j < s1 ? __ldg(ws + k0 + j) : 0.f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int row = t.t0 + col + i;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              v[i][j] = row < t.t1 && k0 + j < s1 ? __ldg(p.xs + row * p.ldxs + k0 + j) : 0.f;
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (k0 + j >= s1) break;
-            if (!r.first && !(ok = wait(sempty + 8 * r.stage, r.parity ^ 1))) break;
-            *reinterpret_cast<float4*>(smem + C::kOffScale + (r.stage * C::NT + col) * 4) =
-                make_float4(v[0][j] * w[j], v[1][j] * w[j], v[2][j] * w[j], v[3][j] * w[j]);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(sfull + 8 * r.stage);
-            r.next();
-          }
-        }
-      }
-    }
-    __syncwarp();
-    cta_barrier();
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
-  } else {
-    // ---- scale, accumulate and store: a channel to a lane, nt / 2 rows to a thread
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsAcc));
-    const int q = warp & 3, h = (warp - kEpiWarp0) >> 2;
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
-    Ring<2> d;
-    Ring<C::SS> r;
-    bool ok = true;
-    for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
-      const Tile t = order.at(p, tile);
-      const int half = t.nt / 2;
-      uint64_t acc[C::ACC / 2];
-#pragma unroll
-      for (int i = 0; i < C::ACC / 2; ++i) acc[i] = 0;
-      for (int k = s0; k < s1; ++k, d.next(), r.next()) {
-        if (!(ok = wait(sfull + 8 * r.stage, r.parity) && wait(dfull + 8 * d.stage, d.parity))) break;
-        tc_fence_after();
-        const uint32_t from = lanes + d.stage * C::NT + h * half;
-        const uint32_t sc = base + C::kOffScale + (r.stage * C::NT + h * half) * 4;
-        // the next 16 sums and their scales are on their way while these are added
-        uint32_t v[2][16];
-        uint64_t f[2][8];
-        auto fetch = [&](int c) {
-          tmem_ld16(from + c, v[c / 16 % 2]);
-#pragma unroll
-          for (int i = 0; i < 8; i += 2) lds_2x64(sc + (c + i * 2) * 4, f[c / 16 % 2][i], f[c / 16 % 2][i + 1]);
-        };
-        fetch(0);
-#pragma unroll
-        for (int c = 0; c < C::ACC; c += 16) {
-          if (c >= half) break;
-          uint32_t(&now)[16] = v[c / 16 % 2];
-          tmem_wait(now);
-          if (c + 16 < half) {
-            fetch(c + 16);
-          } else {   // all of it is in registers
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_at(dempty + 8 * d.stage, leader);
-          }
-#pragma unroll
-          for (int i = 0; i < 16; i += 2) fma2(acc[(c + i) / 2], now[i], now[i + 1], f[c / 16 % 2][i / 2]);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(sempty + 8 * r.stage);
-      }
-      if (!ok) break;
-      if (split == 1) {
-        const int n = t.n0 + static_cast<int>(side) * kM + q * 32 + lane, ts = t.t0 + h * half;
-        float bias = 0.f;
-        if (p.bias && n < p.N) bias = to_f32<O>(static_cast<const O*>(p.bias)[static_cast<int64_t>(t.e) * p.N + n]);
-        O* out = static_cast<O*>(p.out) + ts * p.ldo + n;
-#pragma unroll
-        for (int i = 0; i < C::ACC; ++i) {
-          const float2 f = halves(acc[i / 2]);
-          if (n < p.N && i < half && ts + i < t.t1) *out = from_f32<O>((i & 1 ? f.y : f.x) + bias);
-          out += p.ldo;
-        }
-      } else {
-        // every stage of the ring has been read: its space takes the sums
-        float* sums = reinterpret_cast<float*>(smem);
-#pragma unroll
-        for (int i = 0; i < C::ACC; ++i) {
-          const float2 f = halves(acc[i / 2]);
-          if (i < half) sums[(h * half + i) * kM + q * 32 + lane] = i & 1 ? f.y : f.x;
-        }
-      }
-    }
-    __syncwarp();
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
-    cta_barrier();
+  static __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
   }
-
-  __syncwarp();
-  if (split > 1) {
-    // the parts of one tile: each CTA adds and stores its share of the rows
-    cluster_sync();
-    if (!*abort && tile0 < tiles) {
-      const Tile t = order.at(p, tile0);
-      const int j0 = t.nt * part / split, j1 = t.nt * (part + 1) / split;
-      const int n = t.n0 + static_cast<int>(side) * kM + tid % (kM / 4) * 4;   // four channels, the thread's for all rows
-      float bias[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        bias[c] = p.bias && n + c < p.N ? to_f32<O>(static_cast<const O*>(p.bias)[static_cast<int64_t>(t.e) * p.N + n + c]) : 0.f;
-      for (int i = j0 * (kM / 4) + tid; i < j1 * (kM / 4); i += C::kThreads) {
-        const int row = t.t0 + i / (kM / 4);
-        if (row >= t.t1) break;
-        float sum[4] = {};
-        for (int s = 0; s < split; ++s) {
-          const float4 v = ld_cluster(base + i * 16, s * 2 + side);
-          sum[0] += v.x, sum[1] += v.y, sum[2] += v.z, sum[3] += v.w;
-        }
-        O* out = static_cast<O*>(p.out) + row * p.ldo + n;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (n + c < p.N) out[c] = from_f32<O>(sum[c] + bias[c]);
-      }
-    }
+  static __device__ __forceinline__ void commit(uint32_t bar, uint32_t leader) {
+    commit_pair(bar, static_cast<uint16_t>(3u << leader));
   }
-  tc_fence_before();
-  __syncthreads();
-  cluster_sync();   // nothing of this CTA is read or signalled any more
-  tc_fence_after();
-  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols));
-}
-
-// ---------------------------------------------------------------- many rows
-
-// As k_tc_f8 with the operands' parts exchanged: the rows are the MMA's M (256 to a pair,
-// 128 to a CTA) and the channels its N (256).  A lane of tensor memory is then a row, so
-// the sums of 128 channels (a block of the weights' scales) take one factor to a thread.
-// Warps 2 and 3 write those into a ring of SS and report them with the loads of the block:
-// an MMA that has ended says that its block's factors are there, and one that starts, that
-// those of two blocks before have been read.
-struct Wide {
-  static constexpr int NT = 256, EW = 8, ACC = NT / (EW / 4);
-  static constexpr int kThreads = 32 * (kEpiWarp0 + EW);
-  static constexpr int X = kM * kB, W = NT / 2 * kB;      // bytes of a stage's operands
-  static constexpr int S = 5;
-  static constexpr int kOffOut = S * (X + W);
-  static constexpr int kPiece = 32 * 128;                 // a warp stores 32 rows x 128 bytes at a time
-  static constexpr int SS = 8;
-  static constexpr int kOffScale = kOffOut + EW * kPiece; // [SS][half of the channels][row]
-  static constexpr int kOffBar = kOffScale + SS * 2 * kM * 4;
-  static constexpr int kBars = 2 * S + 5;
-  static constexpr int kOffMisc = kOffBar + 8 * kBars;
-  static constexpr int kSmem = kOffMisc + 16 + 4 * (PW_MAX_GROUPS + 1);
-  static constexpr uint32_t kCols = 2 * NT;
-  static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
-  static_assert(SS >= S + 2, "the factors of a block that may be fetched have been read");
 };
-static_assert(Wide::kThreads == Tc::kThreads, "one register split");
+// D f32, A and B e4m3, N / 8 and M / 16.
+__host__ __device__ constexpr uint32_t idesc_of(int m, int n) {
+  return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
 
 // 32 consecutive fp32 columns of this thread's TMEM lane (after tmem_wait32).
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
@@ -713,19 +381,80 @@ __device__ __forceinline__ float lds4(uint32_t a) {
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
   return v;
 }
-
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(x), "r"(y), "r"(src)
-               : "memory");
+__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
 }
 
-template <typename O>
-__global__ void __launch_bounds__(Wide::kThreads, 1)
-k_wide_f8(const F8Args p, const __grid_constant__ CUtensorMap mapx, const __grid_constant__ CUtensorMap mapw,
-          const __grid_constant__ CUtensorMap mapo, int bulk) {
-  using C = Wide;
+// Tensor maps: rows in boxes of 128, 64, 32 and 16, weights in boxes of a CTA's channels,
+// outputs in boxes of 32 rows x 32 channels.
+struct Maps {
+  CUtensorMap x[4], w, out;
+};
+
+// A position in a ring of a size known at run time.
+struct Turn {
+  uint32_t stage = 0, parity = 0;
+  bool first = true;   // no stage has been used before
+  __device__ __forceinline__ void next(uint32_t n) {
+    if (++stage == n) stage = 0, parity ^= 1, first = false;
+  }
+};
+
+// A tile: its group, rows [t0, t1) and first channel.
+struct Tile {
+  int e, t0, t1, n0;
+};
+
+// The tiles in order of the groups, `start` the first of each; within a group bands of
+// kBand row tiles, so that CTAs at work share operands in the L2.
+constexpr int kBand = 8;
+template <int M>
+struct Tiles {
+  const int* start;
+  int ntn, nw, e = 0;
+  __device__ __forceinline__ Tile at(const F8Args& p, int tile) {
+    while (tile >= start[e + 1]) ++e;
+    const Rows r = rows_of(p, e);
+    const int local = tile - start[e], band = local / (kBand * ntn), rest = local - band * kBand * ntn;
+    const int width = min(kBand, (r.end - r.begin + M - 1) / M - band * kBand);
+    const int t0 = r.begin + (band * kBand + rest % width) * M;
+    return {e, t0, min(r.end, t0 + M), rest / width * nw};
+  }
+};
+
+// The first tile of each group, and behind them the number of tiles, by one warp.
+template <int M>
+__device__ __forceinline__ void first_tiles(const F8Args& p, int ntn, int* start) {
+  const int lane = threadIdx.x & 31;
+  int before = 0;
+  for (int e0 = 0; e0 < p.E; e0 += 32) {
+    int n = 0;
+    if (e0 + lane < p.E) {
+      const Rows r = rows_of(p, e0 + lane);
+      n = (r.end - r.begin + M - 1) / M * ntn;
+    }
+    int sum = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    if (e0 + lane < p.E) start[e0 + lane] = before + sum - n;
+    before += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  if (lane == 0) start[p.E] = before;
+}
+
+template <typename O, int CTAS>
+__global__ void __launch_bounds__(Tc::kThreads, 1)
+k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int bulk) {
+  using C = Tc;
+  using G = Cta<CTAS>;
+  constexpr int M = kM * CTAS;
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t base = saddr(smem);
   if (base % 1024) {   // the swizzled tiles would lie wrong (the array is aligned, so it never is)
@@ -733,63 +462,69 @@ k_wide_f8(const F8Args p, const __grid_constant__ CUtensorMap mapx, const __grid
     return;
   }
   const uint32_t full = base + C::kOffBar, empty = full + 8 * C::S;
-  const uint32_t dfull = empty + 8 * C::S, dempty = dfull + 16, fin = dempty + 16;
+  const uint32_t dfull = empty + 8 * C::S, dempty = dfull + 8 * C::D, fin = dempty + 8 * C::D;
   int* s_misc = reinterpret_cast<int*>(smem + C::kOffMisc);   // tmem, abort
   int* s_start = s_misc + 4;
   volatile int* abort = s_misc + 1;
   const int tid = threadIdx.x, lane = tid & 31;
-  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  uint32_t side;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(side));
-  const int ntn = (p.N + C::NT - 1) / C::NT;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // the compiler then knows that it is uniform
+  // the CTA's place: in its pair, and among the parts of K
+  uint32_t rank;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  const int side = static_cast<int>(rank % CTAS), part = static_cast<int>(rank / CTAS);
+  const uint32_t leader = rank - side;
+  const int nw = plan.nw, split = plan.split, ntn = (p.N + nw - 1) / nw;
 
-  if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(s_misc)),
-                 "r"(C::kCols));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
-  }
+  if (warp == 1) G::alloc(saddr(s_misc));
   if (tid == 0) {
     for (int i = 0; i < C::S; ++i) {
-      mbar_init(full + 8 * i, side ? 3 : 4);   // the CTA's loads and factors, and the odd CTA's report
+      // the CTA's loads, its scales by two warps, and the odd CTA's report
+      mbar_init(full + 8 * i, CTAS == 2 && side == 0 ? 4 : 3);
       mbar_init(empty + 8 * i, 1);
     }
-    for (int i = 0; i < 2; ++i) mbar_init(dfull + 8 * i, 1), mbar_init(dempty + 8 * i, 2 * C::EW);
+    for (int i = 0; i < C::D; ++i) mbar_init(dfull + 8 * i, 1), mbar_init(dempty + 8 * i, CTAS * C::EW);
     mbar_init(fin, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     s_misc[1] = 0;
   }
-  if (warp == 2) first_tiles(p, ntn, s_start);
+  if (warp == 2) first_tiles<M>(p, ntn, s_start);
   tc_fence_before();
   __syncthreads();
-  cluster_sync();
+  if (CTAS == 2) cluster_sync();   // the other CTA's barriers and tensor memory
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, static_cast<uint32_t>(s_misc[0]), 0);
+
   // (a look at a barrier takes 41 clocks by the whole warp, and 96 by one thread that
   // tells the others)
   auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, poll(bar, parity, abort)); };
-  const int tiles = s_start[p.E], steps = (p.K + kB - 1) / kB;
-  const int tile0 = blockIdx.x / 2, tile_step = gridDim.x / 2;
-  Tiles order{s_start, ntn};
+
+  const int tiles = s_start[p.E], blocks = (p.K + kB - 1) / kB;
+  const int s0 = static_cast<int>(static_cast<int64_t>(blocks) * part / split);
+  const int s1 = static_cast<int>(static_cast<int64_t>(blocks) * (part + 1) / split);
+  const int tile0 = blockIdx.x / (CTAS * split), tile_step = gridDim.x / (CTAS * split);
+  Tiles<M> order{s_start, ntn, nw};
 
   if (warp < kEpiWarp0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
     if (warp == 0 && lane == 0) {
       // ---- operands by TMA
-      Ring<C::S> r;
+      Turn r;
       bool ok = true;
       for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
         const Tile t = order.at(p, tile);
-        for (int k = 0; k < steps; ++k, r.next()) {
+        const int t0 = t.t0 + side * kM, rows = t.t1 - t0, wn = nw / CTAS;
+        const int box = rows > 64 ? 0 : rows > 32 ? 1 : rows > 16 ? 2 : 3;   // the least that holds the rows
+        for (int k = s0; k < s1; ++k, r.next(plan.stages)) {
           if (!r.first && !(ok = poll(empty + 8 * r.stage, r.parity ^ 1, abort))) break;
-          const uint32_t bar = full + 8 * r.stage, to = base + r.stage * (C::X + C::W);
-          mbar_expect_tx(bar, C::X + C::W);
-          tma_load_2d(to, &mapx, k * kB, t.t0 + static_cast<int>(side) * kM, bar);
-          tma_load_3d(to + C::X, &mapw, k * kB, t.n0 + static_cast<int>(side) * kM, p.gw ? t.e : 0, bar);
+          const uint32_t bar = full + 8 * r.stage, to = base + r.stage * plan.stage;
+          mbar_expect_tx(bar, ((128 >> box) + wn) * kB);
+          tma_load_2d(to, &maps.x[box], k * kB, t0, bar);
+          tma_load_3d(to + plan.x_bytes, &maps.w, k * kB, t.n0 + side * wn, p.gw ? t.e : 0, bar);
         }
       }
       if (*abort) {   // what is in flight still ends before the CTA does
         volatile int none = 0;
-        for (uint32_t i = 0; i < C::S; ++i) {
+        for (uint32_t i = 0; i < static_cast<uint32_t>(plan.stages); ++i) {
           if (i < r.stage)
             poll(full + 8 * i, r.parity, &none);
           else if (!r.first)
@@ -798,36 +533,37 @@ k_wide_f8(const F8Args p, const __grid_constant__ CUtensorMap mapx, const __grid
       }
     }
     if (warp >= 2) {
-      // ---- factors: four rows to a lane, half of the channels to a warp, four blocks at a time
-      Ring<C::S> r;
+      // ---- scales: two rows to a lane, four blocks at a time, and those of the weights
+      const int row = (warp - 2) * 64 + lane * 2;
+      Turn r;
       uint32_t slot = 0;
       bool ok = true;
       for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
         const Tile t = order.at(p, tile);
-        const float* ws = p.ws + t.e * p.gws + min(t.n0 / kB + warp - 2, (p.N - 1) / kB) * p.ldws;
-        const float* xs[4];
+        const float* xs[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          xs[i] = p.xs + min(t.t0 + static_cast<int>(side) * kM + lane * 4 + i, t.t1 - 1) * p.ldxs;
-        for (int k0 = 0; k0 < steps && ok; k0 += 4) {
-          float v[4][4], w[4];
+        for (int i = 0; i < 2; ++i) xs[i] = p.xs + min(t.t0 + side * kM + row + i, t.t1 - 1) * p.ldxs;
+        const float* ws = p.ws + t.e * p.gws + min(t.n0 + (lane & 3) * 64, p.N - 1) / kB * p.ldws;
+        for (int k0 = s0; k0 < s1 && ok; k0 += 4) {
+          float v[2][4], w[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const int k = min(k0 + j, steps - 1);
+            const int k = min(k0 + j, s1 - 1);
             w[j] = __ldg(ws + k);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i][j] = __ldg(xs[i] + k);
+            for (int i = 0; i < 2; ++i) v[i][j] = __ldg(xs[i] + k);
           }
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            if (k0 + j >= steps) break;
+            if (k0 + j >= s1) break;
             if (!r.first && !(ok = wait(empty + 8 * r.stage, r.parity ^ 1))) break;
-            *reinterpret_cast<float4*>(smem + C::kOffScale + ((slot * 2 + warp - 2) * kM + lane * 4) * 4) =
-                make_float4(v[0][j] * w[j], v[1][j] * w[j], v[2][j] * w[j], v[3][j] * w[j]);
+            float* to = reinterpret_cast<float*>(smem + C::kOffScale) + slot * C::kScale;
+            *reinterpret_cast<float2*>(to + row) = make_float2(v[0][j], v[1][j]);
+            if (warp == 2 && lane < 4) to[kM + lane] = w[j];
             __syncwarp();
             if (lane == 0) mbar_arrive(full + 8 * r.stage);
-            r.next();
-            slot = (slot + 1) % C::SS;
+            r.next(plan.stages);
+            if (++slot == C::SS) slot = 0;
           }
         }
       }
@@ -835,39 +571,39 @@ k_wide_f8(const F8Args p, const __grid_constant__ CUtensorMap mapx, const __grid
     if (warp == 1 && side) {
       // ---- the odd CTA's loads are reported to the even one
       if (lane == 0) {
-        Ring<C::S> r;
-        const int64_t all = static_cast<int64_t>(steps) * (tiles > tile0 ? (tiles - tile0 + tile_step - 1) / tile_step : 0);
-        for (int64_t g = 0; g < all && poll(full + 8 * r.stage, r.parity, abort); ++g, r.next())
-          arrive_at(full + 8 * r.stage, 0);
+        Turn r;
+        const int64_t all = static_cast<int64_t>(s1 - s0) * (tiles > tile0 ? (tiles - tile0 + tile_step - 1) / tile_step : 0);
+        for (int64_t g = 0; g < all && poll(full + 8 * r.stage, r.parity, abort); ++g, r.next(plan.stages))
+          arrive_at(full + 8 * r.stage, leader);
       }
     } else if (warp == 1) {
       // ---- MMA issue: the whole warp in step, so that the operands stay in uniform
       // registers, and an elected thread for the instructions
-      Ring<C::S> r;
-      Ring<2> d;
+      const uint32_t idesc = idesc_of(M, nw), cols = C::kCols / plan.accs;
+      Turn r, d;
       bool ok = true;
       for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
-        for (int k = 0; k < steps; ++k) {
+        for (int k = s0; k < s1; ++k) {
           if (!(ok = wait(full + 8 * r.stage, r.parity))) break;
+          const uint32_t at = base + r.stage * plan.stage;
+          const uint64_t da = smem_desc(at), db = smem_desc(at + plan.x_bytes);
           if (!d.first && !(ok = wait(dempty + 8 * d.stage, d.parity ^ 1))) break;
           tc_fence_after();
-          const uint32_t acc = tmem + d.stage * C::NT, at = base + r.stage * (C::X + C::W);
-          const uint32_t done = dfull + 8 * d.stage, free = empty + 8 * r.stage;
-          d.next(), r.next();
           if (elect_one()) {
-            const uint64_t da = smem_desc(at), db = da + (C::X >> 4);
 #pragma unroll
-            for (int kk = 0; kk < kB / 32; ++kk) mma_f8_pair(acc, da + kk * 2, db + kk * 2, Tc::idesc(C::NT), kk);
-            commit_pair(done, 3);
-            commit_pair(free, 3);
+            for (int kk = 0; kk < kB / 32; ++kk) G::mma(tmem + d.stage * cols, da + kk * 2, db + kk * 2, idesc, kk);
+            G::commit(dfull + 8 * d.stage, leader);
+            G::commit(empty + 8 * r.stage, leader);
           }
           __syncwarp();
+          r.next(plan.stages), d.next(plan.accs);
         }
       }
       if (*abort) {   // the MMAs in flight end before the CTA does
         if (elect_one()) {
           volatile int none = 0;
-          commit_pair(fin, 1);
+          if (CTAS == 2) commit_pair(fin, static_cast<uint16_t>(1u << leader));
+          else mma_commit(fin);
           poll(fin, 0, &none);
         }
         __syncwarp();
@@ -877,82 +613,106 @@ k_wide_f8(const F8Args p, const __grid_constant__ CUtensorMap mapx, const __grid
     cta_barrier();
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
   } else {
-    // ---- scale, accumulate and store: a row to a lane, 128 channels to a thread
+    // ---- scale, accumulate and store: a row to a lane, half of the channels to a thread
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsAcc));
-    const int q = warp & 3, h = (warp - kEpiWarp0) >> 2;
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * C::ACC;
-    unsigned char* stage = smem + C::kOffOut + (warp - kEpiWarp0) * C::kPiece;
-    const uint32_t factors = base + C::kOffScale + (h * kM + q * 32 + lane) * 4;
+    const int q = warp & 3, h = (warp - kEpiWarp0) >> 2, mine = nw / 2;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * mine, cols = C::kCols / plan.accs;
+    const uint32_t scales = base + C::kOffScale, row_at = (q * 32 + lane) * 4, w_at = (kM + h * mine / 64) * 4;
+    const int odd = h * mine % 64;   // where the second half of the channels starts in its 64
+    unsigned char* const piece = smem + C::kOffOut + (warp - kEpiWarp0) * C::kPiece;
     uint32_t slot = 0;
-    Ring<2> d;
+    int turn = 0;
+    Turn d;
     bool ok = true;
     for (int tile = tile0; tile < tiles; tile += tile_step) {
+      const Tile t = order.at(p, tile);
+      const int row0 = t.t0 + side * kM + q * 32;
+      const bool busy = row0 < t.t1;
       float acc[C::ACC];
 #pragma unroll
       for (int i = 0; i < C::ACC; ++i) acc[i] = 0.f;
-      for (int k = 0; k < steps; ++k) {
+      for (int k = s0; k < s1; ++k) {
         if (!(ok = wait(dfull + 8 * d.stage, d.parity))) break;
         tc_fence_after();
-        const uint32_t from = lanes + d.stage * C::NT, free = dempty + 8 * d.stage;
-        const float f = lds4(factors + slot * (2 * kM * 4));
-        d.next();
-        slot = (slot + 1) % C::SS;
-        uint32_t v[32];
-        // (two warps share the FMA pipe, so that one's loads are behind the other's sums)
-#pragma unroll
-        for (int c = 0; c < C::ACC; c += 32) {
-          tmem_ld32(from + c, v);
-          tmem_wait32(v);
-          if (c + 32 == C::ACC) {   // all of it is in registers
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              if (side) arrive_at(free, 0);
-              else mbar_arrive(free);
-            }
+        const uint32_t from = lanes + d.stage * cols, free = dempty + 8 * d.stage;
+        const uint32_t at = scales + slot * (C::kScale * 4);
+        auto release = [&]() {   // all of it is in registers
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (side) arrive_at(free, leader);
+            else mbar_arrive(free);
           }
+        };
+        if (busy) {
+          const float xs = lds4(at + row_at);
+          // (two warps share the FMA pipe, so that one's loads are behind the other's sums)
 #pragma unroll
-          for (int i = 0; i < 32; ++i) acc[c + i] = fmaf(__uint_as_float(v[i]), f, acc[c + i]);
+          for (int c = 0; c < C::ACC; c += 32) {
+            if (c >= mine) break;
+            uint32_t v[32];
+            tmem_ld32(from + c, v);
+            const float f = xs * lds4(at + w_at + (odd + c) / 64 * 4);
+            tmem_wait32(v);
+            if (c + 32 >= mine) release();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) acc[c + i] = fmaf(__uint_as_float(v[i]), f, acc[c + i]);
+          }
+        } else {
+          release();
         }
+        d.next(plan.accs);
+        if (++slot == C::SS) slot = 0;
       }
       if (!ok) break;
-      const Tile t = order.at(p, tile);
-      const int row0 = t.t0 + static_cast<int>(side) * kM + q * 32, n0 = t.n0 + h * C::ACC;
-      // 128 bytes of each of the warp's rows at a time, through shared memory: by TMA where
-      // all of the rows are the group's, else row by row
-      constexpr int N = 128 / sizeof(O), V = 16 / sizeof(O);   // channels of a turn, of 16 bytes
+      if (!busy) continue;
+      const int n0 = t.n0 + h * mine;
+      if (split > 1) {
+        // every stage of the ring has been read: its space takes the sums
+        float* sums = reinterpret_cast<float*>(smem) + (q * 32 + lane) * (nw + 1) + h * mine;
+#pragma unroll
+        for (int i = 0; i < C::ACC; ++i)
+          if (i < mine) sums[i] = acc[i];
+        continue;
+      }
       if (p.bias) {
         const O* bias = static_cast<const O*>(p.bias) + static_cast<int64_t>(t.e) * p.N + n0;
 #pragma unroll
         for (int i = 0; i < C::ACC; ++i)
-          if (n0 + i < p.N) acc[i] += to_f32<O>(__ldg(bias + i));
+          if (i < mine && n0 + i < p.N) acc[i] += to_f32<O>(__ldg(bias + i));
       }
+      // 32 channels of each of the warp's rows at a time, through shared memory: by TMA where
+      // all of the rows are the group's, else row by row
+      constexpr int V = 16 / sizeof(O), P = 32 / V;   // channels of 16 bytes; such pieces of a row
+      constexpr int kTurns = C::kPiece / (32 * 32 * sizeof(O));   // that fit beside one another
       const bool whole = bulk && row0 + 32 <= t.t1;
+      // the TMA's swizzle: 128 bytes (8 pieces) or 64 (4)
+      auto place = [](int r, int i) { return r * (P * 16) + ((i ^ (P == 8 ? r & 7 : (r >> 1) & 3)) << 4); };
 #pragma unroll
-      for (int c = 0; c < C::ACC; c += N) {
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // of the last turn
+      for (int c = 0; c < C::ACC; c += 32) {
+        if (c >= mine) break;
+        unsigned char* stage = piece + turn * (32 * 32 * sizeof(O));
+        turn = (turn + 1) % kTurns;
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kTurns - 1) : "memory");   // its last use
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {   // with the TMA's 128-byte swizzle
+        for (int i = 0; i < P; ++i) {
           alignas(16) O o[V];
 #pragma unroll
           for (int e = 0; e < V; ++e) o[e] = from_f32<O>(acc[c + i * V + e]);
-          *reinterpret_cast<uint4*>(stage + lane * 128 + ((i ^ (lane & 7)) << 4)) = *reinterpret_cast<const uint4*>(o);
+          *reinterpret_cast<uint4*>(stage + place(lane, i)) = *reinterpret_cast<const uint4*>(o);
         }
         if (whole) {
           proxy_fence_smem();
           __syncwarp();
-          if (lane == 0 && n0 + c < p.N) {
-            tma_store_2d(&mapo, n0 + c, row0, saddr(stage));
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-          }
+          if (lane == 0 && n0 + c < p.N) tma_store_2d(&maps.out, n0 + c, row0, saddr(stage));
         } else {
           __syncwarp();
-          const int n = n0 + c + (lane & 7) * V;
+          const int n = n0 + c + lane % P * V;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = i * 4 + (lane >> 3), row = row0 + r;
-            const uint4 raw = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+          for (int i = 0; i < P; ++i) {
+            const int r = i * (32 / P) + lane / P, row = row0 + r;
+            const uint4 raw = *reinterpret_cast<const uint4*>(stage + place(r, lane % P));
             if (row >= t.t1) continue;
             O* out = static_cast<O*>(p.out) + row * p.ldo + n;
             if (bulk && n + V <= p.N) {
@@ -965,6 +725,7 @@ k_wide_f8(const F8Args p, const __grid_constant__ CUtensorMap mapx, const __grid
             }
           }
         }
+        if (lane == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");   // one for every turn
       }
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -972,32 +733,54 @@ k_wide_f8(const F8Args p, const __grid_constant__ CUtensorMap mapx, const __grid
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLaunch));
     cta_barrier();
   }
+
   __syncwarp();
+  if (split > 1) {
+    // the parts of one tile: each CTA adds and stores its share of the rows
+    cluster_sync();
+    if (!*abort && tile0 < tiles) {
+      const Tile t = order.at(p, tile0);
+      const int t0 = t.t0 + side * kM, rows = min(kM, t.t1 - t0), cols = min(nw, p.N - t.n0);
+      const int r0 = rows > 0 ? rows * part / split : 0, r1 = rows > 0 ? rows * (part + 1) / split : 0;
+      for (int i = tid; i < (r1 - r0) * nw; i += C::kThreads) {
+        const int r = r0 + i / nw, c = i % nw;
+        if (c >= cols) continue;
+        float v[4], sum = 0.f;
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+          v[s] = s < split ? ld_cluster(base + (r * (nw + 1) + c) * 4, s * CTAS + side) : 0.f;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) sum += v[s];
+        if (p.bias) sum += to_f32<O>(static_cast<const O*>(p.bias)[static_cast<int64_t>(t.e) * p.N + t.n0 + c]);
+        static_cast<O*>(p.out)[(t0 + r) * p.ldo + t.n0 + c] = from_f32<O>(sum);
+      }
+    }
+  }
   tc_fence_before();
   __syncthreads();
-  cluster_sync();   // nothing of this CTA is read or signalled any more
+  if (CTAS * split > 1) cluster_sync();   // nothing of this CTA is read or signalled any more
   tc_fence_after();
-  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols));
+  if (warp == 1) G::dealloc(tmem);
 }
 
-// Boxes of `cols_box` columns (128 bytes) x `box` rows of a tensor [groups][rows][cols]
-// (groups 0: a matrix) with strides in bytes; columns and rows past the ends read as zero,
-// and are not written.
-cudaError_t map_tile(CUtensorMap* m, CUtensorMapDataType type, const void* base, int64_t ld, int64_t group, int groups,
-                     int rows, int cols, int box, int cols_box) {
+// Boxes of `cols_box` columns x `box` rows of a tensor [groups][rows][cols] (groups 0: a
+// matrix) with strides in bytes; columns and rows past the ends read as zero, and are not
+// written.
+cudaError_t map_tile(CUtensorMap* m, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, const void* base, int64_t ld,
+                     int64_t group, int groups, int rows, int cols, int box, int cols_box) {
   const auto encode = encoder();
   if (!encode) return cudaErrorNotSupported;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(groups)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld), static_cast<cuuint64_t>(group)};
   const cuuint32_t boxes[3] = {static_cast<cuuint32_t>(cols_box), static_cast<cuuint32_t>(box), 1}, es[3] = {1, 1, 1};
   const CUresult r = encode(m, type, groups ? 3 : 2, const_cast<void*>(base), dims, strides, boxes, es,
-                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 // e4m3 rows in boxes of 128 columns, [groups][rows][cols].
 cudaError_t map_rows(CUtensorMap* m, const void* base, int64_t ld, int64_t group, int groups, int rows, int cols, int box) {
-  return map_tile(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, ld, group, groups, rows, cols, box, kB);
+  return map_tile(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, base, ld, group, groups, rows, cols, box, kB);
 }
 
 // What the kernel's launches need to know about a device, asked once.
@@ -1006,7 +789,7 @@ struct OnDevice {
   int clusters[4] = {};   // of 1, 2, 4 and 8 CTAs, at once
 };
 template <typename K>
-cudaError_t prepare(OnDevice* all, K* kernel, int smem, OnDevice** out) {
+cudaError_t prepare(OnDevice* all, K* kernel, OnDevice** out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -1017,85 +800,85 @@ cudaError_t prepare(OnDevice* all, K* kernel, int smem, OnDevice** out) {
   static std::mutex asking;
   const std::lock_guard<std::mutex> lock(asking);
   if (d.ready.load(std::memory_order_relaxed)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Tc::kSmem);
   cudaFuncAttributes at{};
   if (e == cudaSuccess) e = cudaFuncGetAttributes(&at, kernel);
   if (e != cudaSuccess) return e;
   // the register split must be what the CTA is launched with
   if (at.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
-  for (int i = 0; i < 4; ++i) d.clusters[i] = max_clusters(kernel, Tc::kThreads, smem, 1 << i);
+  for (int i = 0; i < 4; ++i) d.clusters[i] = max_clusters(kernel, Tc::kThreads, Tc::kSmem, 1 << i);
   d.ready.store(true, std::memory_order_release);
   return cudaSuccess;
 }
 
-// Parts of K, 1, 2 or 4: while all of them still run at once and have four blocks or
-// more each.
-int parts_of_k(const OnDevice& d, int64_t tiles, int steps) {
-  int i = 0;
-  while (i < 2 && tiles <= d.clusters[i + 2] && steps >= 8 << i) ++i;
-  return 1 << i;
+// Channels of a tile and parts of K: what gives the SMs the least to do in turn, a
+// block's time being some constant and a part that grows with the channels.  K is split
+// (in 2 or 4) while all parts still run at once and have four blocks or more each.
+template <int CTAS>
+Plan plan_of(const F8Args& p, const OnDevice& d) {
+  constexpr int M = kM * CTAS;
+  const int blocks = (p.K + kB - 1) / kB, units = sm_count() / CTAS;
+  // row tiles: of rows in groups about half a tile more for each
+  const int64_t ntt = p.offsets ? std::max<int64_t>(1, std::min<int64_t>(p.T, p.T / M + (p.E + 1) / 2)) : (p.T + M - 1) / M;
+  Plan best{};
+  double least = 0;
+  for (int nw = Tc::NT; nw >= 64; nw -= 64) {
+    const int64_t tiles = ntt * ((p.N + nw - 1) / nw);
+    int split = 1;
+    while (!p.offsets && split < 4 && tiles <= d.clusters[(split == 1 ? 1 : 2) + (CTAS - 1)] && blocks >= 8 * split) split *= 2;
+    const double turns = static_cast<double>((tiles + units - 1) / units);
+    const double cost = turns * (nw + 64) / split;
+    if (best.nw == 0 || cost < least) best.nw = nw, best.split = split, least = cost;
+  }
+  best.x_bytes = (!p.offsets && p.T <= 16 ? 16 : !p.offsets && p.T <= 32 ? 32 : !p.offsets && p.T <= 64 ? 64 : kM) * kB;
+  best.stage = best.x_bytes + best.nw / CTAS * kB;
+  best.stages = std::min(Tc::S, Tc::kRing / best.stage);
+  best.accs = best.nw > 128 ? 2 : 4;
+  return best;
 }
 
-template <typename... P, typename... A>
-cudaError_t launch_clusters(void (*kernel)(P...), int64_t grid, int smem, int cluster, cudaStream_t s, const A&... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(Tc::kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute a{};
-  a.id = cudaLaunchAttributeClusterDimension;
-  a.val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
-  cfg.attrs = &a;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-// Tiles of 256 x 256 that a product has; of rows in groups there may be as many more
-// as groups, in each of which the last one may be short.
-int64_t most_tiles(const F8Args& p) {
-  const int64_t ntn = (p.N + 2 * kM - 1) / (2 * kM), ntt = (p.T + Tc::NT - 1) / Tc::NT;
-  return ntn * (p.offsets ? std::min<int64_t>(p.T, ntt + p.E) : ntt);
-}
-
-template <typename O>
+template <typename O, int CTAS>
 cudaError_t launch_tc(const F8Args& p, cudaStream_t s) {
   static OnDevice all[kMaxDev];
   OnDevice* d;
-  cudaError_t e = prepare(all, k_tc_f8<O>, Tc::kSmem, &d);
-  Maps maps;
-  if (e == cudaSuccess) e = map_rows(&maps.w, p.w, p.ldw, p.gw ? p.gw : p.ldw, p.gw ? p.E : 1, p.N, p.K, kM);
-  for (int i = 0; i < 4 && e == cudaSuccess; ++i) e = map_rows(&maps.x[i], p.x, p.ldx, 0, 0, p.T, p.K, 128 >> i);
+  cudaError_t e = prepare(all, k_tc_f8<O, CTAS>, &d);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = most_tiles(p);
-  const int split = p.offsets ? 1 : parts_of_k(*d, tiles, (p.K + kB - 1) / kB);
-  const int64_t pairs = split > 1 ? tiles * split : std::min<int64_t>(tiles, sm_count() / 2);
-  return launch_clusters(k_tc_f8<O>, 2 * pairs, Tc::kSmem, 2 * split, s, p, maps, split);
-}
-
-template <typename O>
-cudaError_t launch_wide(const F8Args& p, cudaStream_t s) {
-  static OnDevice all[kMaxDev];
-  OnDevice* d;
-  cudaError_t e = prepare(all, k_wide_f8<O>, Wide::kSmem, &d);
-  CUtensorMap mapx, mapw, mapo{};
+  const Plan plan = plan_of<CTAS>(p, *d);
+  Maps maps{};
   // stores by TMA, and of 16 bytes
   const bool bulk = aligned(p.out, 16) && p.ldo * sizeof(O) % 16 == 0;
-  if (e == cudaSuccess) e = map_rows(&mapx, p.x, p.ldx, 0, 0, p.T, p.K, kM);
-  if (e == cudaSuccess) e = map_rows(&mapw, p.w, p.ldw, p.gw ? p.gw : p.ldw, p.gw ? p.E : 1, p.N, p.K, kM);
+  for (int i = 0; i < 4 && e == cudaSuccess; ++i) e = map_rows(&maps.x[i], p.x, p.ldx, 0, 0, p.T, p.K, 128 >> i);
+  if (e == cudaSuccess) e = map_rows(&maps.w, p.w, p.ldw, p.gw ? p.gw : p.ldw, p.gw ? p.E : 1, p.N, p.K, plan.nw / CTAS);
   if (e == cudaSuccess && bulk)
-    e = map_tile(&mapo, std::is_same_v<O, float> ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, p.out,
-                 p.ldo * sizeof(O), 0, 0, p.T, p.N, 32, 128 / sizeof(O));
+    e = std::is_same_v<O, float>
+            ? map_tile(&maps.out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, CU_TENSOR_MAP_SWIZZLE_128B, p.out, p.ldo * 4, 0, 0, p.T,
+                       p.N, 32, 32)
+            : map_tile(&maps.out, CU_TENSOR_MAP_DATA_TYPE_UINT16, CU_TENSOR_MAP_SWIZZLE_64B, p.out, p.ldo * 2, 0, 0, p.T,
+                       p.N, 32, 32);
   if (e != cudaSuccess) return e;
-  return launch_clusters(k_wide_f8<O>, 2 * std::min<int64_t>(most_tiles(p), sm_count() / 2), Wide::kSmem, 2, s, p, mapx, mapw,
-                         mapo, static_cast<int>(bulk));
+  constexpr int M = kM * CTAS;
+  // every tile that there is; of rows in groups there may be as many more as groups
+  const int64_t ntt = (p.T + M - 1) / M, ntn = (p.N + plan.nw - 1) / plan.nw;
+  const int64_t tiles = ntn * (p.offsets ? std::min<int64_t>(p.T, ntt + p.E) : ntt);
+  const int64_t grid = plan.split > 1 ? tiles * plan.split : std::min<int64_t>(tiles, sm_count() / CTAS);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid * CTAS));
+  cfg.blockDim = dim3(Tc::kThreads);
+  cfg.dynamicSmemBytes = Tc::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute a{};
+  a.id = cudaLaunchAttributeClusterDimension;
+  a.val.clusterDim = {static_cast<unsigned>(CTAS * plan.split), 1, 1};
+  cfg.attrs = &a;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_tc_f8<O, CTAS>, p, maps, plan, static_cast<int>(bulk));
 }
 
 template <typename O>
 cudaError_t launch_f8(const F8Args& p, cudaStream_t s) {
   const int64_t rows = p.offsets ? (p.T + p.E - 1) / p.E : p.T;   // of a group, about
-  if (rows > 256) return launch_wide<O>(p, s);
-  if (rows > 16) return launch_tc<O>(p, s);
+  if (rows > kM) return launch_tc<O, 2>(p, s);
+  if (rows > 16) return launch_tc<O, 1>(p, s);
   const int nt = rows <= 8 ? 1 : 2;
   const int turns = static_cast<int>(std::min<int64_t>((rows + nt * 8 - 1) / (nt * 8), 65535 / p.E));
   return nt == 1 ? launch_few<O, 1>(p, turns, s) : launch_few<O, 2>(p, turns, s);
@@ -1115,7 +898,7 @@ int linear_f8(const char* what, const F8Args& p, int out_dtype, pw_stream_t s) {
   if (!aligned(p.x, 16) || !aligned(p.w, 16) || p.ldx % 16 || p.ldw % 16 || p.gw % 16)
     return failf(PW_EINVAL, "%s: rows of x and w must start on 16-byte boundaries", what);
   if (p.E > 1 && (p.gw < 0 || p.gws < 0)) return failf(PW_EINVAL, "%s: a group stride is negative", what);
-  if (((static_cast<int64_t>(p.T) + 255) / 256 + p.E) * ((static_cast<int64_t>(p.N) + 255) / 256) > PW_MAX_VOCAB)
+  if ((p.T / 128 + 1 + static_cast<int64_t>(p.E)) * (p.N / 64 + 1) > PW_MAX_VOCAB)   // tiles
     return failf(PW_EINVAL, "%s: an output of %d x %d is too large", what, p.T, p.N);
   const size_t es = dtype_bytes(out_dtype);
   if (!aligned(p.out, es) || !aligned(p.bias, es) || !aligned(p.xs, 4) || !aligned(p.ws, 4) || !aligned(p.offsets, 4))
