@@ -264,10 +264,11 @@ struct Tc {
   static_assert(kM * kSumRow * 4 <= kRing, "a CTA's sums fit the ring");
 };
 
-// What a launch chose: channels of a tile (a multiple of 64) and parts of K; and what
-// follows: bytes of a stage's rows and of the stage, stages, accumulators.
+// What a launch chose: rows of a tile (of a CTA's part: 128, or fewer in a CTA alone),
+// channels of it (a multiple of 64) and parts of K; and what follows: bytes of a stage's
+// rows and of the stage, stages, accumulators.
 struct Plan {
-  int nw, split, x_bytes, stage, stages, accs;
+  int rows, nw, split, x_bytes, stage, stages, accs;
 };
 
 // Registers by role: 384 threads are launched with kRegsLaunch each, and the
@@ -412,10 +413,9 @@ struct Tile {
 // The tiles in order of the groups, `start` the first of each; within a group bands of
 // kBand row tiles, so that CTAs at work share operands in the L2.
 constexpr int kBand = 8;
-template <int M>
 struct Tiles {
   const int* start;
-  int ntn, nw, e = 0;
+  int ntn, M, nw, e = 0;
   __device__ __forceinline__ Tile at(const F8Args& p, int tile) {
     while (tile >= start[e + 1]) ++e;
     const Rows r = rows_of(p, e);
@@ -427,8 +427,7 @@ struct Tiles {
 };
 
 // The first tile of each group, and behind them the number of tiles, by one warp.
-template <int M>
-__device__ __forceinline__ void first_tiles(const F8Args& p, int ntn, int* start) {
+__device__ __forceinline__ void first_tiles(const F8Args& p, int ntn, int M, int* start) {
   const int lane = threadIdx.x & 31;
   int before = 0;
   for (int e0 = 0; e0 < p.E; e0 += 32) {
@@ -449,12 +448,12 @@ __device__ __forceinline__ void first_tiles(const F8Args& p, int ntn, int* start
   if (lane == 0) start[p.E] = before;
 }
 
-template <typename O, int CTAS>
+// FULL: tiles of 256 channels, where a thread's 128 are one block of the weights' scales.
+template <typename O, int CTAS, bool FULL>
 __global__ void __launch_bounds__(Tc::kThreads, 1)
 k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int bulk) {
   using C = Tc;
   using G = Cta<CTAS>;
-  constexpr int M = kM * CTAS;
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t base = saddr(smem);
   if (base % 1024) {   // the swizzled tiles would lie wrong (the array is aligned, so it never is)
@@ -473,7 +472,8 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int 
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   const int side = static_cast<int>(rank % CTAS), part = static_cast<int>(rank / CTAS);
   const uint32_t leader = rank - side;
-  const int nw = plan.nw, split = plan.split, ntn = (p.N + nw - 1) / nw;
+  const int nw = FULL ? C::NT : plan.nw, split = plan.split, ntn = (p.N + nw - 1) / nw;
+  const uint32_t accs = FULL ? C::kCols / C::NT : plan.accs, acc_cols = C::kCols / accs;
 
   if (warp == 1) G::alloc(saddr(s_misc));
   if (tid == 0) {
@@ -487,7 +487,7 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int 
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     s_misc[1] = 0;
   }
-  if (warp == 2) first_tiles<M>(p, ntn, s_start);
+  if (warp == 2) first_tiles(p, ntn, CTAS * plan.rows, s_start);
   tc_fence_before();
   __syncthreads();
   if (CTAS == 2) cluster_sync();   // the other CTA's barriers and tensor memory
@@ -502,7 +502,7 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int 
   const int s0 = static_cast<int>(static_cast<int64_t>(blocks) * part / split);
   const int s1 = static_cast<int>(static_cast<int64_t>(blocks) * (part + 1) / split);
   const int tile0 = blockIdx.x / (CTAS * split), tile_step = gridDim.x / (CTAS * split);
-  Tiles<M> order{s_start, ntn, nw};
+  Tiles order{s_start, ntn, CTAS * plan.rows, nw};
 
   if (warp < kEpiWarp0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
@@ -579,7 +579,7 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int 
     } else if (warp == 1) {
       // ---- MMA issue: the whole warp in step, so that the operands stay in uniform
       // registers, and an elected thread for the instructions
-      const uint32_t idesc = idesc_of(M, nw), cols = C::kCols / plan.accs;
+      const uint32_t idesc = idesc_of(CTAS * kM, nw);
       Turn r, d;
       bool ok = true;
       for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
@@ -591,12 +591,12 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int 
           tc_fence_after();
           if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < kB / 32; ++kk) G::mma(tmem + d.stage * cols, da + kk * 2, db + kk * 2, idesc, kk);
+            for (int kk = 0; kk < kB / 32; ++kk) G::mma(tmem + d.stage * acc_cols, da + kk * 2, db + kk * 2, idesc, kk);
             G::commit(dfull + 8 * d.stage, leader);
             G::commit(empty + 8 * r.stage, leader);
           }
           __syncwarp();
-          r.next(plan.stages), d.next(plan.accs);
+          r.next(plan.stages), d.next(accs);
         }
       }
       if (*abort) {   // the MMAs in flight end before the CTA does
@@ -615,8 +615,8 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int 
   } else {
     // ---- scale, accumulate and store: a row to a lane, half of the channels to a thread
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsAcc));
-    const int q = warp & 3, h = (warp - kEpiWarp0) >> 2, mine = nw / 2;
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * mine, cols = C::kCols / plan.accs;
+    const int q = warp & 3, h = (warp - kEpiWarp0) >> 2, mine = FULL ? C::ACC : nw / 2;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * mine;
     const uint32_t scales = base + C::kOffScale, row_at = (q * 32 + lane) * 4, w_at = (kM + h * mine / 64) * 4;
     const int odd = h * mine % 64;   // where the second half of the channels starts in its 64
     unsigned char* const piece = smem + C::kOffOut + (warp - kEpiWarp0) * C::kPiece;
@@ -634,7 +634,7 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int 
       for (int k = s0; k < s1; ++k) {
         if (!(ok = wait(dfull + 8 * d.stage, d.parity))) break;
         tc_fence_after();
-        const uint32_t from = lanes + d.stage * cols, free = dempty + 8 * d.stage;
+        const uint32_t from = lanes + d.stage * acc_cols, free = dempty + 8 * d.stage;
         const uint32_t at = scales + slot * (C::kScale * 4);
         auto release = [&]() {   // all of it is in registers
           tc_fence_before();
@@ -644,24 +644,30 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int 
             else mbar_arrive(free);
           }
         };
-        if (busy) {
+        // (two warps share the FMA pipe, so that one's loads are behind the other's sums)
+        auto add = [&](int c, float f, bool last) {
+          uint32_t v[32];
+          tmem_ld32(from + c, v);
+          tmem_wait32(v);
+          if (last) release();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) acc[c + i] = fmaf(__uint_as_float(v[i]), f, acc[c + i]);
+        };
+        if (!busy) {
+          release();
+        } else if (FULL) {
+          const float f = lds4(at + row_at) * lds4(at + w_at);
+#pragma unroll
+          for (int c = 0; c < C::ACC; c += 32) add(c, f, c + 32 == C::ACC);
+        } else {
           const float xs = lds4(at + row_at);
-          // (two warps share the FMA pipe, so that one's loads are behind the other's sums)
 #pragma unroll
           for (int c = 0; c < C::ACC; c += 32) {
             if (c >= mine) break;
-            uint32_t v[32];
-            tmem_ld32(from + c, v);
-            const float f = xs * lds4(at + w_at + (odd + c) / 64 * 4);
-            tmem_wait32(v);
-            if (c + 32 >= mine) release();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) acc[c + i] = fmaf(__uint_as_float(v[i]), f, acc[c + i]);
+            add(c, xs * lds4(at + w_at + (odd + c) / 64 * 4), c + 32 >= mine);
           }
-        } else {
-          release();
         }
-        d.next(plan.accs);
+        d.next(accs);
         if (++slot == C::SS) slot = 0;
       }
       if (!ok) break;
@@ -814,41 +820,38 @@ cudaError_t prepare(OnDevice* all, K* kernel, OnDevice** out) {
 // Channels of a tile and parts of K: what gives the SMs the least to do in turn, a
 // block's time being some constant and a part that grows with the channels.  K is split
 // (in 2 or 4) while all parts still run at once and have four blocks or more each.
-template <int CTAS>
-Plan plan_of(const F8Args& p, const OnDevice& d) {
-  constexpr int M = kM * CTAS;
-  const int blocks = (p.K + kB - 1) / kB, units = sm_count() / CTAS;
+Plan plan_of(const F8Args& p, const OnDevice& d, int ctas) {
+  const int blocks = (p.K + kB - 1) / kB, units = sm_count() / ctas;
+  Plan best{};
+  // rows of a tile: no more than there are, and for small groups 32, so that more stages fit
+  const int most = p.offsets && p.T / p.E < 16 ? 32 : kM;
+  best.rows = ctas == 2 || p.T > 64 ? most : p.T > 32 ? std::min(most, 64) : p.T > 16 ? 32 : 16;
+  const int M = best.rows * ctas;
   // row tiles: of rows in groups about half a tile more for each
   const int64_t ntt = p.offsets ? std::max<int64_t>(1, std::min<int64_t>(p.T, p.T / M + (p.E + 1) / 2)) : (p.T + M - 1) / M;
-  Plan best{};
   double least = 0;
   for (int nw = Tc::NT; nw >= 64; nw -= 64) {
     const int64_t tiles = ntt * ((p.N + nw - 1) / nw);
     int split = 1;
-    while (!p.offsets && split < 4 && tiles <= d.clusters[(split == 1 ? 1 : 2) + (CTAS - 1)] && blocks >= 8 * split) split *= 2;
+    while (!p.offsets && split < 4 && tiles <= d.clusters[(split == 1 ? 1 : 2) + (ctas - 1)] && blocks >= 8 * split) split *= 2;
     const double turns = static_cast<double>((tiles + units - 1) / units);
     const double cost = turns * (nw + 64) / split;
     if (best.nw == 0 || cost < least) best.nw = nw, best.split = split, least = cost;
   }
-  best.x_bytes = (!p.offsets && p.T <= 16 ? 16 : !p.offsets && p.T <= 32 ? 32 : !p.offsets && p.T <= 64 ? 64 : kM) * kB;
-  best.stage = best.x_bytes + best.nw / CTAS * kB;
+  best.x_bytes = best.rows * kB;
+  best.stage = best.x_bytes + best.nw / ctas * kB;
   best.stages = std::min(Tc::S, Tc::kRing / best.stage);
   best.accs = best.nw > 128 ? 2 : 4;
   return best;
 }
 
-template <typename O, int CTAS>
-cudaError_t launch_tc(const F8Args& p, cudaStream_t s) {
-  static OnDevice all[kMaxDev];
-  OnDevice* d;
-  cudaError_t e = prepare(all, k_tc_f8<O, CTAS>, &d);
-  if (e != cudaSuccess) return e;
-  const Plan plan = plan_of<CTAS>(p, *d);
+template <typename O, int CTAS, bool FULL>
+cudaError_t launch_plan(const F8Args& p, const Plan& plan, cudaStream_t s) {
   Maps maps{};
   // stores by TMA, and of 16 bytes
   const bool bulk = aligned(p.out, 16) && p.ldo * sizeof(O) % 16 == 0;
+  cudaError_t e = map_rows(&maps.w, p.w, p.ldw, p.gw ? p.gw : p.ldw, p.gw ? p.E : 1, p.N, p.K, plan.nw / CTAS);
   for (int i = 0; i < 4 && e == cudaSuccess; ++i) e = map_rows(&maps.x[i], p.x, p.ldx, 0, 0, p.T, p.K, 128 >> i);
-  if (e == cudaSuccess) e = map_rows(&maps.w, p.w, p.ldw, p.gw ? p.gw : p.ldw, p.gw ? p.E : 1, p.N, p.K, plan.nw / CTAS);
   if (e == cudaSuccess && bulk)
     e = std::is_same_v<O, float>
             ? map_tile(&maps.out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, CU_TENSOR_MAP_SWIZZLE_128B, p.out, p.ldo * 4, 0, 0, p.T,
@@ -856,7 +859,7 @@ cudaError_t launch_tc(const F8Args& p, cudaStream_t s) {
             : map_tile(&maps.out, CU_TENSOR_MAP_DATA_TYPE_UINT16, CU_TENSOR_MAP_SWIZZLE_64B, p.out, p.ldo * 2, 0, 0, p.T,
                        p.N, 32, 32);
   if (e != cudaSuccess) return e;
-  constexpr int M = kM * CTAS;
+  const int M = plan.rows * CTAS;
   // every tile that there is; of rows in groups there may be as many more as groups
   const int64_t ntt = (p.T + M - 1) / M, ntn = (p.N + plan.nw - 1) / plan.nw;
   const int64_t tiles = ntn * (p.offsets ? std::min<int64_t>(p.T, ntt + p.E) : ntt);
@@ -871,7 +874,23 @@ cudaError_t launch_tc(const F8Args& p, cudaStream_t s) {
   a.val.clusterDim = {static_cast<unsigned>(CTAS * plan.split), 1, 1};
   cfg.attrs = &a;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_tc_f8<O, CTAS>, p, maps, plan, static_cast<int>(bulk));
+  return cudaLaunchKernelEx(&cfg, k_tc_f8<O, CTAS, FULL>, p, maps, plan, static_cast<int>(bulk));
+}
+
+template <typename O, int CTAS>
+cudaError_t launch_tc(const F8Args& p, cudaStream_t s) {
+  static OnDevice all[kMaxDev], all_full[kMaxDev];
+  OnDevice* d;
+  cudaError_t e = prepare(all, k_tc_f8<O, CTAS, false>, &d);
+  if (e != cudaSuccess) return e;
+  const Plan plan = plan_of(p, *d, CTAS);
+  if constexpr (CTAS == 2) {
+    if (plan.nw == Tc::NT) {
+      e = prepare(all_full, k_tc_f8<O, CTAS, true>, &d);
+      return e != cudaSuccess ? e : launch_plan<O, CTAS, true>(p, plan, s);
+    }
+  }
+  return launch_plan<O, CTAS, false>(p, plan, s);
 }
 
 template <typename O>
@@ -898,7 +917,7 @@ int linear_f8(const char* what, const F8Args& p, int out_dtype, pw_stream_t s) {
   if (!aligned(p.x, 16) || !aligned(p.w, 16) || p.ldx % 16 || p.ldw % 16 || p.gw % 16)
     return failf(PW_EINVAL, "%s: rows of x and w must start on 16-byte boundaries", what);
   if (p.E > 1 && (p.gw < 0 || p.gws < 0)) return failf(PW_EINVAL, "%s: a group stride is negative", what);
-  if ((p.T / 128 + 1 + static_cast<int64_t>(p.E)) * (p.N / 64 + 1) > PW_MAX_VOCAB)   // tiles
+  if ((p.T / 16 + 1 + static_cast<int64_t>(p.E)) * (p.N / 64 + 1) > PW_MAX_VOCAB)   // tiles
     return failf(PW_EINVAL, "%s: an output of %d x %d is too large", what, p.T, p.N);
   const size_t es = dtype_bytes(out_dtype);
   if (!aligned(p.out, es) || !aligned(p.bias, es) || !aligned(p.xs, 4) || !aligned(p.ws, 4) || !aligned(p.offsets, 4))
