@@ -130,19 +130,29 @@ __global__ void __launch_bounds__(kFewWarps * 32, kFewCtas) k_few_f8(const F8Arg
       for (int i = 0; i < 2; ++i) xs[j][i] = p.xs + (t0 + min(j * 8 + q * 2 + i, T - 1)) * p.ldxs;
     }
     float acc[NT][4] = {};
-    // a block: two runs of 64 columns, 16 of them to a lane
-    auto add = [&](const uint4 (&a)[2][2], const uint4 (&v)[2][NT], int b) {
+    // the block b: two runs of 64 columns, 16 of them to a lane
+    struct Part {
+      uint4 a[2][2], v[2][NT];
+      float s, f[NT][2];
+    };
+    auto scales = [&](Part& m, int b) {
+      m.s = __ldg(ws + b);
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) m.f[j][i] = __ldg(xs[j][i] + b);
+    };
+    auto add = [&](const Part& m) {
       float part[NT][4] = {};
-      const float s = __ldg(ws + b);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         uint32_t ha[2][8];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) widen16(a[u][i], ha[i]);
+        widen16(m.a[u][0], ha[0]);
+        widen16(m.a[u][1], ha[1]);
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           uint32_t hx[8];
-          widen16(v[u][j], hx);
+          widen16(m.v[u][j], hx);
 #pragma unroll
           for (int i = 0; i < 8; i += 2)
             mma_16816(part[j], ha[0][i], ha[1][i], ha[0][i + 1], ha[1][i + 1], hx[i], hx[i + 1]);
@@ -150,39 +160,56 @@ __global__ void __launch_bounds__(kFewWarps * 32, kFewCtas) k_few_f8(const F8Arg
       }
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        const float s0 = __ldg(xs[j][0] + b) * s, s1 = __ldg(xs[j][1] + b) * s;
+        const float s0 = m.f[j][0] * m.s, s1 = m.f[j][1] * m.s;
         acc[j][0] = fmaf(part[j][0], s0, acc[j][0]);
         acc[j][1] = fmaf(part[j][1], s1, acc[j][1]);
         acc[j][2] = fmaf(part[j][2], s0, acc[j][2]);
         acc[j][3] = fmaf(part[j][3], s1, acc[j][3]);
       }
     };
+    auto fetch = [&](Part& m, int b) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) m.a[u][i] = load_once(w[i] + b * kB + u * 64);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) m.v[u][j] = __ldg(reinterpret_cast<const uint4*>(x[j] + b * kB + u * 64));
+      scales(m, b);
+    };
+    const int end = min(b1, whole);
     int b = b0;
-    for (; b < min(b1, whole); ++b) {
-      uint4 a[2][2], v[2][NT];
+    // blocks whose loads are in flight together
+    auto together = [&](auto n) {
+      for (; b + n.value <= end; b += n.value) {
+        Part m[n.value];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < n.value; ++u) fetch(m[u], b + u);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) a[u][i] = load_once(w[i] + b * kB + u * 64);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) v[u][j] = __ldg(reinterpret_cast<const uint4*>(x[j] + b * kB + u * 64));
+        for (int u = 0; u < n.value; ++u) add(m[u]);
       }
-      add(a, v, b);
+    };
+    if constexpr (NT == 1) {
+      together(std::integral_constant<int, 4>());
+      together(std::integral_constant<int, 2>());
     }
-    if (b < b1) {   // the last block, not whole
-      uint4 a[2][2], v[2][NT];
+    together(std::integral_constant<int, 1>());
+    if (end < b1) {   // the last block, not whole
+      Part m;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int at = b * kB + u * 64, left = p.K - at - q * 16;
+        const int at = end * kB + u * 64, left = p.K - at - q * 16;
         auto part = [&](const uint8_t* from) {
           return left >= 16 ? __ldg(reinterpret_cast<const uint4*>(from + at)) : load_tail(from + at, left);
         };
 #pragma unroll
-        for (int i = 0; i < 2; ++i) a[u][i] = part(w[i]);
+        for (int i = 0; i < 2; ++i) m.a[u][i] = part(w[i]);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) v[u][j] = part(x[j]);
+        for (int j = 0; j < NT; ++j) m.v[u][j] = part(x[j]);
       }
-      add(a, v, b);
+      scales(m, end);
+      add(m);
     }
     // acc[j][0..3]: channels g, g, g + 8, g + 8; rows 8 j + 2 q + 0, 1, 0, 1
 #pragma unroll
@@ -264,11 +291,11 @@ struct Tc {
   static_assert(kM * kSumRow * 4 <= kRing, "a CTA's sums fit the ring");
 };
 
-// What a launch chose: rows of a tile (of a CTA's part: 128, or fewer in a CTA alone),
+// What a launch chose: CTAs to a tile, rows of it (of a CTA's part: 128, or fewer in a CTA alone),
 // channels of it (a multiple of 64) and parts of K; and what follows: bytes of a stage's
 // rows and of the stage, stages, accumulators.
 struct Plan {
-  int rows, nw, split, x_bytes, stage, stages, accs;
+  int ctas, rows, nw, split, x_bytes, stage, stages, accs;
 };
 
 // Registers by role: 384 threads are launched with kRegsLaunch each, and the
@@ -817,29 +844,37 @@ cudaError_t prepare(OnDevice* all, K* kernel, OnDevice** out) {
   return cudaSuccess;
 }
 
-// Channels of a tile and parts of K: what gives the SMs the least to do in turn, a
-// block's time being some constant and a part that grows with the channels.  K is split
-// (in 2 or 4) while all parts still run at once and have four blocks or more each.
-Plan plan_of(const F8Args& p, const OnDevice& d, int ctas) {
-  const int blocks = (p.K + kB - 1) / kB, units = sm_count() / ctas;
+// CTAs to a tile, its channels and parts of K: what gives the SMs the least to do in turn,
+// a block's time being some constant and a part that grows with the channels.  A pair takes
+// 2 x the rows in 0.93 of the time, in whole tiles (2048 x 28672 x 4096: 210 us, and 227 with
+// CTAs alone; 300 x 28672 x 4096: 58 and 54; 4096 rows by 8 experts of 4096 x 14336: 370 and
+// 262).  Channels: 64 x 28672 x 4096 26 us with 192, 28 with 256, two turns.  K is split (in
+// 2 or 4) while all parts still run at once and have four blocks or more each.
+template <typename K>
+Plan plan_of(const F8Args& p, K&& clusters) {
+  const int blocks = (p.K + kB - 1) / kB;
   Plan best{};
-  // rows of a tile: no more than there are, and for small groups 32, so that more stages fit
-  const int most = p.offsets && p.T / p.E < 16 ? 32 : kM;
-  best.rows = ctas == 2 || p.T > 64 ? most : p.T > 32 ? std::min(most, 64) : p.T > 16 ? 32 : 16;
-  const int M = best.rows * ctas;
-  // row tiles: of rows in groups about half a tile more for each
-  const int64_t ntt = p.offsets ? std::max<int64_t>(1, std::min<int64_t>(p.T, p.T / M + (p.E + 1) / 2)) : (p.T + M - 1) / M;
   double least = 0;
-  for (int nw = Tc::NT; nw >= 64; nw -= 64) {
-    const int64_t tiles = ntt * ((p.N + nw - 1) / nw);
-    int split = 1;
-    while (!p.offsets && split < 4 && tiles <= d.clusters[(split == 1 ? 1 : 2) + (ctas - 1)] && blocks >= 8 * split) split *= 2;
-    const double turns = static_cast<double>((tiles + units - 1) / units);
-    const double cost = turns * (nw + 64) / split;
-    if (best.nw == 0 || cost < least) best.nw = nw, best.split = split, least = cost;
+  for (int ctas = 1; ctas <= 2; ++ctas) {
+    const int units = sm_count() / ctas;
+    // rows of a tile: no more than there are, and for small groups 32, so that more stages fit
+    const int most = p.offsets && p.T / p.E < 16 ? 32 : kM;
+    const int rows = p.T > 64 ? most : p.T > 32 ? std::min(most, 64) : p.T > 16 ? 32 : 16;
+    if (ctas == 2 && (rows < kM || p.T <= kM)) break;
+    // row tiles: of rows in groups about half a tile more for each
+    const int M = rows * ctas;
+    const int64_t ntt = p.offsets ? std::max<int64_t>(1, std::min<int64_t>(p.T, p.T / M + (p.E + 1) / 2)) : (p.T + M - 1) / M;
+    for (int nw = Tc::NT; nw >= 64; nw -= 64) {
+      const int64_t tiles = ntt * ((p.N + nw - 1) / nw);
+      int split = 1;
+      while (!p.offsets && split < 4 && blocks >= 8 * split && tiles <= clusters(ctas, 2 * split * ctas)) split *= 2;
+      const double turns = static_cast<double>((tiles + units - 1) / units);
+      const double cost = turns * (nw + 64) / split * (ctas == 1 ? 1.08 : 1.0);
+      if (best.ctas == 0 || cost < least) best = {ctas, rows, nw, split, 0, 0, 0, 0}, least = cost;
+    }
   }
   best.x_bytes = best.rows * kB;
-  best.stage = best.x_bytes + best.nw / ctas * kB;
+  best.stage = best.x_bytes + best.nw / best.ctas * kB;
   best.stages = std::min(Tc::S, Tc::kRing / best.stage);
   best.accs = best.nw > 128 ? 2 : 4;
   return best;
@@ -877,28 +912,36 @@ cudaError_t launch_plan(const F8Args& p, const Plan& plan, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, k_tc_f8<O, CTAS, FULL>, p, maps, plan, static_cast<int>(bulk));
 }
 
-template <typename O, int CTAS>
+template <typename O>
 cudaError_t launch_tc(const F8Args& p, cudaStream_t s) {
-  static OnDevice all[kMaxDev], all_full[kMaxDev];
-  OnDevice* d;
-  cudaError_t e = prepare(all, k_tc_f8<O, CTAS, false>, &d);
+  static OnDevice all[3][kMaxDev];
+  OnDevice *one, *two, *full;
+  cudaError_t e = prepare(all[0], k_tc_f8<O, 1, false>, &one);
+  if (e == cudaSuccess) e = prepare(all[1], k_tc_f8<O, 2, false>, &two);
+  if (e == cudaSuccess) e = prepare(all[2], k_tc_f8<O, 2, true>, &full);
   if (e != cudaSuccess) return e;
-  const Plan plan = plan_of(p, *d, CTAS);
-  if constexpr (CTAS == 2) {
-    if (plan.nw == Tc::NT) {
-      e = prepare(all_full, k_tc_f8<O, CTAS, true>, &d);
-      return e != cudaSuccess ? e : launch_plan<O, CTAS, true>(p, plan, s);
-    }
-  }
-  return launch_plan<O, CTAS, false>(p, plan, s);
+  const Plan plan = plan_of(p, [&](int ctas, int size) { return (ctas == 1 ? one : two)->clusters[size == 2 ? 1 : size == 4 ? 2 : 3]; });
+  if (plan.ctas == 1) return launch_plan<O, 1, false>(p, plan, s);
+  return plan.nw == Tc::NT ? launch_plan<O, 2, true>(p, plan, s) : launch_plan<O, 2, false>(p, plan, s);
 }
 
 template <typename O>
 cudaError_t launch_f8(const F8Args& p, cudaStream_t s) {
+  // Few rows, or little to do: k_few_f8, us against k_tc_f8: 8 x 28672 x 4096 24.3 and 25.7,
+  // 64 x 60 x 4096 3.9 and 9.6, 32 x 1024 x 4096 4.8 and 9.1, 128 x 2048 x 2048 9.8 and 10.1,
+  // 64 x 4096 x 4096 16.5 and 13.2; 16 x 4096 x 14336 16.2 and 19.1, 16 x 28672 x 4096 28.8 and
+  // 26.0.  Rows in groups, about two to each or less: 8 rows by 8 experts of 28672 x 4096
+  // 75 and 80, 16 rows by 60 of 2816 x 2048 17 and 27, 64 rows 37 and 41; 32 rows by 8 131 and
+  // 119, 256 rows by 60 of 2048 x 1408 42 and 34.
   const int64_t rows = p.offsets ? (p.T + p.E - 1) / p.E : p.T;   // of a group, about
-  if (rows > kM) return launch_tc<O, 2>(p, s);
-  if (rows > 16) return launch_tc<O, 1>(p, s);
-  const int nt = rows <= 8 ? 1 : 2;
+  const double work = static_cast<double>(p.T) * p.N * p.K;
+  const bool few = p.offsets ? p.T <= 2 * static_cast<int64_t>(p.E) || work <= 7e8
+                             : p.T <= 8 || work <= (p.T <= 16 ? 1e9 : 7e8);
+  if (!few) return launch_tc<O>(p, s);
+  // in blocks of 8 rows as long as about one wave of CTAs holds them, then of 16, which read
+  // the weights half as often: 64 x 1024 x 4096 7.4 and 6.2, 256 x 60 x 4096 3.9 and 4.5
+  const int64_t blocks = (static_cast<int64_t>(p.N) + 15) / 16 * ((rows + 7) / 8);
+  const int nt = rows <= 8 || blocks <= sm_count() * 2 ? 1 : 2;
   const int turns = static_cast<int>(std::min<int64_t>((rows + nt * 8 - 1) / (nt * 8), 65535 / p.E));
   return nt == 1 ? launch_few<O, 1>(p, turns, s) : launch_few<O, 2>(p, turns, s);
 }
