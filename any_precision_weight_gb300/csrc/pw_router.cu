@@ -7,7 +7,7 @@
 //
 // A warp takes a token; a CTA takes a run of tokens and counts its pairs by expert.
 // The sort is a counting sort: an expert's pairs start behind those of the experts and
-// the CTAs before.  Up to kSmallPairs pairs one CTA does all of it (one launch, bound
+// the CTAs before.  Up to kSmallTokens tokens one CTA does all of it (one launch, bound
 // by its latencies); above, a second launch places them once every CTA has counted.
 // Each of its CTAs adds up the counts of those before it by itself, which costs less
 // than a launch between the two.
@@ -21,7 +21,7 @@ namespace pw {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kSmallPairs = 1024;
+constexpr int kSmallTokens = 32;
 constexpr int kMaxCtas = 128;
 
 struct RouteArgs {
@@ -46,15 +46,18 @@ __device__ __forceinline__ uint32_t order_of(float v) {
 // number above -inf have weights 0; where +inf is among the logits, those share the
 // weight.
 template <int NPER>
-__device__ __forceinline__ void route_token(const RouteArgs& p, int64_t t) {
+__device__ __forceinline__ void load_token(const RouteArgs& p, int64_t t, float (&v)[NPER]) {
   const int lane = threadIdx.x & 31;
-  const float* row = p.logits + t * p.ld;
-  float v[NPER];
+#pragma unroll
+  for (int i = 0; i < NPER; ++i) v[i] = lane + 32 * i < p.E ? __ldg(p.logits + t * p.ld + lane + 32 * i) : -INFINITY;
+}
+template <int NPER>
+__device__ __forceinline__ void route_token(const RouteArgs& p, int64_t t, float (&v)[NPER]) {
+  const int lane = threadIdx.x & 31;
   uint32_t key[NPER];   // 0: taken, or past E
 #pragma unroll
   for (int i = 0; i < NPER; ++i) {
     const int e = lane + 32 * i;
-    v[i] = e < p.E ? __ldg(row + e) : -INFINITY;
     if (isnan(v[i])) v[i] = -INFINITY;
     key[i] = e < p.E ? order_of(v[i]) : 0;
   }
@@ -171,7 +174,14 @@ __global__ void __launch_bounds__(kThreads) k_route_count(const RouteArgs p) {
   const int warp = threadIdx.x >> 5;
   const int t0 = blockIdx.x * p.tokens, t1 = min(p.T, t0 + p.tokens);
   for (int e = threadIdx.x; e < p.E; e += kThreads) s_n[e] = 0;
-  for (int t = t0 + warp; t < t1; t += kWarps) route_token<NPER>(p, t);
+  float v[NPER], next[NPER];   // the next token's logits are on their way while this one is routed
+  if (t0 + warp < t1) load_token<NPER>(p, t0 + warp, next);
+  for (int t = t0 + warp; t < t1; t += kWarps) {
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) v[i] = next[i];
+    if (t + kWarps < t1) load_token<NPER>(p, t + kWarps, next);
+    route_token<NPER>(p, t, v);
+  }
   __syncthreads();
   for (int q = t0 * p.k + threadIdx.x; q < t1 * p.k; q += kThreads) atomicAdd(&s_n[p.idx[q]], 1);
   __syncthreads();
@@ -188,15 +198,19 @@ __global__ void __launch_bounds__(kThreads) k_route_count(const RouteArgs p) {
 __global__ void __launch_bounds__(kThreads) k_route_place(const RouteArgs p) {
   extern __shared__ int s_mem[];
   int *s_base = s_mem, *s_off = s_mem + p.E, *s_c = s_off + p.E + 1;
-  for (int e = threadIdx.x; e < p.E; e += kThreads) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int e = threadIdx.x; e < p.E; e += kThreads) s_base[e] = s_off[e] = 0;
+  __syncthreads();
+  for (int e = lane; e < p.E; e += 32) {   // a warp adds the counts of every 16th CTA
     int before = 0, all = 0;
-    for (int c = 0; c < static_cast<int>(gridDim.x); ++c) {
+#pragma unroll 8
+    for (int c = warp; c < static_cast<int>(gridDim.x); c += kWarps) {
       const int n = p.counts[c * p.E + e];
       if (c < static_cast<int>(blockIdx.x)) before += n;
       all += n;
     }
-    s_base[e] = before;
-    s_off[e] = all;
+    atomicAdd(&s_base[e], before);
+    atomicAdd(&s_off[e], all);
   }
   __syncthreads();
   if (threadIdx.x < 32) scan_counts(s_off, p.E);
@@ -210,14 +224,14 @@ __global__ void __launch_bounds__(kThreads) k_route_place(const RouteArgs p) {
 }
 
 // CTAs of a batch.
-int ctas_of(int T, int k) {
-  if (static_cast<int64_t>(T) * k <= kSmallPairs) return 1;
+int ctas_of(int T) {
+  if (T <= kSmallTokens) return 1;
   return std::min((T + kWarps - 1) / kWarps, kMaxCtas);
 }
 
 template <int NPER>
 cudaError_t launch_route(RouteArgs p, cudaStream_t s) {
-  const int n = ctas_of(p.T, p.k);
+  const int n = ctas_of(p.T);
   p.tokens = (p.T + n - 1) / n;
   const unsigned grid = static_cast<unsigned>((p.T + p.tokens - 1) / p.tokens);
   const size_t smem = sizeof(int) * (2 * p.E + 1 + static_cast<size_t>(kWarps) * p.E);
@@ -239,7 +253,7 @@ extern "C" {
 
 size_t pw_route_workspace_bytes(int T, int E, int k) {
   if (!pw::route_shape_ok(T, E, k)) return 0;
-  const int n = pw::ctas_of(T, k);
+  const int n = pw::ctas_of(T);
   return n > 1 ? static_cast<size_t>(n) * E * sizeof(int32_t) : 0;
 }
 
