@@ -984,7 +984,8 @@ def pw_combine(y, weight, inv, residual=None, out=None, out_dtype=None, stream=N
         lr, pr = _rows(residual, "residual", dt, (T, H), dev), residual.data_ptr()
     if weight.dtype is not torch.float32 or not weight.is_contiguous() or _away(weight, dev):
         raise ValueError(f"weight: a contiguous float32 matrix [{T}][{k}] on the call's GPU is needed")
-    if inv.dtype is not torch.int32 or inv.numel() != T * k or not inv.is_contiguous() or _away(inv, dev):
+    if (inv.dtype is not torch.int32 or (inv.shape != (T * k,) and inv.shape != (T, k)) or not inv.is_contiguous()
+            or _away(inv, dev)):
         raise ValueError(f"inv: {T * k} consecutive int32 on the call's GPU are needed")
     _check(lib().pw_combine(y.data_ptr(), _rows(y, "y", y.dtype, (R, H), dev), R, _code(y.dtype), weight.data_ptr(),
                             inv.data_ptr(), pr, lr, T, k, H, _code(dt), out.data_ptr(), _rows(out, "out", dt, (T, H), dev),
