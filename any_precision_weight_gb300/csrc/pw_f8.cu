@@ -285,10 +285,10 @@ struct Tc {
   static constexpr int kOffMisc = kOffBar + 8 * kBars;    // tmem, abort, first tile of each group
   static constexpr int kSmem = kOffMisc + 16 + 4 * (PW_MAX_GROUPS + 1);
   static constexpr uint32_t kCols = 512;                  // of tensor memory
-  static constexpr int kSumRow = NT + 1;                  // of a row's sums in the ring, padded
+  static constexpr int kSumPad = 4;                       // floats behind a row's sums in the ring
   static_assert(kOffBar % 8 == 0 && kSmem <= 227 * 1024, "shared memory of a CTA");
   static_assert(SS >= S + D, "the scales of a block that may be fetched have been read");
-  static_assert(kM * kSumRow * 4 <= kRing, "a CTA's sums fit the ring");
+  static_assert(kM * (NT + kSumPad) * 4 <= kRing, "a CTA's sums fit the ring");
 };
 
 // What a launch chose: CTAs to a tile, rows of it (of a CTA's part: 128, or fewer in a CTA alone),
@@ -409,11 +409,14 @@ __device__ __forceinline__ float lds4(uint32_t a) {
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
   return v;
 }
-__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr, uint32_t rank) {
   uint32_t a;
-  float v;
+  float4 v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a)
+               : "memory");
   return v;
 }
 
@@ -475,7 +478,8 @@ __device__ __forceinline__ void first_tiles(const F8Args& p, int ntn, int M, int
   if (lane == 0) start[p.E] = before;
 }
 
-// FULL: tiles of 256 channels, where a thread's 128 are one block of the weights' scales.
+// FULL: tiles of 256 channels, where a thread's 128 are one block of the weights' scales, and
+// K whole.
 template <typename O, int CTAS, bool FULL>
 __global__ void __launch_bounds__(Tc::kThreads, 1)
 k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int bulk) {
@@ -499,9 +503,14 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int 
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   const int side = static_cast<int>(rank % CTAS), part = static_cast<int>(rank / CTAS);
   const uint32_t leader = rank - side;
-  const int nw = FULL ? C::NT : plan.nw, split = plan.split, ntn = (p.N + nw - 1) / nw;
+  const int nw = FULL ? C::NT : plan.nw, split = FULL ? 1 : plan.split, ntn = (p.N + nw - 1) / nw;
   const uint32_t accs = FULL ? C::kCols / C::NT : plan.accs, acc_cols = C::kCols / accs;
 
+  if (tid == 96) {   // a map's first use otherwise waits for it
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.w)) : "memory");
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.x[i])) : "memory");
+  }
   if (warp == 1) G::alloc(saddr(s_misc));
   if (tid == 0) {
     for (int i = 0; i < C::S; ++i) {
@@ -702,10 +711,10 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int 
       const int n0 = t.n0 + h * mine;
       if (split > 1) {
         // every stage of the ring has been read: its space takes the sums
-        float* sums = reinterpret_cast<float*>(smem) + (q * 32 + lane) * (nw + 1) + h * mine;
+        float* sums = reinterpret_cast<float*>(smem) + (q * 32 + lane) * (nw + C::kSumPad) + h * mine;
 #pragma unroll
-        for (int i = 0; i < C::ACC; ++i)
-          if (i < mine) sums[i] = acc[i];
+        for (int i = 0; i < C::ACC; i += 4)
+          if (i < mine) *reinterpret_cast<float4*>(sums + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
         continue;
       }
       if (p.bias) {
@@ -739,6 +748,13 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int 
           proxy_fence_smem();
           __syncwarp();
           if (lane == 0 && n0 + c < p.N) tma_store_2d(&maps.out, n0 + c, row0, saddr(stage));
+        } else if (!bulk) {   // rows that start anywhere: a channel to a lane
+          __syncwarp();
+          const int n = n0 + c + lane, r1 = n < p.N ? min(32, t.t1 - row0) : 0;
+          O* out = static_cast<O*>(p.out) + row0 * p.ldo + n;
+#pragma unroll 8
+          for (int r = 0; r < r1; ++r, out += p.ldo)
+            *out = reinterpret_cast<const O*>(stage + place(r, lane / V))[lane % V];
         } else {
           __syncwarp();
           const int n = n0 + c + lane % P * V;
@@ -748,7 +764,7 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int 
             const uint4 raw = *reinterpret_cast<const uint4*>(stage + place(r, lane % P));
             if (row >= t.t1) continue;
             O* out = static_cast<O*>(p.out) + row * p.ldo + n;
-            if (bulk && n + V <= p.N) {
+            if (n + V <= p.N) {
               *reinterpret_cast<uint4*>(out) = raw;
             } else {
               const O* v = reinterpret_cast<const O*>(&raw);
@@ -775,17 +791,30 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int 
       const Tile t = order.at(p, tile0);
       const int t0 = t.t0 + side * kM, rows = min(kM, t.t1 - t0), cols = min(nw, p.N - t.n0);
       const int r0 = rows > 0 ? rows * part / split : 0, r1 = rows > 0 ? rows * (part + 1) / split : 0;
-      for (int i = tid; i < (r1 - r0) * nw; i += C::kThreads) {
-        const int r = r0 + i / nw, c = i % nw;
-        if (c >= cols) continue;
-        float v[4], sum = 0.f;
+      // four channels of a row to a thread, U such at a time with all of their reads on the way
+      constexpr int U = 2;
+      const int per = nw / 4, units = (r1 - r0) * per;
+      for (int i0 = tid; i0 < units; i0 += U * C::kThreads) {
+        float4 v[U][4];
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
-          v[s] = s < split ? ld_cluster(base + (r * (nw + 1) + c) * 4, s * CTAS + side) : 0.f;
+        for (int u = 0; u < U; ++u) {
+          const int i = min(i0 + u * C::kThreads, units - 1);
+          const uint32_t at = base + ((r0 + i / per) * (nw + C::kSumPad) + i % per * 4) * 4;
 #pragma unroll
-        for (int s = 0; s < 4; ++s) sum += v[s];
-        if (p.bias) sum += to_f32<O>(static_cast<const O*>(p.bias)[static_cast<int64_t>(t.e) * p.N + t.n0 + c]);
-        static_cast<O*>(p.out)[(t0 + r) * p.ldo + t.n0 + c] = from_f32<O>(sum);
+          for (int s = 0; s < 4; ++s) v[u][s] = s < split ? ld_cluster(at, s * CTAS + side) : make_float4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = i0 + u * C::kThreads, c = i % per * 4;
+          if (i >= units) break;
+          float sum[4] = {((v[u][0].x + v[u][1].x) + v[u][2].x) + v[u][3].x, ((v[u][0].y + v[u][1].y) + v[u][2].y) + v[u][3].y,
+                          ((v[u][0].z + v[u][1].z) + v[u][2].z) + v[u][3].z, ((v[u][0].w + v[u][1].w) + v[u][2].w) + v[u][3].w};
+          O* out = static_cast<O*>(p.out) + (t0 + r0 + i / per) * p.ldo + t.n0 + c;
+          const O* bias = p.bias ? static_cast<const O*>(p.bias) + static_cast<int64_t>(t.e) * p.N + t.n0 + c : nullptr;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (c + e < cols) out[e] = from_f32<O>(sum[e] + (bias ? to_f32<O>(__ldg(bias + e)) : 0.f));
+        }
       }
     }
   }
@@ -844,12 +873,14 @@ cudaError_t prepare(OnDevice* all, K* kernel, OnDevice** out) {
   return cudaSuccess;
 }
 
-// CTAs to a tile, its channels and parts of K: what gives the SMs the least to do in turn,
-// a block's time being some constant and a part that grows with the channels.  A pair takes
-// 2 x the rows in 0.93 of the time, in whole tiles (2048 x 28672 x 4096: 210 us, and 227 with
-// CTAs alone; 300 x 28672 x 4096: 58 and 54; 4096 rows by 8 experts of 4096 x 14336: 370 and
-// 262).  Channels: 64 x 28672 x 4096 26 us with 192, 28 with 256, two turns.  K is split (in
-// 2 or 4) while all parts still run at once and have four blocks or more each.
+// CTAs to a tile, its channels and parts of K: what takes the least by this model.  A block
+// takes some 1.9 ns for each channel and 64 more, and 350 at least.  A pair takes 2 x the rows in 0.93 of the
+// time, in whole tiles (2048 x 28672 x 4096: 210 us, and 227 with CTAs alone; 300 x 28672 x
+// 4096: 58 and 54; 4096 rows by 8 experts of 4096 x 14336: 370 and 262).  Channels: 64 x 28672
+// x 4096 26 us with 192, 28 with 256, two turns.  K is split (in 2 or 4) where all parts run
+// at once and have two blocks or more; to join them takes 2.5 us, and more with their sums
+// (64 x 4096 x 4096: 12.2 us in 4 parts of 128 channels; 201 x 2891 x 1411: 11.1 in 2 of 128,
+// 9.6 whole with 64; 256 x 4096 x 4096: 16.9 in 4 of 256, 14.3 whole with 64).
 template <typename K>
 Plan plan_of(const F8Args& p, K&& clusters) {
   const int blocks = (p.K + kB - 1) / kB;
@@ -866,11 +897,13 @@ Plan plan_of(const F8Args& p, K&& clusters) {
     const int64_t ntt = p.offsets ? std::max<int64_t>(1, std::min<int64_t>(p.T, p.T / M + (p.E + 1) / 2)) : (p.T + M - 1) / M;
     for (int nw = Tc::NT; nw >= 64; nw -= 64) {
       const int64_t tiles = ntt * ((p.N + nw - 1) / nw);
-      int split = 1;
-      while (!p.offsets && split < 4 && blocks >= 8 * split && tiles <= clusters(ctas, 2 * split * ctas)) split *= 2;
       const double turns = static_cast<double>((tiles + units - 1) / units);
-      const double cost = turns * (nw + 64) / split * (ctas == 1 ? 1.08 : 1.0);
-      if (best.ctas == 0 || cost < least) best = {ctas, rows, nw, split, 0, 0, 0, 0}, least = cost;
+      for (int split = 1; split <= 4; split *= 2) {
+        if (split > 1 && (p.offsets || blocks < 2 * split || tiles > clusters(ctas, split * ctas))) break;
+        const double join = split > 1 ? 2500. + 0.085 * std::min(p.T, kM) * nw : 0.;
+        const double cost = turns * blocks / split * std::max(350., 1.9 * (nw + 64)) * (ctas == 1 ? 1.08 : 1.) + join;
+        if (best.ctas == 0 || cost < least) best = {ctas, rows, nw, split, 0, 0, 0, 0}, least = cost;
+      }
     }
   }
   best.x_bytes = best.rows * kB;
@@ -922,7 +955,7 @@ cudaError_t launch_tc(const F8Args& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const Plan plan = plan_of(p, [&](int ctas, int size) { return (ctas == 1 ? one : two)->clusters[size == 2 ? 1 : size == 4 ? 2 : 3]; });
   if (plan.ctas == 1) return launch_plan<O, 1, false>(p, plan, s);
-  return plan.nw == Tc::NT ? launch_plan<O, 2, true>(p, plan, s) : launch_plan<O, 2, false>(p, plan, s);
+  return plan.nw == Tc::NT && plan.split == 1 ? launch_plan<O, 2, true>(p, plan, s) : launch_plan<O, 2, false>(p, plan, s);
 }
 
 template <typename O>
