@@ -98,8 +98,7 @@ _SIGS = {
     "pw_linear_i8_status": (_i, [_vp, _pi]),
     "pw_debug_linear_timeout": (_i, [_vp]),
     "pw_logprobs": (_i, [_vp, _i64, _i, _i, _i, _vp, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp]),
-    "pw_route_workspace_bytes": (_sz, [_i, _i, _i]),
-    "pw_route": (_i, [_vp, _i64, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "pw_route": (_i, [_vp, _i64, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp]),
     "pw_quant_f8": (_i, [_vp, _i64, _i64, _vp, _i, _i, _i, _i, _vp, _i64, _vp, _i64, _vp]),
     "pw_silu_quant_f8": (_i, [_vp, _i64, _i, _i, _i, _vp, _i64, _vp, _i64, _vp]),
     "pw_quant_f8_blocks": (_i, [_vp, _i64, _i, _i, _i, _vp, _i64, _vp, _i64, _vp]),
@@ -821,17 +820,11 @@ class Routing(NamedTuple):
     inv: object
 
 
-def pw_route_workspace_bytes(T: int, E: int, k: int) -> int:
-    return lib().pw_route_workspace_bytes(T, E, k)
-
-
-def pw_route(logits, top_k: int, renorm: bool = False, out=None, ws=None, stream=None):
+def pw_route(logits, top_k: int, renorm: bool = False, out=None, stream=None):
     """A Routing of logits [T][E] float32: the top_k experts of every token and their
     softmax weights [T][top_k] (renorm: over the chosen ones), offsets [E + 1] of the
     routed pairs in expert order, the pair id t * top_k + j at each place (perm) and
-    the place of each pair (inv).  out: a Routing (or tuple) to write into.  ws: a
-    uint8 workspace of pw_route_workspace_bytes bytes (allocated here where it is
-    needed and not given)."""
+    the place of each pair (inv).  out: a Routing (or tuple) to write into."""
     torch = _torch()
     (T, E), (dev, raw) = _matrix(logits, "logits"), _place(torch, logits, "logits", stream)
     f32, i32, P = torch.float32, torch.int32, T * top_k
@@ -842,17 +835,9 @@ def pw_route(logits, top_k: int, renorm: bool = False, out=None, ws=None, stream
     for name, t, dt in (("idx", idx, i32), ("weight", weight, f32)):
         if t.shape != (T, top_k) or t.dtype is not dt or not t.is_contiguous() or _away(t, dev):
             raise ValueError(f"{name}: a contiguous matrix [{T}][{top_k}] of {dt} on the call's GPU is needed")
-    L = lib()
-    if ws is None:
-        need = L.pw_route_workspace_bytes(T, E, top_k)
-        if need:
-            ws = _empty(torch, stream, (need,), torch.uint8, logits.device)
-    elif ws.dtype is not torch.uint8 or not ws.is_contiguous() or _away(ws, dev):
-        raise ValueError(f"ws: a contiguous uint8 tensor on the call's GPU is needed, got {ws.dtype} on {ws.device}")
-    _check(L.pw_route(logits.data_ptr(), _rows(logits, "logits", f32, (T, E), dev), T, E, top_k, int(renorm),
+    _check(lib().pw_route(logits.data_ptr(), _rows(logits, "logits", f32, (T, E), dev), T, E, top_k, int(renorm),
                       idx.data_ptr(), weight.data_ptr(), _vec(offsets, "offsets", i32, E + 1, dev),
-                      _vec(perm, "perm", i32, P, dev), _vec(inv, "inv", i32, P, dev),
-                      None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), raw), "pw_route")
+                      _vec(perm, "perm", i32, P, dev), _vec(inv, "inv", i32, P, dev), raw), "pw_route")
     return Routing(idx, weight, offsets, perm, inv)
 
 

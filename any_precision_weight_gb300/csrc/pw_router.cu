@@ -5,12 +5,13 @@
 //   weight[t][j] = exp(logit_j - max) / sum, the sum over all experts, or over the k
 //   chosen ones (renorm)
 //
-// A warp takes a token; a CTA takes a run of tokens and counts its pairs by expert.
-// The sort is a counting sort: an expert's pairs start behind those of the experts and
-// the CTAs before.  Up to kSmallTokens tokens one CTA does all of it (one launch, bound
-// by its latencies); above, a second launch places them once every CTA has counted.
-// Each of its CTAs adds up the counts of those before it by itself, which costs less
-// than a launch between the two.
+// A warp takes a token.  Up to kSmallTokens tokens one CTA does everything (one launch,
+// bound by its latencies): it counts its pairs by expert and places them by a counting sort.
+// Above, a second launch has CTAs for one, two or four experts each: a CTA reads the experts
+// of all pairs twice, first counting those before its own experts and its own, then placing
+// its own in their order.  So no CTA needs another's results, and there is no workspace; 8192
+// x 60, 4 each, reads 8 MB from the L2 for it.  4 x 60, 4 each, 3.8 us, 256 x 60 4.5, 2048 x 60
+// 6.2, 8192 x 60 10.4: launches, latencies and, in the largest, the issue slots of the choice.
 
 #include <algorithm>
 #include <cmath>
@@ -22,7 +23,7 @@ namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kSmallTokens = 32;
-constexpr int kMaxCtas = 128;
+constexpr int kMaxCtas = 128;   // of the second launch
 
 struct RouteArgs {
   const float* logits;
@@ -32,8 +33,7 @@ struct RouteArgs {
   int32_t* offsets;
   int32_t* perm;
   int32_t* inv;
-  int32_t* counts;   // [CTA][E]
-  int T, E, k, renorm, tokens;   // tokens: of one CTA
+  int T, E, k, renorm;
 };
 
 // A float as an unsigned number of the same order; both zeros are one.
@@ -46,15 +46,12 @@ __device__ __forceinline__ uint32_t order_of(float v) {
 // number above -inf have weights 0; where +inf is among the logits, those share the
 // weight.
 template <int NPER>
-__device__ __forceinline__ void load_token(const RouteArgs& p, int64_t t, float (&v)[NPER]) {
+__device__ __forceinline__ void route_token(const RouteArgs& p, int64_t t) {
   const int lane = threadIdx.x & 31;
+  float v[NPER];
+  uint32_t key[NPER];   // 0: taken, or past E
 #pragma unroll
   for (int i = 0; i < NPER; ++i) v[i] = lane + 32 * i < p.E ? __ldg(p.logits + t * p.ld + lane + 32 * i) : -INFINITY;
-}
-template <int NPER>
-__device__ __forceinline__ void route_token(const RouteArgs& p, int64_t t, float (&v)[NPER]) {
-  const int lane = threadIdx.x & 31;
-  uint32_t key[NPER];   // 0: taken, or past E
 #pragma unroll
   for (int i = 0; i < NPER; ++i) {
     const int e = lane + 32 * i;
@@ -110,13 +107,13 @@ __device__ __forceinline__ void route_token(const RouteArgs& p, int64_t t, float
     for (int j = lane; j < p.k; j += 32) p.weight[t * p.k + j] /= chosen;
 }
 
-// Places the pairs [q0, q1) of this CTA, whose first place for expert e is base[e]:
-// warps count runs of them, the counts are scanned into each warp's first places, and
-// each warp places its run 32 at a time.  s_c: [kWarps][E].
-__device__ __forceinline__ void place_pairs(const RouteArgs& p, int q0, int q1, const int* base, int* s_c) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = p.E;
-  const int run = (q1 - q0 + kWarps - 1) / kWarps;
-  const int a = min(q1, q0 + warp * run), z = min(q1, a + run);
+// Places all pairs by one CTA: warps count runs of them, the counts are scanned into each
+// warp's first places behind base[e], and each warp places its run 32 at a time.
+// s_c: [kWarps][E].
+__device__ __forceinline__ void place_pairs(const RouteArgs& p, const int* base, int* s_c) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = p.E, P = p.T * p.k;
+  const int run = (P + kWarps - 1) / kWarps;
+  const int a = min(P, warp * run), z = min(P, a + run);
   int* mine = s_c + warp * E;
   for (int e = lane; e < E; e += 32) mine[e] = 0;
   __syncwarp();
@@ -166,79 +163,103 @@ __device__ __forceinline__ void scan_counts(int* s, int E) {
   if (lane == 0) s[E] = before;
 }
 
-// A CTA's run of tokens; where it is the only CTA, their places too.
+// A small batch by one CTA.
 template <int NPER>
-__global__ void __launch_bounds__(kThreads) k_route_count(const RouteArgs p) {
+__global__ void __launch_bounds__(kThreads) k_route_small(const RouteArgs p) {
   extern __shared__ int s_mem[];   // counts [E + 1], then [kWarps][E]
-  int* s_n = s_mem;
-  const int warp = threadIdx.x >> 5;
-  const int t0 = blockIdx.x * p.tokens, t1 = min(p.T, t0 + p.tokens);
-  for (int e = threadIdx.x; e < p.E; e += kThreads) s_n[e] = 0;
-  float v[NPER], next[NPER];   // the next token's logits are on their way while this one is routed
-  if (t0 + warp < t1) load_token<NPER>(p, t0 + warp, next);
-  for (int t = t0 + warp; t < t1; t += kWarps) {
-#pragma unroll
-    for (int i = 0; i < NPER; ++i) v[i] = next[i];
-    if (t + kWarps < t1) load_token<NPER>(p, t + kWarps, next);
-    route_token<NPER>(p, t, v);
-  }
+  for (int e = threadIdx.x; e < p.E; e += kThreads) s_mem[e] = 0;
+  for (int t = threadIdx.x >> 5; t < p.T; t += kWarps) route_token<NPER>(p, t);
   __syncthreads();
-  for (int q = t0 * p.k + threadIdx.x; q < t1 * p.k; q += kThreads) atomicAdd(&s_n[p.idx[q]], 1);
+  for (int q = threadIdx.x; q < p.T * p.k; q += kThreads) atomicAdd(&s_mem[p.idx[q]], 1);
   __syncthreads();
-  if (gridDim.x > 1) {
-    for (int e = threadIdx.x; e < p.E; e += kThreads) p.counts[blockIdx.x * p.E + e] = s_n[e];
-    return;
-  }
-  if (threadIdx.x < 32) scan_counts(s_n, p.E);
+  if (threadIdx.x < 32) scan_counts(s_mem, p.E);
   __syncthreads();
-  for (int e = threadIdx.x; e <= p.E; e += kThreads) p.offsets[e] = s_n[e];
-  place_pairs(p, 0, p.T * p.k, s_n, s_mem + p.E + 1);
-}
-
-__global__ void __launch_bounds__(kThreads) k_route_place(const RouteArgs p) {
-  extern __shared__ int s_mem[];
-  int *s_base = s_mem, *s_off = s_mem + p.E, *s_c = s_off + p.E + 1;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int e = threadIdx.x; e < p.E; e += kThreads) s_base[e] = s_off[e] = 0;
-  __syncthreads();
-  for (int e = lane; e < p.E; e += 32) {   // a warp adds the counts of every 16th CTA
-    int before = 0, all = 0;
-#pragma unroll 8
-    for (int c = warp; c < static_cast<int>(gridDim.x); c += kWarps) {
-      const int n = p.counts[c * p.E + e];
-      if (c < static_cast<int>(blockIdx.x)) before += n;
-      all += n;
-    }
-    atomicAdd(&s_base[e], before);
-    atomicAdd(&s_off[e], all);
-  }
-  __syncthreads();
-  if (threadIdx.x < 32) scan_counts(s_off, p.E);
-  __syncthreads();
-  for (int e = threadIdx.x; e < p.E; e += kThreads) s_base[e] += s_off[e];
-  if (blockIdx.x == 0)
-    for (int e = threadIdx.x; e <= p.E; e += kThreads) p.offsets[e] = s_off[e];
-  __syncthreads();
-  const int t0 = blockIdx.x * p.tokens, t1 = min(p.T, t0 + p.tokens);
-  place_pairs(p, t0 * p.k, t1 * p.k, s_base, s_c);
-}
-
-// CTAs of a batch.
-int ctas_of(int T) {
-  if (T <= kSmallTokens) return 1;
-  return std::min((T + kWarps - 1) / kWarps, kMaxCtas);
+  for (int e = threadIdx.x; e <= p.E; e += kThreads) p.offsets[e] = s_mem[e];
+  place_pairs(p, s_mem, s_mem + p.E + 1);
 }
 
 template <int NPER>
-cudaError_t launch_route(RouteArgs p, cudaStream_t s) {
-  const int n = ctas_of(p.T);
-  p.tokens = (p.T + n - 1) / n;
-  const unsigned grid = static_cast<unsigned>((p.T + p.tokens - 1) / p.tokens);
-  const size_t smem = sizeof(int) * (2 * p.E + 1 + static_cast<size_t>(kWarps) * p.E);
-  k_route_count<NPER><<<grid, kThreads, smem, s>>>(p);
+__global__ void __launch_bounds__(256) k_route_tokens(const RouteArgs p) {
+  const int t = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (t < p.T) route_token<NPER>(p, t);
+}
+
+// The pairs of the experts G blockIdx.x + 0 .. G - 1, by warps that take a run of all pairs
+// each.
+template <int G, int W>
+__global__ void __launch_bounds__(W * 32) k_route_place(const RouteArgs p) {
+  constexpr int U = W / 2;   // reads on their way together
+  __shared__ int s_n[W][G + 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = blockIdx.x * G;
+  const int64_t P = static_cast<int64_t>(p.T) * p.k;
+  const int64_t run = (P + W * 32 - 1) / (W * 32) * 32, a = min(P, warp * run), z = min(P, a + run);
+  // f(expert of this lane's pair, or -1, and the pair) for the warp's pairs in order
+  auto each = [&](auto&& f) {
+    for (int64_t b = a; b < z; b += 32 * U) {
+      int v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) v[u] = b + u * 32 + lane < z ? p.idx[b + u * 32 + lane] : -1;
+#pragma unroll
+      for (int u = 0; u < U; ++u) f(v[u], static_cast<int>(b + u * 32 + lane));
+    }
+  };
+  int n[G + 1] = {};   // of the experts before, and of each of its own
+  each([&](int e, int) {
+    n[0] += e >= 0 && e < e0;
+#pragma unroll
+    for (int g = 0; g < G; ++g) n[g + 1] += e == e0 + g;
+  });
+#pragma unroll
+  for (int g = 0; g <= G; ++g) {
+    const int sum = __reduce_add_sync(0xffffffffu, n[g]);
+    if (lane == 0) s_n[warp][g] = sum;
+  }
+  __syncthreads();
+  // a lane has a warp's counts
+  auto sum_of = [&](int g, int warps) { return __reduce_add_sync(0xffffffffu, lane < warps ? s_n[lane][g] : 0); };
+  int at[G], first = sum_of(0, W);
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    if (threadIdx.x == 0 && e0 + g <= p.E) p.offsets[e0 + g] = first;
+    at[g] = first + sum_of(g + 1, warp);
+    first += sum_of(g + 1, W);
+  }
+  if (threadIdx.x == 0 && blockIdx.x == gridDim.x - 1) p.offsets[p.E] = first;
+  each([&](int e, int q) {
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const unsigned same = __ballot_sync(0xffffffffu, e == e0 + g);
+      if (e == e0 + g) {
+        const int pos = at[g] + __popc(same & ((1u << lane) - 1u));
+        p.perm[pos] = q;
+        p.inv[q] = pos;
+      }
+      at[g] += __popc(same);
+    }
+  });
+}
+
+// 16 warps to a CTA, or 32: 256 x 60, 4 each, 4.5 us and 6.2; 8192 x 60 13.1 and 10.4.
+template <int G>
+void launch_place(const RouteArgs& p, bool many, cudaStream_t s) {
+  const unsigned grid = static_cast<unsigned>((p.E + G - 1) / G);
+  if (many) k_route_place<G, 32><<<grid, 1024, 0, s>>>(p);
+  else k_route_place<G, 16><<<grid, 512, 0, s>>>(p);
+}
+
+template <int NPER>
+cudaError_t launch_route(const RouteArgs& p, cudaStream_t s) {
+  if (p.T <= kSmallTokens) {
+    k_route_small<NPER><<<1, kThreads, sizeof(int) * (p.E + 1 + static_cast<size_t>(kWarps) * p.E), s>>>(p);
+    return cudaGetLastError();
+  }
+  k_route_tokens<NPER><<<(p.T + 7) / 8, 256, 0, s>>>(p);
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || grid == 1) return e;
-  k_route_place<<<grid, kThreads, smem, s>>>(p);
+  if (e != cudaSuccess) return e;
+  const bool many = static_cast<int64_t>(p.T) * p.k > 8192;
+  if (p.E <= kMaxCtas) launch_place<1>(p, many, s);
+  else if (p.E <= 2 * kMaxCtas) launch_place<2>(p, many, s);
+  else launch_place<4>(p, many, s);
   return cudaGetLastError();
 }
 
@@ -251,14 +272,8 @@ bool route_shape_ok(int T, int E, int k) {
 
 extern "C" {
 
-size_t pw_route_workspace_bytes(int T, int E, int k) {
-  if (!pw::route_shape_ok(T, E, k)) return 0;
-  const int n = pw::ctas_of(T);
-  return n > 1 ? static_cast<size_t>(n) * E * sizeof(int32_t) : 0;
-}
-
 int pw_route(const float* logits, int64_t ld, int T, int E, int k, int renorm, int32_t* idx, float* weight,
-             int32_t* offsets, int32_t* perm, int32_t* inv, void* workspace, size_t ws_bytes, pw_stream_t s) {
+             int32_t* offsets, int32_t* perm, int32_t* inv, pw_stream_t s) {
   using namespace pw;
   NvtxCall nvtx_range("pw_route");
   if (!route_shape_ok(T, E, k))
@@ -271,11 +286,7 @@ int pw_route(const float* logits, int64_t ld, int T, int E, int k, int renorm, i
   if (ld < E) return failf(PW_EINVAL, "pw_route: the row stride is below E = %d", E);
   if (!aligned(logits, 4) || !aligned(idx, 4) || !aligned(weight, 4) || !aligned(perm, 4) || !aligned(inv, 4))
     return failf(PW_EINVAL, "pw_route: misaligned pointer");
-  const size_t need = pw_route_workspace_bytes(T, E, k);
-  if (ws_bytes < need || (need && !workspace))
-    return failf(PW_ENOMEM, "pw_route: workspace of %zu bytes, %zu are needed", workspace ? ws_bytes : 0, need);
-  if (need && !aligned(workspace, 4)) return failf(PW_EINVAL, "pw_route: the workspace must be 4-byte aligned");
-  const RouteArgs a{logits, ld, idx, weight, offsets, perm, inv, static_cast<int32_t*>(workspace), T, E, k, renorm, 0};
+  const RouteArgs a{logits, ld, idx, weight, offsets, perm, inv, T, E, k, renorm};
   const cudaError_t e = E <= 32    ? launch_route<1>(a, st)
                         : E <= 64  ? launch_route<2>(a, st)
                         : E <= 128 ? launch_route<4>(a, st)

@@ -676,10 +676,6 @@ int pw_logprobs(const void* logits, int64_t ld, int dtype, int T, int V, const v
  */
 #define PW_MAX_GROUPS 512   /* most experts of pw_route and pw_grouped_linear_f8, most slots of pw_combine */
 
-/* Bytes of device workspace that pw_route asks for: 0 for a small batch, else room for
- * a count per expert and part of the batch.  0 for a bad shape. */
-size_t pw_route_workspace_bytes(int T, int E, int k);
-
 /*
  * pw_route -- the routing of pw_moe_forward on its own: top-k experts of every token,
  * and the routed pairs in expert order.
@@ -689,16 +685,13 @@ size_t pw_route_workspace_bytes(int T, int E, int k);
  *   offsets [E+1] int32: the places [offsets[e], offsets[e+1]) are expert e's
  *   perm    [T*k] int32: pair id t*k + j at each place, in (expert, token) order
  *   inv     [T*k] int32: the place of each pair id
- *   workspace  pw_route_workspace_bytes(T, E, k) bytes, 4-byte aligned, or NULL where
- *           that is 0; it may hold anything, and must not be shared by two calls in
- *           flight at once
  * A NaN logit counts as -inf.  A row of nothing else than -inf has weights 0; where
  * +inf is among the logits, the weight is theirs alone.  T = 0 writes offsets (zeros).
  * Errors: PW_EINVAL (shapes, T * k above PW_MAX_VOCAB, strides, null or misaligned
- * pointers), PW_ENOMEM (workspace too small), PW_ECUDA.
+ * pointers), PW_ECUDA.
  */
 int pw_route(const float* logits, int64_t ld, int T, int E, int k, int renorm, int32_t* idx, float* weight,
-             int32_t* offsets, int32_t* perm, int32_t* inv, void* workspace, size_t ws_bytes, pw_stream_t s);
+             int32_t* offsets, int32_t* perm, int32_t* inv, pw_stream_t s);
 
 /*
  * pw_quant_f8 -- rows to e4m3 with one scale for each 128 columns:

@@ -10,7 +10,7 @@ from any_precision_weight_gb300.model import F8Experts
 from test_operator_devices import library  # noqa: F401
 from test_operator_memory import Lib, Shape, Stream, made  # noqa: F401
 
-F16, F32, F8, I32, U8 = torch.float16, torch.float32, torch.float8_e4m3fn, torch.int32, torch.uint8
+F16, F32, F8, I32 = torch.float16, torch.float32, torch.float8_e4m3fn, torch.int32
 T, K, N, E, k = 40, 256, 384, 8, 2
 KB, NB = 2, 3
 
@@ -59,7 +59,7 @@ def grouped(**kw):
 def route(**kw):
     out = dict(idx=t(I32, T, k), weight=t(F32, T, k), offsets=t(I32, E + 1), perm=t(I32, T * k), inv=t(I32, T * k))
     out.update((n, kw.pop(n)) for n in list(kw) if n in out)
-    return pw.pw_route(**{**dict(logits=t(F32, T, E), top_k=k, ws=t(U8, 1 << 16)), **kw}, out=pw.Routing(**out))
+    return pw.pw_route(**{**dict(logits=t(F32, T, E), top_k=k), **kw}, out=pw.Routing(**out))
 
 
 def combine(**kw):
@@ -74,7 +74,7 @@ WHAT = [(quant, dict(x=(F16, T, K), rows=(I32, T), q=(F8, T, K), scale=(F32, T, 
         (grouped, dict(x=(F8, T, K), x_scale=(F32, T, KB), w=(F8, E, N, K), w_scale=(F32, E, NB, KB), offsets=(I32, E + 1),
                        bias=(F16, E, N), out=(F16, T, N))),
         (route, dict(logits=(F32, T, E), idx=(I32, T, k), weight=(F32, T, k), offsets=(I32, E + 1), perm=(I32, T * k),
-                     inv=(I32, T * k), ws=(U8, 1 << 16))),
+                     inv=(I32, T * k))),
         (combine, dict(y=(F16, T * k, N), weight=(F32, T, k), inv=(I32, T * k), residual=(F16, T, N), out=(F16, T, N)))]
 OPERANDS = [(f, name, what) for f, a in WHAT for name, what in a.items()]
 
@@ -89,7 +89,7 @@ def test_an_operand_elsewhere_is_refused(call, name, what, library, monkeypatch)
             library.called.clear()
             with pytest.raises(ValueError):
                 call(**{name: t(*what, at=at)})
-            assert not [c for c in library.called if not c.endswith("_bytes")]
+            assert not library.called
 
 
 @pytest.mark.parametrize("call,name,what", OPERANDS)
@@ -98,11 +98,9 @@ def test_an_operand_of_another_type_or_shape_is_refused(call, name, what, librar
     call()
     library.called.clear()
     for other in ((torch.int64, *shape), (dtype, *shape[:-1], shape[-1] + 1), (dtype, *shape, 1)):
-        if name == "ws" and other[0] is U8:
-            continue   # bytes of any number: the library looks at them
         with pytest.raises((TypeError, ValueError)):
             call(**{name: t(*other)})
-        assert not [c for c in library.called if not c.endswith("_bytes")]
+        assert not library.called
 
 
 @pytest.mark.parametrize("call", [f for f, _ in WHAT])
@@ -116,23 +114,18 @@ def test_another_current_device_or_stream_is_refused(call, library, monkeypatch)
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
     with pytest.raises(ValueError):
         call()
-    assert not [c for c in library.called if not c.endswith("_bytes")]
-
-
-class F8Lib(Lib):
-    def __getattr__(self, name):
-        return (lambda *a: 1000) if name == "pw_route_workspace_bytes" else super().__getattr__(name)
+    assert not library.called
 
 
 @pytest.mark.parametrize("call,n", [
     (lambda s: pw.pw_quant_f8(t(F16, T, K), stream=s), 2), (lambda s: pw.pw_silu_quant_f8(t(F16, T, K), stream=s), 2),
     (lambda s: pw.pw_quant_f8_blocks(t(F16, T, K), stream=s), 2), (lambda s: linear(out=None, stream=s), 1),
     (lambda s: grouped(out=None, stream=s), 1), (lambda s: combine(out=None, stream=s), 1),
-    (lambda s: pw.pw_route(t(F32, T, E), k, stream=s), 6),
+    (lambda s: pw.pw_route(t(F32, T, E), k, stream=s), 5),
     (lambda s: F8Experts(t(F8, E, 2 * N, K), t(F8, E, K, N), t(F32, E, 6, KB), t(F32, E, KB, NB)).forward(
-        t(F16, T, K), t(F32, T, E), k, True, stream=s), 13)])
+        t(F16, T, K), t(F32, T, E), k, True, stream=s), 12)])
 def test_what_a_call_makes_is_its_streams_memory(call, n, made, monkeypatch):  # noqa: F811
-    library = F8Lib()
+    library = Lib()
     monkeypatch.setattr(pw, "lib", lambda: library)
     monkeypatch.setattr(torch, "empty", lambda shape, dtype, device, e=torch.empty: t(dtype, *e(shape, dtype, device).shape))
     stream = Stream()

@@ -66,7 +66,7 @@ def test_grouped(kw):
     refused("pw_grouped_linear_f8", GROUPED, kw)
 
 
-ROUTE = dict(x=P, ld=60, T=4, E=60, k=4, renorm=0, idx=P, w=P, off=P, perm=P, inv=P, ws=None, nb=0)
+ROUTE = dict(x=P, ld=60, T=4, E=60, k=4, renorm=0, idx=P, w=P, off=P, perm=P, inv=P)
 
 
 @pytest.mark.parametrize("kw", [
@@ -75,15 +75,6 @@ ROUTE = dict(x=P, ld=60, T=4, E=60, k=4, renorm=0, idx=P, w=P, off=P, perm=P, in
     dict(idx=P + 1), dict(w=P + 1), dict(off=P + 1), dict(perm=P + 2), dict(inv=P + 2)])
 def test_route(kw):
     refused("pw_route", ROUTE, kw)
-
-
-def test_route_workspace():
-    assert pw.pw_route_workspace_bytes(4, 60, 4) == 0
-    need = pw.pw_route_workspace_bytes(5000, 60, 4)
-    assert need > 0 and pw.pw_route_workspace_bytes(5000, 60, 61) == 0 == pw.pw_route_workspace_bytes(-1, 60, 4)
-    refused("pw_route", ROUTE, dict(T=5000), pw.PW_ENOMEM)
-    refused("pw_route", ROUTE, dict(T=5000, ws=P, nb=need - 1), pw.PW_ENOMEM)
-    refused("pw_route", ROUTE, dict(T=5000, ws=P + 2, nb=need), pw.PW_EINVAL)
 
 
 COMBINE = dict(y=P, ldy=100, n=8, dt=pw.PW_F16, w=P, inv=P, res=None, ldr=0, T=4, k=2, H=100, odt=pw.PW_F32, out=P, ldo=100)

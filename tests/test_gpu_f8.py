@@ -416,8 +416,7 @@ def test_nothing_beside_the_outputs(T, N, K):
     assert torch.isfinite(grouped).all()
     i32, f32 = torch.int32, torch.float32
     r = pw.Routing(new((T, 3), i32), new((T, 3), f32), new((41,), i32), new((3 * T,), i32), new((3 * T,), i32))
-    need = pw.pw_route_workspace_bytes(T, 40, 3)
-    pw.pw_route(cuda(rng.normal(0, 1, (T, 40)), f32), 3, out=r, ws=new((need,), torch.uint8) if need else None)
+    pw.pw_route(cuda(rng.normal(0, 1, (T, 40)), f32), 3, out=r)
     a, sa = new((T, K // 2), F8), new((T, f8.blocks(K // 2)), f32)
     pw.pw_silu_quant_f8(x[:, :K // 2 * 2], q=a, scale=sa)
     c = new((T, N), torch.float16)
