@@ -308,14 +308,32 @@ static_assert(128 * (kRegsIssue + 2 * kRegsAcc) <= Tc::kThreads * kRegsLaunch, "
 __device__ uint32_t g_f8_timeouts;
 __global__ void k_count_timeout() { atomicAdd(&g_f8_timeouts, 1u); }
 
-// Polls up to kPolls times (about a second) for the phase of the given parity; false,
-// and the abort flag, when they run out or another thread has raised it.  (test_wait:
-// a thread that try_wait has put to sleep wakes up some hundred clocks late.)
-constexpr int kPolls = 1 << 23;
+// Waits for the phase of the given parity, up to a second; false, and the abort flag, when
+// that has passed or another thread has raised it.  (With test_wait in the place of try_wait,
+// whose threads sleep, the polls of the warps keep one another and the arrivals waiting: 2048
+// x 28672 x 4096 203 and 193 us.)
+__device__ __forceinline__ uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done;
+}
 __device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, volatile int* abort) {
-  for (int n = 0; !test_wait(bar, parity); ++n) {
+  if (try_wait(bar, parity)) return true;
+  const uint64_t start = now_ns();
+  while (!try_wait(bar, parity)) {
     if (*abort) return false;
-    if (n == kPolls) {
+    if (now_ns() - start > 1000000000ull) {
       atomicAdd(&g_f8_timeouts, 1u);
       *abort = 1;
       return false;
