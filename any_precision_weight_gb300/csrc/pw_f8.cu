@@ -38,15 +38,19 @@ struct F8Args {
   int T, N, K, E;
 };
 
-// Rows of a group.  Offsets come from the device: what is out of order or range is cut,
-// so that no row outside [0, T) is touched.
+// Offsets come from the device: one outside [0, T] is cut to it.  Where they descend the
+// rows between are some group's, or several groups' after another; k_tc_f8, whose tiles are
+// counted, takes the largest so far.  (To look for that in k_few_f8 too takes 2 us.)
+__device__ __forceinline__ int offset_in(const F8Args& p, int i) { return min(max(__ldg(p.offsets + i), 0), p.T); }
+
+// Rows of a group.
 struct Rows {
   int begin, end;
 };
 __device__ __forceinline__ Rows rows_of(const F8Args& p, int e) {
   if (!p.offsets) return {0, p.T};
-  const int a = min(max(__ldg(p.offsets + e), 0), p.T), z = min(max(__ldg(p.offsets + e + 1), 0), p.T);
-  return {a, max(a, z)};
+  const int begin = offset_in(p, e);
+  return {begin, max(begin, offset_in(p, e + 1))};
 }
 
 // ---------------------------------------------------------------- few rows
@@ -282,8 +286,8 @@ struct Tc {
   static constexpr int kOffScale = kOffOut + EW * kPiece;
   static constexpr int kOffBar = kOffScale + SS * kScale * 4;
   static constexpr int kBars = 2 * S + 2 * D + 1;
-  static constexpr int kOffMisc = kOffBar + 8 * kBars;    // tmem, abort, first tile of each group
-  static constexpr int kSmem = kOffMisc + 16 + 4 * (PW_MAX_GROUPS + 1);
+  static constexpr int kOffMisc = kOffBar + 8 * kBars;    // tmem, abort, first tile and row of each group
+  static constexpr int kSmem = kOffMisc + 16 + 2 * 4 * (PW_MAX_GROUPS + 1);
   static constexpr uint32_t kCols = 512;                  // of tensor memory
   static constexpr int kSumPad = 4;                       // floats behind a row's sums in the ring
   static_assert(kOffBar % 8 == 0 && kSmem <= 227 * 1024, "shared memory of a CTA");
@@ -458,42 +462,48 @@ struct Tile {
   int e, t0, t1, n0;
 };
 
-// The tiles in order of the groups, `start` the first of each; within a group bands of
-// kBand row tiles, so that CTAs at work share operands in the L2.
+// The tiles in order of the groups, `start` the first of each and `off` its rows' first;
+// within a group bands of kBand row tiles, so that CTAs at work share operands in the L2.
 constexpr int kBand = 8;
 struct Tiles {
-  const int* start;
+  const int *start, *off;
   int ntn, M, nw, e = 0;
-  __device__ __forceinline__ Tile at(const F8Args& p, int tile) {
+  __device__ __forceinline__ Tile at(int tile) {
     while (tile >= start[e + 1]) ++e;
-    const Rows r = rows_of(p, e);
+    const int begin = off[e], end = off[e + 1];
     const int local = tile - start[e], band = local / (kBand * ntn), rest = local - band * kBand * ntn;
-    const int width = min(kBand, (r.end - r.begin + M - 1) / M - band * kBand);
-    const int t0 = r.begin + (band * kBand + rest % width) * M;
-    return {e, t0, min(r.end, t0 + M), rest / width * nw};
+    const int width = min(kBand, (end - begin + M - 1) / M - band * kBand);
+    const int t0 = begin + (band * kBand + rest % width) * M;
+    return {e, t0, min(end, t0 + M), rest / width * nw};
   }
 };
 
-// The first tile of each group, and behind them the number of tiles, by one warp.
-__device__ __forceinline__ void first_tiles(const F8Args& p, int ntn, int M, int* start) {
+// The first row and the first tile of each group, and behind them the ends, by one warp.
+__device__ __forceinline__ void first_tiles(const F8Args& p, int ntn, int M, int* start, int* off) {
   const int lane = threadIdx.x & 31;
-  int before = 0;
+  int before = 0, begin = p.offsets ? offset_in(p, 0) : 0;
   for (int e0 = 0; e0 < p.E; e0 += 32) {
-    int n = 0;
-    if (e0 + lane < p.E) {
-      const Rows r = rows_of(p, e0 + lane);
-      n = (r.end - r.begin + M - 1) / M * ntn;
+    const bool in = e0 + lane < p.E;
+    int end = !in ? 0 : p.offsets ? offset_in(p, e0 + lane + 1) : p.T;   // then the largest up to here
+    end = max(end, begin);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, end, o);
+      if (lane >= o) end = max(end, v);
     }
+    const int last = __shfl_up_sync(0xffffffffu, end, 1), mine = lane ? last : begin;
+    const int n = in ? (end - mine + M - 1) / M * ntn : 0;
     int sum = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum += v;
     }
-    if (e0 + lane < p.E) start[e0 + lane] = before + sum - n;
+    if (in) start[e0 + lane] = before + sum - n, off[e0 + lane] = mine;
     before += __shfl_sync(0xffffffffu, sum, 31);
+    begin = __shfl_sync(0xffffffffu, end, 31);
   }
-  if (lane == 0) start[p.E] = before;
+  if (lane == 0) start[p.E] = before, off[p.E] = begin;
 }
 
 // FULL: tiles of 256 channels, where a thread's 128 are one block of the weights' scales, and
@@ -512,7 +522,7 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int 
   const uint32_t full = base + C::kOffBar, empty = full + 8 * C::S;
   const uint32_t dfull = empty + 8 * C::S, dempty = dfull + 8 * C::D, fin = dempty + 8 * C::D;
   int* s_misc = reinterpret_cast<int*>(smem + C::kOffMisc);   // tmem, abort
-  int* s_start = s_misc + 4;
+  int *s_start = s_misc + 4, *s_off = s_start + PW_MAX_GROUPS + 1;
   volatile int* abort = s_misc + 1;
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // the compiler then knows that it is uniform
@@ -541,7 +551,7 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int 
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     s_misc[1] = 0;
   }
-  if (warp == 2) first_tiles(p, ntn, CTAS * plan.rows, s_start);
+  if (warp == 2) first_tiles(p, ntn, CTAS * plan.rows, s_start, s_off);
   tc_fence_before();
   __syncthreads();
   if (CTAS == 2) cluster_sync();   // the other CTA's barriers and tensor memory
@@ -556,7 +566,7 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int 
   const int s0 = static_cast<int>(static_cast<int64_t>(blocks) * part / split);
   const int s1 = static_cast<int>(static_cast<int64_t>(blocks) * (part + 1) / split);
   const int tile0 = blockIdx.x / (CTAS * split), tile_step = gridDim.x / (CTAS * split);
-  Tiles order{s_start, ntn, CTAS * plan.rows, nw};
+  Tiles order{s_start, s_off, ntn, CTAS * plan.rows, nw};
 
   if (warp < kEpiWarp0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
@@ -565,7 +575,7 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int 
       Turn r;
       bool ok = true;
       for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
-        const Tile t = order.at(p, tile);
+        const Tile t = order.at(tile);
         const int t0 = t.t0 + side * kM, rows = t.t1 - t0, wn = nw / CTAS;
         const int box = rows > 64 ? 0 : rows > 32 ? 1 : rows > 16 ? 2 : 3;   // the least that holds the rows
         for (int k = s0; k < s1; ++k, r.next(plan.stages)) {
@@ -593,7 +603,7 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int 
       uint32_t slot = 0;
       bool ok = true;
       for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
-        const Tile t = order.at(p, tile);
+        const Tile t = order.at(tile);
         const float* xs[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) xs[i] = p.xs + min(t.t0 + side * kM + row + i, t.t1 - 1) * p.ldxs;
@@ -679,7 +689,7 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int 
     Turn d;
     bool ok = true;
     for (int tile = tile0; tile < tiles; tile += tile_step) {
-      const Tile t = order.at(p, tile);
+      const Tile t = order.at(tile);
       const int row0 = t.t0 + side * kM + q * 32;
       const bool busy = row0 < t.t1;
       float acc[C::ACC];
@@ -806,7 +816,7 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int 
     // the parts of one tile: each CTA adds and stores its share of the rows
     cluster_sync();
     if (!*abort && tile0 < tiles) {
-      const Tile t = order.at(p, tile0);
+      const Tile t = order.at(tile0);
       const int t0 = t.t0 + side * kM, rows = min(kM, t.t1 - t0), cols = min(nw, p.N - t.n0);
       const int r0 = rows > 0 ? rows * part / split : 0, r1 = rows > 0 ? rows * (part + 1) / split : 0;
       // four channels of a row to a thread, U such at a time with all of their reads on the way
@@ -997,7 +1007,8 @@ cudaError_t launch_f8(const F8Args& p, cudaStream_t s) {
   return nt == 1 ? launch_few<O, 1>(p, turns, s) : launch_few<O, 2>(p, turns, s);
 }
 
-int linear_f8(const char* what, const F8Args& p, int out_dtype, pw_stream_t s) {
+int linear_f8(const char* what, F8Args p, int out_dtype, pw_stream_t s) {
+  if (p.E == 1) p.gw = p.gws = 0;   // no other group
   if (p.T < 0 || p.T > PW_MAX_VOCAB || p.N < 1 || p.N > PW_MAX_VOCAB || p.K < 1 || p.K > PW_MAX_VOCAB || p.E < 1 ||
       p.E > PW_MAX_GROUPS)
     return failf(PW_EINVAL, "%s: need 0 <= T, 1 <= N, K up to %d and 1 <= E <= %d (T %d, N %d, K %d, E %d)", what,

@@ -743,8 +743,8 @@ int pw_linear_f8(const uint8_t* x, int64_t ldx, const float* x_scale, int64_t ld
  *   group_w, group_ws  elements from one expert's weights (a multiple of 16) and
  *            scales to the next one's
  * T is the number of rows of x and out.  Rows outside every range are left as they
- * are; an offset outside [0, T], or below the one before it, is cut to where no other
- * row is touched.
+ * are.  An offset outside [0, T] is cut to it.  Where offsets descend, what the rows
+ * between get is not defined; no other memory is touched.
  * Errors: as pw_linear_f8.
  */
 int pw_grouped_linear_f8(const uint8_t* x, int64_t ldx, const float* x_scale, int64_t ldxs, const uint8_t* w,

@@ -206,15 +206,28 @@ def test_grouped(counts, N, K):
                 near(out.view[a:z], ref, dt, product_tol(size, K, dt) + 2 * U * np.abs(ref))
 
 
-@pytest.mark.parametrize("T", [4, 40, 400])
-def test_offsets_out_of_order_touch_no_other_row(T):
+@pytest.mark.parametrize("T,N", [(4, 64), (40, 300), (400, 2000), (3000, 2000)])
+def test_offsets_out_of_order(T, N):
+    """Cut to [0, T]; nothing beside the rows is touched."""
     g = GuardSet(4096)
     rng = gen(T, "offsets")
-    x, w, xs, ws = values(rng, T, 128), values(rng, 4, 64, 128), scales(rng, T, 1), scales(rng, 4, 1, 1)
-    out = g.alloc(T * 64 * 4, "cuda", "out").view(torch.float32).view(T, 64)
-    for off in ([-5, 2, 1, T + 9, 2 ** 31 - 1], [T + 1, 0, -2 ** 31, 3, 2], [7, 7, 7, 7, 7], [2 ** 31 - 1] * 5):
+    E, K = 4, 128 if T < 3000 else 640
+    x, w, xs, ws = values(rng, T, K), values(rng, E, N, K), scales(rng, T, K // 128), scales(rng, E, f8.blocks(N), K // 128)
+    out = g.alloc(T * N * 4, "cuda", "out").view(torch.float32).view(T, N)
+    again = torch.empty_like(out)
+    for off in ([-5, 2, 1, T + 9, 2 ** 31 - 1], [T + 1, 0, -2 ** 31, 3, 2], [7, 7, 7, 7, 7], [2 ** 31 - 1] * 5, [0, T, 0, T, 0],
+                [0] * 5, [3, 1, T // 2, 0, T - 1]):
+        out.fill_(77)
         pw.pw_grouped_linear_f8(x, xs, w, ws, cuda(np.array(off), torch.int32), out=out)
         assert g.corrupted() == []
+        order = np.clip(off, 0, T)
+        if (np.diff(order) < 0).any():
+            continue
+        again.fill_(77)
+        pw.pw_grouped_linear_f8(x, xs, w, ws, cuda(order, torch.int32), out=again)
+        assert torch.equal(out, again)
+        left = torch.cat([again[:order[0]], again[order[-1]:]])
+        assert (left == 77).all()
 
 
 def test_rows_with_no_numbers_stay_alone():
@@ -243,6 +256,17 @@ def test_one_group_is_the_plain_product():
         ref, size = f8.linear(f64(x), f64(xs), f64(w), f64(ws))
         for o in (a, b):
             near(o, ref, "f32", product_tol(size, 640, "f32"))
+
+
+@pytest.mark.parametrize("T,N,K", [(4000, 3, 60001), (4100, 11000, 16), (17, 60, 700000)])
+def test_thin_products(T, N, K):
+    rng = gen(T, N, K, "thin")
+    x, w = values(rng, T, K), values(rng, N, K)
+    xs, ws = scales(rng, T, f8.blocks(K)), scales(rng, f8.blocks(N), f8.blocks(K))
+    out = pw.pw_linear_f8(x, xs, w, ws, out_dtype=torch.float32)
+    t = np.unique(np.linspace(0, T - 1, 200).astype(int))
+    ref, size = f8.linear(f64(x[t]), f64(xs[t]), f64(w), f64(ws))
+    near(out[t], ref, "f32", product_tol(size, K, "f32"))
 
 
 # ---------------------------------------------------------------- routing and the weighted sum
@@ -395,6 +419,14 @@ def test_expert_layer_as_a_graph_and_on_another_stream(T):
         g.replay()
     torch.cuda.synchronize()
     assert torch.equal(cap, want2)
+
+
+def test_no_tokens():
+    m, _ = _layer(8, 256, 512, "f16", 0)
+    x = torch.empty(0, 256, dtype=torch.float16, device="cuda")
+    r = pw.pw_route(torch.empty(0, 8, device="cuda"), 2)
+    assert (r.offsets == 0).all() and r.offsets.numel() == 9
+    assert m.forward(x, torch.empty(0, 8, device="cuda"), 2, True).shape == (0, 256)
 
 
 @pytest.mark.parametrize("T,N,K", [(1, 60, 2048), (9, 300, 1000), (40, 1030, 520), (300, 520, 1411)])
