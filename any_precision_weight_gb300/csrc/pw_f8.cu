@@ -902,7 +902,7 @@ cudaError_t prepare(OnDevice* all, K* kernel, OnDevice** out) {
 }
 
 // CTAs to a tile, its channels and parts of K: what takes the least by this model.  A block
-// takes some 1.9 ns for each channel and 64 more, and 350 at least.  A pair takes 2 x the rows in 0.93 of the
+// takes some 1.9 ns for each channel and 64 more, and 350 at least.  A pair takes 2 x the rows in 0.87 of the
 // time, in whole tiles (2048 x 28672 x 4096: 210 us, and 227 with CTAs alone; 300 x 28672 x
 // 4096: 58 and 54; 4096 rows by 8 experts of 4096 x 14336: 370 and 262).  Channels: 64 x 28672
 // x 4096 26 us with 192, 28 with 256, two turns.  K is split (in 2 or 4) where all parts run
@@ -929,7 +929,7 @@ Plan plan_of(const F8Args& p, K&& clusters) {
       for (int split = 1; split <= 4; split *= 2) {
         if (split > 1 && (p.offsets || blocks < 2 * split || tiles > clusters(ctas, split * ctas))) break;
         const double join = split > 1 ? 2500. + 0.085 * std::min(p.T, kM) * nw : 0.;
-        const double cost = turns * blocks / split * std::max(350., 1.9 * (nw + 64)) * (ctas == 1 ? 1.08 : 1.) + join;
+        const double cost = turns * blocks / split * std::max(350., 1.9 * (nw + 64)) * (ctas == 1 ? 1.15 : 1.) + join;
         if (best.ctas == 0 || cost < least) best = {ctas, rows, nw, split, 0, 0, 0, 0}, least = cost;
       }
     }

@@ -8,8 +8,10 @@ Tolerances.  U = 2^-24 is fp32's rounding; outputs are rounded once to their typ
    up to 8 parts add 8 U;
  * quantiser: scales by U; 16-bit inputs give the e4m3 number nearest to the exact
    quotient, 32-bit ones too but where it lies within 2 U of halfway; silu(gate) * up is
-   off by 8 U (exponential 2, its argument's rounding covered by |g| e^-|g| < 1, sum,
-   quotient and product), the block's largest as much: half a step and 20 U * 448;
+   off by e = (8 + |g| (1 - sigmoid(g))) U: 2 U each for exponential and reciprocal, U for
+   the sum and each product, and the rounding of the exponential's argument g log2 e, by
+   |g log2 e| U, changes 2^argument by |g| U and the sigmoid by 1 - sigmoid of that.  The
+   block's largest is off as much: half a step and (2 e + 4 U) 448;
  * routing: an exponential is off by 2 U and its argument by |x - max| U, at most 32 U
    here; sums of E terms by E U;
  * weighted sum: (k + 2) U of the sum of the absolute terms.
@@ -90,15 +92,20 @@ def test_rows(T, K):
         assert fq.intact() and fs.intact()
 
 
+def check_silu(q, s, x):
+    g = f64(x)[:, :x.shape[1] // 2]
+    e = (8 + np.abs(g) / (1 + np.exp(g))).max() * U   # 1 - sigmoid(g) = 1 / (1 + e^g)
+    v, ref = f8.quotients(f8.silu_up(f64(x)))
+    assert (np.abs(f64(s) - ref) <= ref * (e + 2 * U)).all()
+    assert (np.abs(f64(q) - v) <= np.maximum(np.abs(v) * 2.0 ** -4, 2.0 ** -10) + (2 * e + 4 * U) * 448).all()
+
+
 @pytest.mark.parametrize("T,K", ROWS)
 def test_silu_rows(T, K):
     for dt in DT:
         x = cuda(gen(T, K, dt, "silu").normal(0, 2, (T, 2 * K)), DT[dt])
         q, s = pw.pw_silu_quant_f8(x)
-        y = f8.silu_up(f64(x))
-        v, ref = f8.quotients(y)
-        assert (np.abs(f64(s) - ref) <= ref * 10 * U).all()
-        assert (np.abs(f64(q) - v) <= np.maximum(np.abs(v) * 2.0 ** -4, 2.0 ** -10) + 20 * U * 448).all()
+        check_silu(q, s, x)
 
 
 @pytest.mark.parametrize("N,K", [(1, 1), (128, 128), (129, 257), (300, 1411), (1000, 64), (64, 3000)])
@@ -109,6 +116,19 @@ def test_blocks(N, K):
         pw.pw_quant_f8_blocks(w, q=fq.view.view(F8), scale=fs.view)
         check_q(fq.view.view(F8), fs.view, f64(w), dt, 128)
         assert fq.intact() and fs.intact()
+
+
+def test_silu_of_far_gates():
+    """Gates of any size: no overflow, and a gate of -inf or NaN has that scale."""
+    for dt in DT:
+        top = {"f16": 6e4, "bf16": 1e38, "f32": 1e38}[dt]
+        g = np.array([top, 100.0, 20.0, 0.0, -0.0, -20.0, -88.0, -88.7, -100.0, -top])
+        x = cuda(np.concatenate([g, np.full(10, 1e-3)])[None], DT[dt])
+        q, s = pw.pw_silu_quant_f8(x)
+        check_silu(q, s, x)
+        x[0, 2] = -INF
+        q, s = pw.pw_silu_quant_f8(x)
+        assert np.isnan(f64(s)).all() and (f64(q) == 0).all()
 
 
 def test_rows_of_nothing_and_of_no_numbers():
@@ -373,9 +393,7 @@ def _check_layer(m, x, logits, k, renorm, residual, dt):
     check_route(t.routing, f64(logits), k, renorm)
     off = t.routing.offsets.tolist()
     check_q(t.q, t.scale, f64(x)[f64(t.routing.perm).astype(int) // k], dt)
-    v, s = f8.quotients(f8.silu_up(f64(t.up)))
-    assert (np.abs(f64(t.act_scale) - s) <= s * 10 * U).all()
-    assert (np.abs(f64(t.act) - v) <= np.maximum(np.abs(v) * 2.0 ** -4, 2.0 ** -10) + 20 * U * 448).all()
+    check_silu(t.act, t.act_scale, t.up)
     for q, sc, w, ws, o in ((t.q, t.scale, m.gate_up, m.gate_up_scale, t.up), (t.act, t.act_scale, m.down, m.down_scale, t.y)):
         for e in range(E):
             a, z = off[e], off[e + 1]
