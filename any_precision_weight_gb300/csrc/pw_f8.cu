@@ -112,6 +112,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, kFewCtas) k_few_f8(const F8Arg
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int groups = kFewWarps / kw, turn = warp % kw;
   const int e = blockIdx.y / turns;
+  after_those_before();
   const Rows rows = rows_of(p, e);
   const int n0 = (blockIdx.x * groups + warp / kw) * 16;
   const int blocks = (p.K + kB - 1) / kB, whole = p.K / kB;
@@ -246,8 +247,8 @@ cudaError_t launch_few(const F8Args& p, int turns, cudaStream_t s) {
     if (n == 1 || cost < least) kw = n, least = cost;
   }
   const int per = kFewWarps / kw;
-  k_few_f8<O, NT><<<dim3((groups + per - 1) / per, static_cast<unsigned>(rows)), kFewWarps * 32, 0, s>>>(p, kw, turns);
-  return cudaGetLastError();
+  return launch_close(k_few_f8<O, NT>, dim3((groups + per - 1) / per, static_cast<unsigned>(rows)), kFewWarps * 32, 0, 1, s, p,
+                      kw, turns);
 }
 
 // ---------------------------------------------------------------- tensor cores
@@ -551,6 +552,7 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int 
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     s_misc[1] = 0;
   }
+  after_those_before();
   if (warp == 2) first_tiles(p, ntn, CTAS * plan.rows, s_start, s_off);
   tc_fence_before();
   __syncthreads();
@@ -960,17 +962,8 @@ cudaError_t launch_plan(const F8Args& p, const Plan& plan, cudaStream_t s) {
   const int64_t ntt = (p.T + M - 1) / M, ntn = (p.N + plan.nw - 1) / plan.nw;
   const int64_t tiles = ntn * (p.offsets ? std::min<int64_t>(p.T, ntt + p.E) : ntt);
   const int64_t grid = plan.split > 1 ? tiles * plan.split : std::min<int64_t>(tiles, sm_count() / CTAS);
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid * CTAS));
-  cfg.blockDim = dim3(Tc::kThreads);
-  cfg.dynamicSmemBytes = Tc::kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute a{};
-  a.id = cudaLaunchAttributeClusterDimension;
-  a.val.clusterDim = {static_cast<unsigned>(CTAS * plan.split), 1, 1};
-  cfg.attrs = &a;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_tc_f8<O, CTAS, FULL>, p, maps, plan, static_cast<int>(bulk));
+  return launch_close(k_tc_f8<O, CTAS, FULL>, dim3(static_cast<unsigned>(grid * CTAS)), Tc::kThreads, Tc::kSmem,
+                      CTAS * plan.split, s, p, maps, plan, static_cast<int>(bulk));
 }
 
 template <typename O>

@@ -175,6 +175,8 @@ __global__ void __launch_bounds__(256, LIE != kWhole ? 2 : ACT ? 3 : 4) k_quant(
   constexpr int N = 16, kStep = 4 * kBlock;
   using P = Part<T, LIE, N>;
   const int warp = threadIdx.x >> 5, l = threadIdx.x & 7;
+  after_those_before();
+  let_next_begin();
   for (int64_t c = blockIdx.y * kStep; c < p.K; c += static_cast<int64_t>(gridDim.y) * kStep) {
     const int k0 = static_cast<int>(c) + (threadIdx.x >> 3 & 3) * kBlock;
     const bool in = k0 < p.K;
@@ -230,6 +232,7 @@ template <typename T, Lie LIE>
 __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : LIE == kWhole ? 3 : 2) k_quant_blocks(const QuantArgs p) {
   __shared__ float s_max[8];
   const int l = threadIdx.x & 15, r0 = threadIdx.x >> 4, k0 = blockIdx.x * kBlock;
+  after_those_before();
   for (int64_t b = blockIdx.y; b * kBlock < p.T; b += gridDim.y) {
     const int64_t t0 = b * kBlock + r0;
     const T* x0 = static_cast<const T*>(p.x) + t0 * p.ldx;
@@ -270,10 +273,9 @@ cudaError_t launch_rows(const QuantArgs& p, Lie lie, cudaStream_t s) {
   const unsigned gy = static_cast<unsigned>(std::min<int64_t>(segments, 65535));
   const int64_t rows = (static_cast<int64_t>(p.T) + 7) / 8;
   const unsigned gx = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(rows, sm_count() * int64_t{8} / gy)));
-  if (lie == kWhole) k_quant<T, ACT, kWhole><<<dim3(gx, gy), 256, 0, s>>>(p);
-  else if (lie == kWide) k_quant<T, ACT, kWide><<<dim3(gx, gy), 256, 0, s>>>(p);
-  else k_quant<T, ACT, kAny><<<dim3(gx, gy), 256, 0, s>>>(p);
-  return cudaGetLastError();
+  if (lie == kWhole) return launch_close(k_quant<T, ACT, kWhole>, dim3(gx, gy), 256, 0, 1, s, p);
+  if (lie == kWide) return launch_close(k_quant<T, ACT, kWide>, dim3(gx, gy), 256, 0, 1, s, p);
+  return launch_close(k_quant<T, ACT, kAny>, dim3(gx, gy), 256, 0, 1, s, p);
 }
 
 template <typename T>
@@ -285,10 +287,9 @@ cudaError_t launch_quant(const QuantArgs& p, bool act, bool by_block, cudaStream
   const int blocks = (p.K + kBlock - 1) / kBlock;
   if (by_block) {
     const dim3 grid(blocks, std::min<int64_t>((static_cast<int64_t>(p.T) + kBlock - 1) / kBlock, 65535));
-    if (lie == kWhole) k_quant_blocks<T, kWhole><<<grid, 256, 0, s>>>(p);
-    else if (lie == kWide) k_quant_blocks<T, kWide><<<grid, 256, 0, s>>>(p);
-    else k_quant_blocks<T, kAny><<<grid, 256, 0, s>>>(p);
-    return cudaGetLastError();
+    if (lie == kWhole) return launch_close(k_quant_blocks<T, kWhole>, grid, 256, 0, 1, s, p);
+    if (lie == kWide) return launch_close(k_quant_blocks<T, kWide>, grid, 256, 0, 1, s, p);
+    return launch_close(k_quant_blocks<T, kAny>, grid, 256, 0, 1, s, p);
   }
   return act ? launch_rows<T, true>(p, lie, s) : launch_rows<T, false>(p, lie, s);
 }
@@ -364,6 +365,7 @@ __device__ __forceinline__ void put_cols(T* row, int h, int H, const float (&v)[
 // stay, three to an SM; 65 with one to a token).
 template <typename Y, typename O, bool WIDE, int N, int J>
 __global__ void __launch_bounds__(256, WIDE ? 3 : 2) k_combine_rows(const CombineArgs p) {
+  after_those_before();
   for (int64_t h0 = static_cast<int64_t>(blockIdx.y) * blockDim.x * 8; h0 < p.H; h0 += static_cast<int64_t>(gridDim.y) * blockDim.x * 8) {
     const int64_t hl = h0 + threadIdx.x * 8;
     if (hl >= p.H) continue;
@@ -436,10 +438,9 @@ cudaError_t launch_combine(const CombineArgs& p, cudaStream_t s) {
   const int threads = p.T * ((chunks + 255) / 256) < sm_count() * 2 ? 64 : 256;
   const unsigned gy = static_cast<unsigned>(std::min<int64_t>((chunks + threads - 1) / threads, 65535));
   const unsigned gx = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(p.T, sm_count() * int64_t{3} / gy)));
-  if (!wide) k_combine_rows<Y, O, false, 1, 2><<<dim3(gx, gy), threads, 0, s>>>(p);
-  else if (p.k <= 2 && p.T > sm_count() * 8) k_combine_rows<Y, O, true, 2, 2><<<dim3(gx, gy), threads, 0, s>>>(p);
-  else k_combine_rows<Y, O, true, 1, 4><<<dim3(gx, gy), threads, 0, s>>>(p);
-  return cudaGetLastError();
+  if (!wide) return launch_close(k_combine_rows<Y, O, false, 1, 2>, dim3(gx, gy), threads, 0, 1, s, p);
+  if (p.k <= 2 && p.T > sm_count() * 8) return launch_close(k_combine_rows<Y, O, true, 2, 2>, dim3(gx, gy), threads, 0, 1, s, p);
+  return launch_close(k_combine_rows<Y, O, true, 1, 4>, dim3(gx, gy), threads, 0, 1, s, p);
 }
 
 template <typename Y>

@@ -167,6 +167,8 @@ __device__ __forceinline__ void scan_counts(int* s, int E) {
 template <int NPER>
 __global__ void __launch_bounds__(kThreads) k_route_small(const RouteArgs p) {
   extern __shared__ int s_mem[];   // counts [E + 1], then [kWarps][E]
+  after_those_before();
+  let_next_begin();
   for (int e = threadIdx.x; e < p.E; e += kThreads) s_mem[e] = 0;
   for (int t = threadIdx.x >> 5; t < p.T; t += kWarps) route_token<NPER>(p, t);
   __syncthreads();
@@ -180,6 +182,8 @@ __global__ void __launch_bounds__(kThreads) k_route_small(const RouteArgs p) {
 
 template <int NPER>
 __global__ void __launch_bounds__(256) k_route_tokens(const RouteArgs p) {
+  after_those_before();
+  let_next_begin();
   const int t = blockIdx.x * 8 + (threadIdx.x >> 5);
   if (t < p.T) route_token<NPER>(p, t);
 }
@@ -190,6 +194,8 @@ template <int G, int W>
 __global__ void __launch_bounds__(W * 32) k_route_place(const RouteArgs p) {
   constexpr int U = W / 2;   // reads on their way together
   __shared__ int s_n[W][G + 1];
+  after_those_before();
+  let_next_begin();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = blockIdx.x * G;
   const int64_t P = static_cast<int64_t>(p.T) * p.k;
   const int64_t run = (P + W * 32 - 1) / (W * 32) * 32, a = min(P, warp * run), z = min(P, a + run);
@@ -241,26 +247,22 @@ __global__ void __launch_bounds__(W * 32) k_route_place(const RouteArgs p) {
 
 // 16 warps to a CTA, or 32: 256 x 60, 4 each, 4.5 us and 6.2; 8192 x 60 13.1 and 10.4.
 template <int G>
-void launch_place(const RouteArgs& p, bool many, cudaStream_t s) {
+cudaError_t launch_place(const RouteArgs& p, bool many, cudaStream_t s) {
   const unsigned grid = static_cast<unsigned>((p.E + G - 1) / G);
-  if (many) k_route_place<G, 32><<<grid, 1024, 0, s>>>(p);
-  else k_route_place<G, 16><<<grid, 512, 0, s>>>(p);
+  if (many) return launch_close(k_route_place<G, 32>, grid, 1024, 0, 1, s, p);
+  return launch_close(k_route_place<G, 16>, grid, 512, 0, 1, s, p);
 }
 
 template <int NPER>
 cudaError_t launch_route(const RouteArgs& p, cudaStream_t s) {
-  if (p.T <= kSmallTokens) {
-    k_route_small<NPER><<<1, kThreads, sizeof(int) * (p.E + 1 + static_cast<size_t>(kWarps) * p.E), s>>>(p);
-    return cudaGetLastError();
-  }
-  k_route_tokens<NPER><<<(p.T + 7) / 8, 256, 0, s>>>(p);
-  cudaError_t e = cudaGetLastError();
+  if (p.T <= kSmallTokens)
+    return launch_close(k_route_small<NPER>, 1, kThreads, sizeof(int) * (p.E + 1 + static_cast<size_t>(kWarps) * p.E), 1, s, p);
+  const cudaError_t e = launch_close(k_route_tokens<NPER>, (p.T + 7) / 8, 256, 0, 1, s, p);
   if (e != cudaSuccess) return e;
   const bool many = static_cast<int64_t>(p.T) * p.k > 8192;
-  if (p.E <= kMaxCtas) launch_place<1>(p, many, s);
-  else if (p.E <= 2 * kMaxCtas) launch_place<2>(p, many, s);
-  else launch_place<4>(p, many, s);
-  return cudaGetLastError();
+  if (p.E <= kMaxCtas) return launch_place<1>(p, many, s);
+  if (p.E <= 2 * kMaxCtas) return launch_place<2>(p, many, s);
+  return launch_place<4>(p, many, s);
 }
 
 bool route_shape_ok(int T, int E, int k) {

@@ -66,4 +66,30 @@ inline bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t
 // Streaming multiprocessors of the current device (asked once per device).
 int sm_count();
 
+// A launch that may begin before the one ahead of it in the stream has left the GPU: its
+// kernel calls after_those_before() before it touches memory.
+template <typename... P, typename... A>
+inline cudaError_t launch_close(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, int cluster, cudaStream_t s,
+                                const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute a[2]{};
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  a[1].id = cudaLaunchAttributeClusterDimension;
+  a[1].val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
+  cfg.attrs = a;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+// Everything before this kernel in its stream has ended, and its results can be read.
+__device__ __forceinline__ void after_those_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The next kernel in the stream may begin (up to its own after_those_before()).  Called
+// behind it, so that the next one begins after all that this one waited for; and not by
+// kernels whose results may be router logits, which pw_moe_forward reads before it waits.
+__device__ __forceinline__ void let_next_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 }  // namespace pw
