@@ -105,6 +105,10 @@ constexpr int kFewCtas = 2;   // of an SM
 // row g of every 8: the operand registers of its products, with the columns of K in an
 // order of their own that both operands share.  So the weights go from memory to the
 // tensor cores through registers alone.  Each block's sums are scaled into fp32 sums.
+// The weights' bytes bound it: 1 x 28672 x 4096 takes 22.7 us, 5.2 TB/s or 76 % of a copy's
+// rate (registers hold no more loads in flight than four blocks of two CTAs; 2 us and more are
+// the launch, the first loads and the sums over the warps).  The products, at most 16 rows,
+// take a fifth of the tensor cores' time.
 template <typename O, int NT>
 __global__ void __launch_bounds__(kFewWarps * 32, kFewCtas) k_few_f8(const F8Args p, int kw, int turns) {
   constexpr int kRow = NT * 8 + 1;   // padded against bank conflicts
@@ -269,6 +273,12 @@ cudaError_t launch_few(const F8Args& p, int turns, cudaStream_t s) {
 //    and at the tile's end store.
 // Where there are few tiles a cluster splits K and adds the parts through distributed
 // shared memory, in the order of the parts.
+// 2048 x 28672 x 4096 takes 194 us, 2475 TFLOP/s.  A pair's MMAs of a block take 512 clocks, and
+// its accumulators' way from tensor memory through two warps of each scheduler (read, wait,
+// 256 x 128 multiply-adds of a CTA) some 1150, the tensor cores busy for half of them; the
+// board draws 1385 W, and has 1400.  To sum over K in tensor memory alone has no place for the
+// blocks' scales.  64 x 28672 x 4096 takes 25.9 us, 4.5 TB/s of weights; small products 9 us, of
+// which 5 are the tensor memory, the barriers, the first tiles and the sums' way out.
 constexpr int kM = 128;          // rows of a CTA
 constexpr int kEpiWarp0 = 4;
 
@@ -747,11 +757,13 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int 
           if (i < mine) *reinterpret_cast<float4*>(sums + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
         continue;
       }
-      if (p.bias) {
-        const O* bias = static_cast<const O*>(p.bias) + static_cast<int64_t>(t.e) * p.N + n0;
+      if (p.bias) {   // a channel to a lane, read together (each by all lanes: 3 us more)
+        const O* bias = static_cast<const O*>(p.bias) + static_cast<int64_t>(t.e) * p.N;
+        float b[C::ACC / 32];
 #pragma unroll
-        for (int i = 0; i < C::ACC; ++i)
-          if (i < mine && n0 + i < p.N) acc[i] += to_f32<O>(__ldg(bias + i));
+        for (int c = 0; c < C::ACC; c += 32) b[c / 32] = to_f32<O>(__ldg(bias + min(n0 + c + lane, p.N - 1)));
+#pragma unroll
+        for (int i = 0; i < C::ACC; ++i) acc[i] += __shfl_sync(~0u, b[i / 32], i % 32);
       }
       // 32 channels of each of the warp's rows at a time, through shared memory: by TMA where
       // all of the rows are the group's, else row by row
@@ -904,13 +916,14 @@ cudaError_t prepare(OnDevice* all, K* kernel, OnDevice** out) {
 }
 
 // CTAs to a tile, its channels and parts of K: what takes the least by this model.  A block
-// takes some 1.9 ns for each channel and 64 more, and 350 at least.  A pair takes 2 x the rows in 0.87 of the
-// time, in whole tiles (2048 x 28672 x 4096: 210 us, and 227 with CTAs alone; 300 x 28672 x
-// 4096: 58 and 54; 4096 rows by 8 experts of 4096 x 14336: 370 and 262).  Channels: 64 x 28672
-// x 4096 26 us with 192, 28 with 256, two turns.  K is split (in 2 or 4) where all parts run
-// at once and have two blocks or more; to join them takes 2.5 us, and more with their sums
-// (64 x 4096 x 4096: 12.2 us in 4 parts of 128 channels; 201 x 2891 x 1411: 11.1 in 2 of 128,
-// 9.6 whole with 64; 256 x 4096 x 4096: 16.9 in 4 of 256, 14.3 whole with 64).
+// takes 2.2 ns for each channel and 64 more (a pair of CTAs 1.9, for twice the rows), and
+// 350 (400) at least.  Pairs, us, against CTAs alone: 2048 x 28672 x 4096 194 and 225, 512 x
+// 28672 x 4096 55 and 62, 201 x 2891 x 1411 11.7 and 9.8; 4096 rows by 8 experts of 28672 x
+// 4096 506 and 525, of 4096 x 14336 349 and 248 (five turns of 76 pairs, or four of 152 CTAs).
+// Channels: 64 x 28672 x 4096 25.9 with 192, 26.7 with 256, two turns, 35.6 with 128.  K is
+// split (in 2 or 4) where all parts run at once and have two blocks or more; to join them
+// takes 2.5 us, and more with their sums: 64 x 4096 x 4096 12.3 in 4 parts of 128 channels,
+// 17.0 whole with 64; 201 x 2891 x 1411 11.4 in 2 of 128, 9.8 whole with 64.
 template <typename K>
 Plan plan_of(const F8Args& p, K&& clusters) {
   const int blocks = (p.K + kB - 1) / kB;
@@ -931,7 +944,8 @@ Plan plan_of(const F8Args& p, K&& clusters) {
       for (int split = 1; split <= 4; split *= 2) {
         if (split > 1 && (p.offsets || blocks < 2 * split || tiles > clusters(ctas, split * ctas))) break;
         const double join = split > 1 ? 2500. + 0.085 * std::min(p.T, kM) * nw : 0.;
-        const double cost = turns * blocks / split * std::max(350., 1.9 * (nw + 64)) * (ctas == 1 ? 1.15 : 1.) + join;
+        const double block = ctas == 1 ? std::max(350., 2.2 * (nw + 64)) : std::max(400., 1.9 * (nw + 64));
+        const double cost = turns * blocks / split * block + join;
         if (best.ctas == 0 || cost < least) best = {ctas, rows, nw, split, 0, 0, 0, 0}, least = cost;
       }
     }
