@@ -766,7 +766,8 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int 
         for (int i = 0; i < C::ACC; ++i) acc[i] += __shfl_sync(~0u, b[i / 32], i % 32);
       }
       // 32 channels of each of the warp's rows at a time, through shared memory: by TMA where
-      // all of the rows are the group's, else row by row
+      // all of the rows are the group's and the tensor map does not end inside 16 bytes (all
+      // 16 would be written), else row by row
       constexpr int V = 16 / sizeof(O), P = 32 / V;   // channels of 16 bytes; such pieces of a row
       constexpr int kTurns = C::kPiece / (32 * 32 * sizeof(O));   // that fit beside one another
       const bool whole = bulk && row0 + 32 <= t.t1;
@@ -786,7 +787,7 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int 
           for (int e = 0; e < V; ++e) o[e] = from_f32<O>(acc[c + i * V + e]);
           *reinterpret_cast<uint4*>(stage + place(lane, i)) = *reinterpret_cast<const uint4*>(o);
         }
-        if (whole) {
+        if (whole && (p.N % V == 0 || n0 + c + 32 <= p.N)) {
           proxy_fence_smem();
           __syncwarp();
           if (lane == 0 && n0 + c < p.N) tma_store_2d(&maps.out, n0 + c, row0, saddr(stage));

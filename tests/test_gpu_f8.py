@@ -227,6 +227,40 @@ def test_grouped(counts, N, K):
                 near(out.view[a:z], ref, dt, product_tol(size, K, dt) + 2 * U * np.abs(ref))
 
 
+# sizes that pairs of CTAs take in tiles of 256 x 256, the last of a group's rows few
+LAST = [([257], 9728, 256), ([300], 9500, 300), ([320], 9728, 130), ([321], 9600, 128), ([384], 9665, 200), ([385], 9728, 200),
+        ([513], 9700, 270), ([1100], 9728, 130), ([1, 256, 0, 130, 385, 33, 64, 131], 2048, 300),
+        ([65, 128, 129, 127, 300, 2, 63, 186], 4003, 257)]
+
+
+@pytest.mark.parametrize("counts,N,K", LAST)
+def test_last_rows(counts, N, K):
+    E, T = len(counts), sum(counts)
+    for dt in DT:
+        rng = gen(E, T, N, K, dt, "last")
+        x, w = values(rng, T, K), values(rng, E, N, K)
+        xs, ws = scales(rng, T, f8.blocks(K)), scales(rng, E, f8.blocks(N), f8.blocks(K))
+        if dt == "f16":
+            xs *= 2.0 ** -14
+        b = cuda(rng.normal(0, 1, (E, N)), DT[dt])
+        off = np.concatenate([[0], np.cumsum(counts)])
+        for pad in (0, 1):   # stores by TMA, and channel by channel
+            out = Framed(T, N, DT[dt], pad=pad + (-N) % 8)
+            if E == 1:
+                pw.pw_linear_f8(x, xs, w[0], ws[0], bias=b[0], out=out.view)
+            else:
+                pw.pw_grouped_linear_f8(x, xs, w, ws, cuda(off, torch.int32), bias=b, out=out.view)
+            assert out.intact()
+            if pad == 0:
+                want = out.view.clone()
+            assert torch.equal(out.view, want)
+        for e in range(E):
+            a, z = off[e], off[e + 1]
+            if z > a:
+                ref, size = f8.linear(f64(x)[a:z], f64(xs)[a:z], f64(w[e]), f64(ws[e]), f64(b)[e])
+                near(want[a:z], ref, dt, product_tol(size, K, dt) + 2 * U * np.abs(ref))
+
+
 @pytest.mark.parametrize("T,N", [(4, 64), (40, 300), (400, 2000), (3000, 2000)])
 def test_offsets_out_of_order(T, N):
     """Cut to [0, T]; nothing beside the rows is touched."""
