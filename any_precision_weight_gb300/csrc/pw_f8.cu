@@ -471,21 +471,29 @@ struct Turn {
 // A tile: its group, rows [t0, t1) and first channel.
 struct Tile {
   int e, t0, t1, n0;
+  // Of a pair whose tile is of 256 channels: at most 128 rows, 64 to a CTA.
+  __device__ __forceinline__ bool half() const { return t1 - t0 <= kM; }
 };
 
 // The tiles in order of the groups, `start` the first of each and `off` its rows' first;
-// within a group bands of kBand row tiles, so that CTAs at work share operands in the L2.
+// within a group bands of kBand row tiles, so that CTAs at work share operands in the L2.  A
+// CTA takes every `step`th; from one to its next a band's row tiles go round by one, so that
+// the last of a group, which may have fewer rows, falls to all CTAs alike.
 constexpr int kBand = 8;
 struct Tiles {
   const int *start, *off;
-  int ntn, M, nw, e = 0;
+  int ntn, M, nw, step, e = 0;
+  template <bool HALF>
   __device__ __forceinline__ Tile at(int tile) {
     while (tile >= start[e + 1]) ++e;
     const int begin = off[e], end = off[e + 1];
     const int local = tile - start[e], band = local / (kBand * ntn), rest = local - band * kBand * ntn;
     const int width = min(kBand, (end - begin + M - 1) / M - band * kBand);
-    const int t0 = begin + (band * kBand + rest % width) * M;
-    return {e, t0, min(end, t0 + M), rest / width * nw};
+    const int column = rest / width, row = rest - column * width;
+    const int less = (end - begin) % M;   // rows of the group's last tile, or none
+    const int round = HALF && less && less <= M / 2 ? column * width / step * ((width + 1 - step % width) % width) : 0;
+    const int t0 = begin + (band * kBand + (row + round) % width) * M;
+    return {e, t0, min(end, t0 + M), column * nw};
   }
 };
 
@@ -518,8 +526,11 @@ __device__ __forceinline__ void first_tiles(const F8Args& p, int ntn, int M, int
 }
 
 // FULL: tiles of 256 channels, where a thread's 128 are one block of the weights' scales, and
-// K whole.
-template <typename O, int CTAS, bool FULL>
+// K whole.  HALF: the same, but that of a pair's tile of at most 128 rows each CTA takes 64,
+// in 0.75 of the time: 4096 rows by 8 experts of 28672 x 4096 take 495 us, without 512, 2048
+// rows 288 and 311 (by single CTAs); 300 x 28672 x 4096 51.5 and 55.  (Its choice in every pair
+// costs 2048 x 28672 x 4096 5 us, so it is a kernel of its own.)
+template <typename O, int CTAS, bool FULL, bool HALF>
 __global__ void __launch_bounds__(Tc::kThreads, 1)
 k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int bulk) {
   using C = Tc;
@@ -578,7 +589,7 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int 
   const int s0 = static_cast<int>(static_cast<int64_t>(blocks) * part / split);
   const int s1 = static_cast<int>(static_cast<int64_t>(blocks) * (part + 1) / split);
   const int tile0 = blockIdx.x / (CTAS * split), tile_step = gridDim.x / (CTAS * split);
-  Tiles order{s_start, s_off, ntn, CTAS * plan.rows, nw};
+  Tiles order{s_start, s_off, ntn, CTAS * plan.rows, nw, tile_step};
 
   if (warp < kEpiWarp0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
@@ -587,8 +598,9 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int 
       Turn r;
       bool ok = true;
       for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
-        const Tile t = order.at(tile);
-        const int t0 = t.t0 + side * kM, rows = t.t1 - t0, wn = nw / CTAS;
+        const Tile t = order.template at<HALF>(tile);
+        const bool half = HALF && t.half();
+        const int t0 = t.t0 + side * (half ? kM / 2 : kM), rows = half ? min(t.t1 - t0, kM / 2) : t.t1 - t0, wn = nw / CTAS;
         const int box = rows > 64 ? 0 : rows > 32 ? 1 : rows > 16 ? 2 : 3;   // the least that holds the rows
         for (int k = s0; k < s1; ++k, r.next(plan.stages)) {
           if (!r.first && !(ok = poll(empty + 8 * r.stage, r.parity ^ 1, abort))) break;
@@ -615,10 +627,11 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int 
       uint32_t slot = 0;
       bool ok = true;
       for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
-        const Tile t = order.at(tile);
+        const Tile t = order.template at<HALF>(tile);
+        const int t0 = t.t0 + side * (HALF && t.half() ? kM / 2 : kM);
         const float* xs[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) xs[i] = p.xs + min(t.t0 + side * kM + row + i, t.t1 - 1) * p.ldxs;
+        for (int i = 0; i < 2; ++i) xs[i] = p.xs + min(t0 + row + i, t.t1 - 1) * p.ldxs;
         const float* ws = p.ws + t.e * p.gws + min(t.n0 + (lane & 3) * 64, p.N - 1) / kB * p.ldws;
         for (int k0 = s0; k0 < s1 && ok; k0 += 4) {
           float v[2][4], w[4];
@@ -655,10 +668,10 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int 
     } else if (warp == 1) {
       // ---- MMA issue: the whole warp in step, so that the operands stay in uniform
       // registers, and an elected thread for the instructions
-      const uint32_t idesc = idesc_of(CTAS * kM, nw);
       Turn r, d;
       bool ok = true;
       for (int tile = tile0; tile < tiles && ok; tile += tile_step) {
+        const uint32_t idesc = idesc_of(HALF && order.template at<HALF>(tile).half() ? kM : CTAS * kM, nw);
         for (int k = s0; k < s1; ++k) {
           if (!(ok = wait(full + 8 * r.stage, r.parity))) break;
           const uint32_t at = base + r.stage * plan.stage;
@@ -691,18 +704,24 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int 
   } else {
     // ---- scale, accumulate and store: a row to a lane, half of the channels to a thread
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsAcc));
-    const int q = warp & 3, h = (warp - kEpiWarp0) >> 2, mine = FULL ? C::ACC : nw / 2;
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * mine;
-    const uint32_t scales = base + C::kOffScale, row_at = (q * 32 + lane) * 4, w_at = (kM + h * mine / 64) * 4;
-    const int odd = h * mine % 64;   // where the second half of the channels starts in its 64
+    const int q = warp & 3, h = (warp - kEpiWarp0) >> 2;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    const uint32_t scales = base + C::kOffScale;
     unsigned char* const piece = smem + C::kOffOut + (warp - kEpiWarp0) * C::kPiece;
     uint32_t slot = 0;
     int turn = 0;
     Turn d;
     bool ok = true;
     for (int tile = tile0; tile < tiles; tile += tile_step) {
-      const Tile t = order.at(tile);
-      const int row0 = t.t0 + side * kM + q * 32;
+      const Tile t = order.template at<HALF>(tile);
+      // the warp's channels [c0, c0 + mine) and rows.  Half a pair's rows lie in the lanes 0 to
+      // 63, with the first half of the channels, and in 64 to 127 with the second
+      const bool half = HALF && t.half();
+      const int mine = half ? C::ACC / 2 : FULL ? C::ACC : nw / 2;
+      const int r0 = half ? q % 2 * 32 : q * 32, c0 = half ? q / 2 * C::ACC + h * mine : h * mine;
+      const uint32_t row_at = (r0 + lane) * 4, w_at = (kM + c0 / 64) * 4;
+      const int odd = c0 % 64;   // where they start in their 64
+      const int row0 = t.t0 + side * (half ? kM / 2 : kM) + r0;
       const bool busy = row0 < t.t1;
       float acc[C::ACC];
 #pragma unroll
@@ -710,7 +729,7 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int 
       for (int k = s0; k < s1; ++k) {
         if (!(ok = wait(dfull + 8 * d.stage, d.parity))) break;
         tc_fence_after();
-        const uint32_t from = lanes + d.stage * acc_cols, free = dempty + 8 * d.stage;
+        const uint32_t from = lanes + h * mine + d.stage * acc_cols, free = dempty + 8 * d.stage;
         const uint32_t at = scales + slot * (C::kScale * 4);
         auto release = [&]() {   // all of it is in registers
           tc_fence_before();
@@ -734,7 +753,10 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int 
         } else if (FULL) {
           const float f = lds4(at + row_at) * lds4(at + w_at);
 #pragma unroll
-          for (int c = 0; c < C::ACC; c += 32) add(c, f, c + 32 == C::ACC);
+          for (int c = 0; c < C::ACC; c += 32) {
+            if (HALF && c == C::ACC / 2 && half) break;
+            add(c, f, c + 32 == (HALF ? mine : C::ACC));
+          }
         } else {
           const float xs = lds4(at + row_at);
 #pragma unroll
@@ -748,7 +770,7 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int 
       }
       if (!ok) break;
       if (!busy) continue;
-      const int n0 = t.n0 + h * mine;
+      const int n0 = t.n0 + c0;
       if (split > 1) {
         // every stage of the ring has been read: its space takes the sums
         float* sums = reinterpret_cast<float*>(smem) + (q * 32 + lane) * (nw + C::kSumPad) + h * mine;
@@ -831,7 +853,7 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int 
     // the parts of one tile: each CTA adds and stores its share of the rows
     cluster_sync();
     if (!*abort && tile0 < tiles) {
-      const Tile t = order.at(tile0);
+      const Tile t = order.template at<HALF>(tile0);
       const int t0 = t.t0 + side * kM, rows = min(kM, t.t1 - t0), cols = min(nw, p.N - t.n0);
       const int r0 = rows > 0 ? rows * part / split : 0, r1 = rows > 0 ? rows * (part + 1) / split : 0;
       // four channels of a row to a thread, U such at a time with all of their reads on the way
@@ -916,15 +938,23 @@ cudaError_t prepare(OnDevice* all, K* kernel, OnDevice** out) {
   return cudaSuccess;
 }
 
+// Of a pair's row tiles, those of at most half of its rows: of rows in groups every other
+// group's last one.
+double halves(const F8Args& p) {
+  const int less = p.T % (2 * kM);
+  return p.offsets ? p.E / 2. : less > 0 && less <= kM;
+}
+
 // CTAs to a tile, its channels and parts of K: what takes the least by this model.  A block
 // takes 2.2 ns for each channel and 64 more (a pair of CTAs 1.9, for twice the rows), and
 // 350 (400) at least.  Pairs, us, against CTAs alone: 2048 x 28672 x 4096 194 and 225, 512 x
-// 28672 x 4096 55 and 62, 201 x 2891 x 1411 11.7 and 9.8; 4096 rows by 8 experts of 28672 x
-// 4096 506 and 525, of 4096 x 14336 349 and 248 (five turns of 76 pairs, or four of 152 CTAs).
-// Channels: 64 x 28672 x 4096 25.9 with 192, 26.7 with 256, two turns, 35.6 with 128.  K is
-// split (in 2 or 4) where all parts run at once and have two blocks or more; to join them
-// takes 2.5 us, and more with their sums: 64 x 4096 x 4096 12.3 in 4 parts of 128 channels,
-// 17.0 whole with 64; 201 x 2891 x 1411 11.4 in 2 of 128, 9.8 whole with 64.
+// 28672 x 4096 54 and 62, 201 x 2891 x 1411 11.7 and 9.8; 4096 rows by 8 experts of 28672 x
+// 4096 495 and 525, of 4096 x 14336 349 and 248 (five turns of 76 pairs, or four of 152 CTAs);
+// 4096 rows by 60 of 2048 x 1408 49 and 44.  Channels: 64 x 28672 x 4096 25.9 with 192, 26.7
+// with 256, two turns, 35.6 with 128.  K is split (in 2 or 4) where all parts run at once and
+// have two blocks or more; to join them takes 2.5 us, and more with their sums: 64 x 4096 x
+// 4096 12.3 in 4 parts of 128 channels, 17.0 whole with 64; 201 x 2891 x 1411 11.4 in 2 of
+// 128, 9.8 whole with 64.
 template <typename K>
 Plan plan_of(const F8Args& p, K&& clusters) {
   const int blocks = (p.K + kB - 1) / kB;
@@ -936,12 +966,15 @@ Plan plan_of(const F8Args& p, K&& clusters) {
     const int most = p.offsets && p.T / p.E < 16 ? 32 : kM;
     const int rows = p.T > 64 ? most : p.T > 32 ? std::min(most, 64) : p.T > 16 ? 32 : 16;
     if (ctas == 2 && (rows < kM || p.T <= kM)) break;
-    // row tiles: of rows in groups about half a tile more for each
+    // row tiles: of rows in groups about half a tile more for each (and of a pair's, which
+    // more seldom has several, one at least)
     const int M = rows * ctas;
-    const int64_t ntt = p.offsets ? std::max<int64_t>(1, std::min<int64_t>(p.T, p.T / M + (p.E + 1) / 2)) : (p.T + M - 1) / M;
+    const int64_t more = std::max<int64_t>(p.T / M + (p.E + 1) / 2, ctas == 2 ? p.E : 1);
+    const int64_t ntt = p.offsets ? std::min<int64_t>(p.T, more) : (p.T + M - 1) / M;
     for (int nw = Tc::NT; nw >= 64; nw -= 64) {
       const int64_t tiles = ntt * ((p.N + nw - 1) / nw);
-      const double turns = static_cast<double>((tiles + units - 1) / units);
+      double turns = static_cast<double>((tiles + units - 1) / units);
+      if (ctas == 2 && nw == Tc::NT) turns *= 1. - 0.15 * halves(p) / ntt;
       for (int split = 1; split <= 4; split *= 2) {
         if (split > 1 && (p.offsets || blocks < 2 * split || tiles > clusters(ctas, split * ctas))) break;
         const double join = split > 1 ? 2500. + 0.085 * std::min(p.T, kM) * nw : 0.;
@@ -958,7 +991,7 @@ Plan plan_of(const F8Args& p, K&& clusters) {
   return best;
 }
 
-template <typename O, int CTAS, bool FULL>
+template <typename O, int CTAS, bool FULL, bool HALF>
 cudaError_t launch_plan(const F8Args& p, const Plan& plan, cudaStream_t s) {
   Maps maps{};
   // stores by TMA, and of 16 bytes
@@ -977,21 +1010,23 @@ cudaError_t launch_plan(const F8Args& p, const Plan& plan, cudaStream_t s) {
   const int64_t ntt = (p.T + M - 1) / M, ntn = (p.N + plan.nw - 1) / plan.nw;
   const int64_t tiles = ntn * (p.offsets ? std::min<int64_t>(p.T, ntt + p.E) : ntt);
   const int64_t grid = plan.split > 1 ? tiles * plan.split : std::min<int64_t>(tiles, sm_count() / CTAS);
-  return launch_close(k_tc_f8<O, CTAS, FULL>, dim3(static_cast<unsigned>(grid * CTAS)), Tc::kThreads, Tc::kSmem,
+  return launch_close(k_tc_f8<O, CTAS, FULL, HALF>, dim3(static_cast<unsigned>(grid * CTAS)), Tc::kThreads, Tc::kSmem,
                       CTAS * plan.split, s, p, maps, plan, static_cast<int>(bulk));
 }
 
 template <typename O>
 cudaError_t launch_tc(const F8Args& p, cudaStream_t s) {
-  static OnDevice all[3][kMaxDev];
-  OnDevice *one, *two, *full;
-  cudaError_t e = prepare(all[0], k_tc_f8<O, 1, false>, &one);
-  if (e == cudaSuccess) e = prepare(all[1], k_tc_f8<O, 2, false>, &two);
-  if (e == cudaSuccess) e = prepare(all[2], k_tc_f8<O, 2, true>, &full);
+  static OnDevice all[4][kMaxDev];
+  OnDevice *one, *two, *full, *half;
+  cudaError_t e = prepare(all[0], k_tc_f8<O, 1, false, false>, &one);
+  if (e == cudaSuccess) e = prepare(all[1], k_tc_f8<O, 2, false, false>, &two);
+  if (e == cudaSuccess) e = prepare(all[2], k_tc_f8<O, 2, true, false>, &full);
+  if (e == cudaSuccess) e = prepare(all[3], k_tc_f8<O, 2, true, true>, &half);
   if (e != cudaSuccess) return e;
   const Plan plan = plan_of(p, [&](int ctas, int size) { return (ctas == 1 ? one : two)->clusters[size == 2 ? 1 : size == 4 ? 2 : 3]; });
-  if (plan.ctas == 1) return launch_plan<O, 1, false>(p, plan, s);
-  return plan.nw == Tc::NT && plan.split == 1 ? launch_plan<O, 2, true>(p, plan, s) : launch_plan<O, 2, false>(p, plan, s);
+  if (plan.ctas == 1) return launch_plan<O, 1, false, false>(p, plan, s);
+  if (plan.nw < Tc::NT || plan.split > 1) return launch_plan<O, 2, false, false>(p, plan, s);
+  return halves(p) > 0. ? launch_plan<O, 2, true, true>(p, plan, s) : launch_plan<O, 2, true, false>(p, plan, s);
 }
 
 template <typename O>
