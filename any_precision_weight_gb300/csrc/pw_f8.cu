@@ -239,20 +239,38 @@ __global__ void __launch_bounds__(kFewWarps * 32, kFewCtas) k_few_f8(const F8Arg
   }
 }
 
-template <typename O, int NT>
-cudaError_t launch_few(const F8Args& p, int turns, cudaStream_t s) {
+// The launch: blocks of 8 rows as long as about one wave of CTAs holds them, then of 16, which
+// read the weights half as often (64 x 1024 x 4096 7.4 and 6.2 us, 256 x 60 x 4096 3.9 and
+// 4.5); `turns` and kw as in the kernel; what it takes, about, in ns: each wave of CTAs 2000,
+// half more where a row ends inside 16 bytes, and 500 for a block of K, 1.4 times that for 16
+// rows; groups of several rows differ, and the largest takes more than one.
+struct Few {
+  int nt, turns, kw;
+  double cost;
+};
+Few few_of(const F8Args& p) {
+  Few f{};
   const int groups = (p.N + 15) / 16, blocks = (p.K + kB - 1) / kB, slots = sm_count() * kFewCtas;
-  const int64_t rows = static_cast<int64_t>(p.E) * turns;
-  int kw = 1;
+  const int64_t rows = p.offsets ? (p.T + p.E - 1) / p.E : p.T;   // of a group, about
+  f.nt = rows <= 8 || groups * ((rows + 7) / 8) <= slots ? 1 : 2;
+  const int M = f.nt * 8;
+  f.turns = static_cast<int>(std::min<int64_t>((rows + M - 1) / M, 65535 / p.E));
   float least = 0.f;
   for (int n = 1, i = 0; n <= kFewWarps && (n == 1 || blocks >= n); n *= 2, ++i) {
-    const float waves = static_cast<float>(groups) * rows * n / (kFewWarps * slots);
+    const float waves = static_cast<float>(groups) * p.E * f.turns * n / (kFewWarps * slots);
     const float cost = std::ceil(waves) / waves * (1.f + 0.06f * i);
-    if (n == 1 || cost < least) kw = n, least = cost;
+    if (n == 1 || cost < least) f.kw = n, least = cost;
   }
-  const int per = kFewWarps / kw;
-  return launch_close(k_few_f8<O, NT>, dim3((groups + per - 1) / per, static_cast<unsigned>(rows)), kFewWarps * 32, 0, 1, s, p,
-                      kw, turns);
+  const double in = p.offsets ? std::max<double>(std::min(p.E, p.T), p.T / M + p.E / 2) : (p.T + M - 1) / M;
+  const double waves = std::max((groups * f.kw + kFewWarps - 1) / kFewWarps * in / slots, p.T > p.E && p.offsets ? 1.75 : 1.);
+  f.cost = 1000 + waves * (f.nt == 2 ? 1.4 : 1.) * (2000 * (p.K % 16 ? 1.5 : 1.) + 500 * ((blocks + f.kw - 1) / f.kw));
+  return f;
+}
+template <typename O, int NT>
+cudaError_t launch_few(const F8Args& p, const Few& f, cudaStream_t s) {
+  const int groups = (p.N + 15) / 16, per = kFewWarps / f.kw;
+  return launch_close(k_few_f8<O, NT>, dim3((groups + per - 1) / per, static_cast<unsigned>(p.E * f.turns)), kFewWarps * 32, 0,
+                      1, s, p, f.kw, f.turns);
 }
 
 // ---------------------------------------------------------------- tensor cores
@@ -311,6 +329,7 @@ struct Tc {
 // rows and of the stage, stages, accumulators.
 struct Plan {
   int ctas, rows, nw, split, x_bytes, stage, stages, accs;
+  float cost;   // ns of the tiles, about
 };
 
 // Registers by role: 384 threads are launched with kRegsLaunch each, and the
@@ -955,8 +974,8 @@ double halves(const F8Args& p) {
 // have two blocks or more; to join them takes 2.5 us, and more with their sums: 64 x 4096 x
 // 4096 12.3 in 4 parts of 128 channels, 17.0 whole with 64; 201 x 2891 x 1411 11.4 in 2 of
 // 128, 9.8 whole with 64.
-template <typename K>
-Plan plan_of(const F8Args& p, K&& clusters) {
+Plan plan_of(const F8Args& p, const OnDevice* one, const OnDevice* two) {
+  const auto clusters = [&](int ctas, int size) { return (ctas == 1 ? one : two)->clusters[size == 2 ? 1 : size == 4 ? 2 : 3]; };
   const int blocks = (p.K + kB - 1) / kB;
   Plan best{};
   double least = 0;
@@ -980,7 +999,7 @@ Plan plan_of(const F8Args& p, K&& clusters) {
         const double join = split > 1 ? 2500. + 0.085 * std::min(p.T, kM) * nw : 0.;
         const double block = ctas == 1 ? std::max(350., 2.2 * (nw + 64)) : std::max(400., 1.9 * (nw + 64));
         const double cost = turns * blocks / split * block + join;
-        if (best.ctas == 0 || cost < least) best = {ctas, rows, nw, split, 0, 0, 0, 0}, least = cost;
+        if (best.ctas == 0 || cost < least) best = {ctas, rows, nw, split, 0, 0, 0, 0, static_cast<float>(cost)}, least = cost;
       }
     }
   }
@@ -1015,7 +1034,7 @@ cudaError_t launch_plan(const F8Args& p, const Plan& plan, cudaStream_t s) {
 }
 
 template <typename O>
-cudaError_t launch_tc(const F8Args& p, cudaStream_t s) {
+cudaError_t launch_f8(const F8Args& p, cudaStream_t s) {
   static OnDevice all[4][kMaxDev];
   OnDevice *one, *two, *full, *half;
   cudaError_t e = prepare(all[0], k_tc_f8<O, 1, false, false>, &one);
@@ -1023,31 +1042,25 @@ cudaError_t launch_tc(const F8Args& p, cudaStream_t s) {
   if (e == cudaSuccess) e = prepare(all[2], k_tc_f8<O, 2, true, false>, &full);
   if (e == cudaSuccess) e = prepare(all[3], k_tc_f8<O, 2, true, true>, &half);
   if (e != cudaSuccess) return e;
-  const Plan plan = plan_of(p, [&](int ctas, int size) { return (ctas == 1 ? one : two)->clusters[size == 2 ? 1 : size == 4 ? 2 : 3]; });
+  // Few rows, where memory bounds both, us against k_tc_f8: 8 x 28672 x 4096 24.3 and 25.7, 16 x
+  // 4096 x 14336 16.2 and 19.1, 16 x 28672 x 4096 28.8 and 26.0.  Rows in groups, about two to each
+  // or less: 8 rows by 8 experts of 28672 x 4096 75 and 80, 16 rows by 60 of 2816 x 2048 17 and
+  // 27, 64 rows 37 and 41; 32 rows by 8 131 and 119, 256 rows by 60 of 2048 x 1408 42 and 34.
+  const int64_t least = p.offsets ? 2 * static_cast<int64_t>(p.E) : 8;
+  const double work = static_cast<double>(p.T) * p.N * p.K;
+  const bool little = work <= (p.T <= 16 && !p.offsets ? 1e9 : 7e8);
+  if (p.T <= least || little) {
+    // Little to do: what takes less (k_tc_f8 5 us beside its tiles).  64 x 60 x 4096 3.9 and 9.6, 32
+    // x 1024 x 4096 4.8 and 9.1, 128 x 2048 x 2048 9.8 and 10.1; 67 x 8384 x 890 21.7 and 7.8, 1990
+    // x 576 x 512 18.0 and 6.7, 1833 rows by 26 of 192 x 1408 20.5 and 9.9.
+    const Few few = few_of(p);
+    if (p.T <= least || few.cost < 5000 + plan_of(p, one, two).cost)
+      return few.nt == 1 ? launch_few<O, 1>(p, few, s) : launch_few<O, 2>(p, few, s);
+  }
+  const Plan plan = plan_of(p, one, two);
   if (plan.ctas == 1) return launch_plan<O, 1, false, false>(p, plan, s);
   if (plan.nw < Tc::NT || plan.split > 1) return launch_plan<O, 2, false, false>(p, plan, s);
   return halves(p) > 0. ? launch_plan<O, 2, true, true>(p, plan, s) : launch_plan<O, 2, true, false>(p, plan, s);
-}
-
-template <typename O>
-cudaError_t launch_f8(const F8Args& p, cudaStream_t s) {
-  // Few rows, or little to do: k_few_f8, us against k_tc_f8: 8 x 28672 x 4096 24.3 and 25.7,
-  // 64 x 60 x 4096 3.9 and 9.6, 32 x 1024 x 4096 4.8 and 9.1, 128 x 2048 x 2048 9.8 and 10.1,
-  // 64 x 4096 x 4096 16.5 and 13.2; 16 x 4096 x 14336 16.2 and 19.1, 16 x 28672 x 4096 28.8 and
-  // 26.0.  Rows in groups, about two to each or less: 8 rows by 8 experts of 28672 x 4096
-  // 75 and 80, 16 rows by 60 of 2816 x 2048 17 and 27, 64 rows 37 and 41; 32 rows by 8 131 and
-  // 119, 256 rows by 60 of 2048 x 1408 42 and 34.
-  const int64_t rows = p.offsets ? (p.T + p.E - 1) / p.E : p.T;   // of a group, about
-  const double work = static_cast<double>(p.T) * p.N * p.K;
-  const bool few = p.offsets ? p.T <= 2 * static_cast<int64_t>(p.E) || work <= 7e8
-                             : p.T <= 8 || work <= (p.T <= 16 ? 1e9 : 7e8);
-  if (!few) return launch_tc<O>(p, s);
-  // in blocks of 8 rows as long as about one wave of CTAs holds them, then of 16, which read
-  // the weights half as often: 64 x 1024 x 4096 7.4 and 6.2, 256 x 60 x 4096 3.9 and 4.5
-  const int64_t blocks = (static_cast<int64_t>(p.N) + 15) / 16 * ((rows + 7) / 8);
-  const int nt = rows <= 8 || blocks <= sm_count() * 2 ? 1 : 2;
-  const int turns = static_cast<int>(std::min<int64_t>((rows + nt * 8 - 1) / (nt * 8), 65535 / p.E));
-  return nt == 1 ? launch_few<O, 1>(p, turns, s) : launch_few<O, 2>(p, turns, s);
 }
 
 int linear_f8(const char* what, F8Args p, int out_dtype, pw_stream_t s) {
