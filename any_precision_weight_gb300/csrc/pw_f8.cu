@@ -836,9 +836,16 @@ k_tc_f8(const F8Args p, const __grid_constant__ Maps maps, const Plan plan, int 
           __syncwarp();
           const int n = n0 + c + lane, r1 = n < p.N ? min(32, t.t1 - row0) : 0;
           O* out = static_cast<O*>(p.out) + row0 * p.ldo + n;
-#pragma unroll 8
-          for (int r = 0; r < r1; ++r, out += p.ldo)
-            *out = reinterpret_cast<const O*>(stage + place(r, lane / V))[lane % V];
+          constexpr int U = 16;   // rows read before any is written (one by one: 3171 x 27509 x 1851 216 us, so 194)
+#pragma unroll 1
+          for (int r = 0; r < r1; r += U) {
+            O v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) v[u] = reinterpret_cast<const O*>(stage + place(r + u, lane / V))[lane % V];
+#pragma unroll
+            for (int u = 0; u < U; ++u, out += p.ldo)
+              if (r + u < r1) *out = v[u];
+          }
         } else {
           __syncwarp();
           const int n = n0 + c + lane % P * V;

@@ -169,7 +169,7 @@ __device__ __forceinline__ float largest(const float (&v)[N], float m = 0.f) {
 // A warp takes four blocks of a row, eight lanes to a block (16 lanes took a seventh longer: each
 // lane works out the block's factor), and fetches its next row while it quantises this one;
 // blockIdx.y takes the rest of a row.  28672 x 4096 fp16: 59.5 us, 5.9 TB/s, 87 % of the copy
-// rate; silu 4096 x 14336 fp16: 53 us, 81 %, bound by the issue slots and HBM alike.
+// rate; silu 4096 x 14336 fp16: 51.5 us, 84 %, bound by the issue slots and HBM alike.
 template <typename T, bool ACT, Lie LIE>
 __global__ void __launch_bounds__(256, LIE != kWhole ? 2 : ACT ? 3 : 4) k_quant(const QuantArgs p) {
   constexpr int N = 16, kStep = 4 * kBlock;
@@ -226,8 +226,7 @@ __global__ void __launch_bounds__(256, LIE != kWhole ? 2 : ACT ? 3 : 4) k_quant(
 
 // A CTA to a block of 128 rows x 128 columns, held as it was loaded (as fp32 it would take
 // twice the registers, and half of the loads would be in flight).  28672 x 4096 bf16:
-// 66.6 us, 5.3
-// TB/s, 78 % of the copy rate.
+// 66.5 us, 5.3 TB/s, 78 % of the copy rate.
 template <typename T, Lie LIE>
 __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : LIE == kWhole ? 3 : 2) k_quant_blocks(const QuantArgs p) {
   __shared__ float s_max[8];
@@ -359,10 +358,10 @@ __device__ __forceinline__ void put_cols(T* row, int h, int H, const float (&v)[
 }
 
 // A CTA takes 8 columns a thread of N tokens, blockIdx.y the rest of them.  The rows of J
-// slots of each are on their way together (two of two tokens, or four).  Places outside [0, R) and weights of 0 add nothing,
-// and nothing is read for them.  The sum goes in the order of the slots.  8192 x 4096 fp16,
-// two slots, residual: 51.5 us, 5.2 TB/s, 77 % of the copy rate (CTAs that
-// stay, three to an SM; 65 with one to a token).
+// slots of each are on their way together (two of two tokens, or four).  Places outside [0, R)
+// and weights of 0 add nothing, and nothing is read for them.  The sum goes in the order of
+// the slots.  8192 x 4096 fp16, two slots, residual: 50.6 us, 5.3 TB/s, 78 % of the copy rate
+// (CTAs that stay, three to an SM; 65 with one to a token).
 template <typename Y, typename O, bool WIDE, int N, int J>
 __global__ void __launch_bounds__(256, WIDE ? 3 : 2) k_combine_rows(const CombineArgs p) {
   after_those_before();
