@@ -302,6 +302,44 @@ def test_rows_with_no_numbers_stay_alone():
         assert torch.equal(got[keep], want[keep])
 
 
+@pytest.mark.parametrize("K", [1, 15, 17, 129, 201, 206, 255, 1411])
+def test_bytes_behind_rows(K):
+    """NaN in them change nothing: few rows, single CTAs and pairs, rows in groups."""
+    for T, N in ((3, 300), (16, 70), (40, 3000), (129, 9728), (300, 9728)):
+        rng = gen(T, K, "behind")
+        x, w = values(rng, T, K), values(rng, N, K)
+        xs, ws = scales(rng, T, f8.blocks(K)), scales(rng, f8.blocks(N), f8.blocks(K))
+        off = cuda(np.array([0, T // 3, T]), torch.int32)
+        g = lambda: pw.pw_grouped_linear_f8(x, xs, w[None].expand(2, N, K), ws[None].expand(2, -1, -1), off,
+                                            out_dtype=torch.float32)
+        outs = []
+        for byte in (0, 0x7F):
+            for q in (x, w):
+                ld = q.stride(0)
+                torch.as_strided(q.view(torch.uint8), (q.shape[0], ld - K), (ld, 1), K).fill_(byte)
+            outs.append((pw.pw_linear_f8(x, xs, w, ws, out_dtype=torch.float32), g()))
+        for a, b in zip(*outs):
+            assert torch.isfinite(a).all() and torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,K", [(1, 1), (5, 129), (33, 100), (300, 1408), (7, 14336)])
+def test_silu_and_gathered_rows_in_frames(T, K):
+    for dt in DT:
+        rng = gen(T, K, dt, "frames")
+        x = torch.zeros(T + 2, 2 * K + 3, dtype=DT[dt], device="cuda")[1:T + 1, 1:1 + 2 * K]
+        x.copy_(cuda(rng.normal(0, 2, (T, 2 * K)), DT[dt]))
+        for pad, off in ((0, 0), ((-K) % 16 + 16, 0), (5, 1)):
+            fq, fs = Framed(T, K, torch.uint8, pad=pad, off=off), Framed(T, f8.blocks(K), torch.float32, pad=pad)
+            pw.pw_silu_quant_f8(x, q=fq.view.view(F8), scale=fs.view)
+            check_silu(fq.view.view(F8), fs.view, x)
+            assert fq.intact() and fs.intact()
+            rows = cuda(rng.integers(0, 2 * T, T), torch.int32)
+            fq, fs = Framed(T, K, torch.uint8, pad=pad, off=off), Framed(T, f8.blocks(K), torch.float32, pad=pad)
+            pw.pw_quant_f8(x[:, :K], rows=rows, per=2, q=fq.view.view(F8), scale=fs.view)
+            check_q(fq.view.view(F8), fs.view, f64(x)[rows.cpu().numpy() // 2, :K], dt)
+            assert fq.intact() and fs.intact()
+
+
 def test_one_group_is_the_plain_product():
     for T in (5, 70, 500):
         rng = gen(T, "one")
