@@ -255,10 +255,22 @@ Few few_of(const F8Args& p) {
   f.nt = rows <= 8 || groups * ((rows + 7) / 8) <= slots ? 1 : 2;
   const int M = f.nt * 8;
   f.turns = static_cast<int>(std::min<int64_t>((rows + M - 1) / M, 65535 / p.E));
-  float least = 0.f;
+  double least = 0.;
   for (int n = 1, i = 0; n <= kFewWarps && (n == 1 || blocks >= n); n *= 2, ++i) {
-    const float waves = static_cast<float>(groups) * p.E * f.turns * n / (kFewWarps * slots);
-    const float cost = std::ceil(waves) / waves * (1.f + 0.06f * i);
+    double cost;
+    if (p.offsets) {
+      // some experts have no rows: their CTAs end at once, and the others may be less than a
+      // wave, or end with half of one.  2 rows by 8 experts of 4096 x 14336 with kw 1, 2, 4, 8:
+      // 40.4, 24.7, 16.5, 14.4 us; of 28672 x 4096 24.9, 26.9, 33.2, 46.5; 16 rows by 60 of 2048 x
+      // 1408 11.7, 13.1, 16.7, 24.1; 64 by 128 of 1024 x 4096 40.4, 35.0, 37.0, 47.6
+      const double wave = static_cast<double>((groups * n + kFewWarps - 1) / kFewWarps) / slots;
+      const double in = p.T <= p.E ? 0.6 * p.T : std::min<double>(p.E, 0.6 * p.E + 0.1 * p.T);
+      const double busy = wave * in, idle = std::max(0., wave * p.E * f.turns - busy);
+      cost = (busy > 1 ? busy + 0.5 : 1.) * (1000 + 400 * ((blocks + n - 1) / n)) + 650 * idle;
+    } else {   // how full the waves are, and what the sums over the warps add
+      const double waves = static_cast<double>(groups) * f.turns * n / (kFewWarps * slots);
+      cost = std::ceil(waves) / waves * (1. + 0.06 * i);
+    }
     if (n == 1 || cost < least) f.kw = n, least = cost;
   }
   const double in = p.offsets ? std::max<double>(std::min(p.E, p.T), p.T / M + p.E / 2) : (p.T + M - 1) / M;
