@@ -1061,10 +1061,10 @@ cudaError_t launch_f8(const F8Args& p, cudaStream_t s) {
   if (e == cudaSuccess) e = prepare(all[2], k_tc_f8<O, 2, true, false>, &full);
   if (e == cudaSuccess) e = prepare(all[3], k_tc_f8<O, 2, true, true>, &half);
   if (e != cudaSuccess) return e;
-  // Few rows, where memory bounds both, us against k_tc_f8: 8 x 28672 x 4096 24.3 and 25.7, 16 x
-  // 4096 x 14336 16.2 and 19.1, 16 x 28672 x 4096 28.8 and 26.0.  Rows in groups, about two to each
-  // or less: 8 rows by 8 experts of 28672 x 4096 75 and 80, 16 rows by 60 of 2816 x 2048 17 and
-  // 27, 64 rows 37 and 41; 32 rows by 8 131 and 119, 256 rows by 60 of 2048 x 1408 42 and 34.
+  // Few rows, where memory bounds both, us against k_tc_f8: 8 x 28672 x 4096 24.9 and 25.7, 16 x
+  // 4096 x 14336 15.8 and 19.1, 16 x 28672 x 4096 28.8 and 25.5.  Rows in groups, about two to each
+  // or less: 16 rows by 8 experts of 28672 x 4096 76 and 80, of 4096 x 14336 43 and 55, 120 rows by
+  // 60 of 2048 x 1408 27.8 and 31.4; 32 rows by 8 136 and 120, 256 rows by 60 39.8 and 34.3.
   const int64_t least = p.offsets ? 2 * static_cast<int64_t>(p.E) : 8;
   const double work = static_cast<double>(p.T) * p.N * p.K;
   const bool little = work <= (p.T <= 16 && !p.offsets ? 1e9 : 7e8);
