@@ -10,8 +10,8 @@
 // Above, a second launch has CTAs for one, two or four experts each: a CTA reads the experts
 // of all pairs twice, first counting those before its own experts and its own, then placing
 // its own in their order.  So no CTA needs another's results, and there is no workspace; 8192
-// x 60, 4 each, reads 8 MB from the L2 for it.  4 x 60, 4 each, 3.8 us, 256 x 60 4.5, 2048 x 60
-// 6.2, 8192 x 60 11: launches, latencies and, in the largest, the issue slots of the choice.
+// x 60, 4 each, reads 8 MB from the L2 for it.  4 x 60, 4 each, 3.5 us, 256 x 60 3.8, 2048 x 60
+// 5.6, 8192 x 60 10 to 11: launches, latencies and, in the largest, the issue slots of the choice.
 
 #include <algorithm>
 #include <cmath>
