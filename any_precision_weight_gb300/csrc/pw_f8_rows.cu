@@ -327,13 +327,18 @@ struct CombineArgs {
   int T, H, k;
 };
 
-// Eight columns of a row, as they were loaded: those past H are 0.
-template <typename T, bool WIDE>
+// Eight columns of a row, as they were loaded: those past H are 0.  OUT: of a row that may be
+// the output itself, so by ordinary loads; the read-only path wants memory that the kernel
+// does not write.
+template <typename T, bool WIDE, bool OUT>
 __device__ __forceinline__ void load_cols(const T* row, int h, int H, T (&v)[8]) {
   if (WIDE && h + 8 <= H) {
     constexpr int E = 16 / sizeof(T);
 #pragma unroll
-    for (int i = 0; i < 8; i += E) *reinterpret_cast<uint4*>(v + i) = __ldg(reinterpret_cast<const uint4*>(row + h + i));
+    for (int i = 0; i < 8; i += E) {
+      const uint4* from = reinterpret_cast<const uint4*>(row + h + i);
+      *reinterpret_cast<uint4*>(v + i) = OUT ? *from : __ldg(from);
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = h + i < H ? row[h + i] : from_f32<T>(0.f);
@@ -389,7 +394,7 @@ __global__ void __launch_bounds__(256, WIDE ? 3 : 2) k_combine_rows(const Combin
       if (p.res) {
 #pragma unroll
         for (int n = 0; n < N; ++n)
-          if (t0 + n < p.T) load_cols<O, WIDE>(static_cast<const O*>(p.res) + (t0 + n) * p.ldr, h, p.H, r[n]);
+          if (t0 + n < p.T) load_cols<O, WIDE, true>(static_cast<const O*>(p.res) + (t0 + n) * p.ldr, h, p.H, r[n]);
       }
       for (int j0 = 0; j0 < p.k; j0 += J) {
         if (j0) slots(t0, j0);
@@ -402,7 +407,7 @@ __global__ void __launch_bounds__(256, WIDE ? 3 : 2) k_combine_rows(const Combin
           for (int j = 0; j < J; ++j) {
             at[n][j] = next_at[n][j] >= p.R || next_w[n][j] == 0.f ? -1 : next_at[n][j];
             w[n][j] = next_w[n][j];
-            if (at[n][j] >= 0) load_cols<Y, WIDE>(static_cast<const Y*>(p.y) + at[n][j] * p.ldy, h, p.H, v[n][j]);
+            if (at[n][j] >= 0) load_cols<Y, WIDE, false>(static_cast<const Y*>(p.y) + at[n][j] * p.ldy, h, p.H, v[n][j]);
           }
         if (j0 + J >= p.k) slots(t0 + gridDim.x * N, 0);
 #pragma unroll
