@@ -149,10 +149,12 @@ __device__ __forceinline__ void store_part(uint8_t* row, int k0, int l, int K, f
   }
 }
 
-// silu(g) * u.  The exponential's argument is rounded once, so the result is off by
-// |g| (1 - sigmoid(g)) 2^-24 and a few 2^-24 more: nothing beside the 2^-4 of the quantiser,
-// and nine tenths of the time that expf takes.  The reciprocal is off by 2^-23 and takes a
-// seventh of a division's instructions.
+// silu(g) * u.  The exponential's argument is rounded, and so is the constant in it (by 0.23 of
+// a rounding), so the result is off by (4 + 1.23 |g|) (1 - sigmoid(g)) 2^-24 and 5 x 2^-24 more:
+// nothing beside the 2^-4 of the quantiser, and nine tenths of the time that expf takes.  The
+// reciprocal is off by 2^-23 and takes a seventh of a division's instructions.  Below -87.3 it
+// is one of fp32's subnormals (steps of 2^-149); below -88.7 the exponential is infinite, and
+// the result 0 (exactly it would be above -2^-121.5 |u|).
 __device__ __forceinline__ float silu_up(float g, float u) {
   float e, r;
   asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));   // -log2 e

@@ -704,7 +704,8 @@ int pw_route(const float* logits, int64_t ld, int T, int E, int k, int renorm, i
  * A block of zeros has scale 0 and q 0; one with a NaN or an infinity has that scale
  * and q 0.
  * pw_silu_quant_f8 -- the same of silu(gate) * up in fp32, x [T][2 K] with the gate
- * columns first: what lies between an expert's two products.
+ * columns first: what lies between an expert's two products.  A gate below -88.7,
+ * whose e^-gate leaves fp32's range, gives 0.
  * pw_quant_f8_blocks -- the same with one scale for each 128 rows x 128 columns:
  * weights, scale [ceil(N / 128)][ceil(K / 128)].
  * q [T][K] has any stride; pw_linear_f8 wants its rows on 16-byte boundaries.
