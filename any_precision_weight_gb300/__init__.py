@@ -107,6 +107,8 @@ _SIGS = {
                                   _i, _vp, _i64, _vp]),
     "pw_linear_f8_status": (_i, [_vp, _pi]),
     "pw_debug_linear_f8_timeout": (_i, [_vp]),
+    "pw_debug_linear_f8": (_i, [_i, _i, _i, _i, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _i, _i,
+                                _i, _i, _i, _vp, _i64, _vp]),
     "pw_combine": (_i, [_vp, _i64, _i64, _i, _vp, _vp, _vp, _i64, _i, _i, _i, _i, _vp, _i64, _vp]),
 }
 
@@ -952,6 +954,26 @@ def pw_linear_f8_status(stream=None) -> int:
 
 def pw_debug_linear_f8_timeout(stream=None):
     return _check(lib().pw_debug_linear_f8_timeout(_stream(stream)), "pw_debug_linear_f8_timeout")
+
+
+def pw_debug_linear_f8(way, x, x_scale, w, w_scale, offsets=None, bias=None, out=None, out_dtype=None, stream=None):
+    """Test hook: pw_grouped_linear_f8 (w [1][N][K] without offsets: pw_linear_f8) in a
+    given way, (CTAs, rows, channels, parts of K) as include/pw.h has them."""
+    torch = _torch()
+    T, K = _matrix(x, "x")
+    (E, N, _), (dev, raw) = w.shape, _place(torch, x, "x", stream)
+    out = _f8_out(torch, stream, "pw_debug_linear_f8", x, (T, N), out, out_dtype)
+    dt, f32, f8, kb = out.dtype, torch.float32, torch.float8_e4m3fn, f8_blocks(K)
+    ldw, gw = _stack(w, "w", f8, (E, N, K), dev)
+    ldws, gws = _stack(w_scale, "w_scale", f32, (E, f8_blocks(N), kb), dev)
+    _check(lib().pw_debug_linear_f8(*way, x.data_ptr(), _rows(x, "x", f8, (T, K), dev), x_scale.data_ptr(),
+                                    _rows(x_scale, "x_scale", f32, (T, kb), dev), w.data_ptr(), ldw, gw,
+                                    w_scale.data_ptr(), ldws, gws,
+                                    None if offsets is None else _vec(offsets, "offsets", torch.int32, E + 1, dev),
+                                    None if bias is None else _vec(bias.view(-1), "bias", dt, E * N, dev), T, E, N, K,
+                                    _code(dt), out.data_ptr(), _rows(out, "out", dt, (T, N), dev), raw),
+           "pw_debug_linear_f8")
+    return out
 
 
 def pw_combine(y, weight, inv, residual=None, out=None, out_dtype=None, stream=None):

@@ -983,6 +983,14 @@ double halves(const F8Args& p) {
   return p.offsets ? p.E / 2. : less > 0 && less <= kM;
 }
 
+// What follows from a plan's tile.
+void lay_out(Plan& p) {
+  p.x_bytes = p.rows * kB;
+  p.stage = p.x_bytes + p.nw / p.ctas * kB;
+  p.stages = std::min(Tc::S, Tc::kRing / p.stage);
+  p.accs = p.nw > 128 ? 2 : 4;
+}
+
 // CTAs to a tile, its channels and parts of K: what takes the least by this model.  A block
 // takes 2.2 ns for each channel and 64 more (a pair of CTAs 1.9, for twice the rows), and
 // 350 (400) at least.  Pairs, us, against CTAs alone: 2048 x 28672 x 4096 194 and 225, 512 x
@@ -1022,10 +1030,7 @@ Plan plan_of(const F8Args& p, const OnDevice* one, const OnDevice* two) {
       }
     }
   }
-  best.x_bytes = best.rows * kB;
-  best.stage = best.x_bytes + best.nw / best.ctas * kB;
-  best.stages = std::min(Tc::S, Tc::kRing / best.stage);
-  best.accs = best.nw > 128 ? 2 : 4;
+  lay_out(best);
   return best;
 }
 
@@ -1052,8 +1057,37 @@ cudaError_t launch_plan(const F8Args& p, const Plan& plan, cudaStream_t s) {
                       CTAS * plan.split, s, p, maps, plan, static_cast<int>(bulk));
 }
 
+// A given plan (pw_debug_linear_f8): ctas 1 or 2: k_tc_f8's tile and parts of K; 0: k_few_f8's
+// rows at a time, CTAs that share a group's rows (`channels`) and warps that share out K (`parts`).
+struct Given {
+  int ctas, rows, channels, parts;
+};
+// Whether the kernels take it: every plan that few_of and plan_of can make, for any size.
+bool given_ok(const Given& g, const F8Args& p) {
+  const int blocks = (p.K + kB - 1) / kB;
+  const bool power = g.parts == 1 || g.parts == 2 || g.parts == 4 || (g.ctas == 0 && g.parts == 8);
+  if (!power) return false;
+  if (g.ctas == 0)
+    return (g.rows == 8 || g.rows == 16) && g.channels >= 1 && g.channels <= 65535 / p.E && g.parts <= blocks;
+  if (g.ctas != 1 && g.ctas != 2) return false;
+  if (g.rows != kM && (g.ctas == 2 || (g.rows != 64 && g.rows != 32 && g.rows != 16))) return false;
+  if (g.channels < 64 || g.channels > Tc::NT || g.channels % 64) return false;
+  return g.parts == 1 || (!p.offsets && blocks >= 2 * g.parts);
+}
+
 template <typename O>
-cudaError_t launch_f8(const F8Args& p, cudaStream_t s) {
+cudaError_t launch_few(const F8Args& p, const Few& f, cudaStream_t s) {
+  return f.nt == 1 ? launch_few<O, 1>(p, f, s) : launch_few<O, 2>(p, f, s);
+}
+template <typename O>
+cudaError_t launch_tc(const F8Args& p, const Plan& plan, cudaStream_t s) {
+  if (plan.ctas == 1) return launch_plan<O, 1, false, false>(p, plan, s);
+  if (plan.nw < Tc::NT || plan.split > 1) return launch_plan<O, 2, false, false>(p, plan, s);
+  return halves(p) > 0. ? launch_plan<O, 2, true, true>(p, plan, s) : launch_plan<O, 2, true, false>(p, plan, s);
+}
+
+template <typename O>
+cudaError_t launch_f8(const F8Args& p, const Given* given, cudaStream_t s) {
   static OnDevice all[4][kMaxDev];
   OnDevice *one, *two, *full, *half;
   cudaError_t e = prepare(all[0], k_tc_f8<O, 1, false, false>, &one);
@@ -1061,6 +1095,12 @@ cudaError_t launch_f8(const F8Args& p, cudaStream_t s) {
   if (e == cudaSuccess) e = prepare(all[2], k_tc_f8<O, 2, true, false>, &full);
   if (e == cudaSuccess) e = prepare(all[3], k_tc_f8<O, 2, true, true>, &half);
   if (e != cudaSuccess) return e;
+  if (given) {
+    if (given->ctas == 0) return launch_few<O>(p, Few{given->rows / 8, given->channels, given->parts, 0.}, s);
+    Plan plan{given->ctas, given->rows, given->channels, given->parts, 0, 0, 0, 0, 0.f};
+    lay_out(plan);
+    return launch_tc<O>(p, plan, s);
+  }
   // Few rows, where memory bounds both, us against k_tc_f8: 8 x 28672 x 4096 24.9 and 25.7, 16 x
   // 4096 x 14336 15.8 and 19.1, 16 x 28672 x 4096 28.8 and 25.5.  Rows in groups, about two to each
   // or less: 16 rows by 8 experts of 28672 x 4096 76 and 80, of 4096 x 14336 43 and 55, 120 rows by
@@ -1073,16 +1113,12 @@ cudaError_t launch_f8(const F8Args& p, cudaStream_t s) {
     // x 1024 x 4096 4.8 and 9.1, 128 x 2048 x 2048 9.8 and 10.1; 67 x 8384 x 890 21.7 and 7.8, 1990
     // x 576 x 512 18.0 and 6.7, 1833 rows by 26 of 192 x 1408 20.5 and 9.9.
     const Few few = few_of(p);
-    if (p.T <= least || few.cost < 5000 + plan_of(p, one, two).cost)
-      return few.nt == 1 ? launch_few<O, 1>(p, few, s) : launch_few<O, 2>(p, few, s);
+    if (p.T <= least || few.cost < 5000 + plan_of(p, one, two).cost) return launch_few<O>(p, few, s);
   }
-  const Plan plan = plan_of(p, one, two);
-  if (plan.ctas == 1) return launch_plan<O, 1, false, false>(p, plan, s);
-  if (plan.nw < Tc::NT || plan.split > 1) return launch_plan<O, 2, false, false>(p, plan, s);
-  return halves(p) > 0. ? launch_plan<O, 2, true, true>(p, plan, s) : launch_plan<O, 2, true, false>(p, plan, s);
+  return launch_tc<O>(p, plan_of(p, one, two), s);
 }
 
-int linear_f8(const char* what, F8Args p, int out_dtype, pw_stream_t s) {
+int linear_f8(const char* what, F8Args p, int out_dtype, pw_stream_t s, const Given* given = nullptr) {
   if (p.E == 1) p.gw = p.gws = 0;   // no other group
   if (p.T < 0 || p.T > PW_MAX_VOCAB || p.N < 1 || p.N > PW_MAX_VOCAB || p.K < 1 || p.K > PW_MAX_VOCAB || p.E < 1 ||
       p.E > PW_MAX_GROUPS)
@@ -1102,10 +1138,13 @@ int linear_f8(const char* what, F8Args p, int out_dtype, pw_stream_t s) {
   const size_t es = dtype_bytes(out_dtype);
   if (!aligned(p.out, es) || !aligned(p.bias, es) || !aligned(p.xs, 4) || !aligned(p.ws, 4) || !aligned(p.offsets, 4))
     return failf(PW_EINVAL, "%s: misaligned pointer", what);
+  if (given && !given_ok(*given, p))
+    return failf(PW_EINVAL, "%s: no plan of %d CTAs, %d rows, %d channels and %d parts", what, given->ctas, given->rows,
+                 given->channels, given->parts);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(s);
-  const cudaError_t e = out_dtype == PW_F16    ? launch_f8<__half>(p, st)
-                        : out_dtype == PW_BF16 ? launch_f8<__nv_bfloat16>(p, st)
-                                               : launch_f8<float>(p, st);
+  const cudaError_t e = out_dtype == PW_F16    ? launch_f8<__half>(p, given, st)
+                        : out_dtype == PW_BF16 ? launch_f8<__nv_bfloat16>(p, given, st)
+                                               : launch_f8<float>(p, given, st);
   return launch_status(e, what);
 }
 
@@ -1155,6 +1194,19 @@ int pw_linear_f8_status(pw_stream_t s, int* status) {
   }
   *status = more ? PW_STATUS_TIMEOUT : 0;
   return PW_OK;
+}
+
+int pw_debug_linear_f8(int ctas, int rows, int channels, int parts, const uint8_t* x, int64_t ldx, const float* x_scale,
+                       int64_t ldxs, const uint8_t* w, int64_t ldw, int64_t group_w, const float* w_scale, int64_t ldws,
+                       int64_t group_ws, const int32_t* offsets, const void* bias, int T, int E, int N, int K, int out_dtype,
+                       void* out, int64_t ldo, pw_stream_t s) {
+  pw::NvtxCall nvtx_range("pw_debug_linear_f8");
+  if (!offsets && E != 1) return pw::failf(PW_EINVAL, "pw_debug_linear_f8: null offsets with E = %d", E);
+  const pw::Given given{ctas, rows, channels, parts};
+  return pw::linear_f8("pw_debug_linear_f8",
+                       pw::F8Args{x, w, x_scale, w_scale, bias, offsets, out, ldx, ldxs, ldw, ldws, ldo, group_w,
+                                  group_ws, T, N, K, E},
+                       out_dtype, s, &given);
 }
 
 int pw_debug_linear_f8_timeout(pw_stream_t s) {

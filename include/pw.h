@@ -770,6 +770,22 @@ int pw_linear_f8_status(pw_stream_t s, int* status);
 int pw_debug_linear_f8_timeout(pw_stream_t s);
 
 /*
+ * pw_debug_linear_f8 -- test hook: pw_grouped_linear_f8 (offsets NULL and E 1: pw_linear_f8)
+ * in a given way instead of the one that is chosen for its sizes, so that every one can be
+ * tested at any size.
+ *   ctas 1, 2  tiles of `rows` rows (128; of one CTA also 16, 32 or 64) by `channels` (64,
+ *              128, 192 or 256) to a CTA or a pair of them, K in `parts` (1; without
+ *              offsets 2 or 4, of two blocks of 128 columns or more each)
+ *   ctas 0     few rows: `rows` (8 or 16) at a time, a group's shared by `channels` CTAs (1 to
+ *              65535 / E), K by `parts` warps (1, 2, 4 or 8, no more than its blocks)
+ * Errors: as pw_linear_f8, and PW_EINVAL for any other way.
+ */
+int pw_debug_linear_f8(int ctas, int rows, int channels, int parts, const uint8_t* x, int64_t ldx, const float* x_scale,
+                       int64_t ldxs, const uint8_t* w, int64_t ldw, int64_t group_w, const float* w_scale, int64_t ldws,
+                       int64_t group_ws, const int32_t* offsets, const void* bias, int T, int E, int N, int K, int out_dtype,
+                       void* out, int64_t ldo, pw_stream_t s);
+
+/*
  * pw_combine -- the experts' weighted sum:
  *   out[t] = residual[t] + sum_j weight[t][j] * y[inv[t][j]],  rounded once
  *   y [y_rows][H] of dtype;  weight, inv [T][k] as pw_route writes them;  residual [T][H]
