@@ -673,6 +673,13 @@ int pw_logprobs(const void* logits, int64_t ld, int dtype, int T, int V, const v
  * largest is 448.  A row of K columns has ceil(K / 128) scales; a block at the end of
  * a row (or of the weights' rows) may be short.  A number stands for its e4m3 value
  * times its scale.
+ *
+ * A call's kernels may begin before the one ahead of them on `s` has ended, and wait for it
+ * before they touch memory.  Those of pw_quant_f8, pw_silu_quant_f8 and pw_route let the next
+ * kernel begin once everything ahead of them has ended: logits written before them are safe for
+ * a pw_moe_forward behind them, and what they write themselves is not for its logits.  The
+ * products, pw_quant_f8_blocks and pw_combine let the next begin when they end, and may
+ * write logits.
  */
 #define PW_MAX_GROUPS 512   /* most experts of pw_route and pw_grouped_linear_f8, most slots of pw_combine */
 
