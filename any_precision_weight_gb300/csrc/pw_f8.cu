@@ -241,9 +241,18 @@ __global__ void __launch_bounds__(kFewWarps * 32, kFewCtas) k_few_f8(const F8Arg
 
 // The launch: blocks of 8 rows as long as about one wave of CTAs holds them, then of 16, which
 // read the weights half as often (64 x 1024 x 4096 7.4 and 6.2 us, 256 x 60 x 4096 3.9 and
-// 4.5); `turns` and kw as in the kernel; what it takes, about, in ns: each wave of CTAs 2000,
-// half more where a row ends inside 16 bytes, and 500 for a block of K, 1.4 times that for 16
-// rows; groups of several rows differ, and the largest takes more than one.
+// 4.5); `turns`, from the average group's rows, and kw as in the kernel.  A larger group's rows go
+// through its `turns` CTAs one pass after another, and each pass reads the weights again: 256 rows by
+// 128 experts of 2048 x 1408 take 50 us in groups that differ as a router's do, 104 with half of
+// the rows in one group, 198 with all in one (k_tc_f8 60, 58 and 12; twice or four times the turns
+// cost the even ones a tenth).
+// `cost`, to compare with k_tc_f8, in ns: 1000, and for each wave of CTAs 2000 (half more where a
+// row ends inside 16 bytes) and 500 for a block of K, 1.4 times both for 16 rows at a time.
+// How many groups have rows is not known here.  kw takes 0.6 T up to T = E and 0.6 E + 0.1 T (at
+// most E) above; `cost` takes max(min(E, T), T / M + E / 2) passes, and with more rows than groups
+// 1.75 waves at least; plan_of takes T / M + E / 2 tiles.  256 rows by 60 groups: 60, 60 and 38,
+// where 49 have rows if the shares are uniform over the simplex.  Each was fitted where it is
+// used, over sizes drawn at random, and none is an estimate for the others.
 struct Few {
   int nt, turns, kw;
   double cost;
@@ -303,11 +312,11 @@ cudaError_t launch_few(const F8Args& p, const Few& f, cudaStream_t s) {
 //    and at the tile's end store.
 // Where there are few tiles a cluster splits K and adds the parts through distributed
 // shared memory, in the order of the parts.
-// 2048 x 28672 x 4096 takes 194 us, 2475 TFLOP/s.  A pair's MMAs of a block take 512 clocks, and
-// its accumulators' way from tensor memory through two warps of each scheduler (read, wait,
-// 256 x 128 multiply-adds of a CTA) some 1150, the tensor cores busy for half of them; the
-// board draws 1385 W, and has 1400.  To sum over K in tensor memory alone has no place for the
-// blocks' scales.  64 x 28672 x 4096 takes 25.9 us, 4.5 TB/s of weights; small products 9 us, of
+// 2048 x 28672 x 4096 takes 194 us, 2475 TFLOP/s (206 to 212 a call among others).  A pair's MMAs of
+// a block take 512 clocks, and its accumulators' way from tensor memory through two warps of each
+// scheduler (read, wait, 256 x 128 multiply-adds of a CTA) some 1150, the tensor cores busy for half
+// of them.  (The power cap, 1385 of 1400 W, takes 4 % of the clock.)  To sum over K in tensor memory
+// alone has no place for the blocks' scales.  64 x 28672 x 4096 takes 25.9 us, 4.5 TB/s of weights; small products 9 us, of
 // which 5 are the tensor memory, the barriers, the first tiles and the sums' way out.
 constexpr int kM = 128;          // rows of a CTA
 constexpr int kEpiWarp0 = 4;
@@ -1012,8 +1021,9 @@ Plan plan_of(const F8Args& p, const OnDevice* one, const OnDevice* two) {
     const int most = p.offsets && p.T / p.E < 16 ? 32 : kM;
     const int rows = p.T > 64 ? most : p.T > 32 ? std::min(most, 64) : p.T > 16 ? 32 : 16;
     if (ctas == 2 && (rows < kM || p.T <= kM)) break;
-    // row tiles: of rows in groups about half a tile more for each (and of a pair's, which
-    // more seldom has several, one at least)
+    // row tiles: of rows in groups about half a tile more for each, which holds where groups are
+    // longer than a tile and is low where they are shorter (and of a pair's, which more seldom has
+    // several, one at least)
     const int M = rows * ctas;
     const int64_t more = std::max<int64_t>(p.T / M + (p.E + 1) / 2, ctas == 2 ? p.E : 1);
     const int64_t ntt = p.offsets ? std::min<int64_t>(p.T, more) : (p.T + M - 1) / M;

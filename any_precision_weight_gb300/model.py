@@ -102,7 +102,9 @@ class F8Experts:
 
     gate_up [E][2 I][H] (gate rows, then up rows) and down [E][H][I]: e4m3 with their
     scales [E][blocks of rows][blocks of columns] float32 and rows on 16-byte
-    boundaries, or 16- or 32-bit weights, which are then quantised here.
+    boundaries, or 16- or 32-bit weights, which are then quantised here.  Scales of gate
+    and up that were made apart fit only where I is a multiple of 128: the blocks of 128
+    rows are counted through the joined rows.
     """
 
     def __init__(self, gate_up, down, gate_up_scale=None, down_scale=None):
