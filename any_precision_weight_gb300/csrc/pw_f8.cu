@@ -316,8 +316,9 @@ cudaError_t launch_few(const F8Args& p, const Few& f, cudaStream_t s) {
 // a block take 512 clocks, and its accumulators' way from tensor memory through two warps of each
 // scheduler (read, wait, 256 x 128 multiply-adds of a CTA) some 1150, the tensor cores busy for half
 // of them.  (The power cap, 1385 of 1400 W, takes 4 % of the clock.)  To sum over K in tensor memory
-// alone has no place for the blocks' scales.  64 x 28672 x 4096 takes 25.9 us, 4.5 TB/s of weights; small products 9 us, of
-// which 5 are the tensor memory, the barriers, the first tiles and the sums' way out.
+// alone has no place for the blocks' scales.  64 x 28672 x 4096 takes 25.9 us, 4.5 TB/s of weights;
+// small products 9 us, of which 5 are the tensor memory, the barriers, the first tiles and the sums'
+// way out.
 constexpr int kM = 128;          // rows of a CTA
 constexpr int kEpiWarp0 = 4;
 
@@ -1072,7 +1073,7 @@ cudaError_t launch_plan(const F8Args& p, const Plan& plan, cudaStream_t s) {
 struct Given {
   int ctas, rows, channels, parts;
 };
-// Whether the kernels take it: every plan that few_of and plan_of can make, for any size.
+// Whether the kernels take it: the plans that few_of and plan_of can make, for any size.
 bool given_ok(const Given& g, const F8Args& p) {
   const int blocks = (p.K + kB - 1) / kB;
   const bool power = g.parts == 1 || g.parts == 2 || g.parts == 4 || (g.ctas == 0 && g.parts == 8);
@@ -1082,7 +1083,10 @@ bool given_ok(const Given& g, const F8Args& p) {
   if (g.ctas != 1 && g.ctas != 2) return false;
   if (g.rows != kM && (g.ctas == 2 || (g.rows != 64 && g.rows != 32 && g.rows != 16))) return false;
   if (g.channels < 64 || g.channels > Tc::NT || g.channels % 64) return false;
-  return g.parts == 1 || (!p.offsets && blocks >= 2 * g.parts);
+  // (every tile has a cluster of its own where K is split, and a grid its limit)
+  const int M = g.rows * g.ctas;
+  const int64_t tiles = (static_cast<int64_t>(p.T) + M - 1) / M * ((p.N + g.channels - 1) / g.channels);
+  return g.parts == 1 || (!p.offsets && blocks >= 2 * g.parts && tiles <= 65535);
 }
 
 template <typename O>

@@ -782,7 +782,7 @@ int pw_debug_linear_f8_timeout(pw_stream_t s);
  * tested at any size.
  *   ctas 1, 2  tiles of `rows` rows (128; of one CTA also 16, 32 or 64) by `channels` (64,
  *              128, 192 or 256) to a CTA or a pair of them, K in `parts` (1; without
- *              offsets 2 or 4, of two blocks of 128 columns or more each)
+ *              offsets and up to 65535 tiles 2 or 4, of two blocks of 128 columns or more each)
  *   ctas 0     few rows: `rows` (8 or 16) at a time, a group's shared by `channels` CTAs (1 to
  *              65535 / E), K by `parts` warps (1, 2, 4 or 8, no more than its blocks)
  * Errors: as pw_linear_f8, and PW_EINVAL for any other way.

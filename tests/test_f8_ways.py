@@ -18,9 +18,11 @@ def test_refused(kw):
     refused("pw_debug_linear_f8", {**WAY, **GROUPED}, kw)
 
 
-@pytest.mark.parametrize("kw", [dict(parts=4), dict(parts=8, K=8000), dict(ctas=2, parts=2), dict(ctas=0, rows=16, channels=1, parts=16)])
+@pytest.mark.parametrize("kw", [dict(parts=4), dict(parts=8, K=8000), dict(ctas=2, parts=2), dict(ctas=0, rows=16, channels=1, parts=16),
+                                dict(parts=2, K=8000, T=1 << 20, N=1 << 13), dict(parts=4, K=8000, ctas=2, T=1 << 23, N=600)])
 def test_refused_without_groups(kw):
     one = {**WAY, **GROUPED, "off": None, "E": 1}   # K = 200: two blocks
+    one["ldo"] = max(one["ldo"], kw.get("N", 0))
     wide = dict(ldx=8000, ldw=8000, ldxs=63, ldws=63) if "K" in kw else {}
     refused("pw_debug_linear_f8", one, {**kw, **wide})
 
